@@ -384,6 +384,90 @@ pmoe_status adapter_cayley(int32_t nblk, int32_t b, const float *S, void *R_bf16
 pmoe_status adapter_cayley_grad(int32_t nblk, int32_t b, const float *S, const float *R_f32,
                                 const float *dR, float *dS, cudaStream_t stream);
 
+/*
+ * The vocabulary head and its losses: what a training step of adapter-first
+ * RL on a frozen base scores and differentiates (the Orbit analysis, 机制拆解:
+ * the reference policy is the base with the adapter disabled; NeMo RL FP8
+ * article, Table 1: token-mult-prob-error compares token log-probabilities).
+ * The pages give no head; the operations are the textbook ones:
+ *   z = X W^T (FP32),  p = softmax(scale z),  lse = log sum_v exp(scale z_v)
+ * with X bf16 [T, d] hidden states and W bf16 [V, d] the head.  The logits
+ * are never stored: the forward keeps one (max, sum) pair per token and 128
+ * vocabulary entries, the backward recomputes z in pieces of the vocabulary
+ * and holds G = dL/dz of one piece (at most 512 MiB) in the workspace.
+ *   T >= 0 tokens, d % 64 == 0, d <= 8192, 1 <= V <= 2^24, T <= 2^24
+ *   K  teacher entries per token (distillation), <= 256; ignored otherwise
+ *   scale  factor of every logit, 1 / temperature: finite and > 0
+ * A token's forward results do not depend on the other tokens of the call
+ * (bit-identical across T), and every result is run-to-run identical.
+ * The sums over d run in FP32 chunks of 512 columns added in FP32.
+ */
+typedef struct {
+    int32_t T, d, V, K;
+} pmoe_head_dims;
+
+/* Ops for head_workspace_bytes. */
+enum { PMOE_HEAD_FORWARD = 0, PMOE_HEAD_BACKWARD = 1 };
+
+/* Bytes of device workspace (the error word included); 0 for invalid dims. */
+size_t head_workspace_bytes(pmoe_head_dims dims, int op);
+
+/*
+ * head_logprob_forward -- logp_t = scale z_{t, y_t} - lse_t (the negative
+ * softmax cross entropy) of the token's target y_t.
+ *   target int32 [T]; a negative target is an ignored token: logp = 0, no
+ *          gradient.  A target >= V is ignored and recorded as
+ *          PMOE_ERR_BAD_INDEX in the error word.
+ *   logp   f32 [T] (out)          lse f32 [T] (out; the backward's input)
+ *   ws     >= head_workspace_bytes(dims, PMOE_HEAD_FORWARD)
+ */
+pmoe_status head_logprob_forward(pmoe_head_dims dims, const void *X, const void *W, float scale,
+                                 const int32_t *target, float *logp, float *lse,
+                                 void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * head_logprob_backward -- for upstream gradients g_t = dL/dlogp_t:
+ *   G_tv = g_t scale ([v = y_t] - p_tv);  dX = bf16(G W);  dW = bf16(G^T X)
+ * G enters both products in BF16, and where a block of 128 tokens and 128
+ * entries holds a large one (|[v = y] - p| >= 1/8) as two BF16 terms (16
+ * bits); the sums are FP32.
+ *   lse    f32 [T] from the forward       g   f32 [T] (in)
+ *   dX     bf16 [T, d] or NULL (out)      dW  bf16 [V, d] or NULL (out,
+ *          overwritten; NULL: the head is frozen); one of them is needed
+ *   ws     >= head_workspace_bytes(dims, PMOE_HEAD_BACKWARD)
+ */
+pmoe_status head_logprob_backward(pmoe_head_dims dims, const void *X, const void *W, float scale,
+                                  const int32_t *target, const float *lse, const float *g,
+                                  void *dX, void *dW, void *ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * head_distill_forward -- distance to a teacher known by its top K logits
+ * per token:
+ *   q = softmax(scale t) over the entries present
+ *   loss_t = sum_k q_k (log q_k - log p_{t, idx_k})
+ *   t_idx    int32 [T, K] vocabulary ids in any order; a negative id is an
+ *            absent entry, and an id >= V is absent and recorded as
+ *            PMOE_ERR_BAD_INDEX.  Two entries with one id add up.
+ *   t_logits f32 [T, K]; -inf is an entry of probability zero, others finite
+ *   loss     f32 [T] (out), 0 for a token without entries
+ *   lse      f32 [T] (out)
+ *   ws       >= head_workspace_bytes(dims, PMOE_HEAD_FORWARD)
+ */
+pmoe_status head_distill_forward(pmoe_head_dims dims, const void *X, const void *W, float scale,
+                                 const int32_t *t_idx, const float *t_logits, float *loss,
+                                 float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * head_distill_backward -- for upstream gradients g_t = dL/dloss_t:
+ *   G_tv = g_t scale (p_tv - sum_{k: idx_k = v} q_k)   (0 without entries)
+ * and dX, dW as in head_logprob_backward.
+ */
+pmoe_status head_distill_backward(pmoe_head_dims dims, const void *X, const void *W, float scale,
+                                  const int32_t *t_idx, const float *t_logits, const float *lse,
+                                  const float *g, void *dX, void *dW, void *ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
 /* Bytes of device workspace an op needs (op = PMOE_OP_*).  Includes the
  * 256-byte error word at the start.  In SCRATCH mode this includes the
  * C-expert BF16 dequant buffer, reported separately by

@@ -1,0 +1,501 @@
+// head.cu -- losses of the vocabulary head: token log-probabilities and
+// distillation from a teacher's top logits, forward and backward, without
+// keeping the logits.  The products run on the tensor cores
+// (head_gemm.cuh); this file holds the per-token kernels, the workspace
+// layout, the choice of tiles and the entry points.
+#include <cmath>
+#include <cstring>
+
+#include "gemm_tc_host.cuh"
+#include "head_gemm.cuh"
+
+namespace pmoe {
+namespace hg {
+
+constexpr int kMaxK = 256;                    // teacher entries per token
+constexpr int kSms = 152;                     // SMs of a GB300
+constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece, remainders included
+constexpr int32_t kNoId = 0x7fffffff;
+
+// ------------------------------------------------------------------ targets
+// Distillation: one warp per token turns the teacher's K entries into a
+// probability each, q = softmax(scale t) over the entries present, ordered
+// by vocabulary id (missing ones last, id kNoId, q = 0): the GEMM's
+// epilogue then finds a column range's entries by a binary search.  The
+// place of an entry is the number of entries before it in (id, slot) order.
+__global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float scale, const int32_t *__restrict__ t_idx,
+                                                      const float *__restrict__ t_logits, const float *__restrict__ g,
+                                                      int32_t *__restrict__ ids, float *__restrict__ q,
+                                                      float *__restrict__ lq, float *__restrict__ coef, DevErr *err)
+{
+    __shared__ int32_t skey[4][kMaxK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * 4 + warp;
+    if (t >= T) return;
+    const float inf = __int_as_float(0x7f800000);
+    float x[kMaxK / 32];
+    float m = -inf;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kMaxK / 32; ++i) {
+        const int k = i * 32 + lane;
+        x[i] = -inf;
+        if (k >= K) continue;
+        const int id = t_idx[(int64_t)t * K + k];
+        const float l = t_logits[(int64_t)t * K + k] * scale;
+        if (id >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, id);
+        const bool has = id >= 0 && id < V && l != -inf;   // (a logit of -inf has probability zero)
+        skey[warp][k] = has ? id : kNoId;
+        if (has) {
+            x[i] = l;
+            m = fmaxf(m, l);
+            any = true;
+        }
+    }
+    any = __any_sync(0xffffffffu, any);
+    float s = 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int i = 0; i < kMaxK / 32; ++i)
+        if (any) s += expf(x[i] - m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float ls = logf(s);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kMaxK / 32; ++i) {
+        const int k = i * 32 + lane;
+        if (k >= K) continue;
+        const int32_t key = skey[warp][k];
+        int r = 0;
+        for (int j = 0; j < K; ++j) {
+            const int32_t o = skey[warp][j];
+            r += o < key || (o == key && j < k);
+        }
+        const bool has = key != kNoId;
+        const int64_t at = (int64_t)t * K + r;
+        ids[at] = key;
+        q[at] = has ? expf(x[i] - m) / s : 0.f;
+        if (lq) lq[at] = has ? x[i] - m - ls : 0.f;
+    }
+    if (coef && lane == 0) coef[t] = any ? g[t] * scale : 0.f;
+}
+
+// Log-probability: the row's factor of dz = g s (onehot - p) = coef (p - onehot)
+__global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, const int32_t *__restrict__ target,
+                                                   const float *__restrict__ g, float *__restrict__ coef, DevErr *err)
+{
+    const int t = blockIdx.x * 256 + threadIdx.x;
+    if (t >= T) return;
+    const int y = target[t];
+    if (y >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
+    coef[t] = y >= 0 && y < V ? -g[t] * scale : 0.f;
+}
+
+// ------------------------------------------------------------------ combine
+// One CTA per token joins the NU softmax partials in one fixed order, and
+// forms the token's value from the target logits.
+__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float scale, bool distill,
+                                                      const float2 *__restrict__ part, const float *__restrict__ zt,
+                                                      const int32_t *__restrict__ ids, const float *__restrict__ q,
+                                                      const float *__restrict__ lq, float *__restrict__ value,
+                                                      float *__restrict__ lse, DevErr *err)
+{
+    __shared__ float2 sw[4];
+    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float ninf = -__int_as_float(0x7f800000);
+    const float2 *p = part + (int64_t)t * NU;
+    float m = ninf, s = 0.f;   // base 2
+    for (int i = threadIdx.x; i < NU; i += 128) {
+        const float2 v = p[i];
+        const float n = fmaxf(m, v.x);
+        s = s * exp2f(m - n) + v.y * exp2f(v.x - n);
+        m = n;
+    }
+    // (a thread without partials has m = -inf, s = 0)
+    auto join = [&](float om, float os) {
+        const float n = fmaxf(m, om);
+        const float a = m == ninf ? 0.f : s * exp2f(m - n), b = om == ninf ? 0.f : os * exp2f(om - n);
+        m = n;
+        s = a + b;
+    };
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+        join(om, os);
+    }
+    if (lane == 0) sw[warp] = make_float2(m, s);
+    __syncthreads();
+    if (warp) return;
+    m = sw[0].x;
+    s = sw[0].y;
+    for (int i = 1; i < 4; ++i) join(sw[i].x, sw[i].y);
+    const float l = m * 0.6931471805599453f + logf(s);
+    float v = 0.f;
+    if (distill) {
+        for (int k = lane; k < K; k += 32) {
+            const int64_t at = (int64_t)t * K + k;
+            if (ids[at] != kNoId) v += q[at] * (lq[at] - (zt[at] * scale - l));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+        const int y = ids[t];
+        if (y >= 0 && y < V) v = zt[t] * scale - l;
+        else if (y >= V && lane == 0) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
+    }
+    if (lane == 0) {
+        value[t] = v;
+        lse[t] = l;
+    }
+}
+
+// dX = bf16(sum of the splits' FP32 partials, in order); n elements each, n % 8 == 0
+__global__ void __launch_bounds__(256) k_head_sum(int64_t n, int splits, const float *__restrict__ part,
+                                                  uint16_t *__restrict__ out)
+{
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ll) {
+        float4 a = *(const float4 *)(part + i), b = *(const float4 *)(part + i + 4);
+        for (int s = 1; s < splits; ++s) {
+            const float4 c = *(const float4 *)(part + s * n + i), d = *(const float4 *)(part + s * n + i + 4);
+            a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+            b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+        }
+        *(uint4 *)(out + i) = make_uint4(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w), pack_bf2(b.x, b.y), pack_bf2(b.z, b.w));
+    }
+}
+
+// ------------------------------------------------------------------ plan
+static bool head_ok(const pmoe_head_dims &h)
+{
+    return h.T >= 0 && h.d > 0 && h.d % 64 == 0 && h.d <= 8192 && h.V > 0 && h.V <= (1 << 24) && h.K >= 0 &&
+           h.K <= kMaxK && h.T <= (1 << 24);
+}
+
+// Vocabulary entries per piece of the backward: G of one piece and its
+// remainders are at most kPieceBytes; pieces of equal size, multiples of 256.
+static int piece_of(int T, int V)
+{
+    int64_t most = kPieceBytes / (4ll * std::max(T, 1)) / 256 * 256;
+    most = std::max<int64_t>(most, 256);
+    const int64_t np = cdiv(V, most);
+    return (int)(cdiv(cdiv(V, np), 256) * 256);
+}
+
+struct Tiling {
+    int ctas, bn;
+    int mt, nt;
+    int splits, kper;
+};
+// Tiles of an M x N product.  `split`: K steps may be divided among the
+// SMs that the tiles leave idle (the partial sums are then added up).
+static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
+{
+    Tiling t;
+    t.ctas = 1;
+    t.bn = 128 * t.ctas;
+    t.mt = (int)cdiv(M, 128 * t.ctas);
+    t.nt = (int)cdiv(N, t.bn);
+    const int64_t slots = kSms / t.ctas, tiles = (int64_t)t.mt * t.nt;
+    int64_t s = 1;
+    if (split && tiles > 0) s = std::max<int64_t>(1, std::min(slots / tiles, ksteps / (2 * kChunk)));
+    t.kper = (int)(cdiv(cdiv(std::max<int64_t>(ksteps, 1), s), kChunk) * kChunk);   // whole chunks
+    t.splits = (int)cdiv(std::max<int64_t>(ksteps, 1), t.kper);
+    return t;
+}
+static Tiling dx_tiling(const pmoe_head_dims &h)
+{
+    return tiling(h.T, h.d, cdiv(std::min(piece_of(h.T, h.V), h.V), kBK), true);
+}
+
+struct Ws {
+    DevErr *err;
+    int32_t *ids;            // [T][K] sorted teacher ids
+    float *q, *lq;           // [T][K]
+    float *zt;               // [T][max(K, 1)]
+    float2 *part;            // [T][NU]
+    float *coef;             // [T]
+    uint16_t *G, *Glo;       // [T][piece] and the remainders of its flagged blocks
+    uint8_t *fl, *flt;       // the flags [T / 128][fs] and transposed [piece / 128][fst]
+    int fs, fst;
+    float *dx;               // [splits][T][d]
+    size_t bytes;
+};
+static Ws carve(void *base, const pmoe_head_dims &h, int op)
+{
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        uint8_t *p = base ? (uint8_t *)base + off : nullptr;
+        off += (n + 255) & ~(size_t)255;
+        return p;
+    };
+    Ws w{};
+    const size_t T = h.T, K = h.K;
+    w.err = (DevErr *)take(kHdrBytes);
+    w.ids = (int32_t *)take(T * K * 4);
+    w.q = (float *)take(T * K * 4);
+    if (op == PMOE_HEAD_FORWARD) {
+        w.lq = (float *)take(T * K * 4);
+        w.zt = (float *)take(T * std::max<size_t>(K, 1) * 4);
+        w.part = (float2 *)take(T * cdiv(h.V, kUnit) * 8);
+    } else {
+        const int piece = piece_of(h.T, h.V);
+        const Tiling t = dx_tiling(h);
+        w.coef = (float *)take(T * 4);
+        w.G = (uint16_t *)take(T * piece * 2);
+        w.Glo = (uint16_t *)take(T * piece * 2);
+        const size_t tb = cdiv(h.T, 128), vb = piece / 128;
+        w.fs = (int)cdiv(vb, 16) * 16;
+        w.fst = (int)cdiv(tb, 16) * 16;
+        w.fl = take(tb * w.fs);
+        w.flt = take(vb * w.fst);
+        if (t.splits > 1 || piece < h.V) w.dx = (float *)take((size_t)t.splits * T * h.d * 4);
+    }
+    w.bytes = off;
+    return w;
+}
+
+// ------------------------------------------------------------------ launch
+struct Operand {
+    const void *base;
+    int64_t cols, rows;
+    bool mn;                 // the contiguous axis is M (or N), not K
+};
+static bool map_operand(CUtensorMap *m, const Operand &o)
+{
+    return tc::make_tmap3(m, o.base, false, o.cols, o.rows, 0, kBK, o.mn ? 64 : 128);
+}
+
+template <int CTAS, int BN, int EPI>
+static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap &ml,
+                      const Args &a, cudaStream_t st)
+{
+    auto kern = k_head_gemm<CTAS, BN, EPI>;
+    static const bool attr =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(BN)) == cudaSuccess;
+    if (!attr) return false;
+    const int64_t items = (int64_t)a.mt * a.nt * a.splits;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(items, tc::num_sms() / CTAS) * CTAS));
+    cfg.blockDim = dim3(threads_of(BN));
+    cfg.dynamicSmemBytes = smem_of(BN);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {CTAS, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, ml, a) != cudaSuccess) return false;
+    note_launch();
+    return true;
+}
+
+// One product: M x N outputs over ksteps K steps, with the tiles of `t`;
+// `lo`: the remainders of G (written by GRAD, read by DX and DW as A is)
+template <int EPI>
+static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CUtensorMap *out, const CUtensorMap *lo,
+                   Args a, cudaStream_t st)
+{
+    CUtensorMap ma, mb, mo, ml;
+    if (!map_operand(&ma, A) || !map_operand(&mb, B)) return false;
+    memset(&mo, 0, sizeof mo);
+    memset(&ml, 0, sizeof ml);
+    if (out) mo = *out;
+    if (lo) ml = *lo;
+    a.arows = (int)A.rows;
+    a.mt = t.mt;
+    a.nt = t.nt;
+    a.splits = t.splits;
+    a.kper = t.kper;
+    // m tiles that run together: their rows of A stay in L2 (48 MB) while the n tiles pass
+    const int64_t stripe = 2ll * 128 * t.ctas * a.ksteps * kBK;
+    a.gm = (int)std::max<int64_t>(1, std::min<int64_t>(t.mt, std::max<int64_t>(8, (48ll << 20) / stripe)));
+    return launch_as<1, 128, EPI>(ma, mb, mo, ml, a, st);
+}
+
+// ------------------------------------------------------------------ passes
+static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W, float scale, const int32_t *idx,
+                           const float *t_logits, bool distill, float *value, float *lse, const Ws &w, cudaStream_t st)
+{
+    const int K = distill ? h.K : 1;
+    const int32_t *ids = idx;
+    if (distill) {
+        k_head_teacher<<<(unsigned)cdiv(h.T, 4), 128, 0, st>>>(h.T, h.V, K, scale, idx, t_logits, nullptr, w.ids, w.q,
+                                                               w.lq, nullptr, w.err);
+        note_launch();
+        ids = w.ids;
+    }
+    Args a{};
+    a.M = h.T;
+    a.N = h.V;
+    a.V = h.V;
+    a.ksteps = h.d / kBK;
+    a.c = scale * 1.4426950408889634f;
+    a.NU = (int)cdiv(h.V, kUnit);
+    a.part = w.part;
+    a.zt = w.zt;
+    a.ids = ids;
+    a.K = K;
+    a.err = w.err;
+    if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
+                        st))
+        return PMOE_ERR_CUDA;
+    k_head_combine<<<h.T, 128, 0, st>>>(h.V, K, a.NU, scale, distill, w.part, w.zt, ids, w.q, w.lq, value, lse, w.err);
+    note_launch();
+    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+}
+
+static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *W, float scale, const int32_t *idx,
+                            const float *t_logits, bool distill, const float *lse, const float *g, void *dX, void *dW,
+                            const Ws &w, cudaStream_t st)
+{
+    const int K = distill ? h.K : 1;
+    if (distill)
+        k_head_teacher<<<(unsigned)cdiv(h.T, 4), 128, 0, st>>>(h.T, h.V, K, scale, idx, t_logits, g, w.ids, w.q, nullptr,
+                                                               w.coef, w.err);
+    else
+        k_head_coef<<<(unsigned)cdiv(h.T, 256), 256, 0, st>>>(h.T, h.V, scale, idx, g, w.coef, w.err);
+    note_launch();
+    const int piece = piece_of(h.T, h.V);
+    const Tiling tx = dx_tiling(h);
+    for (int v0 = 0; v0 < h.V; v0 += piece) {
+        const int vc = std::min(piece, h.V - v0);
+        const int64_t ldg = piece;
+        CUtensorMap mo, ml;
+        Args b{};   // what the piece's products share
+        b.fl = w.fl;
+        b.flt = w.flt;
+        b.fs = w.fs;
+        b.fst = w.fst;
+        b.err = w.err;
+        {   // G = coef (softmax(Z) - q) of this piece
+            Args a = b;
+            a.M = h.T;
+            a.N = (int)ldg;
+            a.n0 = v0;
+            a.V = h.V;
+            a.ksteps = h.d / kBK;
+            a.c = scale * 1.4426950408889634f;
+            a.ids = distill ? w.ids : idx;
+            a.q = distill ? w.q : nullptr;
+            a.K = K;
+            a.lse = lse;
+            a.coef = w.coef;
+            if (!tc::make_tmap3(&mo, w.G, false, ldg, h.T, 1, 64, 128) ||
+                !tc::make_tmap3(&ml, w.Glo, false, ldg, h.T, 1, 64, 128) ||
+                !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo, &ml,
+                                 a, st))
+                return PMOE_ERR_CUDA;
+        }
+        if (dX) {
+            Args a = b;
+            a.M = h.T;
+            a.N = h.d;
+            a.ksteps = (int)cdiv(vc, kBK);
+            a.kb0 = v0;
+            a.bf16_out = w.dx == nullptr;
+            a.accumulate = v0 > 0;
+            Tiling t = tx;
+            const bool made = w.dx ? tc::make_tmap3(&mo, w.dx, true, h.d, h.T, t.splits, 32, 128)
+                                   : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 128);
+            // (a last, shorter piece may leave the last splits without K steps)
+            t.splits = (int)cdiv(a.ksteps, t.kper);
+            if (!made || !map_operand(&ml, {w.Glo, ldg, h.T, false}) ||
+                !launch<HG_DX>(t, {w.G, ldg, h.T, false}, {W, h.d, h.V, true}, &mo, &ml, a, st))
+                return PMOE_ERR_CUDA;
+        }
+        if (dW) {
+            Args a = b;
+            a.M = vc;
+            a.N = h.d;
+            a.ksteps = (int)cdiv(h.T, kBK);
+            if (!tc::make_tmap3(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 128) ||
+                !map_operand(&ml, {w.Glo, ldg, h.T, true}) ||
+                !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {X, h.d, h.T, true}, &mo, &ml, a,
+                               st))
+                return PMOE_ERR_CUDA;
+        }
+    }
+    if (dX && w.dx) {
+        const int64_t n = (int64_t)h.T * h.d;
+        k_head_sum<<<(unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, st>>>(n, tx.splits, w.dx, (uint16_t *)dX);
+        note_launch();
+    }
+    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+}
+
+// Argument checks shared by the entry points; PMOE_OK to go on
+static pmoe_status check(const pmoe_head_dims &h, float scale, std::initializer_list<const void *> needed,
+                         std::initializer_list<const void *> optional, const void *ws, size_t ws_bytes, size_t need)
+{
+    if (!(scale > 0.f) || !std::isfinite(scale)) return PMOE_ERR_INVALID_ARG;
+    for (const void *p : needed)
+        if ((h.T > 0 && !p) || ((uintptr_t)p & 15)) return PMOE_ERR_INVALID_ARG;
+    for (const void *p : optional)
+        if ((uintptr_t)p & 15) return PMOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return PMOE_ERR_WORKSPACE;
+    return PMOE_OK;
+}
+
+}  // namespace hg
+}  // namespace pmoe
+
+using namespace pmoe;
+
+extern "C" {
+
+size_t head_workspace_bytes(pmoe_head_dims dims, int op)
+{
+    if (!hg::head_ok(dims) || (op != PMOE_HEAD_FORWARD && op != PMOE_HEAD_BACKWARD)) return 0;
+    return hg::carve(nullptr, dims, op).bytes;
+}
+
+pmoe_status head_logprob_forward(pmoe_head_dims dims, const void *X, const void *W, float scale, const int32_t *target,
+                                 float *logp, float *lse, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!hg::head_ok(dims)) return PMOE_ERR_INVALID_ARG;
+    const hg::Ws w = hg::carve(ws, dims, PMOE_HEAD_FORWARD);
+    const pmoe_status s = hg::check(dims, scale, {X, W, target, logp, lse}, {}, ws, ws_bytes, w.bytes);
+    if (s != PMOE_OK || dims.T == 0) return s;
+    return hg::forward(dims, X, W, scale, target, nullptr, false, logp, lse, w, stream);
+}
+
+pmoe_status head_logprob_backward(pmoe_head_dims dims, const void *X, const void *W, float scale, const int32_t *target,
+                                  const float *lse, const float *g, void *dX, void *dW, void *ws, size_t ws_bytes,
+                                  cudaStream_t stream)
+{
+    if (!hg::head_ok(dims) || (!dX && !dW)) return PMOE_ERR_INVALID_ARG;
+    const hg::Ws w = hg::carve(ws, dims, PMOE_HEAD_BACKWARD);
+    const pmoe_status s = hg::check(dims, scale, {X, W, target, lse, g}, {dX, dW}, ws, ws_bytes, w.bytes);
+    if (s != PMOE_OK) return s;
+    if (dims.T == 0)
+        return !dW || cudaMemsetAsync(dW, 0, (size_t)dims.V * dims.d * 2, stream) == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+    return hg::backward(dims, X, W, scale, target, nullptr, false, lse, g, dX, dW, w, stream);
+}
+
+pmoe_status head_distill_forward(pmoe_head_dims dims, const void *X, const void *W, float scale, const int32_t *t_idx,
+                                 const float *t_logits, float *loss, float *lse, void *ws, size_t ws_bytes,
+                                 cudaStream_t stream)
+{
+    if (!hg::head_ok(dims) || dims.K < 1) return PMOE_ERR_INVALID_ARG;
+    const hg::Ws w = hg::carve(ws, dims, PMOE_HEAD_FORWARD);
+    const pmoe_status s = hg::check(dims, scale, {X, W, t_idx, t_logits, loss, lse}, {}, ws, ws_bytes, w.bytes);
+    if (s != PMOE_OK || dims.T == 0) return s;
+    return hg::forward(dims, X, W, scale, t_idx, t_logits, true, loss, lse, w, stream);
+}
+
+pmoe_status head_distill_backward(pmoe_head_dims dims, const void *X, const void *W, float scale, const int32_t *t_idx,
+                                  const float *t_logits, const float *lse, const float *g, void *dX, void *dW, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream)
+{
+    if (!hg::head_ok(dims) || dims.K < 1 || (!dX && !dW)) return PMOE_ERR_INVALID_ARG;
+    const hg::Ws w = hg::carve(ws, dims, PMOE_HEAD_BACKWARD);
+    const pmoe_status s = hg::check(dims, scale, {X, W, t_idx, t_logits, lse, g}, {dX, dW}, ws, ws_bytes, w.bytes);
+    if (s != PMOE_OK) return s;
+    if (dims.T == 0)
+        return !dW || cudaMemsetAsync(dW, 0, (size_t)dims.V * dims.d * 2, stream) == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+    return hg::backward(dims, X, W, scale, t_idx, t_logits, true, lse, g, dX, dW, w, stream);
+}
+
+}  // extern "C"

@@ -21,6 +21,7 @@ W_INT4_G32_BF16, W_MXFP4_G32_E8M0, W_FP8_B128_F32 = 0, 1, 2
 MODE_FUSED, MODE_SCRATCH = 0, 1
 ROUTE_FAST, ROUTE_EXACT = 0, 1
 OP_PERMUTE, OP_FORWARD, OP_BACKWARD = 0, 1, 2
+HEAD_FORWARD, HEAD_BACKWARD = 0, 1
 
 EXPORTS = ("moe_route", "moe_permute", "moe_chunked_forward", "moe_backward_data", "moe_dequant",
            "adapter_apply", "adapter_grad", "adapter_cayley", "adapter_cayley_grad",
@@ -29,7 +30,9 @@ EXPORTS = ("moe_route", "moe_permute", "moe_chunked_forward", "moe_backward_data
            "pmoe_status_string", "pmoe_launch_count", "pmoe_kernel_timing", "pmoe_kernel_time",
            "moe_grouped_gemm", "moe_grouped_gemm_ws_bytes", "moe_permute_noalloc",
            "dense_linear_ws_bytes", "dense_linear_forward", "dense_linear_backward",
-           "moe_adapter_publish", "moe_chunked_forward_slots", "pmoe_debug_expire_gemm_wait")
+           "moe_adapter_publish", "moe_chunked_forward_slots", "pmoe_debug_expire_gemm_wait",
+           "head_workspace_bytes", "head_logprob_forward", "head_logprob_backward",
+           "head_distill_forward", "head_distill_backward")
 PERMUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 KT_GEMM_GATE_UP, KT_GEMM_DOWN, KT_GEMM_BWD_G, KT_GEMM_BWD_DX, KT_ROUTER = 0, 1, 2, 3, 4
 
@@ -43,6 +46,11 @@ class PmoeError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("k", ctypes.c_int32), ("inter", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class HeadDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("K", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):
@@ -87,6 +95,7 @@ def lib() -> ctypes.CDLL:
 def _declare(L):
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     st = ctypes.c_int
+    H, f32 = HeadDims, ctypes.c_float
     D, PW, PA, PR = Dims, ctypes.POINTER(Weights), ctypes.POINTER(Adapter), ctypes.POINTER(Routing)
     sig = {
         "moe_route": [D, p, p, p, p, p, p, ctypes.c_int, p, sz, p],
@@ -105,6 +114,10 @@ def _declare(L):
         "adapter_grad": [i32, i32, i32, p, p, p, p, p, p],
         "adapter_cayley": [i32, i32, p, p, p, p],
         "adapter_cayley_grad": [i32, i32, p, p, p, p, p],
+        "head_logprob_forward": [H, p, p, f32, p, p, p, p, sz, p],
+        "head_logprob_backward": [H, p, p, f32, p, p, p, p, p, p, sz, p],
+        "head_distill_forward": [H, p, p, f32, p, p, p, p, p, sz, p],
+        "head_distill_backward": [H, p, p, f32, p, p, p, p, p, p, p, sz, p],
         "moe_clear_status": [p, p],
         "moe_query_status": [p, p],
     }
@@ -120,6 +133,8 @@ def _declare(L):
     L.dense_linear_ws_bytes.restype = sz
     L.moe_scratch_bytes.argtypes = [D, i32, ctypes.c_int]
     L.moe_scratch_bytes.restype = sz
+    L.head_workspace_bytes.argtypes = [H, ctypes.c_int]
+    L.head_workspace_bytes.restype = sz
     L.moe_ctx_bytes.argtypes = [D]
     L.moe_ctx_bytes.restype = sz
     L.pmoe_debug_expire_gemm_wait.argtypes = [ctypes.c_uint64]
@@ -300,6 +315,38 @@ def adapter_cayley(nblk, b, S, R_bf16, R_f32, stream=None):
 def adapter_cayley_grad(nblk, b, S, R_f32, dR, dS, stream=None):
     _check(lib().adapter_cayley_grad(nblk, b, _ptr(S), _ptr(R_f32), _ptr(dR), _ptr(dS),
                                      _stream(stream)), "adapter_cayley_grad")
+
+
+def head_dims(T, d, V, K=0) -> HeadDims:
+    return HeadDims(T, d, V, K)
+
+
+def head_workspace_bytes(hd: HeadDims, op: int) -> int:
+    return lib().head_workspace_bytes(hd, op)
+
+
+def head_logprob_forward(hd, X, W, scale, target, logp, lse, ws, stream=None):
+    _check(lib().head_logprob_forward(hd, _ptr(X), _ptr(W), scale, _ptr(target), _ptr(logp),
+                                      _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "head_logprob_forward")
+
+
+def head_logprob_backward(hd, X, W, scale, target, lse, g, dX, dW, ws, stream=None):
+    _check(lib().head_logprob_backward(hd, _ptr(X), _ptr(W), scale, _ptr(target), _ptr(lse),
+                                       _ptr(g), _ptr(dX), _ptr(dW), _ptr(ws), _nbytes(ws),
+                                       _stream(stream)), "head_logprob_backward")
+
+
+def head_distill_forward(hd, X, W, scale, t_idx, t_logits, loss, lse, ws, stream=None):
+    _check(lib().head_distill_forward(hd, _ptr(X), _ptr(W), scale, _ptr(t_idx), _ptr(t_logits),
+                                      _ptr(loss), _ptr(lse), _ptr(ws), _nbytes(ws),
+                                      _stream(stream)), "head_distill_forward")
+
+
+def head_distill_backward(hd, X, W, scale, t_idx, t_logits, lse, g, dX, dW, ws, stream=None):
+    _check(lib().head_distill_backward(hd, _ptr(X), _ptr(W), scale, _ptr(t_idx), _ptr(t_logits),
+                                       _ptr(lse), _ptr(g), _ptr(dX), _ptr(dW), _ptr(ws),
+                                       _nbytes(ws), _stream(stream)), "head_distill_backward")
 
 
 def moe_clear_status(ws, stream=None):

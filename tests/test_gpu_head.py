@@ -1,0 +1,217 @@
+"""The vocabulary head's losses on the GPU against FP64: token
+log-probabilities and distillation from a teacher's top logits, forward and
+backward.
+
+Tolerances.  lse and the values come from FP32 sums of exact BF16 products.
+A sum of d products in chunks of 512 columns: the tensor cores lose at most
+about one unit in 2^24 of the running sum per 16 columns, 32 times a chunk,
+and the FP32 additions of the chunks less than that again, so a logit is
+within 2^-24 (32 + d / 512) sum |x w| <= 48 * 2^-24 sum |x w| of the exact
+one; exp2, the sums of the softmax and the logarithm add a few units in 2^24
+of |lse| and of 1.  Gradients are BF16 results of BF16 G: the layer's own
+tolerance for BF16 outputs (tests/helpers.py).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from helpers import assert_close
+from precision_moe_adapter_gb300 import build, pmoe
+from precision_moe_adapter_gb300.head import DeviceHead
+
+pytestmark = pytest.mark.gpu
+D = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    pmoe.lib()
+
+
+def make(T, d, V, seed=0, lean=8.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    W = (torch.randn((V, d), generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    X = torch.randn((T, d), generator=g, device="cuda")
+    X += lean * torch.rand((T, 1), generator=g, device="cuda") * W[y].float() / (4e-4 * d)
+    up = torch.randn(T, generator=g, device="cuda")
+    return X.to(torch.bfloat16), W, y.to(torch.int32), up, g
+
+
+def reference(X, W, scale, Q, Qx, g, sign):
+    """FP64: lse, the value sum_v Q (logQ - logp) or logp, dX, dW for the
+    target distribution Q [T, V] (rows may be empty)."""
+    z = scale * (X.to(D) @ W.to(D).T)
+    lse = torch.logsumexp(z, 1)
+    logp = z - lse[:, None]
+    G = (logp.exp() * Q.sum(1, keepdim=True) - Q) * (sign * scale * g.to(D))[:, None]
+    value = Qx - sign * (Q * logp).sum(1)
+    return lse, value, G @ W.to(D), G.T @ X.to(D)
+
+
+def logit_bound(X, W, scale):
+    return scale * 48 * 2.0 ** -24 * (X.to(D).abs() @ W.to(D).abs().T).amax(1)
+
+
+def run_logprob(X, W, y, up, scale, dW=True):
+    T = X.shape[0]
+    h = DeviceHead(W, T, scale=scale)
+    logp, lse = (torch.full((T,), float("nan"), device="cuda") for _ in range(2))
+    dX = torch.full_like(X, float("nan"))
+    dWt = torch.full_like(W, float("nan")) if dW else None
+    h.logprob(X, y, logp, lse)
+    h.logprob_backward(X, y, lse, up, dX, dWt)
+    torch.cuda.synchronize()
+    return h, logp, lse, dX, dWt
+
+
+def check_values(X, W, scale, lse, value, rlse, rvalue):
+    b = logit_bound(X, W, scale) + 2.0 ** -20 * (1 + rlse.abs())
+    assert torch.all((lse.to(D) - rlse).abs() <= b), ((lse.to(D) - rlse).abs() / b).max()
+    b = 2 * b + 2.0 ** -20 * (1 + rvalue.abs())
+    assert torch.all((value.to(D) - rvalue).abs() <= b), ((value.to(D) - rvalue).abs() / b).max()
+
+
+def check_grad(got, ref, what):
+    assert_close(got.float().cpu().numpy(), ref.cpu().numpy(), what)
+
+
+@pytest.mark.parametrize("T,d,V,scale", [
+    (1, 64, 1, 1.0), (1, 64, 2, 1.0), (1, 2048, 4099, 1.0), (2, 128, 127, 0.5), (7, 576, 129, 2.0),
+    (127, 256, 128, 1.0), (128, 512, 1000, 1.0), (129, 1088, 257, 1 / 0.7), (300, 256, 5003, 1.0),
+    (513, 192, 3001, 1.0), (64, 8192, 600, 1.0), (2100, 64, 640, 1.0), (260, 2048, 20011, 1.0)])
+def test_logprob(T, d, V, scale):
+    X, W, y, up, g = make(T, d, V, seed=T + d + V)
+    y = torch.where(torch.rand(T, generator=g, device="cuda") < 0.2, torch.full_like(y, -1), y)
+    h, logp, lse, dX, dW = run_logprob(X, W, y, up, scale)
+    assert h.status() == pmoe.PMOE_OK
+    Q = torch.zeros((T, V), dtype=D, device="cuda")
+    r = torch.nonzero(y >= 0)[:, 0]
+    Q[r, y[r].long()] = 1
+    rlse, rv, rdX, rdW = reference(X, W, scale, Q, 0.0, up, -1.0)
+    check_values(X, W, scale, lse, logp, rlse, rv)
+    assert torch.all(logp[y < 0] == 0) and torch.all(dX[y < 0] == 0)
+    check_grad(dX, rdX, "dX")
+    check_grad(dW, rdW, "dW")
+
+
+@pytest.mark.parametrize("T,d,V,K,scale", [
+    (1, 64, 3, 1, 1.0), (5, 64, 100, 7, 0.5), (130, 256, 1003, 64, 0.5), (33, 128, 256, 256, 1.0),
+    (300, 320, 5003, 33, 2.0), (16, 2048, 300, 129, 1.0)])
+def test_distill(T, d, V, K, scale):
+    X, W, y, up, g = make(T, d, V, seed=T + K)
+    perm = torch.rand((T, V), generator=g, device="cuda").argsort(1)[:, :K].to(torch.int32)
+    ids = perm.contiguous()
+    t = 2 * torch.randn((T, K), generator=g, device="cuda")
+    gone = torch.rand((T, K), generator=g, device="cuda") < 0.2
+    ids[gone] = -1
+    if T > 2:
+        ids[1] = -1                                   # a row without entries
+        t[2, K // 2] = -math.inf                      # an entry of probability zero
+    if T > 4 and K > 3:
+        ids[3] = ids[3, 0].clamp(min=0)               # one id many times
+        ids[4] = V - 1 - torch.arange(K, device="cuda", dtype=torch.int32).clamp(max=V - 1)
+    h = DeviceHead(W, T, K=K, scale=scale)
+    loss, lse = (torch.full((T,), float("nan"), device="cuda") for _ in range(2))
+    dX, dW = torch.full_like(X, float("nan")), torch.full_like(W, float("nan"))
+    h.distill(X, ids, t, loss, lse)
+    h.distill_backward(X, ids, t, lse, up, dX, dW)
+    assert h.status() == pmoe.PMOE_OK
+    td = (scale * t.to(D)).masked_fill(ids < 0, -math.inf)
+    q = torch.nan_to_num(torch.softmax(td, 1))
+    Q = torch.zeros((T, V), dtype=D, device="cuda").scatter_add_(1, ids.clamp(min=0).long(), q)
+    rlse, rv, rdX, rdW = reference(X, W, scale, Q, torch.xlogy(q, q).sum(1), up, 1.0)
+    check_values(X, W, scale, lse, loss, rlse, rv)
+    if T > 2:
+        assert loss[1] == 0 and torch.all(dX[1] == 0)
+    check_grad(dX, rdX, "dX")
+    check_grad(dW, rdW, "dW")
+
+
+def test_vocabulary_in_several_pieces():
+    """T = 8192 tokens bound a piece to 32768 entries: three pieces, the last one ragged."""
+    T, d, V = 8192, 64, 70001
+    X, W, y, up, _ = make(T, d, V)
+    h, logp, lse, dX, dW = run_logprob(X, W, y, up, 1.0)
+    assert h.status() == pmoe.PMOE_OK
+    rdW = torch.zeros((V, d), dtype=D, device="cuda")
+    for a in range(0, T, 1024):
+        r = slice(a, a + 1024)
+        Q = torch.zeros((1024, V), dtype=D, device="cuda")
+        Q[torch.arange(1024, device="cuda"), y[r].long()] = 1
+        rlse, rv, rdX, dw = reference(X[r], W, 1.0, Q, 0.0, up[r], -1.0)
+        rdW += dw
+        check_values(X[r], W, 1.0, lse[r], logp[r], rlse, rv)
+        check_grad(dX[r], rdX, "dX")
+    check_grad(dW, rdW, "dW")
+
+
+def test_gradient_against_differences():
+    """dL/dX along random sign directions against central differences of the
+    forward.  X lies on a grid of 1/64 below 2, so X +- 1/64 is exact in
+    BF16; the step's third-order term and the FP32 forward leave under 1%."""
+    T, d, V = 37, 128, 1003
+    X, W, y, up, g = make(T, d, V)
+    W = (W.float() * 8).to(torch.bfloat16)
+    X = ((X.float().clamp(-1.9, 1.9) * 64).round() / 64).to(torch.bfloat16)
+    h, _, _, dX, dW = run_logprob(X, W, y, up, 1.0)
+    logp, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+
+    def L(x):
+        h.logprob(x, y, logp, lse)
+        return logp.to(D) * up.to(D)
+
+    for _ in range(3):
+        U = torch.randint(0, 2, (T, d), generator=g, device="cuda").float() * 2 - 1
+        num = (L((X.float() + U / 64).to(torch.bfloat16)) - L((X.float() - U / 64).to(torch.bfloat16))) * 32
+        ana = (dX.to(D) * U.to(D)).sum(1)
+        assert (num - ana).norm() <= 1e-2 * ana.norm()
+
+
+def test_a_token_does_not_depend_on_the_batch():
+    T, d, V = 700, 2048, 20011
+    X, W, y, up, _ = make(T, d, V)
+    full = run_logprob(X, W, y, up, 1.0, dW=False)
+    for n in (1, 7, 128, 129, 300):
+        part = run_logprob(X[:n].clone(), W, y[:n].clone(), up[:n].clone(), 1.0, dW=False)
+        assert torch.equal(part[1], full[1][:n]) and torch.equal(part[2], full[2][:n]), n
+
+
+def test_runs_are_identical_and_use_the_given_stream():
+    T, d, V = 333, 256, 9001
+    X, W, y, up, _ = make(T, d, V)
+    ref = run_logprob(X, W, y, up, 1.0)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        again = run_logprob(X, W, y, up, 1.0)
+    for a, b in zip(ref[1:], again[1:]):
+        assert torch.equal(a, b)
+
+
+def test_no_tokens_and_ids_out_of_range():
+    W = torch.ones((50, 64), dtype=torch.bfloat16, device="cuda")
+    e = torch.empty(0, device="cuda")
+    h = DeviceHead(W, 0)
+    dW = torch.full_like(W, 3.0)
+    X = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    h.logprob(X, e.to(torch.int32), e, e)
+    h.logprob_backward(X, e.to(torch.int32), e, e, X, dW)
+    assert torch.all(dW == 0) and h.status() == pmoe.PMOE_OK
+    # a target past the vocabulary is ignored and reported
+    X, W, y, up, _ = make(4, 64, 50)
+    y[2] = 50
+    h, logp, lse, dX, _ = run_logprob(X, W, y, up, 1.0)
+    assert h.status() == pmoe.PMOE_ERR_BAD_INDEX
+    assert logp[2] == 0 and torch.all(dX[2] == 0) and torch.all(torch.isfinite(lse))
+    h = DeviceHead(W, 4, K=2)
+    ids = torch.tensor([[0, 1], [50, 3], [2, -1], [2 ** 31 - 1, 60]], dtype=torch.int32, device="cuda")
+    t = torch.zeros((4, 2), device="cuda")
+    loss, lse = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    h.distill(X, ids, t, loss, lse)
+    assert h.status() == pmoe.PMOE_ERR_BAD_INDEX
+    assert loss[3] == 0 and np.isfinite(loss.cpu().numpy()).all()
