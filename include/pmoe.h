@@ -468,6 +468,51 @@ pmoe_status head_distill_backward(pmoe_head_dims dims, const void *X, const void
                                   const float *g, void *dX, void *dW, void *ws, size_t ws_bytes,
                                   cudaStream_t stream);
 
+/*
+ * moe_balance_forward / moe_route_backward -- the router's training side
+ * (moe_backward_data leaves d_topk_w to the caller; the pages give no router
+ * loss, the balance loss is the usual product of load and probability).
+ * Tokens lie in nseq packed sequences, tokens seq[s] .. seq[s+1]-1 in
+ * sequence s; the loss is per sequence (one sequence: per batch):
+ *   p_t = softmax(logits_t) over all E experts
+ *   c_e = times that expert e was selected, n = tokens, both over the
+ *         sequence's valid tokens;   pmean_e = mean of p_te over them
+ *   loss = E sum_e (c_e / (k n)) pmean_e      (1 when perfectly even; 0 for n = 0)
+ * and, for upstream gradients g_s = dL/dloss_s and dw = d_topk_w,
+ *   dlogits_te = g_s E / (k n^2) p_te (c_e - sum_e' p_te' c_e')
+ *                + sum_{j: idx_tj = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+ * (the counts are held fixed; w is the softmax over the selected logits, as
+ * moe_route gives it).  The first term is zero for tokens that are not valid
+ * or in no sequence.
+ *   logits  f32 [T, E] as moe_route writes them (bias included); -inf is an
+ *           expert that cannot be chosen, else finite
+ *   idx     int32 [T, k]; an id outside [0, E) is left out and recorded as
+ *           PMOE_ERR_BAD_INDEX (of valid tokens, in the forward)
+ *   w, d_topk_w  f32 [T, k]; d_topk_w NULL leaves out the second term
+ *   valid   uint8 [T] or NULL (every token): 0 for padding
+ *   seq     int32 [nseq + 1], nondecreasing in [0, T] (else
+ *           PMOE_ERR_BAD_INDEX is recorded by the forward and the results are
+ *           unspecified), or NULL: one sequence of all T tokens
+ *   counts  int32 [nseq, E], ntok int32 [nseq], pmean f32 [nseq, E], loss f32
+ *           [nseq]: outputs of the forward; counts and ntok go into the backward
+ *   g_loss  f32 [nseq]; NULL leaves out the first term (logits, counts and
+ *           ntok are then not read)
+ *   dlogits f32 [T, E] (out, overwritten); its column sums are the gradient of
+ *           the router bias
+ *   ws      >= moe_balance_ws_bytes(dims, nseq)
+ * dims: T, E and k are used; 1 <= nseq <= 2^20.  Fixed summation order.
+ */
+size_t moe_balance_ws_bytes(pmoe_dims dims, int32_t nseq);
+pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32_t *idx,
+                                const uint8_t *valid, const int32_t *seq, int32_t nseq,
+                                int32_t *counts, int32_t *ntok, float *pmean, float *loss,
+                                void *ws, size_t ws_bytes, cudaStream_t stream);
+pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_t *idx,
+                               const float *w, const float *d_topk_w, const uint8_t *valid,
+                               const int32_t *seq, int32_t nseq, const int32_t *counts,
+                               const int32_t *ntok, const float *g_loss, float *dlogits,
+                               void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Bytes of device workspace an op needs (op = PMOE_OP_*).  Includes the
  * 256-byte error word at the start.  In SCRATCH mode this includes the
  * C-expert BF16 dequant buffer, reported separately by

@@ -1,0 +1,407 @@
+// balance.cu -- the router's training side: the load-balance loss with the
+// per-expert counts, and the gradient of the router logits from that loss and
+// from the routing weights (moe_backward_data's d_topk_w).
+//
+// Both passes read the [T, E] logits once and hold a token's row in
+// registers, NI values per thread of its group: a warp per token up to 1024
+// experts, a CTA per token above (rows of up to 4096 do not fit a warp's
+// registers).
+#include <cmath>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace pmoe {
+namespace bal {
+
+constexpr int kThreads = 256;
+constexpr float kNegInf = -INFINITY;
+
+struct Ws {
+    DevErr *err;
+    float *psum;             // [slots][Ep] probability sums of a (slab, sequence) overlap
+    int32_t *cnt;            // [slots][Ep] counts
+    int32_t *ntok;           // [slots] tokens
+    int L, slots, Ep;
+    size_t bytes;
+};
+// Tokens are cut into slabs of L; a slab and a sequence that overlap own the
+// partial sums in slot slab + sequence (overlaps form a staircase, so the
+// slots are distinct).
+static Ws carve(void *base, int T, int E, int nseq)
+{
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        uint8_t *p = base ? (uint8_t *)base + off : nullptr;
+        off += (n + 255) & ~(size_t)255;
+        return p;
+    };
+    Ws w;
+    w.L = (int)std::max<int64_t>(8, cdiv(cdiv(T, 2 * 152), 8) * 8);
+    w.slots = (int)cdiv(std::max(T, 1), w.L) + nseq;
+    w.Ep = (E + 3) & ~3;
+    w.err = (DevErr *)take(kHdrBytes);
+    w.psum = (float *)take((size_t)w.slots * w.Ep * 4);
+    w.cnt = (int32_t *)take((size_t)w.slots * w.Ep * 4);
+    w.ntok = (int32_t *)take((size_t)w.slots * 4);
+    w.bytes = off;
+    return w;
+}
+
+// Sequence bounds, held inside [0, T] whatever the caller's array says
+__device__ __forceinline__ int seq_at(const int32_t *seq, int s, int nseq, int T)
+{
+    if (!seq) return s == 0 ? 0 : T;
+    return min(max(seq[s], 0), T);
+}
+// The sequence that holds token t: the last s with seq[s] <= t (nseq if t is
+// past the last sequence's end, -1 before the first)
+__device__ __forceinline__ int seq_of(const int32_t *seq, int nseq, int T, int t)
+{
+    int lo = 0, hi = nseq + 1;   // first s in [0, nseq + 1) with seq[s] > t
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (seq_at(seq, m, nseq, T) > t) hi = m;
+        else lo = m + 1;
+    }
+    return lo - 1;
+}
+
+// Reductions over a group of TPT threads (a warp, or the whole CTA)
+template <int TPT, class Op>
+__device__ __forceinline__ float group_reduce(float v, Op op, float *sh)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (TPT > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = sh[0];
+        for (int i = 1; i < TPT / 32; ++i) v = op(v, sh[i]);
+    }
+    return v;
+}
+struct Max {
+    __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Add {
+    __device__ float operator()(float a, float b) const { return a + b; }
+};
+
+// softmax of one row, thread `tid` of the group holding columns tid + TPT i.
+// A row of -inf only has p = 0.
+template <int TPT, int NI>
+__device__ __forceinline__ void row_softmax(const float *__restrict__ l, int E, int tid, float (&p)[NI], float *sh)
+{
+    float m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = tid + TPT * i;
+        p[i] = e < E ? l[e] : kNegInf;
+        m = fmaxf(m, p[i]);
+    }
+    m = group_reduce<TPT>(m, Max(), sh);
+    const float mm = m == kNegInf ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        p[i] = expf(p[i] - mm);
+        s += p[i];
+    }
+    s = group_reduce<TPT>(s, Add(), sh);
+    const float inv = m == kNegInf ? 0.f : 1.f / s;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) p[i] *= inv;
+}
+
+// ------------------------------------------------------------------ forward
+// Partial sums of one slab: per overlapping sequence, the token groups' sums
+// of p (added in group order), the counts (integer atomics: order-free) and
+// the number of tokens.
+template <int TPT, int NI>
+__global__ void __launch_bounds__(kThreads) k_balance_partial(int T, int E, int k, int L, int Ep,
+                                                              const float *__restrict__ logits,
+                                                              const int32_t *__restrict__ idx,
+                                                              const uint8_t *__restrict__ valid,
+                                                              const int32_t *__restrict__ seq, int nseq,
+                                                              float *__restrict__ psum, int32_t *__restrict__ cnt,
+                                                              int32_t *__restrict__ ntok, DevErr *err)
+{
+    extern __shared__ float sm[];   // [groups][Ep] sums, then [Ep] counts
+    __shared__ float sh[kThreads / 32];
+    __shared__ int sn;
+    constexpr int kGroups = kThreads / TPT;
+    int *sc = (int *)(sm + kGroups * Ep);
+    const int grp = threadIdx.x / TPT, tid = threadIdx.x % TPT;
+    const int t0 = blockIdx.x * L, t1 = min(T, t0 + L);
+    for (int s = max(0, seq_of(seq, nseq, T, t0)); s < nseq; ++s) {
+        const int a0 = seq_at(seq, s, nseq, T), b0 = seq_at(seq, s + 1, nseq, T);
+        if (a0 >= t1) break;
+        const int a = max(a0, t0), b = min(b0, t1);
+        if (a >= b) continue;
+        __syncthreads();   // the previous sequence's sums have been written out
+        for (int e = threadIdx.x; e < E; e += kThreads) sc[e] = 0;
+        if (threadIdx.x == 0) sn = 0;
+        __syncthreads();
+        float acc[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i] = 0.f;
+        int n = 0;
+        for (int t = a + grp; t < b; t += kGroups) {
+            if (valid && !valid[t]) continue;
+            float p[NI];
+            row_softmax<TPT, NI>(logits + (int64_t)t * E, E, tid, p, sh);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) acc[i] += p[i];
+            if (tid < k) {
+                const int e = idx[(int64_t)t * k + tid];
+                if (e >= 0 && e < E) atomicAdd(&sc[e], 1);
+                else record_error(err, PMOE_ERR_BAD_INDEX, t, e);
+            }
+            ++n;
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (tid + TPT * i < E) sm[grp * Ep + tid + TPT * i] = acc[i];
+        if (tid == 0) atomicAdd(&sn, n);
+        __syncthreads();
+        const int64_t slot = (int64_t)blockIdx.x + s;
+        for (int e = threadIdx.x; e < Ep; e += kThreads) {
+            float v = 0.f;
+            if (e < E)
+                for (int g = 0; g < kGroups; ++g) v += sm[g * Ep + e];
+            psum[slot * Ep + e] = v;
+            cnt[slot * Ep + e] = e < E ? sc[e] : 0;
+        }
+        if (threadIdx.x == 0) ntok[slot] = sn;
+    }
+}
+
+// One CTA per sequence: its slots are added in order (in `groups` interleaved
+// strands, then the strands in order); loss = E / (k n) sum_e c_e pmean_e.
+__global__ void __launch_bounds__(1024) k_balance_reduce(int T, int E, int k, int L, int Ep,
+                                                         const int32_t *__restrict__ seq, int nseq,
+                                                         const float *__restrict__ psum,
+                                                         const int32_t *__restrict__ cnt,
+                                                         const int32_t *__restrict__ ntok, int32_t *__restrict__ counts,
+                                                         int32_t *__restrict__ n_out, float *__restrict__ pmean,
+                                                         float *__restrict__ loss, DevErr *err)
+{
+    extern __shared__ float4 sp[];   // [1024] strand sums, then [1024] strand counts
+    __shared__ float sw[32];
+    __shared__ int sn;
+    int4 *sq = (int4 *)(sp + 1024);
+    const int s = blockIdx.x, E4 = Ep / 4;
+    const int a = seq_at(seq, s, nseq, T), b = seq_at(seq, s + 1, nseq, T);
+    if (seq && threadIdx.x == 0 &&
+        (seq[s] < 0 || seq[s + 1] < seq[s] || seq[s + 1] > T))
+        record_error(err, PMOE_ERR_BAD_INDEX, s, seq[s]);
+    const int first = a / L, last = b > a ? (b - 1) / L : first - 1;
+    if (threadIdx.x == 0) sn = 0;
+    __syncthreads();
+    int n = 0;
+    for (int i = first + threadIdx.x; i <= last; i += 1024) n += ntok[i + s];
+    if (n) atomicAdd(&sn, n);
+    const int groups = 1024 / E4, grp = threadIdx.x / E4, c4 = threadIdx.x % E4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 c = make_int4(0, 0, 0, 0);
+    if (grp < groups)
+#pragma unroll 4
+        for (int i = first + grp; i <= last; i += groups) {
+            const float4 x = *(const float4 *)(psum + (int64_t)(i + s) * Ep + c4 * 4);
+            const int4 y = *(const int4 *)(cnt + (int64_t)(i + s) * Ep + c4 * 4);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            c.x += y.x, c.y += y.y, c.z += y.z, c.w += y.w;
+        }
+    sp[threadIdx.x] = v;
+    sq[threadIdx.x] = c;
+    __syncthreads();
+    n = sn;
+    const float inv = n > 0 ? 1.f / (float)n : 0.f;
+    float part = 0.f;
+    if (threadIdx.x < E4) {
+        for (int g = 1; g < groups; ++g) {
+            const float4 x = sp[g * E4 + c4];
+            const int4 y = sq[g * E4 + c4];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            c.x += y.x, c.y += y.y, c.z += y.z, c.w += y.w;
+        }
+        const float pv[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+        const int cv[4] = {c.x, c.y, c.z, c.w};
+        for (int j = 0; j < 4; ++j) {
+            const int e = c4 * 4 + j;
+            if (e >= E) break;
+            counts[(int64_t)s * E + e] = cv[j];
+            pmean[(int64_t)s * E + e] = pv[j];
+            part += (float)cv[j] * pv[j];
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if ((threadIdx.x & 31) == 0) sw[threadIdx.x >> 5] = part;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float t = 0.f;
+        for (int i = 0; i < 32; ++i) t += sw[i];
+        loss[s] = t * ((float)E / (float)k) * inv;
+        n_out[s] = n;
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// dlogit_e = p_e (a_e - sum_e' p_e' a_e') with a_e = g E c_e / (k n^2) of the
+// token's sequence, plus w_j (dw_j - sum_i w_i dw_i) at the selected experts.
+template <int TPT, int NI>
+__global__ void __launch_bounds__(kThreads) k_route_backward(int T, int E, int k, const float *__restrict__ logits,
+                                                             const int32_t *__restrict__ idx,
+                                                             const float *__restrict__ w, const float *__restrict__ dw,
+                                                             const uint8_t *__restrict__ valid,
+                                                             const int32_t *__restrict__ seq, int nseq,
+                                                             const int32_t *__restrict__ counts,
+                                                             const int32_t *__restrict__ ntok,
+                                                             const float *__restrict__ gl, float *__restrict__ dlogits,
+                                                             DevErr *err)
+{
+    __shared__ float sh[kThreads / 32];
+    const int tid = threadIdx.x % TPT;
+    const int t = blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+    if (t >= T) return;
+    float d[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) d[i] = 0.f;
+    if (gl && (!valid || valid[t])) {
+        const int s = seq_of(seq, nseq, T, t);
+        const int n = s >= 0 && s < nseq ? ntok[s] : 0;
+        if (n > 0) {
+            row_softmax<TPT, NI>(logits + (int64_t)t * E, E, tid, d, sh);
+            const float f = gl[s] * ((float)E / (float)k) / ((float)n * (float)n);
+            float av[NI], dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = tid + TPT * i;
+                av[i] = e < E ? f * (float)counts[(int64_t)s * E + e] : 0.f;
+                dot += d[i] * av[i];
+            }
+            dot = group_reduce<TPT>(dot, Add(), sh);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) d[i] *= av[i] - dot;
+        }
+    }
+    if (dw) {
+        // every warp forms the k terms (lane j: slot j), then each thread adds those of its columns
+        const int lane = threadIdx.x & 31;
+        int e = -1;
+        float wj = 0.f, gj = 0.f;
+        if (lane < k) {
+            e = idx[(int64_t)t * k + lane];
+            wj = w[(int64_t)t * k + lane];
+            gj = dw[(int64_t)t * k + lane];
+            if (e < 0 || e >= E) {
+                if (tid < 32) record_error(err, PMOE_ERR_BAD_INDEX, t, e);
+                e = -1;
+                wj = 0.f;
+            }
+        }
+        float dot = wj * gj;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        const float vj = wj * (gj - dot);
+        for (int j = 0; j < k; ++j) {
+            const int ej = __shfl_sync(0xffffffffu, e, j);
+            const float x = __shfl_sync(0xffffffffu, vj, j);
+            const int i0 = ej >= 0 && ej % TPT == tid ? ej / TPT : -1;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) d[i] += i == i0 ? x : 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (tid + TPT * i < E) dlogits[(int64_t)t * E + tid + TPT * i] = d[i];
+}
+
+// The variant by the number of experts: f(threads per token, values per thread)
+template <class F>
+static void by_experts(int E, F f)
+{
+    using std::integral_constant;
+    if (E <= 32) f(integral_constant<int, 32>(), integral_constant<int, 1>());
+    else if (E <= 128) f(integral_constant<int, 32>(), integral_constant<int, 4>());
+    else if (E <= 256) f(integral_constant<int, 32>(), integral_constant<int, 8>());
+    else if (E <= 384) f(integral_constant<int, 32>(), integral_constant<int, 12>());
+    else if (E <= 512) f(integral_constant<int, 32>(), integral_constant<int, 16>());
+    else if (E <= 1024) f(integral_constant<int, 32>(), integral_constant<int, 32>());
+    else f(integral_constant<int, 256>(), integral_constant<int, 16>());
+}
+
+static bool aligned(std::initializer_list<const void *> ps)
+{
+    for (const void *p : ps)
+        if ((uintptr_t)p & 15) return false;
+    return true;
+}
+
+}  // namespace bal
+}  // namespace pmoe
+
+using namespace pmoe;
+
+extern "C" {
+
+size_t moe_balance_ws_bytes(pmoe_dims dims, int32_t nseq)
+{
+    if (!dims_ok(dims) || nseq < 1 || nseq > (1 << 20)) return 0;
+    return bal::carve(nullptr, dims.T, dims.E, nseq).bytes;
+}
+
+pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32_t *idx, const uint8_t *valid,
+                                const int32_t *seq, int32_t nseq, int32_t *counts, int32_t *ntok, float *pmean,
+                                float *loss, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!dims_ok(dims) || nseq < 1 || nseq > (1 << 20) || (!seq && nseq != 1)) return PMOE_ERR_INVALID_ARG;
+    if ((dims.T > 0 && (!logits || !idx)) || !counts || !ntok || !pmean || !loss) return PMOE_ERR_INVALID_ARG;
+    if (!bal::aligned({logits, idx, valid, seq, counts, ntok, pmean, loss})) return PMOE_ERR_INVALID_ARG;
+    const bal::Ws w = bal::carve(ws, dims.T, dims.E, nseq);
+    if (!ws || ws_bytes < w.bytes || !bal::aligned({ws})) return PMOE_ERR_WORKSPACE;
+    bool ok = true;
+    if (dims.T > 0)
+        bal::by_experts(dims.E, [&](auto tpt, auto ni) {
+            auto kern = bal::k_balance_partial<tpt.value, ni.value>;
+            const size_t sm = (size_t)(bal::kThreads / tpt.value + 1) * w.Ep * 4;
+            ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) == cudaSuccess;
+            if (!ok) return;
+            kern<<<(unsigned)cdiv(dims.T, w.L), bal::kThreads, sm, stream>>>(dims.T, dims.E, dims.k, w.L, w.Ep, logits,
+                                                                           idx, valid, seq, nseq, w.psum, w.cnt, w.ntok,
+                                                                           w.err);
+            note_launch();
+        });
+    if (!ok) return PMOE_ERR_CUDA;
+    bal::k_balance_reduce<<<nseq, 1024, 1024 * 32, stream>>>(dims.T, dims.E, dims.k, w.L, w.Ep, seq, nseq, w.psum, w.cnt,
+                                                             w.ntok, counts, ntok, pmean, loss, w.err);
+    note_launch();
+    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+}
+
+pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_t *idx, const float *w,
+                               const float *d_topk_w, const uint8_t *valid, const int32_t *seq, int32_t nseq,
+                               const int32_t *counts, const int32_t *ntok, const float *g_loss, float *dlogits, void *ws,
+                               size_t ws_bytes, cudaStream_t stream)
+{
+    if (!dims_ok(dims) || nseq < 1 || nseq > (1 << 20) || (!seq && nseq != 1)) return PMOE_ERR_INVALID_ARG;
+    if (!d_topk_w && !g_loss) return PMOE_ERR_INVALID_ARG;
+    if (dims.T > 0 && (!dlogits || (d_topk_w && (!idx || !w)) || (g_loss && (!logits || !counts || !ntok))))
+        return PMOE_ERR_INVALID_ARG;
+    if (!bal::aligned({logits, idx, w, d_topk_w, valid, seq, counts, ntok, g_loss, dlogits})) return PMOE_ERR_INVALID_ARG;
+    const bal::Ws b = bal::carve(ws, dims.T, dims.E, nseq);
+    if (!ws || ws_bytes < b.bytes || !bal::aligned({ws})) return PMOE_ERR_WORKSPACE;
+    if (dims.T == 0) return PMOE_OK;
+    bal::by_experts(dims.E, [&](auto tpt, auto ni) {
+        bal::k_route_backward<tpt.value, ni.value>
+            <<<(unsigned)cdiv(dims.T, bal::kThreads / tpt.value), bal::kThreads, 0, stream>>>(
+                dims.T, dims.E, dims.k, logits, idx, w, d_topk_w, valid, seq, nseq, counts, ntok, g_loss, dlogits, b.err);
+        note_launch();
+    });
+    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -32,7 +32,8 @@ EXPORTS = ("moe_route", "moe_permute", "moe_chunked_forward", "moe_backward_data
            "dense_linear_ws_bytes", "dense_linear_forward", "dense_linear_backward",
            "moe_adapter_publish", "moe_chunked_forward_slots", "pmoe_debug_expire_gemm_wait",
            "head_workspace_bytes", "head_logprob_forward", "head_logprob_backward",
-           "head_distill_forward", "head_distill_backward")
+           "head_distill_forward", "head_distill_backward",
+           "moe_balance_ws_bytes", "moe_balance_forward", "moe_route_backward")
 PERMUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 KT_GEMM_GATE_UP, KT_GEMM_DOWN, KT_GEMM_BWD_G, KT_GEMM_BWD_DX, KT_ROUTER = 0, 1, 2, 3, 4
 
@@ -118,6 +119,8 @@ def _declare(L):
         "head_logprob_backward": [H, p, p, f32, p, p, p, p, p, p, sz, p],
         "head_distill_forward": [H, p, p, f32, p, p, p, p, p, sz, p],
         "head_distill_backward": [H, p, p, f32, p, p, p, p, p, p, p, sz, p],
+        "moe_balance_forward": [D, p, p, p, p, i32, p, p, p, p, p, sz, p],
+        "moe_route_backward": [D, p, p, p, p, p, p, i32, p, p, p, p, p, sz, p],
         "moe_clear_status": [p, p],
         "moe_query_status": [p, p],
     }
@@ -133,6 +136,8 @@ def _declare(L):
     L.dense_linear_ws_bytes.restype = sz
     L.moe_scratch_bytes.argtypes = [D, i32, ctypes.c_int]
     L.moe_scratch_bytes.restype = sz
+    L.moe_balance_ws_bytes.argtypes = [D, i32]
+    L.moe_balance_ws_bytes.restype = sz
     L.head_workspace_bytes.argtypes = [H, ctypes.c_int]
     L.head_workspace_bytes.restype = sz
     L.moe_ctx_bytes.argtypes = [D]
@@ -315,6 +320,25 @@ def adapter_cayley(nblk, b, S, R_bf16, R_f32, stream=None):
 def adapter_cayley_grad(nblk, b, S, R_f32, dR, dS, stream=None):
     _check(lib().adapter_cayley_grad(nblk, b, _ptr(S), _ptr(R_f32), _ptr(dR), _ptr(dS),
                                      _stream(stream)), "adapter_cayley_grad")
+
+
+def moe_balance_ws_bytes(dm: Dims, nseq: int = 1) -> int:
+    return lib().moe_balance_ws_bytes(dm, nseq)
+
+
+def moe_balance_forward(dm, logits, idx, valid, seq, nseq, counts, ntok, pmean, loss, ws,
+                        stream=None):
+    _check(lib().moe_balance_forward(dm, _ptr(logits), _ptr(idx), _ptr(valid), _ptr(seq), nseq,
+                                     _ptr(counts), _ptr(ntok), _ptr(pmean), _ptr(loss), _ptr(ws),
+                                     _nbytes(ws), _stream(stream)), "moe_balance_forward")
+
+
+def moe_route_backward(dm, logits, idx, w, d_topk_w, valid, seq, nseq, counts, ntok, g_loss,
+                       dlogits, ws, stream=None):
+    _check(lib().moe_route_backward(dm, _ptr(logits), _ptr(idx), _ptr(w), _ptr(d_topk_w),
+                                    _ptr(valid), _ptr(seq), nseq, _ptr(counts), _ptr(ntok),
+                                    _ptr(g_loss), _ptr(dlogits), _ptr(ws), _nbytes(ws),
+                                    _stream(stream)), "moe_route_backward")
 
 
 def head_dims(T, d, V, K=0) -> HeadDims:
