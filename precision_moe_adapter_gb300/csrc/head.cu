@@ -193,7 +193,9 @@ struct Tiling {
 static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
 {
     Tiling t;
-    t.ctas = 1;
+    // A pair of CTAs on a 256 x 256 tile reads each operand half as often as
+    // single CTAs on 128 x 128; single CTAs fill the GPU with smaller products.
+    t.ctas = cdiv(M, 256) * cdiv(N, 256) >= kSms / 2 && M > 128 ? 2 : 1;
     t.bn = 128 * t.ctas;
     t.mt = (int)cdiv(M, 128 * t.ctas);
     t.nt = (int)cdiv(N, t.bn);
@@ -311,7 +313,7 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
     // m tiles that run together: their rows of A stay in L2 (48 MB) while the n tiles pass
     const int64_t stripe = 2ll * 128 * t.ctas * a.ksteps * kBK;
     a.gm = (int)std::max<int64_t>(1, std::min<int64_t>(t.mt, std::max<int64_t>(8, (48ll << 20) / stripe)));
-    return launch_as<1, 128, EPI>(ma, mb, mo, ml, a, st);
+    return t.ctas == 2 ? launch_as<2, 256, EPI>(ma, mb, mo, ml, a, st) : launch_as<1, 128, EPI>(ma, mb, mo, ml, a, st);
 }
 
 // ------------------------------------------------------------------ passes

@@ -330,96 +330,13 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     };
     auto flag_at = [](uint32_t w, int j) { return ((w >> ((j >> 1) * 8)) & 1u) != 0; };
     bool ok = true;
-    if (warp == 0) {
-        // ---------------- producer
-        if (lane == 0) {
-            uint32_t g = 0;
-            for (int i = first; ok && i < n_items; i += step) {
-                const Item t = item_of(a, i);
-                int k0, k1;
-                krange(t, k0, k1);
-                const int ma = (t.m * CTAS + (int)rank) * 128;
-                const int nb = a.n0 + t.n * BN + (int)rank * 128;
-                // one K step; `mine`: A holds data (else it is filled with zeros, from
-                // past its last row)
-                auto load = [&](const CUtensorMap *tma, int k, bool mine) {
-                    const uint32_t s = g % kStages;
-                    if (!(ok = mbar_wait(empty(s), ((g / kStages) & 1) ^ 1, a.err, 1, tc::kWaitNs))) return;
-                    if (rank == 0) mbar_expect_tx(full(s), CTAS * kStageBytes);
-                    const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
-                    const uint32_t sa = s0 + s * kStageBytes, sb = sa + kOpBytes;
-                    const int ka = k * kBK, kb = a.kb0 + k * kBK;
-                    if constexpr (kAMn) {
-                        load_2d<CTAS>(sa, tma, ma, mine ? ka : a.arows, fb);
-                        load_2d<CTAS>(sa + 8192, tma, ma + 64, mine ? ka : a.arows, fb);
-                    } else {
-                        load_2d<CTAS>(sa, tma, ka, mine ? ma : a.arows, fb);
-                    }
-                    if constexpr (kBMn) {
-                        load_2d<CTAS>(sb, &tmB, nb, kb, fb);
-                        load_2d<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);
-                    } else {
-                        load_2d<CTAS>(sb, &tmB, kb, nb, fb);
-                    }
-                    ++g;
-                };
-                uint32_t w[CTAS], wn[CTAS];
-                flags(t, k0, w);
-                for (int c0 = k0; ok && c0 < k1; c0 += kChunk) {
-                    flags(t, c0 + kChunk, wn);
-                    const int c1 = min(c0 + kChunk, k1);
-                    for (int k = c0; ok && k < c1; ++k) {
-                        load(&tmA, k, true);
-                        if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) load(&tmLo, k, flag_at(w[rank], k - c0));
-                    }
-#pragma unroll
-                    for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
-                }
-            }
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::idesc_bf16(CTAS * 128, BN, kAMn) | ((uint32_t)kBMn << 16);
-            constexpr uint32_t kAStep = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 k
-            constexpr uint32_t kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
-            const uint64_t da0 = desc_of<kAMn>(s0), db0 = desc_of<kBMn>(s0 + kOpBytes);
-            uint32_t g = 0, gc = 0;
-            for (int i = first; ok && i < n_items; i += step) {
-                const Item t = item_of(a, i);
-                int k0, k1;
-                krange(t, k0, k1);
-                uint32_t w[CTAS], wn[CTAS];
-                flags(t, k0, w);
-                for (int c0 = k0; ok && c0 < k1; c0 += kChunk, ++gc) {
-                    flags(t, c0 + kChunk, wn);
-                    const uint32_t b = gc & 1;
-                    if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
-                    tc_fence_after();
-                    const int c1 = min(c0 + kChunk, k1);
-                    auto kstep = [&](bool add) {
-                        const uint32_t s = g % kStages;
-                        if (!(ok = mbar_wait(full(s), (g / kStages) & 1, a.err, 3, tc::kWaitNs))) return;
-                        tc_fence_after();
-                        const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, add || j > 0);
-                        commit<CTAS>(empty(s));
-                        ++g;
-                    };
-                    for (int k = c0; ok && k < c1; ++k) {
-                        kstep(k > c0);
-                        if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) kstep(true);
-                    }
-                    if (ok) commit<CTAS>(tfull(b));
-#pragma unroll
-                    for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
-                }
-            }
-        }
-    } else if (warp >= 4) {
+    // The epilogue's 128 sums a thread need more registers than an even split
+    // of 384 threads gives (168): the first four warps hand theirs over.  Of
+    // the launch's 384 x 168 = 64512: 128 x 40 + 256 x 232, and where the
+    // producer and the MMA issuer follow flags 128 x 72 + 256 x 216.
+    if (warp >= 4) {
         // ---------------- epilogue
+        if constexpr (kEpi == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLo ? 216 : 232));
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const int rl = quad * 32 + lane;   // row of the CTA's 128
         const uint32_t tld = tmem + ((uint32_t)(quad * 32) << 16) + half * kUnit;
@@ -590,6 +507,97 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             }
         }
         if (EPI != HG_FWD && quad == 0 && lane == 0) store_wait_all();
+    } else {
+        if constexpr (kEpi == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLo ? 72 : 40));
+        if (warp == 0) {
+            // ---------------- producer
+            if (lane == 0) {
+                uint32_t g = 0;
+                for (int i = first; ok && i < n_items; i += step) {
+                    const Item t = item_of(a, i);
+                    int k0, k1;
+                    krange(t, k0, k1);
+                    const int ma = (t.m * CTAS + (int)rank) * 128;
+                    const int nb = a.n0 + t.n * BN + (int)rank * 128;
+                    // one K step; `mine`: A holds data (else it is filled with zeros, from
+                    // past its last row)
+                    auto load = [&](const CUtensorMap *tma, int k, bool mine) {
+                        const uint32_t s = g % kStages;
+                        if (!(ok = mbar_wait(empty(s), ((g / kStages) & 1) ^ 1, a.err, 1, tc::kWaitNs))) return;
+                        if (rank == 0) mbar_expect_tx(full(s), CTAS * kStageBytes);
+                        const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
+                        const uint32_t sa = s0 + s * kStageBytes, sb = sa + kOpBytes;
+                        const int ka = k * kBK, kb = a.kb0 + k * kBK;
+                        if constexpr (kAMn) {
+                            load_2d<CTAS>(sa, tma, ma, mine ? ka : a.arows, fb);
+                            load_2d<CTAS>(sa + 8192, tma, ma + 64, mine ? ka : a.arows, fb);
+                        } else {
+                            load_2d<CTAS>(sa, tma, ka, mine ? ma : a.arows, fb);
+                        }
+                        if constexpr (kBMn) {
+                            load_2d<CTAS>(sb, &tmB, nb, kb, fb);
+                            load_2d<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);
+                        } else {
+                            load_2d<CTAS>(sb, &tmB, kb, nb, fb);
+                        }
+                        ++g;
+                    };
+                    uint32_t w[CTAS], wn[CTAS];
+                    flags(t, k0, w);
+                    for (int c0 = k0; ok && c0 < k1; c0 += kChunk) {
+                        flags(t, c0 + kChunk, wn);
+                        const int c1 = min(c0 + kChunk, k1);
+                        for (int k = c0; ok && k < c1; ++k) {
+                            load(&tmA, k, true);
+                            if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) load(&tmLo, k, flag_at(w[rank], k - c0));
+                        }
+    #pragma unroll
+                        for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer
+            if (lane == 0 && rank == 0) {
+                const uint32_t idesc = tc::idesc_bf16(CTAS * 128, BN, kAMn) | ((uint32_t)kBMn << 16);
+                constexpr uint32_t kAStep = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 k
+                constexpr uint32_t kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
+                const uint64_t da0 = desc_of<kAMn>(s0), db0 = desc_of<kBMn>(s0 + kOpBytes);
+                uint32_t g = 0, gc = 0;
+                for (int i = first; ok && i < n_items; i += step) {
+                    const Item t = item_of(a, i);
+                    int k0, k1;
+                    krange(t, k0, k1);
+                    uint32_t w[CTAS], wn[CTAS];
+                    flags(t, k0, w);
+                    for (int c0 = k0; ok && c0 < k1; c0 += kChunk, ++gc) {
+                        flags(t, c0 + kChunk, wn);
+                        const uint32_t b = gc & 1;
+                        if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
+                        tc_fence_after();
+                        const int c1 = min(c0 + kChunk, k1);
+                        auto kstep = [&](bool add) {
+                            const uint32_t s = g % kStages;
+                            if (!(ok = mbar_wait(full(s), (g / kStages) & 1, a.err, 3, tc::kWaitNs))) return;
+                            tc_fence_after();
+                            const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+    #pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, add || j > 0);
+                            commit<CTAS>(empty(s));
+                            ++g;
+                        };
+                        for (int k = c0; ok && k < c1; ++k) {
+                            kstep(k > c0);
+                            if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) kstep(true);
+                        }
+                        if (ok) commit<CTAS>(tfull(b));
+    #pragma unroll
+                        for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
+                    }
+                }
+            }
+        }
     }
     // After a wait that ran out, copies or MMAs may still be in flight: give
     // them a millisecond to land before shared memory and TMEM go.
