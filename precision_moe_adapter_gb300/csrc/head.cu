@@ -13,20 +13,22 @@ namespace pmoe {
 namespace hg {
 
 constexpr int kMaxK = 256;                    // teacher entries per token
+constexpr uint16_t kNone = 0xFFFF;
 constexpr int kSms = 152;                     // SMs of a GB300
 constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece, remainders included
-constexpr int32_t kNoId = 0x7fffffff;
 
 // ------------------------------------------------------------------ targets
 // Distillation: one warp per token turns the teacher's K entries into a
 // probability each, q = softmax(scale t) over the entries present, ordered
-// by vocabulary id (missing ones last, id kNoId, q = 0): the GEMM's
-// epilogue then finds a column range's entries by a binary search.  The
-// place of an entry is the number of entries before it in (id, slot) order.
+// by vocabulary id (missing ones last, id kNoId, q = 0).  The place of an
+// entry is the number of entries before it in (id, slot) order.  first[u] is
+// the place of the first entry of the 128 vocabulary entries u (kNone: it has
+// none), so that the GEMM's epilogue finds a unit's entries with one load.
 __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float scale, const int32_t *__restrict__ t_idx,
                                                       const float *__restrict__ t_logits, const float *__restrict__ g,
                                                       int32_t *__restrict__ ids, float *__restrict__ q,
-                                                      float *__restrict__ lq, float *__restrict__ coef, DevErr *err)
+                                                      float *__restrict__ lq, uint16_t *__restrict__ first, int NU,
+                                                      float *__restrict__ coef, DevErr *err)
 {
     __shared__ int32_t skey[4][kMaxK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -62,6 +64,7 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float ls = logf(s);
+    for (int u = lane; u < NU; u += 32) first[(int64_t)t * NU + u] = kNone;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kMaxK / 32; ++i) {
@@ -69,15 +72,19 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
         if (k >= K) continue;
         const int32_t key = skey[warp][k];
         int r = 0;
+        bool lead = true;   // no entry of its unit comes before it
         for (int j = 0; j < K; ++j) {
             const int32_t o = skey[warp][j];
-            r += o < key || (o == key && j < k);
+            const bool before = o < key || (o == key && j < k);
+            r += before;
+            lead &= !(before && o / kUnit == key / kUnit);
         }
         const bool has = key != kNoId;
         const int64_t at = (int64_t)t * K + r;
         ids[at] = key;
         q[at] = has ? expf(x[i] - m) / s : 0.f;
         if (lq) lq[at] = has ? x[i] - m - ls : 0.f;
+        if (has && lead) first[(int64_t)t * NU + key / kUnit] = (uint16_t)r;
     }
     if (coef && lane == 0) coef[t] = any ? g[t] * scale : 0.f;
 }
@@ -95,8 +102,11 @@ __global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, co
 
 // ------------------------------------------------------------------ combine
 // One CTA per token joins the NU softmax partials in one fixed order, and
-// forms the token's value from the target logits.
-__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float scale, bool distill,
+// forms the token's value from the target logits.  Everything stays relative
+// to the largest logit m, in base 2: a log-probability is ln 2 (c z - m -
+// log2 sum), with c z - m in one rounding, so that the value of a confident
+// token keeps its relative accuracy although its logit and lse cancel.
+__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float c, bool distill,
                                                       const float2 *__restrict__ part, const float *__restrict__ zt,
                                                       const int32_t *__restrict__ ids, const float *__restrict__ q,
                                                       const float *__restrict__ lq, float *__restrict__ value,
@@ -131,23 +141,25 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     m = sw[0].x;
     s = sw[0].y;
     for (int i = 1; i < 4; ++i) join(sw[i].x, sw[i].y);
-    const float l = m * 0.6931471805599453f + logf(s);
+    constexpr float kLn2 = 0.6931471805599453f;
+    const float ls = log2f(s);
+    auto logp = [&](float z) { return kLn2 * (fmaf(z, c, -m) - ls); };
     float v = 0.f;
     if (distill) {
         for (int k = lane; k < K; k += 32) {
             const int64_t at = (int64_t)t * K + k;
-            if (ids[at] != kNoId) v += q[at] * (lq[at] - (zt[at] * scale - l));
+            if (ids[at] != kNoId) v += q[at] * (lq[at] - logp(zt[at]));
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     } else {
         const int y = ids[t];
-        if (y >= 0 && y < V) v = zt[t] * scale - l;
+        if (y >= 0 && y < V) v = logp(zt[t]);
         else if (y >= V && lane == 0) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
     }
     if (lane == 0) {
         value[t] = v;
-        lse[t] = l;
+        lse[t] = fmaf(m, kLn2, kLn2 * ls);
     }
 }
 
@@ -201,8 +213,8 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
     t.nt = (int)cdiv(N, t.bn);
     const int64_t slots = kSms / t.ctas, tiles = (int64_t)t.mt * t.nt;
     int64_t s = 1;
-    if (split && tiles > 0) s = std::max<int64_t>(1, std::min(slots / tiles, ksteps / (2 * kChunk)));
-    t.kper = (int)(cdiv(cdiv(std::max<int64_t>(ksteps, 1), s), kChunk) * kChunk);   // whole chunks
+    if (split && tiles > 0) s = std::max<int64_t>(1, std::min(slots / tiles, ksteps / 16));
+    t.kper = (int)(cdiv(cdiv(std::max<int64_t>(ksteps, 1), s), kFlagRun) * kFlagRun);   // whole words of flags
     t.splits = (int)cdiv(std::max<int64_t>(ksteps, 1), t.kper);
     return t;
 }
@@ -215,6 +227,7 @@ struct Ws {
     DevErr *err;
     int32_t *ids;            // [T][K] sorted teacher ids
     float *q, *lq;           // [T][K]
+    uint16_t *first;         // [T][NU]
     float *zt;               // [T][max(K, 1)]
     float2 *part;            // [T][NU]
     float *coef;             // [T]
@@ -237,6 +250,7 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
     w.err = (DevErr *)take(kHdrBytes);
     w.ids = (int32_t *)take(T * K * 4);
     w.q = (float *)take(T * K * 4);
+    w.first = (uint16_t *)take(K ? T * cdiv(h.V, kUnit) * 2 : 0);
     if (op == PMOE_HEAD_FORWARD) {
         w.lq = (float *)take(T * K * 4);
         w.zt = (float *)take(T * std::max<size_t>(K, 1) * 4);
@@ -324,7 +338,7 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     const int32_t *ids = idx;
     if (distill) {
         k_head_teacher<<<(unsigned)cdiv(h.T, 4), 128, 0, st>>>(h.T, h.V, K, scale, idx, t_logits, nullptr, w.ids, w.q,
-                                                               w.lq, nullptr, w.err);
+                                                               w.lq, w.first, (int)cdiv(h.V, kUnit), nullptr, w.err);
         note_launch();
         ids = w.ids;
     }
@@ -338,12 +352,13 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     a.part = w.part;
     a.zt = w.zt;
     a.ids = ids;
+    a.first = distill ? w.first : nullptr;
     a.K = K;
     a.err = w.err;
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
-    k_head_combine<<<h.T, 128, 0, st>>>(h.V, K, a.NU, scale, distill, w.part, w.zt, ids, w.q, w.lq, value, lse, w.err);
+    k_head_combine<<<h.T, 128, 0, st>>>(h.V, K, a.NU, a.c, distill, w.part, w.zt, ids, w.q, w.lq, value, lse, w.err);
     note_launch();
     return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
 }
@@ -355,7 +370,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     const int K = distill ? h.K : 1;
     if (distill)
         k_head_teacher<<<(unsigned)cdiv(h.T, 4), 128, 0, st>>>(h.T, h.V, K, scale, idx, t_logits, g, w.ids, w.q, nullptr,
-                                                               w.coef, w.err);
+                                                               w.first, (int)cdiv(h.V, kUnit), w.coef, w.err);
     else
         k_head_coef<<<(unsigned)cdiv(h.T, 256), 256, 0, st>>>(h.T, h.V, scale, idx, g, w.coef, w.err);
     note_launch();
@@ -381,11 +396,13 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.c = scale * 1.4426950408889634f;
             a.ids = distill ? w.ids : idx;
             a.q = distill ? w.q : nullptr;
+            a.first = distill ? w.first : nullptr;
+            a.NU = (int)cdiv(h.V, kUnit);
             a.K = K;
             a.lse = lse;
             a.coef = w.coef;
-            if (!tc::make_tmap3(&mo, w.G, false, ldg, h.T, 1, 64, 128) ||
-                !tc::make_tmap3(&ml, w.Glo, false, ldg, h.T, 1, 64, 128) ||
+            if (!tc::make_tmap3(&mo, w.G, false, ldg, h.T, 1, 64, 32) ||
+                !tc::make_tmap3(&ml, w.Glo, false, ldg, h.T, 1, 64, 32) ||
                 !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo, &ml,
                                  a, st))
                 return PMOE_ERR_CUDA;
@@ -399,8 +416,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.bf16_out = w.dx == nullptr;
             a.accumulate = v0 > 0;
             Tiling t = tx;
-            const bool made = w.dx ? tc::make_tmap3(&mo, w.dx, true, h.d, h.T, t.splits, 32, 128)
-                                   : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 128);
+            const bool made = w.dx ? tc::make_tmap3(&mo, w.dx, true, h.d, h.T, t.splits, 32, 32)
+                                   : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 32);
             // (a last, shorter piece may leave the last splits without K steps)
             t.splits = (int)cdiv(a.ksteps, t.kper);
             if (!made || !map_operand(&ml, {w.Glo, ldg, h.T, false}) ||
@@ -412,7 +429,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.M = vc;
             a.N = h.d;
             a.ksteps = (int)cdiv(h.T, kBK);
-            if (!tc::make_tmap3(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 128) ||
+            if (!tc::make_tmap3(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 32) ||
                 !map_operand(&ml, {w.Glo, ldg, h.T, true}) ||
                 !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {X, h.d, h.T, true}, &mo, &ml, a,
                                st))

@@ -21,16 +21,18 @@
 //
 // The tensor cores' FP32 accumulation truncates: its error grows linearly
 // with the number of K steps (about one part in 2^24 per 16 columns).  Every
-// run of kChunk K steps is therefore summed in its own TMEM buffer and added
-// to the tile's FP32 sum in registers (round to nearest), which holds the
-// relative error near 5e-7 at any length.  The two buffers alternate, so the
-// tensor cores work on the next chunk while one is drained, and on the next
-// tile's first two chunks during the epilogue proper.
+// run of chunk_of(EPI) K steps is therefore summed in its own TMEM buffer and
+// added to the tile's FP32 sum in registers (round to nearest), which bounds
+// the error at any length.  The forward's values are FP32 outputs: chunks of
+// 512 columns, relative error about 5e-7.  The other results are rounded to
+// BF16, so longer chunks do.  The two buffers alternate, so the tensor cores
+// work on the next chunk while one is drained, and on the next tile's first
+// two chunks during the epilogue proper.
 //
 // G is the BF16 operand of two products.  Where a token's distribution is
 // concentrated, the few large entries of G carry the whole gradient, and
 // their rounding to 8 bits would be its error.  A 128 x 128 block of G that
-// holds an entry |p - q| >= kLarge therefore keeps the rounding's remainder
+// holds an entry with p or q >= kLarge therefore keeps the rounding's remainder
 // too (a second BF16, 16 bits together), and is flagged; the products run a
 // second K step on the remainders of flagged blocks only (a token has at most
 // 1 / kLarge such entries of p, spread over the vocabulary).
@@ -60,15 +62,18 @@ constexpr int kUnit = 128;               // columns per softmax partial and per 
 constexpr int kStages = 6;               // 32 KB each: 16 KB of A, 16 KB of B
 constexpr int kOpBytes = 128 * kBK * 2;  // one operand tile of a stage
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kOutBytes = 128 * 128;     // one staged output box: 128 rows of 128 bytes
-constexpr int kChunk = 8;                // K steps summed in one TMEM buffer
-constexpr float kLarge = 0.125f;         // entries of p - q whose block keeps its remainder
+constexpr int kWarpOut = 32 * 128;       // a warp's staged output box: 32 rows of 128 bytes
+constexpr int kFlagRun = 8;              // K steps per word of flags
+// K steps summed in one TMEM buffer
+constexpr int chunk_of(int epi) { return epi == HG_FWD ? 8 : epi == HG_GRAD ? 16 : 32; }
+constexpr int32_t kNoId = 0x7fffffff;
+constexpr float kLarge = 0.125f;         // entries of p or q whose block keeps its remainder
 constexpr int kThreads0 = 128;           // producer, MMA and allocator warps
 
 constexpr int epi_warps(int BN) { return BN / kUnit * 4; }
 constexpr int threads_of(int BN) { return kThreads0 + 32 * epi_warps(BN); }
 // 1024 bytes of slack to align the swizzled tiles, 256 for the barriers
-constexpr int smem_of(int BN) { return kStages * kStageBytes + BN / kUnit * kOutBytes + 256 + 1024; }
+constexpr int smem_of(int BN) { return kStages * kStageBytes + epi_warps(BN) * kWarpOut + 256 + 1024; }
 
 struct Args {
     int M, N;                // output rows and columns of this launch
@@ -79,10 +84,12 @@ struct Args {
     int arows;               // rows of A's tensor map: the row past its end
     int V;                   // FWD, GRAD: number of vocabulary entries
     float c;                 // FWD, GRAD: scale * log2(e)
-    int NU;                  // FWD: partials per token
+    int NU;                  // FWD, GRAD: units of the vocabulary
     float2 *part;            // FWD: [T][NU] (max, sum) in base 2
     float *zt;               // FWD: [T][K] raw logits of the target entries
-    const int32_t *ids;      // FWD, GRAD: [T][K] target entries, ascending
+    const int32_t *ids;      // FWD, GRAD: [T][K] target entries, ascending, kNoId last
+    const uint16_t *first;   // FWD, GRAD: [T][NU] place of a unit's first entry (>= K: none),
+                             // or NULL: K is 1
     const float *q;          // GRAD: [T][K] their probabilities, or NULL: 1
     int K;
     const float *lse;        // GRAD: [T]
@@ -208,28 +215,32 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t saddr)
     return d;
 }
 
-// Value j of a register array (j varies between the lanes)
-__device__ __forceinline__ float pick(const float (&v)[kUnit], int j)
+// 32 TMEM columns of the warp's lanes; complete after tmem_wait on the same registers
+__device__ __forceinline__ void tmem_issue32(uint32_t taddr, float *v)
 {
-    float r = 0.f;
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) r = i == j ? v[i] : r;
-    return r;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
 }
-// First of the K ascending ids that is >= v
-__device__ __forceinline__ int lower_bound(const int32_t *ids, int K, int v)
+__device__ __forceinline__ void tmem_wait(float *v)
 {
-    int lo = 0, n = K;
-    while (n > 0) {
-        const int h = n >> 1;
-        if (ids[lo + h] < v) {
-            lo += h + 1;
-            n -= h + 1;
-        } else {
-            n = h;
-        }
-    }
-    return lo;
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                   "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
+                   "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ uint32_t bf2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 struct Item {
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t s0 = smem_u32(smem);
     const uint32_t out0 = s0 + kStages * kStageBytes;
-    const uint32_t bar0 = out0 + BN / kUnit * kOutBytes;
+    const uint32_t bar0 = out0 + kEpi * kWarpOut;
     auto full = [&](uint32_t s) { return bar0 + 8 * s; };
     auto empty = [&](uint32_t s) { return bar0 + 8 * (kStages + s); };
     auto tfull = [&](uint32_t b) { return bar0 + 8 * (2 * kStages + b); };
@@ -313,10 +324,11 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         k0 = t.s * a.kper;
         k1 = min(k0 + a.kper, a.ksteps);
     };
-    // DX, DW: the flags of the next kChunk K steps of A's row blocks, a byte per
+    // DX, DW: the flags of the next kFlagRun K steps of A's row blocks, a byte per
     // 128 k, one word per CTA of the cluster
     constexpr bool kLo = EPI == HG_DX || EPI == HG_DW;
-    static_assert(kChunk == 8 && kBK == 64, "a chunk is four flag bytes");
+    constexpr int kChunk = chunk_of(EPI);
+    static_assert(kFlagRun == 8 && kBK == 64 && kChunk % kFlagRun == 0, "a run is four flag bytes");
     auto flags = [&](const Item &t, int k, uint32_t (&w)[CTAS]) {
 #pragma unroll
         for (int r = 0; r < CTAS; ++r) {
@@ -340,27 +352,67 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const int rl = quad * 32 + lane;   // row of the CTA's 128
         const uint32_t tld = tmem + ((uint32_t)(quad * 32) << 16) + half * kUnit;
-        const uint32_t ob = out0 + half * kOutBytes;
+        const uint32_t ob = out0 + (warp - 4) * kWarpOut, orow = ob + lane * 128;
+        const float inf = __int_as_float(0x7f800000);
         uint32_t gc = 0;
         for (int i = first; ok && i < n_items; i += step) {
             const Item t = item_of(a, i);
             int k0, k1;
             krange(t, k0, k1);
+            const int mrow = (t.m * CTAS + (int)rank) * 128;
+            const int row = mrow + rl;
+            const int cb = a.n0 + t.n * BN + half * kUnit;   // first column
+            const int nv = min(kUnit, a.V - cb);             // FWD, GRAD: valid columns (may be <= 0)
+            const bool live = row < a.M && nv > 0;
+            // the row's first target entry among the columns (kNoId: none), its
+            // normaliser and factor: fetched while the tensor cores work
+            const int32_t *ids = a.ids + (int64_t)row * a.K;
+            int pos = 0, id = kNoId;
+            float l2 = 0.f, cf = 0.f;
+            if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
+                if (live) {
+                    if (a.first) pos = a.first[(int64_t)row * a.NU + cb / kUnit];
+                    if (pos < a.K) id = ids[pos];
+                    if (id < cb || id >= a.V) id = kNoId;
+                }
+                if (EPI == HG_GRAD && row < a.M) {
+                    l2 = a.lse[row] * 1.4426950408889634f;
+                    cf = a.coef[row];
+                }
+            }
             float acc[kUnit];
-#pragma unroll
-            for (int j = 0; j < kUnit; ++j) acc[j] = 0.f;
             for (int c0 = k0; c0 < k1; c0 += kChunk, ++gc) {
                 const uint32_t b = gc & 1;
                 // (warp-uniform: every lane sees the same outcome before the aligned loads)
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(tfull(b), (gc >> 1) & 1, a.err, 4, tc::kWaitNs))))
                     break;
                 tc_fence_after();
+                if constexpr (kLo) {   // (16 columns at a time: fewer registers)
+                    if (c0 == k0) {
 #pragma unroll
-                for (int j = 0; j < kUnit; j += 16) {
-                    float v[16];
-                    tc::tmem_ld16(tld + b * BN + j, v);
+                        for (int j = 0; j < kUnit; ++j) acc[j] = 0.f;
+                    }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[j + e] += v[e];
+                    for (int j = 0; j < kUnit; j += 16) {
+                        float v[16];
+                        tc::tmem_ld16(tld + b * BN + j, v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[j + e] += v[e];
+                    }
+                } else if (c0 == k0) {
+#pragma unroll
+                    for (int j = 0; j < kUnit; j += 32) tmem_issue32(tld + b * BN + j, acc + j);
+#pragma unroll
+                    for (int j = 0; j < kUnit; j += 32) tmem_wait(acc + j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kUnit; j += 32) {
+                        float v[32];
+                        tmem_issue32(tld + b * BN + j, v);
+                        tmem_wait(v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) acc[j + e] += v[e];
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -369,144 +421,138 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     else mbar_arrive(tempty(b));
                 }
             }
-            // the group's four warps leave together (the barriers below are unbounded)
-            if (EPI != HG_FWD) ok = bar_group_and(1 + half, ok);
+            // the group's four warps leave together (GRAD's barrier below is unbounded)
+            if (EPI == HG_GRAD) ok = bar_group_and(1 + half, ok);
             if (!ok) break;
-            const int mrow = (t.m * CTAS + (int)rank) * 128;
-            const int row = mrow + rl;
-            const int cb = a.n0 + t.n * BN + half * kUnit;   // first column
-            bool lo = false;   // GRAD: this block's remainders are kept
-            if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
-                const int nv = min(kUnit, a.V - cb);         // valid columns (may be <= 0)
-                const bool live = row < a.M && nv > 0;
-                const int32_t *ids = a.ids + (int64_t)row * a.K;
-                int pos = 0, id = 0x7fffffff;
-                if (live) {
-                    pos = a.K > 1 ? lower_bound(ids, a.K, cb) : 0;
-                    if (pos < a.K) id = ids[pos];
-                    if (id < cb) id = 0x7fffffff;   // K == 1: an earlier column, or no target
-                }
-                if constexpr (EPI == HG_FWD) {
-                    while (__any_sync(0xffffffffu, id - cb < nv)) {
-                        const bool has = id - cb < nv;
-                        const float z = pick(acc, has ? id - cb : -1);
-                        if (has) {
+            if constexpr (EPI == HG_FWD) {
+#pragma unroll
+                for (int q = 0; q < kUnit; q += 32) {
+                    const int e0 = cb + q;   // entries of columns e0 .. e0 + 31
+                    while (__any_sync(0xffffffffu, id < e0 + 32)) {
+                        const int j0 = id - e0;   // (kNoId is beyond every column)
+                        float z = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z = j == j0 ? acc[q + j] : z;
+                        if (id < e0 + 32) {
                             a.zt[(int64_t)row * a.K + pos] = z;
                             ++pos;
-                            id = pos < a.K ? ids[pos] : 0x7fffffff;
+                            id = pos < a.K ? ids[pos] : kNoId;
                         }
                     }
-                    if (live) {
+                }
+                if (nv < kUnit) {
+#pragma unroll
+                    for (int j = 0; j < kUnit; ++j)
+                        if (j >= nv) acc[j] = -inf;
+                }
+                float mx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = acc[e];
+#pragma unroll
+                for (int j = 4; j < kUnit; ++j) mx[j & 3] = fmaxf(mx[j & 3], acc[j]);
+                const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < kUnit; ++j) sm[j & 3] += ex2(fmaf(acc[j], a.c, -m2));
+                if (live)
+                    a.part[(int64_t)row * a.NU + cb / kUnit] = make_float2(m2, (sm[0] + sm[1]) + (sm[2] + sm[3]));
+            } else {
+                // through shared memory (the warp's 32 rows of 128 bytes, 128-byte
+                // swizzle) to TMA stores, which clip rows and columns past the end
+                const int xc = t.n * BN + half * kUnit, yr = mrow + quad * 32;
+                auto put = [&](const CUtensorMap *tm, int x) {   // the staged box goes out at column x
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && x < a.N && yr < a.M) store_3d(tm, ob, x, yr, t.s, a.accumulate != 0);
+                };
+                auto reuse = [&]() {                             // the previous box has been read
+                    if (lane == 0) store_wait_read();
+                    __syncwarp();
+                };
+                auto stage16 = [&](int e0) {                     // columns e0 .. e0 + 63 in BF16
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = e0 + j * 8;
+                        tc::st_shared_v4(orow + ((j ^ (lane & 7)) << 4),
+                                         make_uint4(bf2(acc[e], acc[e + 1]), bf2(acc[e + 2], acc[e + 3]),
+                                                    bf2(acc[e + 4], acc[e + 5]), bf2(acc[e + 6], acc[e + 7])));
+                    }
+                };
+                if constexpr (EPI == HG_GRAD) {
+                    float big = 0.f;   // largest p or q of the row's columns
+#pragma unroll
+                    for (int q = 0; q < kUnit; q += 32) {
+                        const int e0 = cb + q;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            acc[q + j] = ex2(fmaf(acc[q + j], a.c, -l2));
+                            big = fmaxf(big, acc[q + j]);   // (columns past V: p of a zero logit, no harm)
+                        }
+                        while (__any_sync(0xffffffffu, id < e0 + 32)) {
+                            const int j0 = id - e0;
+                            float qv = 0.f;
+                            if (id < e0 + 32) {
+                                qv = a.q ? a.q[(int64_t)row * a.K + pos] : 1.f;
+                                ++pos;
+                                id = pos < a.K ? ids[pos] : kNoId;
+                            }
+                            big = fmaxf(big, qv);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) acc[q + j] -= j == j0 ? qv : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
                         if (nv < kUnit) {
 #pragma unroll
-                            for (int j = 0; j < kUnit; ++j)
-                                if (j >= nv) acc[j] = -__int_as_float(0x7f800000);
+                            for (int j = 0; j < 32; ++j)
+                                if (q + j >= nv) acc[q + j] = 0.f;
                         }
-                        float mx[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = acc[e];
-#pragma unroll
-                        for (int j = 4; j < kUnit; ++j) mx[j & 3] = fmaxf(mx[j & 3], acc[j]);
-                        const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-                        float sm[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int j = 0; j < kUnit; ++j) sm[j & 3] += ex2(fmaf(acc[j], a.c, -m2));
-                        a.part[(int64_t)row * a.NU + cb / kUnit] =
-                            make_float2(m2, (sm[0] + sm[1]) + (sm[2] + sm[3]));
-                    }
-                } else {
-                    const float l2 = row < a.M ? a.lse[row] * 1.4426950408889634f : 0.f;
-                    const float cf = row < a.M ? a.coef[row] : 0.f;
-#pragma unroll
-                    for (int j = 0; j < kUnit; ++j) acc[j] = ex2(fmaf(acc[j], a.c, -l2));
-                    while (__any_sync(0xffffffffu, id - cb < nv)) {
-                        const bool has = id - cb < nv;
-                        const int j0 = has ? id - cb : -1;
-                        const float qv = !has ? 0.f : a.q ? a.q[(int64_t)row * a.K + pos] : 1.f;
-#pragma unroll
-                        for (int j = 0; j < kUnit; ++j) acc[j] = j == j0 ? acc[j] - qv : acc[j];
-                        if (has) {
-                            ++pos;
-                            id = pos < a.K ? ids[pos] : 0x7fffffff;
+                        if (q & 32) {
+                            reuse();
+                            stage16(q - 32);
+                            put(&tmOut, xc + q - 32);
                         }
                     }
-                    bool big = false;
-#pragma unroll
-                    for (int j = 0; j < kUnit; ++j) {
-                        big |= j < nv && fabsf(acc[j]) >= kLarge;
-                        acc[j] = j < nv ? acc[j] * cf : 0.f;
-                    }
-                    lo = bar_group_or(1 + half, big && cf != 0.f);
+                    const bool lo = bar_group_or(1 + half, big >= kLarge && cf != 0.f && nv > 0);
                     if (quad == 0 && lane == 0 && mrow < a.M) {
                         const int tb = mrow >> 7, vb = (t.n * BN >> 7) + half;
                         a.fl[(int64_t)tb * a.fs + vb] = lo;
                         a.flt[(int64_t)vb * a.fst + tb] = lo;
                     }
-                }
-            }
-            if constexpr (EPI != HG_FWD) {
-                // through shared memory (128-byte rows, 128-byte swizzle) to TMA
-                // stores, which clip rows and columns past the output's end
-                const int xc = t.n * BN + half * kUnit;
-                const bool f32 = EPI == HG_DX && !a.bf16_out;
-                const uint32_t srow = ob + rl * 128;
-                auto box = [&](const CUtensorMap *tm, int x) {   // the group's staged box goes out at column x
-                    tc::fence_proxy_async();
-                    bar_group(1 + half);
-                    if (quad == 0 && lane == 0) store_3d(tm, ob, x, mrow, t.s, a.accumulate != 0);
-                };
-                auto reuse = [&]() {      // the group's previous box has been read
-                    if (quad == 0 && lane == 0) store_wait_read();
-                    bar_group(1 + half);
-                };
-                if (f32) {
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        reuse();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int e = q4 * 32 + j * 4;
-                            tc::st_shared_v4(srow + ((j ^ (rl & 7)) << 4),
-                                             make_uint4(__float_as_uint(acc[e]), __float_as_uint(acc[e + 1]),
-                                                        __float_as_uint(acc[e + 2]), __float_as_uint(acc[e + 3])));
-                        }
-                        if (xc + q4 * 32 < a.N) box(&tmOut, xc + q4 * 32);
-                    }
-                } else {
-#pragma unroll
-                    for (int q2 = 0; q2 < 2; ++q2) {
-                        reuse();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int e = q2 * 64 + j * 8;
-                            tc::st_shared_v4(srow + ((j ^ (rl & 7)) << 4),
-                                             make_uint4(pack_bf2(acc[e], acc[e + 1]), pack_bf2(acc[e + 2], acc[e + 3]),
-                                                        pack_bf2(acc[e + 4], acc[e + 5]),
-                                                        pack_bf2(acc[e + 6], acc[e + 7])));
-                        }
-                        if (xc + q2 * 64 < a.N) box(&tmOut, xc + q2 * 64);
-                    }
-                    if (EPI == HG_GRAD && lo) {
+                    if (lo) {
 #pragma unroll
                         for (int j = 0; j < kUnit; ++j) acc[j] -= bf2f(f2bf(acc[j]));   // exact
 #pragma unroll
-                        for (int q2 = 0; q2 < 2; ++q2) {
+                        for (int q = 0; q < kUnit; q += 64) {
                             reuse();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int e = q2 * 64 + j * 8;
-                                tc::st_shared_v4(
-                                    srow + ((j ^ (rl & 7)) << 4),
-                                    make_uint4(pack_bf2(acc[e], acc[e + 1]), pack_bf2(acc[e + 2], acc[e + 3]),
-                                               pack_bf2(acc[e + 4], acc[e + 5]), pack_bf2(acc[e + 6], acc[e + 7])));
-                            }
-                            if (xc + q2 * 64 < a.N) box(&tmLo, xc + q2 * 64);
+                            stage16(q);
+                            put(&tmLo, xc + q);
                         }
+                    }
+                } else if (EPI == HG_DX && !a.bf16_out) {
+#pragma unroll
+                    for (int q = 0; q < kUnit; q += 32) {
+                        reuse();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int e = q + j * 4;
+                            tc::st_shared_v4(orow + ((j ^ (lane & 7)) << 4),
+                                             make_uint4(__float_as_uint(acc[e]), __float_as_uint(acc[e + 1]),
+                                                        __float_as_uint(acc[e + 2]), __float_as_uint(acc[e + 3])));
+                        }
+                        put(&tmOut, xc + q);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kUnit; q += 64) {
+                        reuse();
+                        stage16(q);
+                        put(&tmOut, xc + q);
                     }
                 }
             }
         }
-        if (EPI != HG_FWD && quad == 0 && lane == 0) store_wait_all();
+        if (EPI != HG_FWD && lane == 0) store_wait_all();
     } else {
         if constexpr (kEpi == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLo ? 72 : 40));
         if (warp == 0) {
@@ -544,9 +590,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     };
                     uint32_t w[CTAS], wn[CTAS];
                     flags(t, k0, w);
-                    for (int c0 = k0; ok && c0 < k1; c0 += kChunk) {
-                        flags(t, c0 + kChunk, wn);
-                        const int c1 = min(c0 + kChunk, k1);
+                    for (int c0 = k0; ok && c0 < k1; c0 += kFlagRun) {
+                        flags(t, c0 + kFlagRun, wn);
+                        const int c1 = min(c0 + kFlagRun, k1);
                         for (int k = c0; ok && k < c1; ++k) {
                             load(&tmA, k, true);
                             if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) load(&tmLo, k, flag_at(w[rank], k - c0));
@@ -570,29 +616,35 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     krange(t, k0, k1);
                     uint32_t w[CTAS], wn[CTAS];
                     flags(t, k0, w);
-                    for (int c0 = k0; ok && c0 < k1; c0 += kChunk, ++gc) {
-                        flags(t, c0 + kChunk, wn);
+                    for (int c0 = k0; ok && c0 < k1; c0 += kFlagRun) {
+                        flags(t, c0 + kFlagRun, wn);
                         const uint32_t b = gc & 1;
-                        if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
-                        tc_fence_after();
-                        const int c1 = min(c0 + kChunk, k1);
+                        const bool begin = (c0 - k0) % kChunk == 0;   // a chunk's first K step
+                        if (begin) {
+                            if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
+                            tc_fence_after();
+                        }
+                        const int c1 = min(c0 + kFlagRun, k1);
                         auto kstep = [&](bool add) {
                             const uint32_t s = g % kStages;
                             if (!(ok = mbar_wait(full(s), (g / kStages) & 1, a.err, 3, tc::kWaitNs))) return;
                             tc_fence_after();
                             const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, add || j > 0);
                             commit<CTAS>(empty(s));
                             ++g;
                         };
                         for (int k = c0; ok && k < c1; ++k) {
-                            kstep(k > c0);
+                            kstep(!begin || k > c0);
                             if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) kstep(true);
                         }
-                        if (ok) commit<CTAS>(tfull(b));
-    #pragma unroll
+                        if (ok && (c1 == k1 || (c1 - k0) % kChunk == 0)) {
+                            commit<CTAS>(tfull(b));
+                            ++gc;
+                        }
+#pragma unroll
                         for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
                     }
                 }
