@@ -428,9 +428,8 @@ pmoe_status head_logprob_forward(pmoe_head_dims dims, const void *X, const void 
 /*
  * head_logprob_backward -- for upstream gradients g_t = dL/dlogp_t:
  *   G_tv = g_t scale ([v = y_t] - p_tv);  dX = bf16(G W);  dW = bf16(G^T X)
- * G enters both products in BF16, and where a block of 128 tokens and 128
- * entries holds a large one (|[v = y] - p| >= 1/8) as two BF16 terms (16
- * bits); the sums are FP32.
+ * G enters both products in BF16, its large entries (|[v = y] - p| >= 1/4)
+ * as two BF16 terms (16 bits); the sums are FP32.
  *   lse    f32 [T] from the forward       g   f32 [T] (in)
  *   dX     bf16 [T, d] or NULL (out)      dW  bf16 [V, d] or NULL (out,
  *          overwritten; NULL: the head is frozen); one of them is needed

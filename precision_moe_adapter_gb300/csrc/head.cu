@@ -15,7 +15,7 @@ namespace hg {
 constexpr int kMaxK = 256;                    // teacher entries per token
 constexpr uint16_t kNone = 0xFFFF;
 constexpr int kSms = 152;                     // SMs of a GB300
-constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece, remainders included
+constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece
 
 // ------------------------------------------------------------------ targets
 // Distillation: one warp per token turns the teacher's K entries into a
@@ -163,6 +163,113 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     }
 }
 
+// ------------------------------------------------------------------ large entries
+// The extra K steps of one product, one CTA per 256 output rows.  The
+// entries of the rows take consecutive columns of A, in (token, vocabulary
+// id) order whatever order GRAD's threads listed them in; a block's steps
+// are taken from a counter, so blocks may come in any order, but a block's
+// own columns, and with them its sums, are fixed.
+//   DX (kDw 0): rows are tokens, a column's row of B is its vocabulary entry
+//   DW (kDw 1): rows are vocabulary entries, the row of B is the token; `fl`
+//   names the blocks of 128 tokens to look at
+template <int kDw>
+__global__ void __launch_bounds__(256) k_head_large(int T, const int *__restrict__ cnt, const int2 *__restrict__ large,
+                                                    const uint8_t *__restrict__ fl, int fs, int *__restrict__ steps,
+                                                    int2 *__restrict__ lists, int32_t *__restrict__ lidx,
+                                                    uint16_t *__restrict__ lo)
+{
+    __shared__ int sw[8], s_base;
+    const int blk = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int2 e[kMaxLarge];
+    int n = 0;
+    // this thread's entries of token t, ascending by vocabulary id
+    auto fetch = [&](int t) {
+        n = 0;
+        if (t >= T) return;
+        const int c = min(cnt[t], kMaxLarge);
+        int last = -1;
+        for (int i = 0; i < c; ++i) {
+            int2 best = make_int2(kNoId, 0);
+            for (int j = 0; j < c; ++j) {
+                const int2 v = large[(int64_t)t * kMaxLarge + j];
+                if (v.x > last && v.x < best.x) best = v;
+            }
+            last = best.x;
+            if (!kDw || best.x / kListRows == blk) {
+#pragma unroll
+                for (int j = 0; j < kMaxLarge; ++j)
+                    if (j == n) e[j] = best;
+                ++n;
+            }
+        }
+    };
+    // exclusive sum of n over the CTA's threads, and the total
+    auto scan = [&](int &total) {
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sw[warp] = x;
+        __syncthreads();
+        int base = 0;
+        total = 0;
+        for (int i = 0; i < 8; ++i) {
+            if (i < warp) base += sw[i];
+            total += sw[i];
+        }
+        return base + x - n;
+    };
+    auto put = [&](int at, int t) {   // the thread's entries from column `at` of the block's steps
+#pragma unroll
+        for (int j = 0; j < kMaxLarge; ++j)
+            if (j < n) {
+                const int64_t st = s_base + (at + j) / 64;
+                const int c = (at + j) % 64;
+                lidx[st * 64 + c] = kDw ? t : e[j].x;
+                lo[st * 64 * kListRows + (kDw ? c * kListRows + e[j].x % kListRows : (t % kListRows) * 64 + c)] =
+                    (uint16_t)e[j].y;
+            }
+    };
+    // tokens 256 at a time; for DW only where a flag is set
+    const int t0 = kDw ? 0 : blk * kListRows, t1 = kDw ? T : min(T, t0 + kListRows);
+    auto wanted = [&](int t) {
+        if (!kDw) return true;
+        const uint8_t *f = fl + (int64_t)blk * fs + (t >> 7);
+        return f[0] != 0 || ((t >> 7) + 1 < fs && f[1] != 0);
+    };
+    int total = 0;
+    for (int t = t0; t < t1; t += 256) {
+        if (!wanted(t)) continue;
+        int c;
+        fetch(t + tid);
+        scan(c);
+        total += c;
+    }
+    const int ns = (total + 63) / 64;
+    if (tid == 0) {
+        s_base = ns ? atomicAdd(steps, ns) : 0;
+        lists[blk] = make_int2(s_base, ns);
+    }
+    __syncthreads();
+    if (!ns) return;
+    uint4 *z = (uint4 *)(lo + (int64_t)s_base * 64 * kListRows);
+    for (int i = tid; i < ns * 64 * kListRows / 8; i += 256) z[i] = make_uint4(0, 0, 0, 0);
+    for (int i = total + tid; i < ns * 64; i += 256) lidx[(int64_t)s_base * 64 + i] = 0;   // (its column of A is zero)
+    __syncthreads();
+    int at = 0;
+    for (int t = t0; t < t1; t += 256) {
+        if (!wanted(t)) continue;
+        int c;
+        if (kDw) fetch(t + tid);   // (DX: the only batch is still in registers)
+        const int off = scan(c);
+        put(at + off, t + tid);
+        at += c;
+    }
+}
+
 // dX = bf16(sum of the splits' FP32 partials, in order); n elements each, n % 8 == 0
 __global__ void __launch_bounds__(256) k_head_sum(int64_t n, int splits, const float *__restrict__ part,
                                                   uint16_t *__restrict__ out)
@@ -185,11 +292,11 @@ static bool head_ok(const pmoe_head_dims &h)
            h.K <= kMaxK && h.T <= (1 << 24);
 }
 
-// Vocabulary entries per piece of the backward: G of one piece and its
-// remainders are at most kPieceBytes; pieces of equal size, multiples of 256.
+// Vocabulary entries per piece of the backward: G of one piece is at most
+// kPieceBytes; pieces of equal size, multiples of 256.
 static int piece_of(int T, int V)
 {
-    int64_t most = kPieceBytes / (4ll * std::max(T, 1)) / 256 * 256;
+    int64_t most = kPieceBytes / (2ll * std::max(T, 1)) / 256 * 256;
     most = std::max<int64_t>(most, 256);
     const int64_t np = cdiv(V, most);
     return (int)(cdiv(cdiv(V, np), 256) * 256);
@@ -214,7 +321,7 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
     const int64_t slots = kSms / t.ctas, tiles = (int64_t)t.mt * t.nt;
     int64_t s = 1;
     if (split && tiles > 0) s = std::max<int64_t>(1, std::min(slots / tiles, ksteps / 16));
-    t.kper = (int)(cdiv(cdiv(std::max<int64_t>(ksteps, 1), s), kFlagRun) * kFlagRun);   // whole words of flags
+    t.kper = (int)cdiv(std::max<int64_t>(ksteps, 1), s);
     t.splits = (int)cdiv(std::max<int64_t>(ksteps, 1), t.kper);
     return t;
 }
@@ -231,9 +338,18 @@ struct Ws {
     float *zt;               // [T][max(K, 1)]
     float2 *part;            // [T][NU]
     float *coef;             // [T]
-    uint16_t *G, *Glo;       // [T][piece] and the remainders of its flagged blocks
-    uint8_t *fl, *flt;       // the flags [T / 128][fs] and transposed [piece / 128][fst]
-    int fs, fst;
+    uint16_t *G;             // [T][piece]
+    // G's large entries: per token, then as the extra K steps of DX and DW
+    int *cnt;                // [T], then the flags and two step counters: zeroed per piece
+    uint8_t *fl;             // [piece / 256][fs]
+    int *steps;              // [2]
+    size_t zero_bytes;
+    int fs;
+    int2 *large;             // [T][kMaxLarge]
+    int2 *lists[2];          // per 256 rows: first step and number of steps
+    int32_t *lidx[2];        // [steps][64]
+    uint16_t *lo[2];         // [steps] remainders: DX [256 tokens][64], DW [64][256 entries]
+    int max_steps[2];
     float *dx;               // [splits][T][d]
     size_t bytes;
 };
@@ -260,12 +376,20 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
         const Tiling t = dx_tiling(h);
         w.coef = (float *)take(T * 4);
         w.G = (uint16_t *)take(T * piece * 2);
-        w.Glo = (uint16_t *)take(T * piece * 2);
-        const size_t tb = cdiv(h.T, 128), vb = piece / 128;
-        w.fs = (int)cdiv(vb, 16) * 16;
-        w.fst = (int)cdiv(tb, 16) * 16;
-        w.fl = take(tb * w.fs);
-        w.flt = take(vb * w.fst);
+        const int blocks[2] = {(int)cdiv(h.T, kListRows), piece / kListRows};
+        w.fs = (int)cdiv(h.T, 128);
+        uint8_t *z = take(T * 4 + (size_t)blocks[1] * w.fs + 8 + 4);
+        w.cnt = (int *)z;
+        w.steps = w.cnt + T;
+        w.fl = (uint8_t *)(w.steps + 2);
+        w.zero_bytes = T * 4 + 8 + (size_t)blocks[1] * w.fs;
+        w.large = (int2 *)take(T * kMaxLarge * 8);
+        for (int i = 0; i < 2; ++i) {
+            w.max_steps[i] = (int)(cdiv((int64_t)h.T * kMaxLarge, 64) + blocks[i]);
+            w.lists[i] = (int2 *)take((size_t)blocks[i] * 8);
+            w.lidx[i] = (int32_t *)take((size_t)w.max_steps[i] * 64 * 4);
+            w.lo[i] = (uint16_t *)take((size_t)w.max_steps[i] * 64 * kListRows * 2);
+        }
         if (t.splits > 1 || piece < h.V) w.dx = (float *)take((size_t)t.splits * T * h.d * 4);
     }
     w.bytes = off;
@@ -284,7 +408,7 @@ static bool map_operand(CUtensorMap *m, const Operand &o)
 }
 
 template <int CTAS, int BN, int EPI>
-static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap &ml,
+static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap (&ml)[2],
                       const Args &a, cudaStream_t st)
 {
     auto kern = k_head_gemm<CTAS, BN, EPI>;
@@ -302,24 +426,24 @@ static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtens
     at[0].val.clusterDim = {CTAS, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, ml, a) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, ml[0], ml[1], a) != cudaSuccess) return false;
     note_launch();
     return true;
 }
 
 // One product: M x N outputs over ksteps K steps, with the tiles of `t`;
-// `lo`: the remainders of G (written by GRAD, read by DX and DW as A is)
+// `lo`: DX, DW: the remainders of G's large entries
 template <int EPI>
-static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CUtensorMap *out, const CUtensorMap *lo,
-                   Args a, cudaStream_t st)
+static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CUtensorMap *out, const Operand *lo, Args a,
+                   cudaStream_t st)
 {
-    CUtensorMap ma, mb, mo, ml;
+    CUtensorMap ma, mb, mo, ml[2];
     if (!map_operand(&ma, A) || !map_operand(&mb, B)) return false;
     memset(&mo, 0, sizeof mo);
-    memset(&ml, 0, sizeof ml);
+    memset(ml, 0, sizeof ml);
     if (out) mo = *out;
-    if (lo) ml = *lo;
-    a.arows = (int)A.rows;
+    // (rows of B are gathered one by one: boxes of one row)
+    if (lo && (!map_operand(&ml[0], *lo) || !tc::make_tmap3(&ml[1], B.base, false, B.cols, B.rows, 0, kBK, 1))) return false;
     a.mt = t.mt;
     a.nt = t.nt;
     a.splits = t.splits;
@@ -379,13 +503,14 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     for (int v0 = 0; v0 < h.V; v0 += piece) {
         const int vc = std::min(piece, h.V - v0);
         const int64_t ldg = piece;
-        CUtensorMap mo, ml;
+        CUtensorMap mo;
         Args b{};   // what the piece's products share
-        b.fl = w.fl;
-        b.flt = w.flt;
+        b.cnt = w.cnt;
+        b.large = w.large;
+        b.fl = dW ? w.fl : nullptr;
         b.fs = w.fs;
-        b.fst = w.fst;
         b.err = w.err;
+        if (cudaMemsetAsync(w.cnt, 0, w.zero_bytes, st) != cudaSuccess) return PMOE_ERR_CUDA;
         {   // G = coef (softmax(Z) - q) of this piece
             Args a = b;
             a.M = h.T;
@@ -402,9 +527,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.lse = lse;
             a.coef = w.coef;
             if (!tc::make_tmap3(&mo, w.G, false, ldg, h.T, 1, 64, 32) ||
-                !tc::make_tmap3(&ml, w.Glo, false, ldg, h.T, 1, 64, 32) ||
-                !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo, &ml,
-                                 a, st))
+                !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo,
+                                 nullptr, a, st))
                 return PMOE_ERR_CUDA;
         }
         if (dX) {
@@ -420,8 +544,14 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
                                    : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 32);
             // (a last, shorter piece may leave the last splits without K steps)
             t.splits = (int)cdiv(a.ksteps, t.kper);
-            if (!made || !map_operand(&ml, {w.Glo, ldg, h.T, false}) ||
-                !launch<HG_DX>(t, {w.G, ldg, h.T, false}, {W, h.d, h.V, true}, &mo, &ml, a, st))
+            k_head_large<0><<<(unsigned)cdiv(h.T, kListRows), 256, 0, st>>>(h.T, w.cnt, w.large, nullptr, 0, w.steps,
+                                                                            w.lists[0], w.lidx[0], w.lo[0]);
+            note_launch();
+            a.lists = w.lists[0];
+            a.lidx = w.lidx[0];
+            a.lb0 = v0;
+            const Operand lo{w.lo[0], 64, (int64_t)w.max_steps[0] * kListRows, false};
+            if (!made || !launch<HG_DX>(t, {w.G, ldg, h.T, false}, {W, h.d, h.V, true}, &mo, &lo, a, st))
                 return PMOE_ERR_CUDA;
         }
         if (dW) {
@@ -429,9 +559,14 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.M = vc;
             a.N = h.d;
             a.ksteps = (int)cdiv(h.T, kBK);
+            k_head_large<1><<<(unsigned)cdiv(vc, kListRows), 256, 0, st>>>(h.T, w.cnt, w.large, w.fl, w.fs, w.steps + 1,
+                                                                           w.lists[1], w.lidx[1], w.lo[1]);
+            note_launch();
+            a.lists = w.lists[1];
+            a.lidx = w.lidx[1];
+            const Operand lo{w.lo[1], kListRows, (int64_t)w.max_steps[1] * 64, true};
             if (!tc::make_tmap3(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 32) ||
-                !map_operand(&ml, {w.Glo, ldg, h.T, true}) ||
-                !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {X, h.d, h.T, true}, &mo, &ml, a,
+                !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {X, h.d, h.T, true}, &mo, &lo, a,
                                st))
                 return PMOE_ERR_CUDA;
         }

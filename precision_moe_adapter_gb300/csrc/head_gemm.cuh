@@ -30,12 +30,15 @@
 // two chunks during the epilogue proper.
 //
 // G is the BF16 operand of two products.  Where a token's distribution is
-// concentrated, the few large entries of G carry the whole gradient, and
-// their rounding to 8 bits would be its error.  A 128 x 128 block of G that
-// holds an entry with p or q >= kLarge therefore keeps the rounding's remainder
-// too (a second BF16, 16 bits together), and is flagged; the products run a
-// second K step on the remainders of flagged blocks only (a token has at most
-// 1 / kLarge such entries of p, spread over the vocabulary).
+// concentrated, a few large entries of G carry the whole gradient, and their
+// rounding to 8 bits would be its error.  GRAD lists the entries with
+// |p - q| >= kLarge (a token has at most 8, as sum |p - q| <= 2), and the
+// products run extra K steps of 64 such entries each on the roundings'
+// remainders (a second BF16, 16 bits together): A holds one remainder per
+// column (built by head.cu, one list per 256 output rows), B the matching
+// rows of W or X, gathered by TMA.  That is one or two steps per tile of the
+// hundreds the product has; remainders of whole tiles would double the
+// steps of every tile that holds a large entry.
 //
 // Every element's sum runs over k in the same order whatever the tile shape,
 // and the softmax partials cover 128 aligned columns: the results do not
@@ -63,11 +66,12 @@ constexpr int kStages = 6;               // 32 KB each: 16 KB of A, 16 KB of B
 constexpr int kOpBytes = 128 * kBK * 2;  // one operand tile of a stage
 constexpr int kStageBytes = 2 * kOpBytes;
 constexpr int kWarpOut = 32 * 128;       // a warp's staged output box: 32 rows of 128 bytes
-constexpr int kFlagRun = 8;              // K steps per word of flags
 // K steps summed in one TMEM buffer
 constexpr int chunk_of(int epi) { return epi == HG_FWD ? 8 : epi == HG_GRAD ? 16 : 32; }
 constexpr int32_t kNoId = 0x7fffffff;
-constexpr float kLarge = 0.125f;         // entries of p or q whose block keeps its remainder
+constexpr float kLarge = 0.25f;          // entries of |p - q| that keep their remainder
+constexpr int kMaxLarge = 8;             // of a token
+constexpr int kListRows = 256;           // output rows that share a list of remainders
 constexpr int kThreads0 = 128;           // producer, MMA and allocator warps
 
 constexpr int epi_warps(int BN) { return BN / kUnit * 4; }
@@ -81,7 +85,6 @@ struct Args {
     int mt, nt, gm;          // tiles, and m tiles that run together
     int splits, ksteps, kper;   // K steps of 64 in all and per split
     int kb0;                 // first k coordinate of B (A: 0)
-    int arows;               // rows of A's tensor map: the row past its end
     int V;                   // FWD, GRAD: number of vocabulary entries
     float c;                 // FWD, GRAD: scale * log2(e)
     int NU;                  // FWD, GRAD: units of the vocabulary
@@ -94,8 +97,13 @@ struct Args {
     int K;
     const float *lse;        // GRAD: [T]
     const float *coef;       // GRAD: [T] factor of the row (0: no gradient)
-    uint8_t *fl, *flt;       // flagged blocks of G: [token block][fs], and transposed
-    int fs, fst;             // [vocabulary block][fst]; row strides, multiples of 4
+    int *cnt;                // GRAD: [T] large entries of each token, listed in
+    int2 *large;             // [T][kMaxLarge] as (vocabulary column - n0, remainder)
+    uint8_t *fl;             // GRAD: [vocabulary block of 256][fs] 1 where a block of 128
+    int fs;                  // tokens holds a large entry (NULL: not wanted)
+    const int2 *lists;       // DX, DW: per 256 rows (first step, number of steps) of remainders
+    const int32_t *lidx;     // DX, DW: [step][64] row of B
+    int lb0;                 // DX, DW: offset of these rows
     int accumulate;          // DX: add to the FP32 partials
     int bf16_out;            // DX: the output map is the BF16 dX itself
     DevErr *err;
@@ -135,6 +143,23 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *tm, int
     else
         tc::tma_load_2d(dst, tm, x, y, bar);
 }
+// Rows r.x .. r.w of a map whose boxes are one row of 128 bytes, from column x
+template <int CTAS>
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap *tm, int x, int4 r, uint32_t bar)
+{
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+            "l"((uint64_t)tm), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+            "l"((uint64_t)tm), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+            : "memory");
+}
 __device__ __forceinline__ void store_3d(const CUtensorMap *tm, uint32_t src, int x, int y, int z, bool add)
 {
     if (add)
@@ -154,18 +179,6 @@ __device__ __forceinline__ void store_wait_read()
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void bar_group(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool bar_group_and(int id, bool v)
-{
-    uint32_t r;
-    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %2, 0;\n"
-                 "barrier.cta.red.and.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
-                 : "=r"(r)
-                 : "r"(id), "r"((uint32_t)v)
-                 : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ bool bar_group_or(int id, bool v) { return !bar_group_and(id, !v); }
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -265,7 +278,8 @@ template <int CTAS, int BN, int EPI>
 __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_constant__ CUtensorMap tmA,
                                                                  const __grid_constant__ CUtensorMap tmB,
                                                                  const __grid_constant__ CUtensorMap tmOut,
-                                                                 const __grid_constant__ CUtensorMap tmLo,
+                                                                 const __grid_constant__ CUtensorMap tmLoA,
+                                                                 const __grid_constant__ CUtensorMap tmLoB,
                                                                  const Args a)
 {
     constexpr bool kAMn = EPI == HG_DW, kBMn = EPI == HG_DX || EPI == HG_DW;
@@ -324,28 +338,19 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         k0 = t.s * a.kper;
         k1 = min(k0 + a.kper, a.ksteps);
     };
-    // DX, DW: the flags of the next kFlagRun K steps of A's row blocks, a byte per
-    // 128 k, one word per CTA of the cluster
+    // DX, DW: the item's extra K steps on remainders (with the first split)
     constexpr bool kLo = EPI == HG_DX || EPI == HG_DW;
     constexpr int kChunk = chunk_of(EPI);
-    static_assert(kFlagRun == 8 && kBK == 64 && kChunk % kFlagRun == 0, "a run is four flag bytes");
-    auto flags = [&](const Item &t, int k, uint32_t (&w)[CTAS]) {
-#pragma unroll
-        for (int r = 0; r < CTAS; ++r) {
-            w[r] = 0;
-            if constexpr (kLo) {
-                const int mb = t.m * CTAS + r;
-                const uint8_t *f = EPI == HG_DX ? a.fl + (int64_t)mb * a.fs : a.flt + (int64_t)mb * a.fst;
-                if (k < a.ksteps && mb * 128 < a.M) w[r] = *(const uint32_t *)(f + (k >> 1));
-            }
-        }
+    auto extra = [&](const Item &t) {
+        if constexpr (kLo)
+            if (t.s == 0) return a.lists[t.m * CTAS * 128 / kListRows];
+        return make_int2(0, 0);
     };
-    auto flag_at = [](uint32_t w, int j) { return ((w >> ((j >> 1) * 8)) & 1u) != 0; };
     bool ok = true;
     // The epilogue's 128 sums a thread need more registers than an even split
     // of 384 threads gives (168): the first four warps hand theirs over.  Of
     // the launch's 384 x 168 = 64512: 128 x 40 + 256 x 232, and where the
-    // producer and the MMA issuer follow flags 128 x 72 + 256 x 216.
+    // producer and the MMA issuer run extra steps 128 x 72 + 256 x 216.
     if (warp >= 4) {
         // ---------------- epilogue
         if constexpr (kEpi == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLo ? 216 : 232));
@@ -421,8 +426,6 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     else mbar_arrive(tempty(b));
                 }
             }
-            // the group's four warps leave together (GRAD's barrier below is unbounded)
-            if (EPI == HG_GRAD) ok = bar_group_and(1 + half, ok);
             if (!ok) break;
             if constexpr (EPI == HG_FWD) {
 #pragma unroll
@@ -479,15 +482,11 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     }
                 };
                 if constexpr (EPI == HG_GRAD) {
-                    float big = 0.f;   // largest p or q of the row's columns
 #pragma unroll
                     for (int q = 0; q < kUnit; q += 32) {
                         const int e0 = cb + q;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            acc[q + j] = ex2(fmaf(acc[q + j], a.c, -l2));
-                            big = fmaxf(big, acc[q + j]);   // (columns past V: p of a zero logit, no harm)
-                        }
+                        for (int j = 0; j < 32; ++j) acc[q + j] = ex2(fmaf(acc[q + j], a.c, -l2));
                         while (__any_sync(0xffffffffu, id < e0 + 32)) {
                             const int j0 = id - e0;
                             float qv = 0.f;
@@ -496,37 +495,44 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                                 ++pos;
                                 id = pos < a.K ? ids[pos] : kNoId;
                             }
-                            big = fmaxf(big, qv);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) acc[q + j] -= j == j0 ? qv : 0.f;
                         }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
                         if (nv < kUnit) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (q + j >= nv) acc[q + j] = 0.f;
                         }
+                        float big = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(acc[q + j]));
+                        const bool keep = big >= kLarge && cf != 0.f;
+                        uint32_t large = 0;   // the columns to list
+                        if (__any_sync(0xffffffffu, keep)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                large |= keep && fabsf(acc[q + j]) >= kLarge ? 1u << j : 0u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
+                        while (__any_sync(0xffffffffu, large != 0)) {
+                            const int j0 = __ffs(large) - 1;
+                            float v = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v = j == j0 ? acc[q + j] : v;
+                            if (large) {
+                                const int n = atomicAdd(&a.cnt[row], 1);
+                                if (n < kMaxLarge)
+                                    a.large[(int64_t)row * kMaxLarge + n] =
+                                        make_int2(e0 - a.n0 + j0, f2bf(v - bf2f(f2bf(v))));
+                                if (a.fl) a.fl[(int64_t)((e0 - a.n0) / kListRows) * a.fs + (row >> 7)] = 1;
+                                large &= large - 1;
+                            }
+                        }
                         if (q & 32) {
                             reuse();
                             stage16(q - 32);
                             put(&tmOut, xc + q - 32);
-                        }
-                    }
-                    const bool lo = bar_group_or(1 + half, big >= kLarge && cf != 0.f && nv > 0);
-                    if (quad == 0 && lane == 0 && mrow < a.M) {
-                        const int tb = mrow >> 7, vb = (t.n * BN >> 7) + half;
-                        a.fl[(int64_t)tb * a.fs + vb] = lo;
-                        a.flt[(int64_t)vb * a.fst + tb] = lo;
-                    }
-                    if (lo) {
-#pragma unroll
-                        for (int j = 0; j < kUnit; ++j) acc[j] -= bf2f(f2bf(acc[j]));   // exact
-#pragma unroll
-                        for (int q = 0; q < kUnit; q += 64) {
-                            reuse();
-                            stage16(q);
-                            put(&tmLo, xc + q);
                         }
                     }
                 } else if (EPI == HG_DX && !a.bf16_out) {
@@ -556,49 +562,54 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     } else {
         if constexpr (kEpi == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLo ? 72 : 40));
         if (warp == 0) {
-            // ---------------- producer
-            if (lane == 0) {
-                uint32_t g = 0;
-                for (int i = first; ok && i < n_items; i += step) {
-                    const Item t = item_of(a, i);
-                    int k0, k1;
-                    krange(t, k0, k1);
-                    const int ma = (t.m * CTAS + (int)rank) * 128;
-                    const int nb = a.n0 + t.n * BN + (int)rank * 128;
-                    // one K step; `mine`: A holds data (else it is filled with zeros, from
-                    // past its last row)
-                    auto load = [&](const CUtensorMap *tma, int k, bool mine) {
-                        const uint32_t s = g % kStages;
-                        if (!(ok = mbar_wait(empty(s), ((g / kStages) & 1) ^ 1, a.err, 1, tc::kWaitNs))) return;
+            // ---------------- producer (the whole warp; lane 0 issues, and lanes
+            // 0-15 gather four rows of B each in an extra step)
+            uint32_t g = 0;
+            for (int i = first; ok && i < n_items; i += step) {
+                const Item t = item_of(a, i);
+                int k0, k1;
+                krange(t, k0, k1);
+                const int2 ex = extra(t);
+                const int ma = (t.m * CTAS + (int)rank) * 128;
+                const int nb = a.n0 + t.n * BN + (int)rank * 128;
+                for (int k = k0; k < k1 + ex.y; ++k, ++g) {
+                    const uint32_t s = g % kStages;
+                    const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
+                    const uint32_t sa = s0 + s * kStageBytes, sb = sa + kOpBytes;
+                    const bool main = !kLo || k < k1;
+                    const int st = ex.x + k - k1;   // an extra step's list
+                    int4 r = make_int4(0, 0, 0, 0);
+                    if (kLo && !main && lane < 16) r = *(const int4 *)(a.lidx + (int64_t)st * 64 + lane * 4);
+                    ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ((g / kStages) & 1) ^ 1, a.err, 1, tc::kWaitNs));
+                    if (!ok) break;
+                    if (lane == 0) {
                         if (rank == 0) mbar_expect_tx(full(s), CTAS * kStageBytes);
-                        const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
-                        const uint32_t sa = s0 + s * kStageBytes, sb = sa + kOpBytes;
                         const int ka = k * kBK, kb = a.kb0 + k * kBK;
-                        if constexpr (kAMn) {
-                            load_2d<CTAS>(sa, tma, ma, mine ? ka : a.arows, fb);
-                            load_2d<CTAS>(sa + 8192, tma, ma + 64, mine ? ka : a.arows, fb);
-                        } else {
-                            load_2d<CTAS>(sa, tma, ka, mine ? ma : a.arows, fb);
+                        if (main) {
+                            if constexpr (kAMn) {
+                                load_2d<CTAS>(sa, &tmA, ma, ka, fb);
+                                load_2d<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
+                            } else {
+                                load_2d<CTAS>(sa, &tmA, ka, ma, fb);
+                            }
+                            if constexpr (kBMn) {
+                                load_2d<CTAS>(sb, &tmB, nb, kb, fb);
+                                load_2d<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);
+                            } else {
+                                load_2d<CTAS>(sb, &tmB, kb, nb, fb);
+                            }
+                        } else if constexpr (kAMn) {   // remainders [step][64][256 rows]
+                            load_2d<CTAS>(sa, &tmLoA, ma % kListRows, st * 64, fb);
+                            load_2d<CTAS>(sa + 8192, &tmLoA, ma % kListRows + 64, st * 64, fb);
+                        } else {                       // [step][256 rows][64]
+                            load_2d<CTAS>(sa, &tmLoA, 0, st * kListRows + ma % kListRows, fb);
                         }
-                        if constexpr (kBMn) {
-                            load_2d<CTAS>(sb, &tmB, nb, kb, fb);
-                            load_2d<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);
-                        } else {
-                            load_2d<CTAS>(sb, &tmB, kb, nb, fb);
-                        }
-                        ++g;
-                    };
-                    uint32_t w[CTAS], wn[CTAS];
-                    flags(t, k0, w);
-                    for (int c0 = k0; ok && c0 < k1; c0 += kFlagRun) {
-                        flags(t, c0 + kFlagRun, wn);
-                        const int c1 = min(c0 + kFlagRun, k1);
-                        for (int k = c0; ok && k < c1; ++k) {
-                            load(&tmA, k, true);
-                            if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) load(&tmLo, k, flag_at(w[rank], k - c0));
-                        }
-    #pragma unroll
-                        for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
+                    }
+                    __syncwarp();
+                    if (kLo && !main && lane < 16) {
+                        r.x += a.lb0, r.y += a.lb0, r.z += a.lb0, r.w += a.lb0;
+                        gather4<CTAS>(sb + lane * 512, &tmLoB, nb, r, fb);
+                        gather4<CTAS>(sb + 8192 + lane * 512, &tmLoB, nb + 64, r, fb);
                     }
                 }
             }
@@ -614,38 +625,24 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     const Item t = item_of(a, i);
                     int k0, k1;
                     krange(t, k0, k1);
-                    uint32_t w[CTAS], wn[CTAS];
-                    flags(t, k0, w);
-                    for (int c0 = k0; ok && c0 < k1; c0 += kFlagRun) {
-                        flags(t, c0 + kFlagRun, wn);
+                    const int2 ex = extra(t);
+                    for (int c0 = k0; ok && c0 < k1; c0 += kChunk, ++gc) {
                         const uint32_t b = gc & 1;
-                        const bool begin = (c0 - k0) % kChunk == 0;   // a chunk's first K step
-                        if (begin) {
-                            if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
-                            tc_fence_after();
-                        }
-                        const int c1 = min(c0 + kFlagRun, k1);
-                        auto kstep = [&](bool add) {
+                        if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
+                        tc_fence_after();
+                        int c1 = c0 + kChunk;
+                        if (c1 >= k1) c1 = k1 + ex.y;   // (the extra steps join the last chunk)
+                        for (int k = c0; k < c1; ++k, ++g) {
                             const uint32_t s = g % kStages;
-                            if (!(ok = mbar_wait(full(s), (g / kStages) & 1, a.err, 3, tc::kWaitNs))) return;
+                            if (!(ok = mbar_wait(full(s), (g / kStages) & 1, a.err, 3, tc::kWaitNs))) break;
                             tc_fence_after();
                             const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, add || j > 0);
+                                mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, k > c0 || j > 0);
                             commit<CTAS>(empty(s));
-                            ++g;
-                        };
-                        for (int k = c0; ok && k < c1; ++k) {
-                            kstep(!begin || k > c0);
-                            if (ok && kLo && flag_at(w[0] | w[CTAS - 1], k - c0)) kstep(true);
                         }
-                        if (ok && (c1 == k1 || (c1 - k0) % kChunk == 0)) {
-                            commit<CTAS>(tfull(b));
-                            ++gc;
-                        }
-#pragma unroll
-                        for (int r = 0; r < CTAS; ++r) w[r] = wn[r];
+                        if (ok) commit<CTAS>(tfull(b));
                     }
                 }
             }
