@@ -408,7 +408,7 @@ static bool map_operand(CUtensorMap *m, const Operand &o)
 }
 
 template <int CTAS, int BN, int EPI>
-static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap (&ml)[2],
+static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap (&ml)[2],
                       const Args &a, cudaStream_t st)
 {
     auto kern = k_head_gemm<CTAS, BN, EPI>;
@@ -426,7 +426,7 @@ static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mb, const CUtens
     at[0].val.clusterDim = {CTAS, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, ml[0], ml[1], a) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, kern, ma, mt, mb, mo, ml[0], ml[1], a) != cudaSuccess) return false;
     note_launch();
     return true;
 }
@@ -437,8 +437,11 @@ template <int EPI>
 static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CUtensorMap *out, const Operand *lo, Args a,
                    cudaStream_t st)
 {
-    CUtensorMap ma, mb, mo, ml[2];
+    CUtensorMap ma, mt, mb, mo, ml[2];
     if (!map_operand(&ma, A) || !map_operand(&mb, B)) return false;
+    a.tail = (int)std::min<int64_t>(128, cdiv(A.rows % 128, 8) * 8);
+    memset(&mt, 0, sizeof mt);
+    if (!A.mn && a.tail && !tc::make_tmap3(&mt, A.base, false, A.cols, A.rows, 0, kBK, a.tail)) return false;
     memset(&mo, 0, sizeof mo);
     memset(ml, 0, sizeof ml);
     if (out) mo = *out;
@@ -451,7 +454,7 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
     // m tiles that run together: their rows of A stay in L2 (48 MB) while the n tiles pass
     const int64_t stripe = 2ll * 128 * t.ctas * a.ksteps * kBK;
     a.gm = (int)std::max<int64_t>(1, std::min<int64_t>(t.mt, std::max<int64_t>(8, (48ll << 20) / stripe)));
-    return t.ctas == 2 ? launch_as<2, 256, EPI>(ma, mb, mo, ml, a, st) : launch_as<1, 128, EPI>(ma, mb, mo, ml, a, st);
+    return t.ctas == 2 ? launch_as<2, 256, EPI>(ma, mt, mb, mo, ml, a, st) : launch_as<1, 128, EPI>(ma, mt, mb, mo, ml, a, st);
 }
 
 // ------------------------------------------------------------------ passes

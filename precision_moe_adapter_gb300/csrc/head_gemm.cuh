@@ -85,6 +85,8 @@ struct Args {
     int mt, nt, gm;          // tiles, and m tiles that run together
     int splits, ksteps, kper;   // K steps of 64 in all and per split
     int kb0;                 // first k coordinate of B (A: 0)
+    int tail;                // FWD, GRAD, DX: rows of tmAt's boxes, the M % 128 last rows of A
+                             // rounded up to 8 (a box with many rows past the end loads slowly)
     int V;                   // FWD, GRAD: number of vocabulary entries
     float c;                 // FWD, GRAD: scale * log2(e)
     int NU;                  // FWD, GRAD: units of the vocabulary
@@ -276,6 +278,7 @@ __device__ __forceinline__ Item item_of(const Args &a, int i)
 // ------------------------------------------------------------------ kernel
 template <int CTAS, int BN, int EPI>
 __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_constant__ CUtensorMap tmA,
+                                                                 const __grid_constant__ CUtensorMap tmAt,
                                                                  const __grid_constant__ CUtensorMap tmB,
                                                                  const __grid_constant__ CUtensorMap tmOut,
                                                                  const __grid_constant__ CUtensorMap tmLoA,
@@ -572,6 +575,14 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 const int2 ex = extra(t);
                 const int ma = (t.m * CTAS + (int)rank) * 128;
                 const int nb = a.n0 + t.n * BN + (int)rank * 128;
+                // rows of A that each CTA of the cluster loads (what lies below them in
+                // shared memory only reaches rows that are not stored)
+                auto arows = [&](int r) {
+                    const int left = a.M - (t.m * CTAS + r) * 128;
+                    return kAMn || left >= 128 ? 128 : left > 0 ? a.tail : 0;
+                };
+                const uint32_t bytes = CTAS * kOpBytes + (arows(0) + (CTAS == 2 ? arows(1) : 0)) * 128u;
+                const int mine = arows(rank);
                 for (int k = k0; k < k1 + ex.y; ++k, ++g) {
                     const uint32_t s = g % kStages;
                     const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
@@ -583,14 +594,14 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ((g / kStages) & 1) ^ 1, a.err, 1, tc::kWaitNs));
                     if (!ok) break;
                     if (lane == 0) {
-                        if (rank == 0) mbar_expect_tx(full(s), CTAS * kStageBytes);
+                        if (rank == 0) mbar_expect_tx(full(s), main ? bytes : CTAS * kStageBytes);
                         const int ka = k * kBK, kb = a.kb0 + k * kBK;
                         if (main) {
                             if constexpr (kAMn) {
                                 load_2d<CTAS>(sa, &tmA, ma, ka, fb);
                                 load_2d<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
-                            } else {
-                                load_2d<CTAS>(sa, &tmA, ka, ma, fb);
+                            } else if (mine) {
+                                load_2d<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka, ma, fb);
                             }
                             if constexpr (kBMn) {
                                 load_2d<CTAS>(sb, &tmB, nb, kb, fb);
