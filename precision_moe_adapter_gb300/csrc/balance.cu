@@ -5,16 +5,20 @@
 // Both passes read the [T, E] logits once and hold a token's row in
 // registers, NI values per thread of its group: a warp per token up to 1024
 // experts, a CTA per token above (rows of up to 4096 do not fit a warp's
-// registers).
+// registers).  The work per token is a chain of short steps (row, maximum,
+// sum, dot), so what counts is that all of a token's loads are on their way
+// at once and that enough tokens are in flight; three launches in a chain.
 #include <cmath>
 
 #include "common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace pmoe {
 namespace bal {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;      // backward
+constexpr int kRedThreads = 512;
 constexpr float kNegInf = -INFINITY;
 
 struct Ws {
@@ -37,7 +41,7 @@ static Ws carve(void *base, int T, int E, int nseq)
         return p;
     };
     Ws w;
-    w.L = (int)std::max<int64_t>(8, cdiv(cdiv(T, 2 * 152), 8) * 8);
+    w.L = (int)std::max<int64_t>(16, cdiv(cdiv(T, 2 * 152), 16) * 16);
     w.slots = (int)cdiv(std::max(T, 1), w.L) + nseq;
     w.Ep = (E + 3) & ~3;
     w.err = (DevErr *)take(kHdrBytes);
@@ -67,6 +71,10 @@ __device__ __forceinline__ int seq_of(const int32_t *seq, int nseq, int T, int t
     return lo - 1;
 }
 
+// Threads of the forward's CTAs: 16 warps share a slab, or one group of TPT
+// threads is the CTA (its reductions are CTA barriers)
+constexpr int fwd_threads(int tpt) { return tpt > 32 ? tpt : 512; }
+
 // Reductions over a group of TPT threads (a warp, or the whole CTA)
 template <int TPT, class Op>
 __device__ __forceinline__ float group_reduce(float v, Op op, float *sh)
@@ -89,18 +97,20 @@ struct Add {
     __device__ float operator()(float a, float b) const { return a + b; }
 };
 
-// softmax of one row, thread `tid` of the group holding columns tid + TPT i.
-// A row of -inf only has p = 0.
+// One row of logits, thread `tid` of the group holding columns tid + TPT i
 template <int TPT, int NI>
-__device__ __forceinline__ void row_softmax(const float *__restrict__ l, int E, int tid, float (&p)[NI], float *sh)
+__device__ __forceinline__ void row_load(const float *__restrict__ l, int E, int tid, float (&p)[NI])
+{
+#pragma unroll
+    for (int i = 0; i < NI; ++i) p[i] = tid + TPT * i < E ? l[tid + TPT * i] : kNegInf;
+}
+// softmax of such a row; a row of -inf only has p = 0
+template <int TPT, int NI>
+__device__ __forceinline__ void row_softmax(float (&p)[NI], float *sh)
 {
     float m = kNegInf;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = tid + TPT * i;
-        p[i] = e < E ? l[e] : kNegInf;
-        m = fmaxf(m, p[i]);
-    }
+    for (int i = 0; i < NI; ++i) m = fmaxf(m, p[i]);
     m = group_reduce<TPT>(m, Max(), sh);
     const float mm = m == kNegInf ? 0.f : m;
     float s = 0.f;
@@ -118,44 +128,52 @@ __device__ __forceinline__ void row_softmax(const float *__restrict__ l, int E, 
 // ------------------------------------------------------------------ forward
 // Partial sums of one slab: per overlapping sequence, the token groups' sums
 // of p (added in group order), the counts (integer atomics: order-free) and
-// the number of tokens.
+// the number of tokens.  A group loads its next row while it works on one.
 template <int TPT, int NI>
-__global__ void __launch_bounds__(kThreads) k_balance_partial(int T, int E, int k, int L, int Ep,
-                                                              const float *__restrict__ logits,
-                                                              const int32_t *__restrict__ idx,
-                                                              const uint8_t *__restrict__ valid,
-                                                              const int32_t *__restrict__ seq, int nseq,
-                                                              float *__restrict__ psum, int32_t *__restrict__ cnt,
-                                                              int32_t *__restrict__ ntok, DevErr *err)
+__global__ void __launch_bounds__(fwd_threads(TPT)) k_balance_partial(int T, int E, int k, int L, int Ep,
+                                                                 const float *__restrict__ logits,
+                                                                 const int32_t *__restrict__ idx,
+                                                                 const uint8_t *__restrict__ valid,
+                                                                 const int32_t *__restrict__ seq, int nseq,
+                                                                 float *__restrict__ psum, int32_t *__restrict__ cnt,
+                                                                 int32_t *__restrict__ ntok, DevErr *err)
 {
+    constexpr int kFwdThreads = fwd_threads(TPT);
     extern __shared__ float sm[];   // [groups][Ep] sums, then [Ep] counts
-    __shared__ float sh[kThreads / 32];
+    __shared__ float sh[kFwdThreads / 32];
     __shared__ int sn;
-    constexpr int kGroups = kThreads / TPT;
+    constexpr int kGroups = kFwdThreads / TPT;
     int *sc = (int *)(sm + kGroups * Ep);
     const int grp = threadIdx.x / TPT, tid = threadIdx.x % TPT;
     const int t0 = blockIdx.x * L, t1 = min(T, t0 + L);
+    grid_wait();
+    grid_go();
     for (int s = max(0, seq_of(seq, nseq, T, t0)); s < nseq; ++s) {
         const int a0 = seq_at(seq, s, nseq, T), b0 = seq_at(seq, s + 1, nseq, T);
         if (a0 >= t1) break;
         const int a = max(a0, t0), b = min(b0, t1);
         if (a >= b) continue;
         __syncthreads();   // the previous sequence's sums have been written out
-        for (int e = threadIdx.x; e < E; e += kThreads) sc[e] = 0;
+        for (int e = threadIdx.x; e < E; e += kFwdThreads) sc[e] = 0;
         if (threadIdx.x == 0) sn = 0;
         __syncthreads();
-        float acc[NI];
+        float acc[NI], next[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[i] = 0.f;
-        int n = 0;
-        for (int t = a + grp; t < b; t += kGroups) {
-            if (valid && !valid[t]) continue;
+        int n = 0, t = a + grp;
+        if (t < b) row_load<TPT, NI>(logits + (int64_t)t * E, E, tid, next);
+        for (; t < b; t += kGroups) {
             float p[NI];
-            row_softmax<TPT, NI>(logits + (int64_t)t * E, E, tid, p, sh);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) p[i] = next[i];
+            const bool use = !valid || valid[t];
+            const int e = tid < k ? idx[(int64_t)t * k + tid] : 0;
+            if (t + kGroups < b) row_load<TPT, NI>(logits + (int64_t)(t + kGroups) * E, E, tid, next);
+            if (!use) continue;
+            row_softmax<TPT, NI>(p, sh);
 #pragma unroll
             for (int i = 0; i < NI; ++i) acc[i] += p[i];
             if (tid < k) {
-                const int e = idx[(int64_t)t * k + tid];
                 if (e >= 0 && e < E) atomicAdd(&sc[e], 1);
                 else record_error(err, PMOE_ERR_BAD_INDEX, t, e);
             }
@@ -167,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_partial(int T, int E, int 
         if (tid == 0) atomicAdd(&sn, n);
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
-        for (int e = threadIdx.x; e < Ep; e += kThreads) {
+        for (int e = threadIdx.x; e < Ep; e += kFwdThreads) {
             float v = 0.f;
             if (e < E)
                 for (int g = 0; g < kGroups; ++g) v += sm[g * Ep + e];
@@ -178,64 +196,61 @@ __global__ void __launch_bounds__(kThreads) k_balance_partial(int T, int E, int 
     }
 }
 
-// One CTA per sequence: its slots are added in order (in `groups` interleaved
-// strands, then the strands in order); loss = E / (k n) sum_e c_e pmean_e.
-__global__ void __launch_bounds__(1024) k_balance_reduce(int T, int E, int k, int L, int Ep,
-                                                         const int32_t *__restrict__ seq, int nseq,
-                                                         const float *__restrict__ psum,
-                                                         const int32_t *__restrict__ cnt,
-                                                         const int32_t *__restrict__ ntok, int32_t *__restrict__ counts,
-                                                         int32_t *__restrict__ n_out, float *__restrict__ pmean,
-                                                         float *__restrict__ loss, DevErr *err)
+// One cluster of C CTAs per sequence, each with `cols` (a multiple of 32) of
+// the experts: the slots are added in kRedThreads / cols interleaved strands,
+// then the strands, then the CTAs' shares of the loss, always in order.
+// loss = E / (k n) sum_e c_e pmean_e.
+__global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, int k, int L, int Ep, int cols, int C,
+                                                                const int32_t *__restrict__ seq, int nseq,
+                                                                const float *__restrict__ psum,
+                                                                const int32_t *__restrict__ cnt,
+                                                                const int32_t *__restrict__ ntok,
+                                                                int32_t *__restrict__ counts,
+                                                                int32_t *__restrict__ n_out,
+                                                                float *__restrict__ pmean, float *__restrict__ loss,
+                                                                DevErr *err)
 {
-    extern __shared__ float4 sp[];   // [1024] strand sums, then [1024] strand counts
-    __shared__ float sw[32];
+    __shared__ float sp[kRedThreads];
+    __shared__ int sq[kRedThreads];
+    __shared__ float sw[kRedThreads / 32], sl[8];   // sl: the CTAs' shares (CTA 0)
     __shared__ int sn;
-    int4 *sq = (int4 *)(sp + 1024);
-    const int s = blockIdx.x, E4 = Ep / 4;
+    const int s = blockIdx.x / C, r = blockIdx.x % C;
+    grid_wait();
+    grid_go();
     const int a = seq_at(seq, s, nseq, T), b = seq_at(seq, s + 1, nseq, T);
-    if (seq && threadIdx.x == 0 &&
-        (seq[s] < 0 || seq[s + 1] < seq[s] || seq[s + 1] > T))
+    if (seq && threadIdx.x == 0 && r == 0 && (seq[s] < 0 || seq[s + 1] < seq[s] || seq[s + 1] > T))
         record_error(err, PMOE_ERR_BAD_INDEX, s, seq[s]);
     const int first = a / L, last = b > a ? (b - 1) / L : first - 1;
     if (threadIdx.x == 0) sn = 0;
     __syncthreads();
     int n = 0;
-    for (int i = first + threadIdx.x; i <= last; i += 1024) n += ntok[i + s];
+    for (int i = first + threadIdx.x; i <= last; i += kRedThreads) n += ntok[i + s];
     if (n) atomicAdd(&sn, n);
-    const int groups = 1024 / E4, grp = threadIdx.x / E4, c4 = threadIdx.x % E4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    int4 c = make_int4(0, 0, 0, 0);
-    if (grp < groups)
-#pragma unroll 4
-        for (int i = first + grp; i <= last; i += groups) {
-            const float4 x = *(const float4 *)(psum + (int64_t)(i + s) * Ep + c4 * 4);
-            const int4 y = *(const int4 *)(cnt + (int64_t)(i + s) * Ep + c4 * 4);
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            c.x += y.x, c.y += y.y, c.z += y.z, c.w += y.w;
+    const int strands = kRedThreads / cols, strand = threadIdx.x / cols, col = threadIdx.x % cols;
+    const int e = r * cols + col;
+    float v = 0.f;
+    int c = 0;
+    if (strand < strands && e < E) {
+#pragma unroll 8
+        for (int i = first + strand; i <= last; i += strands) {
+            v += psum[(int64_t)(i + s) * Ep + e];
+            c += cnt[(int64_t)(i + s) * Ep + e];
         }
+    }
     sp[threadIdx.x] = v;
     sq[threadIdx.x] = c;
     __syncthreads();
     n = sn;
     const float inv = n > 0 ? 1.f / (float)n : 0.f;
     float part = 0.f;
-    if (threadIdx.x < E4) {
-        for (int g = 1; g < groups; ++g) {
-            const float4 x = sp[g * E4 + c4];
-            const int4 y = sq[g * E4 + c4];
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            c.x += y.x, c.y += y.y, c.z += y.z, c.w += y.w;
+    if (threadIdx.x < cols && e < E) {
+        for (int g = 1; g < strands; ++g) {
+            v += sp[g * cols + col];
+            c += sq[g * cols + col];
         }
-        const float pv[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-        const int cv[4] = {c.x, c.y, c.z, c.w};
-        for (int j = 0; j < 4; ++j) {
-            const int e = c4 * 4 + j;
-            if (e >= E) break;
-            counts[(int64_t)s * E + e] = cv[j];
-            pmean[(int64_t)s * E + e] = pv[j];
-            part += (float)cv[j] * pv[j];
-        }
+        counts[(int64_t)s * E + e] = c;
+        pmean[(int64_t)s * E + e] = v * inv;
+        part = (float)c * (v * inv);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
@@ -243,7 +258,21 @@ __global__ void __launch_bounds__(1024) k_balance_reduce(int T, int E, int k, in
     __syncthreads();
     if (threadIdx.x == 0) {
         float t = 0.f;
-        for (int i = 0; i < 32; ++i) t += sw[i];
+        for (int i = 0; i < kRedThreads / 32; ++i) t += sw[i];
+        if (C == 1) {
+            sl[0] = t;
+        } else {   // into CTA 0's sl[r]
+            uint32_t ad = (uint32_t)__cvta_generic_to_shared(&sl[r]), remote;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(ad));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(t) : "memory");
+        }
+    }
+    __syncwarp();
+    if (C > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (threadIdx.x == 0 && r == 0) {
+        float t = 0.f;
+        for (int i = 0; i < C; ++i) t += sl[i];
         loss[s] = t * ((float)E / (float)k) * inv;
         n_out[s] = n;
     }
@@ -266,48 +295,60 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(int T, int E, int k
     __shared__ float sh[kThreads / 32];
     const int tid = threadIdx.x % TPT;
     const int t = blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
+    grid_wait();
+    grid_go();
     if (t >= T) return;
+    // all loads first: the row, the selection, the sequence's counts
     float d[NI];
+    if (gl) {
+        row_load<TPT, NI>(logits + (int64_t)t * E, E, tid, d);
+    }
+    const int lane = threadIdx.x & 31;
+    int e = -1;
+    float wj = 0.f, gj = 0.f;
+    if (dw && lane < k) {   // every warp forms the k terms, lane j slot j
+        e = idx[(int64_t)t * k + lane];
+        wj = w[(int64_t)t * k + lane];
+        gj = dw[(int64_t)t * k + lane];
+    }
+    const bool counted = gl && (!valid || valid[t]);
+    int n = 0;
+    float av[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) d[i] = 0.f;
-    if (gl && (!valid || valid[t])) {
+    for (int i = 0; i < NI; ++i) av[i] = 0.f;
+    if (counted) {
         const int s = seq_of(seq, nseq, T, t);
-        const int n = s >= 0 && s < nseq ? ntok[s] : 0;
+        n = s >= 0 && s < nseq ? ntok[s] : 0;
         if (n > 0) {
-            row_softmax<TPT, NI>(logits + (int64_t)t * E, E, tid, d, sh);
             const float f = gl[s] * ((float)E / (float)k) / ((float)n * (float)n);
-            float av[NI], dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int e = tid + TPT * i;
-                av[i] = e < E ? f * (float)counts[(int64_t)s * E + e] : 0.f;
-                dot += d[i] * av[i];
-            }
-            dot = group_reduce<TPT>(dot, Add(), sh);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) d[i] *= av[i] - dot;
+            for (int i = 0; i < NI; ++i)
+                if (tid + TPT * i < E) av[i] = f * (float)counts[(int64_t)s * E + tid + TPT * i];
         }
     }
+    if (n > 0) {
+        row_softmax<TPT, NI>(d, sh);
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) dot += d[i] * av[i];
+        dot = group_reduce<TPT>(dot, Add(), sh);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) d[i] *= av[i] - dot;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) d[i] = 0.f;
+    }
     if (dw) {
-        // every warp forms the k terms (lane j: slot j), then each thread adds those of its columns
-        const int lane = threadIdx.x & 31;
-        int e = -1;
-        float wj = 0.f, gj = 0.f;
-        if (lane < k) {
-            e = idx[(int64_t)t * k + lane];
-            wj = w[(int64_t)t * k + lane];
-            gj = dw[(int64_t)t * k + lane];
-            if (e < 0 || e >= E) {
-                if (tid < 32) record_error(err, PMOE_ERR_BAD_INDEX, t, e);
-                e = -1;
-                wj = 0.f;
-            }
+        if (lane < k && (e < 0 || e >= E)) {
+            if (tid < 32) record_error(err, PMOE_ERR_BAD_INDEX, t, e);
+            e = -1;
+            wj = 0.f;
         }
         float dot = wj * gj;
 #pragma unroll
         for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         const float vj = wj * (gj - dot);
-        for (int j = 0; j < k; ++j) {
+        for (int j = 0; j < k; ++j) {   // each thread adds the terms of its columns
             const int ej = __shfl_sync(0xffffffffu, e, j);
             const float x = __shfl_sync(0xffffffffu, vj, j);
             const int i0 = ej >= 0 && ej % TPT == tid ? ej / TPT : -1;
@@ -331,7 +372,7 @@ static void by_experts(int E, F f)
     else if (E <= 384) f(integral_constant<int, 32>(), integral_constant<int, 12>());
     else if (E <= 512) f(integral_constant<int, 32>(), integral_constant<int, 16>());
     else if (E <= 1024) f(integral_constant<int, 32>(), integral_constant<int, 32>());
-    else f(integral_constant<int, 256>(), integral_constant<int, 16>());
+    else f(integral_constant<int, 256>(), integral_constant<int, 16>());   // E <= 4096
 }
 
 static bool aligned(std::initializer_list<const void *> ps)
@@ -367,19 +408,17 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
     if (dims.T > 0)
         bal::by_experts(dims.E, [&](auto tpt, auto ni) {
             auto kern = bal::k_balance_partial<tpt.value, ni.value>;
-            const size_t sm = (size_t)(bal::kThreads / tpt.value + 1) * w.Ep * 4;
-            ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) == cudaSuccess;
-            if (!ok) return;
-            kern<<<(unsigned)cdiv(dims.T, w.L), bal::kThreads, sm, stream>>>(dims.T, dims.E, dims.k, w.L, w.Ep, logits,
-                                                                           idx, valid, seq, nseq, w.psum, w.cnt, w.ntok,
-                                                                           w.err);
-            note_launch();
+            const size_t sm = (size_t)(bal::fwd_threads(tpt.value) / tpt.value + 1) * w.Ep * 4;
+            ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) == cudaSuccess &&
+                 launch_chained(kern, (unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
+                                w.L, w.Ep, logits, idx, valid, seq, nseq, w.psum, w.cnt, w.ntok, w.err);
         });
-    if (!ok) return PMOE_ERR_CUDA;
-    bal::k_balance_reduce<<<nseq, 1024, 1024 * 32, stream>>>(dims.T, dims.E, dims.k, w.L, w.Ep, seq, nseq, w.psum, w.cnt,
-                                                             w.ntok, counts, ntok, pmean, loss, w.err);
-    note_launch();
-    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+    // CTAs per sequence: 32 experts each up to 8 CTAs, then more experts each
+    const int cols = (int)(cdiv(dims.E, 256) * 32), C = (int)cdiv(dims.E, cols);
+    ok = ok && launch_chained(bal::k_balance_reduce, (unsigned)(nseq * C), bal::kRedThreads, 0, C, stream, dims.T, dims.E,
+                              dims.k, w.L, w.Ep, cols, C, seq, nseq, w.psum, w.cnt, w.ntok, counts, ntok, pmean, loss,
+                              w.err);
+    return ok ? PMOE_OK : PMOE_ERR_CUDA;
 }
 
 pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_t *idx, const float *w,
@@ -395,13 +434,13 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
     const bal::Ws b = bal::carve(ws, dims.T, dims.E, nseq);
     if (!ws || ws_bytes < b.bytes || !bal::aligned({ws})) return PMOE_ERR_WORKSPACE;
     if (dims.T == 0) return PMOE_OK;
+    bool ok = true;
     bal::by_experts(dims.E, [&](auto tpt, auto ni) {
-        bal::k_route_backward<tpt.value, ni.value>
-            <<<(unsigned)cdiv(dims.T, bal::kThreads / tpt.value), bal::kThreads, 0, stream>>>(
-                dims.T, dims.E, dims.k, logits, idx, w, d_topk_w, valid, seq, nseq, counts, ntok, g_loss, dlogits, b.err);
-        note_launch();
+        ok = launch_chained(bal::k_route_backward<tpt.value, ni.value>, (unsigned)cdiv(dims.T, bal::kThreads / tpt.value),
+                            bal::kThreads, 0, 1, stream, dims.T, dims.E, dims.k, logits, idx, w, d_topk_w, valid, seq,
+                            nseq, counts, ntok, g_loss, dlogits, b.err);
     });
-    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+    return ok ? PMOE_OK : PMOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -18,6 +18,12 @@ constexpr int kSms = 152;                     // SMs of a GB300
 constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece
 
 // ------------------------------------------------------------------ targets
+// The backward's first kernel also clears the counters of its first piece.
+__device__ __forceinline__ void clear(int *p, int n)
+{
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) p[i] = 0;
+}
+
 // Distillation: one warp per token turns the teacher's K entries into a
 // probability each, q = softmax(scale t) over the entries present, ordered
 // by vocabulary id (missing ones last, id kNoId, q = 0).  The place of an
@@ -28,11 +34,15 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
                                                       const float *__restrict__ t_logits, const float *__restrict__ g,
                                                       int32_t *__restrict__ ids, float *__restrict__ q,
                                                       float *__restrict__ lq, uint16_t *__restrict__ first, int NU,
-                                                      float *__restrict__ coef, DevErr *err)
+                                                      float *__restrict__ coef, int *__restrict__ zero, int nzero,
+                                                      DevErr *err)
 {
     __shared__ int32_t skey[4][kMaxK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * 4 + warp;
+    grid_wait();
+    grid_go();
+    clear(zero, nzero);
     if (t >= T) return;
     const float inf = __int_as_float(0x7f800000);
     float x[kMaxK / 32];
@@ -91,9 +101,13 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
 
 // Log-probability: the row's factor of dz = g s (onehot - p) = coef (p - onehot)
 __global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, const int32_t *__restrict__ target,
-                                                   const float *__restrict__ g, float *__restrict__ coef, DevErr *err)
+                                                   const float *__restrict__ g, float *__restrict__ coef,
+                                                   int *__restrict__ zero, int nzero, DevErr *err)
 {
     const int t = blockIdx.x * 256 + threadIdx.x;
+    grid_wait();
+    grid_go();
+    clear(zero, nzero);
     if (t >= T) return;
     const int y = target[t];
     if (y >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
@@ -115,6 +129,8 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     __shared__ float2 sw[4];
     const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float ninf = -__int_as_float(0x7f800000);
+    grid_wait();
+    grid_go();
     const float2 *p = part + (int64_t)t * NU;
     float m = ninf, s = 0.f;   // base 2
     for (int i = threadIdx.x; i < NU; i += 128) {
@@ -173,13 +189,12 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
 //   DW (kDw 1): rows are vocabulary entries, the row of B is the token; `fl`
 //   names the blocks of 128 tokens to look at
 template <int kDw>
-__global__ void __launch_bounds__(256) k_head_large(int T, const int *__restrict__ cnt, const int2 *__restrict__ large,
-                                                    const uint8_t *__restrict__ fl, int fs, int *__restrict__ steps,
-                                                    int2 *__restrict__ lists, int32_t *__restrict__ lidx,
-                                                    uint16_t *__restrict__ lo)
+__device__ void large_steps(int blk, int T, const int *__restrict__ cnt, const int2 *__restrict__ large,
+                            const uint8_t *__restrict__ fl, int fs, int *__restrict__ steps, int2 *__restrict__ lists,
+                            int32_t *__restrict__ lidx, uint16_t *__restrict__ lo)
 {
     __shared__ int sw[8], s_base;
-    const int blk = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int2 e[kMaxLarge];
     int n = 0;
     // this thread's entries of token t, ascending by vocabulary id
@@ -270,10 +285,23 @@ __global__ void __launch_bounds__(256) k_head_large(int T, const int *__restrict
     }
 }
 
+// CTAs 0 .. nx-1: DX's blocks, the others DW's
+__global__ void __launch_bounds__(256) k_head_large(int nx, int T, const int *cnt, const int2 *large, const uint8_t *fl,
+                                                    int fs, int *steps, int2 *lists0, int32_t *lidx0, uint16_t *lo0,
+                                                    int2 *lists1, int32_t *lidx1, uint16_t *lo1)
+{
+    grid_wait();
+    grid_go();
+    if ((int)blockIdx.x < nx) large_steps<0>(blockIdx.x, T, cnt, large, fl, fs, steps, lists0, lidx0, lo0);
+    else large_steps<1>(blockIdx.x - nx, T, cnt, large, fl, fs, steps + 1, lists1, lidx1, lo1);
+}
+
 // dX = bf16(sum of the splits' FP32 partials, in order); n elements each, n % 8 == 0
 __global__ void __launch_bounds__(256) k_head_sum(int64_t n, int splits, const float *__restrict__ part,
                                                   uint16_t *__restrict__ out)
 {
+    grid_wait();
+    grid_go();
     for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ll) {
         float4 a = *(const float4 *)(part + i), b = *(const float4 *)(part + i + 4);
         for (int s = 1; s < splits; ++s) {
@@ -378,11 +406,11 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
         w.G = (uint16_t *)take(T * piece * 2);
         const int blocks[2] = {(int)cdiv(h.T, kListRows), piece / kListRows};
         w.fs = (int)cdiv(h.T, 128);
-        uint8_t *z = take(T * 4 + (size_t)blocks[1] * w.fs + 8 + 4);
+        w.zero_bytes = (T * 4 + 8 + (size_t)blocks[1] * w.fs + 3) & ~(size_t)3;
+        uint8_t *z = take(w.zero_bytes);
         w.cnt = (int *)z;
         w.steps = w.cnt + T;
         w.fl = (uint8_t *)(w.steps + 2);
-        w.zero_bytes = T * 4 + 8 + (size_t)blocks[1] * w.fs;
         w.large = (int2 *)take(T * kMaxLarge * 8);
         for (int i = 0; i < 2; ++i) {
             w.max_steps[i] = (int)(cdiv((int64_t)h.T * kMaxLarge, 64) + blocks[i]);
@@ -416,19 +444,8 @@ static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtens
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(BN)) == cudaSuccess;
     if (!attr) return false;
     const int64_t items = (int64_t)a.mt * a.nt * a.splits;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(items, tc::num_sms() / CTAS) * CTAS));
-    cfg.blockDim = dim3(threads_of(BN));
-    cfg.dynamicSmemBytes = smem_of(BN);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {CTAS, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, ma, mt, mb, mo, ml[0], ml[1], a) != cudaSuccess) return false;
-    note_launch();
-    return true;
+    return launch_chained(kern, (unsigned)(std::min<int64_t>(items, tc::num_sms() / CTAS) * CTAS), threads_of(BN),
+                          smem_of(BN), CTAS, st, ma, mt, mb, mo, ml[0], ml[1], a);
 }
 
 // One product: M x N outputs over ksteps K steps, with the tiles of `t`;
@@ -464,9 +481,9 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     const int K = distill ? h.K : 1;
     const int32_t *ids = idx;
     if (distill) {
-        k_head_teacher<<<(unsigned)cdiv(h.T, 4), 128, 0, st>>>(h.T, h.V, K, scale, idx, t_logits, nullptr, w.ids, w.q,
-                                                               w.lq, w.first, (int)cdiv(h.V, kUnit), nullptr, w.err);
-        note_launch();
+        if (!launch_chained(k_head_teacher, (unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, K, scale, idx, t_logits,
+                            nullptr, w.ids, w.q, w.lq, w.first, (int)cdiv(h.V, kUnit), nullptr, nullptr, 0, w.err))
+            return PMOE_ERR_CUDA;
         ids = w.ids;
     }
     Args a{};
@@ -485,9 +502,10 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
-    k_head_combine<<<h.T, 128, 0, st>>>(h.V, K, a.NU, a.c, distill, w.part, w.zt, ids, w.q, w.lq, value, lse, w.err);
-    note_launch();
-    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+    return launch_chained(k_head_combine, (unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, a.c, distill, w.part, w.zt, ids, w.q,
+                          w.lq, value, lse, w.err)
+               ? PMOE_OK
+               : PMOE_ERR_CUDA;
 }
 
 static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *W, float scale, const int32_t *idx,
@@ -495,12 +513,13 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
                             const Ws &w, cudaStream_t st)
 {
     const int K = distill ? h.K : 1;
-    if (distill)
-        k_head_teacher<<<(unsigned)cdiv(h.T, 4), 128, 0, st>>>(h.T, h.V, K, scale, idx, t_logits, g, w.ids, w.q, nullptr,
-                                                               w.first, (int)cdiv(h.V, kUnit), w.coef, w.err);
-    else
-        k_head_coef<<<(unsigned)cdiv(h.T, 256), 256, 0, st>>>(h.T, h.V, scale, idx, g, w.coef, w.err);
-    note_launch();
+    const int nzero = (int)(w.zero_bytes / 4);
+    const bool made =
+        distill ? launch_chained(k_head_teacher, (unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, K, scale, idx, t_logits, g,
+                                 w.ids, w.q, nullptr, w.first, (int)cdiv(h.V, kUnit), w.coef, w.cnt, nzero, w.err)
+                : launch_chained(k_head_coef, (unsigned)cdiv(h.T, 256), 256, 0, 1, st, h.T, h.V, scale, idx, g, w.coef,
+                                 w.cnt, nzero, w.err);
+    if (!made) return PMOE_ERR_CUDA;
     const int piece = piece_of(h.T, h.V);
     const Tiling tx = dx_tiling(h);
     for (int v0 = 0; v0 < h.V; v0 += piece) {
@@ -513,7 +532,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
         b.fl = dW ? w.fl : nullptr;
         b.fs = w.fs;
         b.err = w.err;
-        if (cudaMemsetAsync(w.cnt, 0, w.zero_bytes, st) != cudaSuccess) return PMOE_ERR_CUDA;
+        if (v0 > 0 && cudaMemsetAsync(w.cnt, 0, w.zero_bytes, st) != cudaSuccess) return PMOE_ERR_CUDA;
         {   // G = coef (softmax(Z) - q) of this piece
             Args a = b;
             a.M = h.T;
@@ -534,6 +553,10 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
                                  nullptr, a, st))
                 return PMOE_ERR_CUDA;
         }
+        const int nx = dX ? (int)cdiv(h.T, kListRows) : 0, nw = dW ? (int)cdiv(vc, kListRows) : 0;
+        if (!launch_chained(k_head_large, (unsigned)(nx + nw), 256, 0, 1, st, nx, h.T, w.cnt, w.large, w.fl, w.fs, w.steps,
+                            w.lists[0], w.lidx[0], w.lo[0], w.lists[1], w.lidx[1], w.lo[1]))
+            return PMOE_ERR_CUDA;
         if (dX) {
             Args a = b;
             a.M = h.T;
@@ -547,9 +570,6 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
                                    : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 32);
             // (a last, shorter piece may leave the last splits without K steps)
             t.splits = (int)cdiv(a.ksteps, t.kper);
-            k_head_large<0><<<(unsigned)cdiv(h.T, kListRows), 256, 0, st>>>(h.T, w.cnt, w.large, nullptr, 0, w.steps,
-                                                                            w.lists[0], w.lidx[0], w.lo[0]);
-            note_launch();
             a.lists = w.lists[0];
             a.lidx = w.lidx[0];
             a.lb0 = v0;
@@ -562,9 +582,6 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.M = vc;
             a.N = h.d;
             a.ksteps = (int)cdiv(h.T, kBK);
-            k_head_large<1><<<(unsigned)cdiv(vc, kListRows), 256, 0, st>>>(h.T, w.cnt, w.large, w.fl, w.fs, w.steps + 1,
-                                                                           w.lists[1], w.lidx[1], w.lo[1]);
-            note_launch();
             a.lists = w.lists[1];
             a.lidx = w.lidx[1];
             const Operand lo{w.lo[1], kListRows, (int64_t)w.max_steps[1] * 64, true};
@@ -576,10 +593,11 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     }
     if (dX && w.dx) {
         const int64_t n = (int64_t)h.T * h.d;
-        k_head_sum<<<(unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, st>>>(n, tx.splits, w.dx, (uint16_t *)dX);
-        note_launch();
+        if (!launch_chained(k_head_sum, (unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, 1, st, n, tx.splits,
+                            w.dx, (uint16_t *)dX))
+            return PMOE_ERR_CUDA;
     }
-    return cudaPeekAtLastError() == cudaSuccess ? PMOE_OK : PMOE_ERR_CUDA;
+    return PMOE_OK;
 }
 
 // Argument checks shared by the entry points; PMOE_OK to go on

@@ -46,6 +46,7 @@
 #pragma once
 
 #include "gemm_tc.cuh"
+#include "pdl.cuh"
 
 namespace pmoe {
 namespace hg {
@@ -336,6 +337,8 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
 
+    grid_wait();
+    grid_go();
     // K steps of an item
     auto krange = [&](const Item &t, int &k0, int &k1) {
         k0 = t.s * a.kper;
@@ -485,6 +488,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     }
                 };
                 if constexpr (EPI == HG_GRAD) {
+                    uint32_t large[kUnit / 32];   // the columns to list
 #pragma unroll
                     for (int q = 0; q < kUnit; q += 32) {
                         const int e0 = cb + q;
@@ -510,32 +514,38 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
 #pragma unroll
                         for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(acc[q + j]));
                         const bool keep = big >= kLarge && cf != 0.f;
-                        uint32_t large = 0;   // the columns to list
+                        large[q / 32] = 0;
                         if (__any_sync(0xffffffffu, keep)) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                large |= keep && fabsf(acc[q + j]) >= kLarge ? 1u << j : 0u;
+                                large[q / 32] |= keep && fabsf(acc[q + j]) >= kLarge ? 1u << j : 0u;
                         }
 #pragma unroll
                         for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
-                        while (__any_sync(0xffffffffu, large != 0)) {
-                            const int j0 = __ffs(large) - 1;
-                            float v = 0.f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v = j == j0 ? acc[q + j] : v;
-                            if (large) {
-                                const int n = atomicAdd(&a.cnt[row], 1);
-                                if (n < kMaxLarge)
-                                    a.large[(int64_t)row * kMaxLarge + n] =
-                                        make_int2(e0 - a.n0 + j0, f2bf(v - bf2f(f2bf(v))));
-                                if (a.fl) a.fl[(int64_t)((e0 - a.n0) / kListRows) * a.fs + (row >> 7)] = 1;
-                                large &= large - 1;
-                            }
-                        }
                         if (q & 32) {
                             reuse();
                             stage16(q - 32);
                             put(&tmOut, xc + q - 32);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, (large[0] | large[1] | large[2] | large[3]) != 0)) {
+                        int n = 0;
+                        if (large[0] | large[1] | large[2] | large[3]) {
+                            n = atomicAdd(&a.cnt[row], __popc(large[0]) + __popc(large[1]) + __popc(large[2]) + __popc(large[3]));
+                            if (a.fl) a.fl[(int64_t)((cb - a.n0) / kListRows) * a.fs + (row >> 7)] = 1;
+                        }
+#pragma unroll
+                        for (int q = 0; q < kUnit; q += 32) {
+                            while (__any_sync(0xffffffffu, large[q / 32] != 0)) {
+                                const int j0 = __ffs(large[q / 32]) - 1;
+                                float v = 0.f;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v = j == j0 ? acc[q + j] : v;
+                                if (large[q / 32] && n < kMaxLarge)
+                                    a.large[(int64_t)row * kMaxLarge + n++] =
+                                        make_int2(cb + q - a.n0 + j0, f2bf(v - bf2f(f2bf(v))));
+                                large[q / 32] &= large[q / 32] - 1;
+                            }
                         }
                     }
                 } else if (EPI == HG_DX && !a.bf16_out) {

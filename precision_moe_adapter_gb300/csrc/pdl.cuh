@@ -1,0 +1,42 @@
+// pdl.cuh -- programmatic dependent launch: a kernel of a chain starts (its
+// launch latency and set-up) while the kernel before it in the stream still
+// runs.  Every kernel launched this way calls grid_wait() before it reads or
+// writes anything in global memory: it returns once the kernel before has
+// completed and its writes are visible, and as that kernel waited in turn,
+// so has everything earlier in the stream.  grid_go() lets the next kernel's
+// CTAs be placed as soon as all of this kernel's have started.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace pmoe {
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launches a kernel that begins with grid_wait(), in clusters of `cluster` CTAs
+template <class... P, class... A>
+bool launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st,
+                    A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, (P)args...) != cudaSuccess) return false;
+    note_launch();
+    return true;
+}
+
+}  // namespace pmoe
