@@ -409,8 +409,9 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
         bal::by_experts(dims.E, [&](auto tpt, auto ni) {
             auto kern = bal::k_balance_partial<tpt.value, ni.value>;
             const size_t sm = (size_t)(bal::fwd_threads(tpt.value) / tpt.value + 1) * w.Ep * 4;
-            ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) == cudaSuccess &&
-                 launch_chained(kern, (unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
+            static const bool attr =   // up to 17 rows of 1024 floats (69 KB)
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 17 * 4096) == cudaSuccess;
+            ok = attr && launch_chained(kern, (unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
                                 w.L, w.Ep, logits, idx, valid, seq, nseq, w.psum, w.cnt, w.ntok, w.err);
         });
     // CTAs per sequence: 32 experts each up to 8 CTAs, then more experts each

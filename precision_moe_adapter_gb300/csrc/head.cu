@@ -296,18 +296,26 @@ __global__ void __launch_bounds__(256) k_head_large(int nx, int T, const int *cn
     else large_steps<1>(blockIdx.x - nx, T, cnt, large, fl, fs, steps + 1, lists1, lidx1, lo1);
 }
 
-// dX = bf16(sum of the splits' FP32 partials, in order); n elements each, n % 8 == 0
-__global__ void __launch_bounds__(256) k_head_sum(int64_t n, int splits, const float *__restrict__ part,
+struct Parts {
+    int mt, nt, gm, whole, tile, splits;   // the tiling of DX (tile: rows and columns)
+};
+// dX = bf16(sum of the FP32 parts, in order): one part where the tile was
+// taken whole.  T x d, a thread 8 columns of a row (d % 64 == 0).
+__global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const float *__restrict__ part,
                                                   uint16_t *__restrict__ out)
 {
     grid_wait();
     grid_go();
+    const int64_t n = (int64_t)T * d;
     for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ll) {
+        const int m = (int)(i / d) / p.tile, c = (int)(i % d) / p.tile, g = m / p.gm;
+        const int item = g * p.gm * p.nt + c * min(p.gm, p.mt - g * p.gm) + m - g * p.gm;
+        const int parts = item < p.whole ? 1 : p.splits;
         float4 a = *(const float4 *)(part + i), b = *(const float4 *)(part + i + 4);
-        for (int s = 1; s < splits; ++s) {
-            const float4 c = *(const float4 *)(part + s * n + i), d = *(const float4 *)(part + s * n + i + 4);
-            a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-            b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+        for (int s = 1; s < parts; ++s) {
+            const float4 x = *(const float4 *)(part + s * n + i), y = *(const float4 *)(part + s * n + i + 4);
+            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+            b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
         }
         *(uint4 *)(out + i) = make_uint4(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w), pack_bf2(b.x, b.y), pack_bf2(b.z, b.w));
     }
@@ -332,11 +340,15 @@ static int piece_of(int T, int V)
 
 struct Tiling {
     int ctas, bn;
-    int mt, nt;
-    int splits, kper;
+    int mt, nt, gm;      // gm: m tiles that run together
+    int whole;           // tiles taken whole, the others cut into
+    int splits, kper;    // `splits` items of kper K steps
 };
-// Tiles of an M x N product.  `split`: K steps may be divided among the
-// SMs that the tiles leave idle (the partial sums are then added up).
+// Tiles of an M x N product over ksteps K steps.  `split`: tiles of the last,
+// partly filled round may be cut along K, their parts then being added up.
+// The number of parts is the one of least time by this estimate: a K step of
+// a tile takes 0.28 us (the tensor cores' rate at 1.8 GHz), each round 2 us
+// to fill and to drain, each part's FP32 tile goes to memory and back.
 static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
 {
     Tiling t;
@@ -346,10 +358,24 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
     t.bn = 128 * t.ctas;
     t.mt = (int)cdiv(M, 128 * t.ctas);
     t.nt = (int)cdiv(N, t.bn);
-    const int64_t slots = kSms / t.ctas, tiles = (int64_t)t.mt * t.nt;
-    int64_t s = 1;
-    if (split && tiles > 0) s = std::max<int64_t>(1, std::min(slots / tiles, ksteps / 16));
-    t.kper = (int)cdiv(std::max<int64_t>(ksteps, 1), s);
+    // m tiles that run together: their rows of A stay in L2 (48 MB) while the n tiles pass
+    const int64_t stripe = 2ll * 128 * t.ctas * ksteps * kBK;
+    t.gm = (int)std::max<int64_t>(1, std::min<int64_t>(t.mt, std::max<int64_t>(8, (48ll << 20) / std::max<int64_t>(stripe, 1))));
+    const int64_t slots = kSms / t.ctas, tiles = (int64_t)t.mt * t.nt, cut = tiles % slots;
+    int64_t best = 1;
+    if (split && cut) {
+        const double part = 2.0 * 128 * t.ctas * t.bn * 4 / 6e6;   // us
+        double least = 0;
+        for (int64_t s = 1; s <= std::min<int64_t>(ksteps, 64); ++s) {
+            const double us = cdiv(cut * s, slots) * (cdiv(ksteps, s) * 0.28 + 2) + (s > 1 ? cut * s * part : 0);
+            if (s == 1 || us < least) {
+                least = us;
+                best = s;
+            }
+        }
+    }
+    t.whole = (int)(best > 1 ? tiles - cut : tiles);
+    t.kper = (int)cdiv(std::max<int64_t>(ksteps, 1), best);
     t.splits = (int)cdiv(std::max<int64_t>(ksteps, 1), t.kper);
     return t;
 }
@@ -443,8 +469,9 @@ static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtens
     static const bool attr =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(BN)) == cudaSuccess;
     if (!attr) return false;
-    const int64_t items = (int64_t)a.mt * a.nt * a.splits;
-    return launch_chained(kern, (unsigned)(std::min<int64_t>(items, tc::num_sms() / CTAS) * CTAS), threads_of(BN),
+    const int64_t items = a.whole + ((int64_t)a.mt * a.nt - a.whole) * a.splits;
+    const int64_t clusters = std::min<int64_t>(items, tc::num_sms() / CTAS);
+    return launch_chained(kern, (unsigned)(clusters * CTAS), threads_of(BN),
                           smem_of(BN), CTAS, st, ma, mt, mb, mo, ml[0], ml[1], a);
 }
 
@@ -468,9 +495,8 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
     a.nt = t.nt;
     a.splits = t.splits;
     a.kper = t.kper;
-    // m tiles that run together: their rows of A stay in L2 (48 MB) while the n tiles pass
-    const int64_t stripe = 2ll * 128 * t.ctas * a.ksteps * kBK;
-    a.gm = (int)std::max<int64_t>(1, std::min<int64_t>(t.mt, std::max<int64_t>(8, (48ll << 20) / stripe)));
+    a.whole = t.whole;
+    a.gm = t.gm;
     return t.ctas == 2 ? launch_as<2, 256, EPI>(ma, mt, mb, mo, ml, a, st) : launch_as<1, 128, EPI>(ma, mt, mb, mo, ml, a, st);
 }
 
@@ -566,9 +592,10 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.bf16_out = w.dx == nullptr;
             a.accumulate = v0 > 0;
             Tiling t = tx;
-            const bool made = w.dx ? tc::make_tmap3(&mo, w.dx, true, h.d, h.T, t.splits, 32, 32)
+            const bool made = w.dx ? tc::make_tmap3(&mo, w.dx, true, h.d, h.T, tx.splits, 32, 32)
                                    : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 32);
-            // (a last, shorter piece may leave the last splits without K steps)
+            // (a last, shorter piece: shorter parts, perhaps fewer; the other sums then stand)
+            t.kper = (int)cdiv(a.ksteps, tx.splits);
             t.splits = (int)cdiv(a.ksteps, t.kper);
             a.lists = w.lists[0];
             a.lidx = w.lidx[0];
@@ -593,8 +620,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     }
     if (dX && w.dx) {
         const int64_t n = (int64_t)h.T * h.d;
-        if (!launch_chained(k_head_sum, (unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, 1, st, n, tx.splits,
-                            w.dx, (uint16_t *)dX))
+        if (!launch_chained(k_head_sum, (unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, 1, st, h.T, h.d,
+                            Parts{tx.mt, tx.nt, tx.gm, tx.whole, tx.bn, tx.splits}, w.dx, (uint16_t *)dX))
             return PMOE_ERR_CUDA;
     }
     return PMOE_OK;

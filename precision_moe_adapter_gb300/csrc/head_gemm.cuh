@@ -84,7 +84,9 @@ struct Args {
     int M, N;                // output rows and columns of this launch
     int n0;                  // GRAD: first vocabulary column; FWD: 0
     int mt, nt, gm;          // tiles, and m tiles that run together
-    int splits, ksteps, kper;   // K steps of 64 in all and per split
+    int ksteps;              // K steps of 64 of a tile
+    int whole;               // tiles taken whole; each of the others is cut into
+    int splits, kper;        // `splits` items of kper K steps
     int kb0;                 // first k coordinate of B (A: 0)
     int tail;                // FWD, GRAD, DX: rows of tmAt's boxes, the M % 128 last rows of A
                              // rounded up to 8 (a box with many rows past the end loads slowly)
@@ -130,9 +132,11 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// (what it orders are TMEM reads, which tcgen05's own fence covers; a release
+// at cluster scope would also wait for the warp's global stores, 2300 clocks)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 template <int CTAS>
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar)
@@ -261,19 +265,29 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi)
 
 struct Item {
     int m, n, s;   // m tile, n tile, split
+    int k0, k1;    // K steps
 };
-__device__ __forceinline__ Item item_of(const Args &a, int i)
+// Work item i (the whole tiles, then the others' first parts, their second
+// parts, ...); false past the last one
+__device__ __forceinline__ bool item_of(const Args &a, int i, Item &t)
 {
-    Item t;
-    const int per = a.mt * a.nt;
-    t.s = i / per;
-    i -= t.s * per;
+    t.s = 0;
+    t.k0 = 0;
+    t.k1 = a.ksteps;
+    if (i >= a.whole) {
+        const int cut = a.mt * a.nt - a.whole;
+        if (i - a.whole >= cut * a.splits) return false;
+        t.s = (i - a.whole) / cut;
+        i -= t.s * cut;
+        t.k0 = t.s * a.kper;
+        t.k1 = min(t.k0 + a.kper, a.ksteps);
+    }
     const int gsz = a.gm * a.nt, g = i / gsz;
     i -= g * gsz;
     const int gm = min(a.gm, a.mt - g * a.gm);   // the last group may be smaller
     t.n = i / gm;
     t.m = g * a.gm + i - t.n * gm;
-    return t;
+    return true;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -302,7 +316,6 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cta_rank() : 0u;
-    const int n_items = a.mt * a.nt * a.splits;
     const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
@@ -339,17 +352,12 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
 
     grid_wait();
     grid_go();
-    // K steps of an item
-    auto krange = [&](const Item &t, int &k0, int &k1) {
-        k0 = t.s * a.kper;
-        k1 = min(k0 + a.kper, a.ksteps);
-    };
-    // DX, DW: the item's extra K steps on remainders (with the first split)
+    // DX, DW: the item's extra K steps on remainders (with a tile's first K step)
     constexpr bool kLo = EPI == HG_DX || EPI == HG_DW;
     constexpr int kChunk = chunk_of(EPI);
     auto extra = [&](const Item &t) {
         if constexpr (kLo)
-            if (t.s == 0) return a.lists[t.m * CTAS * 128 / kListRows];
+            if (t.k0 == 0) return a.lists[t.m * CTAS * 128 / kListRows];
         return make_int2(0, 0);
     };
     bool ok = true;
@@ -366,10 +374,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         const uint32_t ob = out0 + (warp - 4) * kWarpOut, orow = ob + lane * 128;
         const float inf = __int_as_float(0x7f800000);
         uint32_t gc = 0;
-        for (int i = first; ok && i < n_items; i += step) {
-            const Item t = item_of(a, i);
-            int k0, k1;
-            krange(t, k0, k1);
+        Item t;
+        for (int i = first; ok && item_of(a, i, t); i += step) {
+            const int k0 = t.k0, k1 = t.k1;
             const int mrow = (t.m * CTAS + (int)rank) * 128;
             const int row = mrow + rl;
             const int cb = a.n0 + t.n * BN + half * kUnit;   // first column
@@ -578,10 +585,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             // ---------------- producer (the whole warp; lane 0 issues, and lanes
             // 0-15 gather four rows of B each in an extra step)
             uint32_t g = 0;
-            for (int i = first; ok && i < n_items; i += step) {
-                const Item t = item_of(a, i);
-                int k0, k1;
-                krange(t, k0, k1);
+            Item t;
+            for (int i = first; ok && item_of(a, i, t); i += step) {
+                const int k0 = t.k0, k1 = t.k1;
                 const int2 ex = extra(t);
                 const int ma = (t.m * CTAS + (int)rank) * 128;
                 const int nb = a.n0 + t.n * BN + (int)rank * 128;
@@ -642,10 +648,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 constexpr uint32_t kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
                 const uint64_t da0 = desc_of<kAMn>(s0), db0 = desc_of<kBMn>(s0 + kOpBytes);
                 uint32_t g = 0, gc = 0;
-                for (int i = first; ok && i < n_items; i += step) {
-                    const Item t = item_of(a, i);
-                    int k0, k1;
-                    krange(t, k0, k1);
+                Item t;
+                for (int i = first; ok && item_of(a, i, t); i += step) {
+                    const int k0 = t.k0, k1 = t.k1;
                     const int2 ex = extra(t);
                     for (int c0 = k0; ok && c0 < k1; c0 += kChunk, ++gc) {
                         const uint32_t b = gc & 1;

@@ -33,7 +33,7 @@ bool launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t sm
     at[1].val.clusterDim.x = cluster;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, (P)args...) != cudaSuccess) return false;
     note_launch();
     return true;

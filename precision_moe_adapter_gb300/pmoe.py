@@ -82,6 +82,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libpmoe.so (built by ``build.build()``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -169,11 +171,19 @@ def _ptr(x):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """The raw handle of torch's current stream on the current device."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())   # without making a Stream object: 3 us less a call
 
 
 def _nbytes(t):

@@ -132,17 +132,19 @@ def test_distill(T, d, V, K, scale):
     check_grad(dW, rdW, "dW")
 
 
-def test_vocabulary_in_several_pieces():
-    """T = 8192 tokens bound a piece to 32768 entries: three pieces, the last one ragged."""
-    T, d, V = 8192, 64, 70001
+@pytest.mark.parametrize("T,d,V", [(8192, 64, 70001), (4100, 1216, 66001)])
+def test_vocabulary_in_several_pieces(T, d, V):
+    """T = 8192 tokens bound a piece to 32768 entries: three pieces, the last
+    one ragged; at T = 4100 two pieces, with dX's tiles cut among the SMs."""
     X, W, y, up, _ = make(T, d, V)
     h, logp, lse, dX, dW = run_logprob(X, W, y, up, 1.0)
     assert h.status() == pmoe.PMOE_OK
     rdW = torch.zeros((V, d), dtype=D, device="cuda")
     for a in range(0, T, 1024):
-        r = slice(a, a + 1024)
-        Q = torch.zeros((1024, V), dtype=D, device="cuda")
-        Q[torch.arange(1024, device="cuda"), y[r].long()] = 1
+        r = slice(a, min(a + 1024, T))
+        n = r.stop - a
+        Q = torch.zeros((n, V), dtype=D, device="cuda")
+        Q[torch.arange(n, device="cuda"), y[r].long()] = 1
         rlse, rv, rdX, dw = reference(X[r], W, 1.0, Q, 0.0, up[r], -1.0)
         rdW += dw
         check_values(X[r], W, 1.0, lse[r], logp[r], rlse, rv)
