@@ -18,7 +18,7 @@ namespace pmoe {
 namespace bal {
 
 constexpr int kThreads = 256;      // backward
-constexpr int kRedThreads = 512;
+constexpr int kRedThreads = 1024;  // reduction, at most
 constexpr float kNegInf = -INFINITY;
 
 struct Ws {
@@ -97,14 +97,34 @@ struct Add {
     __device__ float operator()(float a, float b) const { return a + b; }
 };
 
-// One row of logits, thread `tid` of the group holding columns tid + TPT i
-template <int TPT, int NI>
+// Thread `tid` of a group holds NI columns of a row, in runs of V (V = 4:
+// 16-byte loads, where E is a multiple of 4; else 1): value i is column
+template <int TPT, int V>
+__device__ __forceinline__ int col_of(int tid, int i) { return (i / V * TPT + tid) * V + i % V; }
+
+template <int TPT, int V, int NI>
 __device__ __forceinline__ void row_load(const float *__restrict__ l, int E, int tid, float (&p)[NI])
 {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) p[i] = tid + TPT * i < E ? l[tid + TPT * i] : kNegInf;
+    for (int i = 0; i < NI; i += V) {
+        const int e = col_of<TPT, V>(tid, i);
+        if constexpr (V == 4) {
+            const float4 x = e < E ? *(const float4 *)(l + e) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+            p[i] = x.x, p[i + 1] = x.y, p[i + 2] = x.z, p[i + 3] = x.w;
+        } else {
+            p[i] = e < E ? l[e] : kNegInf;
+        }
+    }
 }
-// softmax of such a row; a row of -inf only has p = 0
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// softmax of such a row; a row of -inf only has p = 0.  In base 2: the
+// rounding of m log2(e) is common to the row and cancels, the rest is one
+// rounding of each exponent and exp2's own error.
 template <int TPT, int NI>
 __device__ __forceinline__ void row_softmax(float (&p)[NI], float *sh)
 {
@@ -112,11 +132,12 @@ __device__ __forceinline__ void row_softmax(float (&p)[NI], float *sh)
 #pragma unroll
     for (int i = 0; i < NI; ++i) m = fmaxf(m, p[i]);
     m = group_reduce<TPT>(m, Max(), sh);
-    const float mm = m == kNegInf ? 0.f : m;
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float m2 = m == kNegInf ? 0.f : m * kLog2e;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        p[i] = expf(p[i] - mm);
+        p[i] = ex2(fmaf(p[i], kLog2e, -m2));
         s += p[i];
     }
     s = group_reduce<TPT>(s, Add(), sh);
@@ -129,7 +150,7 @@ __device__ __forceinline__ void row_softmax(float (&p)[NI], float *sh)
 // Partial sums of one slab: per overlapping sequence, the token groups' sums
 // of p (added in group order), the counts (integer atomics: order-free) and
 // the number of tokens.  A group loads its next row while it works on one.
-template <int TPT, int NI>
+template <int TPT, int V, int NI>
 __global__ void __launch_bounds__(fwd_threads(TPT)) k_balance_partial(int T, int E, int k, int L, int Ep,
                                                                  const float *__restrict__ logits,
                                                                  const int32_t *__restrict__ idx,
@@ -161,14 +182,14 @@ __global__ void __launch_bounds__(fwd_threads(TPT)) k_balance_partial(int T, int
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[i] = 0.f;
         int n = 0, t = a + grp;
-        if (t < b) row_load<TPT, NI>(logits + (int64_t)t * E, E, tid, next);
+        if (t < b) row_load<TPT, V>(logits + (int64_t)t * E, E, tid, next);
         for (; t < b; t += kGroups) {
             float p[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) p[i] = next[i];
             const bool use = !valid || valid[t];
             const int e = tid < k ? idx[(int64_t)t * k + tid] : 0;
-            if (t + kGroups < b) row_load<TPT, NI>(logits + (int64_t)(t + kGroups) * E, E, tid, next);
+            if (t + kGroups < b) row_load<TPT, V>(logits + (int64_t)(t + kGroups) * E, E, tid, next);
             if (!use) continue;
             row_softmax<TPT, NI>(p, sh);
 #pragma unroll
@@ -180,15 +201,21 @@ __global__ void __launch_bounds__(fwd_threads(TPT)) k_balance_partial(int T, int
             ++n;
         }
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (tid + TPT * i < E) sm[grp * Ep + tid + TPT * i] = acc[i];
+        for (int i = 0; i < NI; i += V) {
+            const int e = col_of<TPT, V>(tid, i);
+            if (e >= E) continue;
+            if constexpr (V == 4) *(float4 *)(sm + grp * Ep + e) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+            else sm[grp * Ep + e] = acc[i];
+        }
         if (tid == 0) atomicAdd(&sn, n);
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
         for (int e = threadIdx.x; e < Ep; e += kFwdThreads) {
             float v = 0.f;
-            if (e < E)
+            if (e < E) {
+#pragma unroll
                 for (int g = 0; g < kGroups; ++g) v += sm[g * Ep + e];
+            }
             psum[slot * Ep + e] = v;
             cnt[slot * Ep + e] = e < E ? sc[e] : 0;
         }
@@ -197,7 +224,7 @@ __global__ void __launch_bounds__(fwd_threads(TPT)) k_balance_partial(int T, int
 }
 
 // One cluster of C CTAs per sequence, each with `cols` (a multiple of 32) of
-// the experts: the slots are added in kRedThreads / cols interleaved strands,
+// the experts: the slots are added in blockDim / cols interleaved strands,
 // then the strands, then the CTAs' shares of the loss, always in order.
 // loss = E / (k n) sum_e c_e pmean_e.
 __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, int k, int L, int Ep, int cols, int C,
@@ -224,9 +251,9 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, in
     if (threadIdx.x == 0) sn = 0;
     __syncthreads();
     int n = 0;
-    for (int i = first + threadIdx.x; i <= last; i += kRedThreads) n += ntok[i + s];
+    for (int i = first + threadIdx.x; i <= last; i += blockDim.x) n += ntok[i + s];
     if (n) atomicAdd(&sn, n);
-    const int strands = kRedThreads / cols, strand = threadIdx.x / cols, col = threadIdx.x % cols;
+    const int strands = blockDim.x / cols, strand = threadIdx.x / cols, col = threadIdx.x % cols;
     const int e = r * cols + col;
     float v = 0.f;
     int c = 0;
@@ -258,7 +285,7 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, in
     __syncthreads();
     if (threadIdx.x == 0) {
         float t = 0.f;
-        for (int i = 0; i < kRedThreads / 32; ++i) t += sw[i];
+        for (int i = 0; i < (int)blockDim.x / 32; ++i) t += sw[i];
         if (C == 1) {
             sl[0] = t;
         } else {   // into CTA 0's sl[r]
@@ -281,7 +308,7 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, in
 // ------------------------------------------------------------------ backward
 // dlogit_e = p_e (a_e - sum_e' p_e' a_e') with a_e = g E c_e / (k n^2) of the
 // token's sequence, plus w_j (dw_j - sum_i w_i dw_i) at the selected experts.
-template <int TPT, int NI>
+template <int TPT, int V, int NI>
 __global__ void __launch_bounds__(kThreads) k_route_backward(int T, int E, int k, const float *__restrict__ logits,
                                                              const int32_t *__restrict__ idx,
                                                              const float *__restrict__ w, const float *__restrict__ dw,
@@ -293,16 +320,15 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(int T, int E, int k
                                                              DevErr *err)
 {
     __shared__ float sh[kThreads / 32];
-    const int tid = threadIdx.x % TPT;
+    extern __shared__ float rows[];   // a row of gradients per group
+    const int tid = threadIdx.x % TPT, Ep = (E + 3) & ~3;
     const int t = blockIdx.x * (kThreads / TPT) + threadIdx.x / TPT;
     grid_wait();
     grid_go();
     if (t >= T) return;
     // all loads first: the row, the selection, the sequence's counts
     float d[NI];
-    if (gl) {
-        row_load<TPT, NI>(logits + (int64_t)t * E, E, tid, d);
-    }
+    if (gl) row_load<TPT, V>(logits + (int64_t)t * E, E, tid, d);
     const int lane = threadIdx.x & 31;
     int e = -1;
     float wj = 0.f, gj = 0.f;
@@ -313,66 +339,109 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(int T, int E, int k
     }
     const bool counted = gl && (!valid || valid[t]);
     int n = 0;
-    float av[NI];
+    float c[NI], f = 0.f;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) av[i] = 0.f;
+    for (int i = 0; i < NI; ++i) c[i] = 0.f;
     if (counted) {
         const int s = seq_of(seq, nseq, T, t);
         n = s >= 0 && s < nseq ? ntok[s] : 0;
         if (n > 0) {
-            const float f = gl[s] * ((float)E / (float)k) / ((float)n * (float)n);
+            f = gl[s] * ((float)E / (float)k) / ((float)n * (float)n);
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (tid + TPT * i < E) av[i] = f * (float)counts[(int64_t)s * E + tid + TPT * i];
+            for (int i = 0; i < NI; i += V) {
+                const int col = col_of<TPT, V>(tid, i);
+                if (col >= E) continue;
+                if constexpr (V == 4) {
+                    const int4 x = *(const int4 *)(counts + (int64_t)s * E + col);
+                    c[i] = (float)x.x, c[i + 1] = (float)x.y, c[i + 2] = (float)x.z, c[i + 3] = (float)x.w;
+                } else {
+                    c[i] = (float)counts[(int64_t)s * E + col];
+                }
+            }
         }
     }
     if (n > 0) {
         row_softmax<TPT, NI>(d, sh);
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) dot += d[i] * av[i];
+        for (int i = 0; i < NI; ++i) dot += d[i] * c[i];
         dot = group_reduce<TPT>(dot, Add(), sh);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) d[i] *= av[i] - dot;
+        for (int i = 0; i < NI; ++i) d[i] *= f * (c[i] - dot);
     } else {
 #pragma unroll
         for (int i = 0; i < NI; ++i) d[i] = 0.f;
     }
     if (dw) {
-        if (lane < k && (e < 0 || e >= E)) {
-            if (tid < 32) record_error(err, PMOE_ERR_BAD_INDEX, t, e);
-            e = -1;
-            wj = 0.f;
-        }
-        float dot = wj * gj;
+        // the selected experts' terms are added in shared memory, by the lane of
+        // each slot; where slots share an expert, the first one's lane adds all
+        float *row = rows + threadIdx.x / TPT * Ep;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float vj = wj * (gj - dot);
-        for (int j = 0; j < k; ++j) {   // each thread adds the terms of its columns
-            const int ej = __shfl_sync(0xffffffffu, e, j);
-            const float x = __shfl_sync(0xffffffffu, vj, j);
-            const int i0 = ej >= 0 && ej % TPT == tid ? ej / TPT : -1;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) d[i] += i == i0 ? x : 0.f;
+        for (int i = 0; i < NI; i += V) {
+            const int col = col_of<TPT, V>(tid, i);
+            if (col >= E) continue;
+            if constexpr (V == 4) *(float4 *)(row + col) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+            else row[col] = d[i];
         }
+        if constexpr (TPT > 32) __syncthreads();
+        else __syncwarp();
+        if (tid < 32) {
+            if (lane < k && (e < 0 || e >= E)) {
+                record_error(err, PMOE_ERR_BAD_INDEX, t, e);
+                e = -1;
+                wj = 0.f;
+            }
+            float dot = wj * gj;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            float x = wj * (gj - dot);
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            if (__any_sync(0xffffffffu, e >= 0 && __popc(same) > 1)) {
+                float sum = 0.f;
+                for (int j = 0; j < k; ++j) {
+                    const float y = __shfl_sync(0xffffffffu, x, j);
+                    if (same >> j & 1u) sum += y;
+                }
+                x = sum;
+            }
+            if (e >= 0 && lane == __ffs(same) - 1) row[e] += x;
+        }
+        if constexpr (TPT > 32) __syncthreads();
+        else __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NI; i += V) {
+            const int col = col_of<TPT, V>(tid, i);
+            if (col >= E) continue;
+            if constexpr (V == 4) *(float4 *)(dlogits + (int64_t)t * E + col) = *(const float4 *)(row + col);
+            else dlogits[(int64_t)t * E + col] = row[col];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (col_of<TPT, V>(tid, i) < E) dlogits[(int64_t)t * E + col_of<TPT, V>(tid, i)] = d[i];
     }
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-        if (tid + TPT * i < E) dlogits[(int64_t)t * E + tid + TPT * i] = d[i];
 }
 
-// The variant by the number of experts: f(threads per token, values per thread)
+// The variant by the number of experts: f(threads per token, values per load,
+// values per thread).  Rows of a multiple of 4 floats are 16-byte aligned.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <int V, class F>
+static void by_width(int E, F f)
+{
+    if (E <= 32 * V) f(Int<32>(), Int<V>(), Int<V>());
+    else if (E <= 128) f(Int<32>(), Int<V>(), Int<4>());
+    else if (E <= 256) f(Int<32>(), Int<V>(), Int<8>());
+    else if (E <= 384) f(Int<32>(), Int<V>(), Int<12>());
+    else if (E <= 512) f(Int<32>(), Int<V>(), Int<16>());
+    else if (E <= 1024) f(Int<32>(), Int<V>(), Int<32>());
+    else f(Int<256>(), Int<V>(), Int<16>());   // E <= 4096
+}
 template <class F>
 static void by_experts(int E, F f)
 {
-    using std::integral_constant;
-    if (E <= 32) f(integral_constant<int, 32>(), integral_constant<int, 1>());
-    else if (E <= 128) f(integral_constant<int, 32>(), integral_constant<int, 4>());
-    else if (E <= 256) f(integral_constant<int, 32>(), integral_constant<int, 8>());
-    else if (E <= 384) f(integral_constant<int, 32>(), integral_constant<int, 12>());
-    else if (E <= 512) f(integral_constant<int, 32>(), integral_constant<int, 16>());
-    else if (E <= 1024) f(integral_constant<int, 32>(), integral_constant<int, 32>());
-    else f(integral_constant<int, 256>(), integral_constant<int, 16>());   // E <= 4096
+    if (E % 4 == 0) by_width<4>(E, f);
+    else by_width<1>(E, f);
 }
 
 static bool aligned(std::initializer_list<const void *> ps)
@@ -406,8 +475,8 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
     if (!ws || ws_bytes < w.bytes || !bal::aligned({ws})) return PMOE_ERR_WORKSPACE;
     bool ok = true;
     if (dims.T > 0)
-        bal::by_experts(dims.E, [&](auto tpt, auto ni) {
-            auto kern = bal::k_balance_partial<tpt.value, ni.value>;
+        bal::by_experts(dims.E, [&](auto tpt, auto v, auto ni) {
+            auto kern = bal::k_balance_partial<tpt.value, v.value, ni.value>;
             const size_t sm = (size_t)(bal::fwd_threads(tpt.value) / tpt.value + 1) * w.Ep * 4;
             static const bool attr =   // up to 17 rows of 1024 floats (69 KB)
                 cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 17 * 4096) == cudaSuccess;
@@ -416,7 +485,10 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
         });
     // CTAs per sequence: 32 experts each up to 8 CTAs, then more experts each
     const int cols = (int)(cdiv(dims.E, 256) * 32), C = (int)cdiv(dims.E, cols);
-    ok = ok && launch_chained(bal::k_balance_reduce, (unsigned)(nseq * C), bal::kRedThreads, 0, C, stream, dims.T, dims.E,
+    // few slots a sequence: smaller CTAs start sooner (37 sequences of 16384 tokens: 8.5 us with 1024
+    // threads); one long sequence: more strands (8192 tokens, 6.3 us with 1024, 8.5 with 512)
+    const unsigned threads = w.slots / nseq >= 64 ? bal::kRedThreads : std::max(256, cols);
+    ok = ok && launch_chained(bal::k_balance_reduce, (unsigned)(nseq * C), threads, 0, C, stream, dims.T, dims.E,
                               dims.k, w.L, w.Ep, cols, C, seq, nseq, w.psum, w.cnt, w.ntok, counts, ntok, pmean, loss,
                               w.err);
     return ok ? PMOE_OK : PMOE_ERR_CUDA;
@@ -436,9 +508,10 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
     if (!ws || ws_bytes < b.bytes || !bal::aligned({ws})) return PMOE_ERR_WORKSPACE;
     if (dims.T == 0) return PMOE_OK;
     bool ok = true;
-    bal::by_experts(dims.E, [&](auto tpt, auto ni) {
-        ok = launch_chained(bal::k_route_backward<tpt.value, ni.value>, (unsigned)cdiv(dims.T, bal::kThreads / tpt.value),
-                            bal::kThreads, 0, 1, stream, dims.T, dims.E, dims.k, logits, idx, w, d_topk_w, valid, seq,
+    bal::by_experts(dims.E, [&](auto tpt, auto v, auto ni) {
+        const unsigned groups = bal::kThreads / tpt.value;   // (rows of at most 32 KB in all)
+        ok = launch_chained(bal::k_route_backward<tpt.value, v.value, ni.value>, (unsigned)cdiv(dims.T, groups),
+                            bal::kThreads, (size_t)groups * b.Ep * 4, 1, stream, dims.T, dims.E, dims.k, logits, idx, w, d_topk_w, valid, seq,
                             nseq, counts, ntok, g_loss, dlogits, b.err);
     });
     return ok ? PMOE_OK : PMOE_ERR_CUDA;
