@@ -348,7 +348,8 @@ struct Tiling {
 // partly filled round may be cut along K, their parts then being added up.
 // The number of parts is the one of least time by this estimate: a K step of
 // a tile takes 0.28 us (the tensor cores' rate at 1.8 GHz), each round 2 us
-// to fill and to drain, each part's FP32 tile goes to memory and back.
+// to fill and to drain, each part's FP32 tile goes to memory and back, and
+// a launch to add them 4 us.
 static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
 {
     Tiling t;
@@ -367,7 +368,7 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
         const double part = 2.0 * 128 * t.ctas * t.bn * 4 / 6e6;   // us
         double least = 0;
         for (int64_t s = 1; s <= std::min<int64_t>(ksteps, 64); ++s) {
-            const double us = cdiv(cut * s, slots) * (cdiv(ksteps, s) * 0.28 + 2) + (s > 1 ? cut * s * part : 0);
+            const double us = cdiv(cut * s, slots) * (cdiv(ksteps, s) * 0.28 + 2) + (s > 1 ? cut * s * part + 4 : 0);
             if (s == 1 || us < least) {
                 least = us;
                 best = s;
@@ -484,6 +485,10 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
     CUtensorMap ma, mt, mb, mo, ml[2];
     if (!map_operand(&ma, A) || !map_operand(&mb, B)) return false;
     a.tail = (int)std::min<int64_t>(128, cdiv(A.rows % 128, 8) * 8);
+    a.abytes = kOpBytes;
+    // (with extra K steps A's tiles are always whole)
+    if ((EPI == HG_FWD || EPI == HG_GRAD) && A.rows < 128) a.abytes = a.tail * 128;
+    a.stages = std::min(kMaxStages, kRingBytes / (kOpBytes + a.abytes));
     memset(&mt, 0, sizeof mt);
     if (!A.mn && a.tail && !tc::make_tmap3(&mt, A.base, false, A.cols, A.rows, 0, kBK, a.tail)) return false;
     memset(&mo, 0, sizeof mo);

@@ -63,9 +63,14 @@ using tc::tc_fence_before;
 enum Epi { HG_FWD = 0, HG_GRAD = 1, HG_DX = 2, HG_DW = 3 };
 
 constexpr int kUnit = 128;               // columns per softmax partial and per epilogue thread
-constexpr int kStages = 6;               // 32 KB each: 16 KB of A, 16 KB of B
-constexpr int kOpBytes = 128 * kBK * 2;  // one operand tile of a stage
-constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kOpBytes = 128 * kBK * 2;  // one operand tile of a stage (16 KB)
+// The ring of stages, each B's tile and then A's: 6 of 32 KB; where A has few
+// rows its tiles are that much smaller and the ring deeper (11 stages for up
+// to 8 tokens), which is what streaming W needs.  The MMA then reads past A's
+// rows into the next stage: those rows of the result are not stored.
+constexpr int kRingBytes = 6 * 2 * kOpBytes;
+constexpr int kMaxStages = 11;
+static_assert(kMaxStages * (kOpBytes + 1024) <= kRingBytes, "deepest ring");
 constexpr int kWarpOut = 32 * 128;       // a warp's staged output box: 32 rows of 128 bytes
 // K steps summed in one TMEM buffer
 constexpr int chunk_of(int epi) { return epi == HG_FWD ? 8 : epi == HG_GRAD ? 16 : 32; }
@@ -78,7 +83,7 @@ constexpr int kThreads0 = 128;           // producer, MMA and allocator warps
 constexpr int epi_warps(int BN) { return BN / kUnit * 4; }
 constexpr int threads_of(int BN) { return kThreads0 + 32 * epi_warps(BN); }
 // 1024 bytes of slack to align the swizzled tiles, 256 for the barriers
-constexpr int smem_of(int BN) { return kStages * kStageBytes + epi_warps(BN) * kWarpOut + 256 + 1024; }
+constexpr int smem_of(int BN) { return kRingBytes + epi_warps(BN) * kWarpOut + 256 + 1024; }
 
 struct Args {
     int M, N;                // output rows and columns of this launch
@@ -88,6 +93,7 @@ struct Args {
     int whole;               // tiles taken whole; each of the others is cut into
     int splits, kper;        // `splits` items of kper K steps
     int kb0;                 // first k coordinate of B (A: 0)
+    int stages, abytes;      // the ring: stages, and bytes of A in one
     int tail;                // FWD, GRAD, DX: rows of tmAt's boxes, the M % 128 last rows of A
                              // rounded up to 8 (a box with many rows past the end loads slowly)
     int V;                   // FWD, GRAD: number of vocabulary entries
@@ -306,20 +312,21 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t s0 = smem_u32(smem);
-    const uint32_t out0 = s0 + kStages * kStageBytes;
+    const uint32_t out0 = s0 + kRingBytes;
     const uint32_t bar0 = out0 + kEpi * kWarpOut;
     auto full = [&](uint32_t s) { return bar0 + 8 * s; };
-    auto empty = [&](uint32_t s) { return bar0 + 8 * (kStages + s); };
-    auto tfull = [&](uint32_t b) { return bar0 + 8 * (2 * kStages + b); };
-    auto tempty = [&](uint32_t b) { return bar0 + 8 * (2 * kStages + 2 + b); };
-    const uint32_t slot = bar0 + 8 * (2 * kStages + 4);
+    auto empty = [&](uint32_t s) { return bar0 + 8 * (kMaxStages + s); };
+    auto tfull = [&](uint32_t b) { return bar0 + 8 * (2 * kMaxStages + b); };
+    auto tempty = [&](uint32_t b) { return bar0 + 8 * (2 * kMaxStages + 2 + b); };
+    const uint32_t slot = bar0 + 8 * (2 * kMaxStages + 4);
+    const uint32_t stages = (uint32_t)a.stages, stage_bytes = kOpBytes + (uint32_t)a.abytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cta_rank() : 0u;
     const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
@@ -386,11 +393,14 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             // normaliser and factor: fetched while the tensor cores work
             const int32_t *ids = a.ids + (int64_t)row * a.K;
             int pos = 0, id = kNoId;
-            float l2 = 0.f, cf = 0.f;
+            float qv = 1.f, l2 = 0.f, cf = 0.f;
             if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
                 if (live) {
                     if (a.first) pos = a.first[(int64_t)row * a.NU + cb / kUnit];
-                    if (pos < a.K) id = ids[pos];
+                    if (pos < a.K) {
+                        id = ids[pos];
+                        if (EPI == HG_GRAD && a.q) qv = a.q[(int64_t)row * a.K + pos];
+                    }
                     if (id < cb || id >= a.V) id = kNoId;
                 }
                 if (EPI == HG_GRAD && row < a.M) {
@@ -503,14 +513,15 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         for (int j = 0; j < 32; ++j) acc[q + j] = ex2(fmaf(acc[q + j], a.c, -l2));
                         while (__any_sync(0xffffffffu, id < e0 + 32)) {
                             const int j0 = id - e0;
-                            float qv = 0.f;
-                            if (id < e0 + 32) {
-                                qv = a.q ? a.q[(int64_t)row * a.K + pos] : 1.f;
-                                ++pos;
-                                id = pos < a.K ? ids[pos] : kNoId;
-                            }
 #pragma unroll
                             for (int j = 0; j < 32; ++j) acc[q + j] -= j == j0 ? qv : 0.f;
+                            if (id < e0 + 32) {
+                                id = kNoId;
+                                if (++pos < a.K) {
+                                    id = ids[pos];
+                                    qv = a.q[(int64_t)row * a.K + pos];   // (K > 1: q is given)
+                                }
+                            }
                         }
                         if (nv < kUnit) {
 #pragma unroll
@@ -584,7 +595,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         if (warp == 0) {
             // ---------------- producer (the whole warp; lane 0 issues, and lanes
             // 0-15 gather four rows of B each in an extra step)
-            uint32_t g = 0;
+            uint32_t s = 0, ph = 1;   // stage, and the parity of its last release
             Item t;
             for (int i = first; ok && item_of(a, i, t); i += step) {
                 const int k0 = t.k0, k1 = t.k1;
@@ -599,18 +610,17 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 };
                 const uint32_t bytes = CTAS * kOpBytes + (arows(0) + (CTAS == 2 ? arows(1) : 0)) * 128u;
                 const int mine = arows(rank);
-                for (int k = k0; k < k1 + ex.y; ++k, ++g) {
-                    const uint32_t s = g % kStages;
+                for (int k = k0; k < k1 + ex.y; ++k) {
                     const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
-                    const uint32_t sa = s0 + s * kStageBytes, sb = sa + kOpBytes;
+                    const uint32_t sb = s0 + s * stage_bytes, sa = sb + kOpBytes;
                     const bool main = !kLo || k < k1;
                     const int st = ex.x + k - k1;   // an extra step's list
                     int4 r = make_int4(0, 0, 0, 0);
                     if (kLo && !main && lane < 16) r = *(const int4 *)(a.lidx + (int64_t)st * 64 + lane * 4);
-                    ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ((g / kStages) & 1) ^ 1, a.err, 1, tc::kWaitNs));
+                    ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ph, a.err, 1, tc::kWaitNs));
                     if (!ok) break;
                     if (lane == 0) {
-                        if (rank == 0) mbar_expect_tx(full(s), main ? bytes : CTAS * kStageBytes);
+                        if (rank == 0) mbar_expect_tx(full(s), main ? bytes : CTAS * 2 * kOpBytes);
                         const int ka = k * kBK, kb = a.kb0 + k * kBK;
                         if (main) {
                             if constexpr (kAMn) {
@@ -638,6 +648,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         gather4<CTAS>(sb + lane * 512, &tmLoB, nb, r, fb);
                         gather4<CTAS>(sb + 8192 + lane * 512, &tmLoB, nb + 64, r, fb);
                     }
+                    if (++s == stages) s = 0, ph ^= 1;
                 }
             }
         } else if (warp == 1) {
@@ -646,8 +657,8 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 const uint32_t idesc = tc::idesc_bf16(CTAS * 128, BN, kAMn) | ((uint32_t)kBMn << 16);
                 constexpr uint32_t kAStep = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 k
                 constexpr uint32_t kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
-                const uint64_t da0 = desc_of<kAMn>(s0), db0 = desc_of<kBMn>(s0 + kOpBytes);
-                uint32_t g = 0, gc = 0;
+                const uint64_t db0 = desc_of<kBMn>(s0), da0 = desc_of<kAMn>(s0 + kOpBytes);
+                uint32_t s = 0, ph = 0, gc = 0;
                 Item t;
                 for (int i = first; ok && item_of(a, i, t); i += step) {
                     const int k0 = t.k0, k1 = t.k1;
@@ -658,15 +669,15 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         tc_fence_after();
                         int c1 = c0 + kChunk;
                         if (c1 >= k1) c1 = k1 + ex.y;   // (the extra steps join the last chunk)
-                        for (int k = c0; k < c1; ++k, ++g) {
-                            const uint32_t s = g % kStages;
-                            if (!(ok = mbar_wait(full(s), (g / kStages) & 1, a.err, 3, tc::kWaitNs))) break;
+                        for (int k = c0; k < c1; ++k) {
+                            if (!(ok = mbar_wait(full(s), ph, a.err, 3, tc::kWaitNs))) break;
                             tc_fence_after();
-                            const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+                            const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, k > c0 || j > 0);
                             commit<CTAS>(empty(s));
+                            if (++s == stages) s = 0, ph ^= 1;
                         }
                         if (ok) commit<CTAS>(tfull(b));
                     }
