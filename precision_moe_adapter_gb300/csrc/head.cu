@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     grid_go();
     const float2 *p = part + (int64_t)t * NU;
     float m = ninf, s = 0.f;   // base 2
+#pragma unroll 4
     for (int i = threadIdx.x; i < NU; i += 128) {
         const float2 v = p[i];
         const float n = fmaxf(m, v.x);
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const f
         const int item = g * p.gm * p.nt + c * min(p.gm, p.mt - g * p.gm) + m - g * p.gm;
         const int parts = item < p.whole ? 1 : p.splits;
         float4 a = *(const float4 *)(part + i), b = *(const float4 *)(part + i + 4);
+#pragma unroll 4
         for (int s = 1; s < parts; ++s) {
             const float4 x = *(const float4 *)(part + s * n + i), y = *(const float4 *)(part + s * n + i + 4);
             a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
@@ -484,10 +486,10 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
 {
     CUtensorMap ma, mt, mb, mo, ml[2];
     if (!map_operand(&ma, A) || !map_operand(&mb, B)) return false;
-    a.tail = (int)std::min<int64_t>(128, cdiv(A.rows % 128, 8) * 8);
+    a.tail = (int)(A.rows % 128);
     a.abytes = kOpBytes;
     // (with extra K steps A's tiles are always whole)
-    if ((EPI == HG_FWD || EPI == HG_GRAD) && A.rows < 128) a.abytes = a.tail * 128;
+    if ((EPI == HG_FWD || EPI == HG_GRAD) && A.rows < 128) a.abytes = (int)cdiv(a.tail, 8) * 1024;
     a.stages = std::min(kMaxStages, kRingBytes / (kOpBytes + a.abytes));
     memset(&mt, 0, sizeof mt);
     if (!A.mn && a.tail && !tc::make_tmap3(&mt, A.base, false, A.cols, A.rows, 0, kBK, a.tail)) return false;

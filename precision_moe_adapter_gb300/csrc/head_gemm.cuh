@@ -13,7 +13,9 @@
 //
 // Roles (CTAS CTAs of one cluster work on one CTAS*128 x BN tile; persistent
 // over the tiles):
-//   warp 0      TMA producer of this CTA's 128 rows of A and BN/CTAS of B
+//   warps 0, 3  TMA producers of this CTA's 128 rows of A, and of its BN/CTAS
+//               rows of B (a warp issues a copy every 150 clocks or so: one
+//               for both would bound the smaller tiles)
 //   warp 1      MMA issuer (CTA 0 of the cluster only), K steps of 64
 //   warp 2      TMEM allocator
 //   warps 4..   epilogue, one warp per 32 TMEM lanes and 128 columns: a
@@ -95,7 +97,7 @@ struct Args {
     int kb0;                 // first k coordinate of B (A: 0)
     int stages, abytes;      // the ring: stages, and bytes of A in one
     int tail;                // FWD, GRAD, DX: rows of tmAt's boxes, the M % 128 last rows of A
-                             // rounded up to 8 (a box with many rows past the end loads slowly)
+                             // (a box with rows past the tensor's end loads slowly)
     int V;                   // FWD, GRAD: number of vocabulary entries
     float c;                 // FWD, GRAD: scale * log2(e)
     int NU;                  // FWD, GRAD: units of the vocabulary
@@ -144,17 +146,34 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The calls named *_warp are made by a whole converged warp, so that their
+// operands stay in uniform registers; one elected lane issues.  (Issued from
+// a branch on the lane, each MMA or copy first moves its operands there: a K
+// step's four MMAs then take 590 clocks whatever their size.)
 template <int CTAS>
-__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar)
+__device__ __forceinline__ void load_2d_warp(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar)
 {
     if constexpr (CTAS == 2)   // the barrier may be the other CTA's
         asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "{ .reg .pred e; elect.sync _|e, 0xffffffff;\n"
+            "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4]; }" ::"r"(dst),
             "l"((uint64_t)tm), "r"(x), "r"(y), "r"(bar)
             : "memory");
     else
-        tc::tma_load_2d(dst, tm, x, y, bar);
+        asm volatile(
+            "{ .reg .pred e; elect.sync _|e, 0xffffffff;\n"
+            "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4]; }" ::"r"(dst),
+            "l"((uint64_t)tm), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+__device__ __forceinline__ void expect_tx_warp(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff;\n"
+                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1; }" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
 }
 // Rows r.x .. r.w of a map whose boxes are one row of 128 bytes, from column x
 template <int CTAS>
@@ -198,33 +217,49 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A K step of 64: four MMAs of K = 16, da and db advancing by sa and sb, and
+// the commit of `bar` (of both CTAs of a pair), which completes when the MMAs
+// issued so far have
 template <int CTAS>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum)
-{
-    if constexpr (CTAS == 2)
-        asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(accum)
-                     : "memory");
-    else
-        asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(accum)
-                     : "memory");
-}
-// The barrier (of both CTAs of a pair) completes when the MMAs issued so far have
-template <int CTAS>
-__device__ __forceinline__ void commit(uint32_t bar)
+__device__ __forceinline__ void mma_step_warp(uint32_t d, uint64_t da, uint64_t db, uint32_t sa, uint32_t sb,
+                                              uint32_t idesc, uint32_t accum, uint32_t bar)
 {
     if constexpr (CTAS == 2)
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            "{ .reg .pred e, p, t; elect.sync _|e, 0xffffffff; setp.ne.b32 p, %10, 0; setp.eq.b32 t, %10, %10;\n"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %5, %9, p;\n"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %2, %6, %9, t;\n"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %3, %7, %9, t;\n"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %4, %8, %9, t;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12; }" ::"r"(
+                d),
+            "l"(da), "l"(da + sa), "l"(da + 2 * sa), "l"(da + 3 * sa), "l"(db), "l"(db + sb), "l"(db + 2 * sb),
+            "l"(db + 3 * sb), "r"(idesc), "r"(accum), "r"(bar), "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred e, p, t; elect.sync _|e, 0xffffffff; setp.ne.b32 p, %10, 0; setp.eq.b32 t, %10, %10;\n"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11]; }" ::"r"(d),
+            "l"(da), "l"(da + sa), "l"(da + 2 * sa), "l"(da + 3 * sa), "l"(db), "l"(db + sb), "l"(db + 2 * sb),
+            "l"(db + 3 * sb), "r"(idesc), "r"(accum), "r"(bar)
+            : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void commit_warp(uint32_t bar)
+{
+    if constexpr (CTAS == 2)
+        asm volatile(
+            "{ .reg .pred e; elect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1; }" ::"r"(
                 bar),
             "h"((uint16_t)3)
             : "memory");
     else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
+        tc::umma_commit_warp(bar);
 }
 // Shared-memory descriptor of a 128 x 64 operand tile, 128-byte swizzle.
 // K-major: 8-row groups 1024 bytes apart.  MN-major: two boxes of 64 mn x 64
@@ -321,7 +356,8 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     const uint32_t slot = bar0 + 8 * (2 * kMaxStages + 4);
     const uint32_t stages = (uint32_t)a.stages, stage_bytes = kOpBytes + (uint32_t)a.abytes;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (through a shuffle: the compiler then knows the warp's number to be uniform)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cta_rank() : 0u;
     const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
@@ -397,11 +433,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
                 if (live) {
                     if (a.first) pos = a.first[(int64_t)row * a.NU + cb / kUnit];
-                    if (pos < a.K) {
-                        id = ids[pos];
-                        if (EPI == HG_GRAD && a.q) qv = a.q[(int64_t)row * a.K + pos];
-                    }
-                    if (id < cb || id >= a.V) id = kNoId;
+                    if (pos < a.K) id = ids[pos];
+                    if (id < cb || id >= a.V) id = kNoId;   // (K = 1: no target among the columns before)
+                    if (EPI == HG_GRAD && a.q && pos < a.K) qv = a.q[(int64_t)row * a.K + pos];
                 }
                 if (EPI == HG_GRAD && row < a.M) {
                     l2 = a.lse[row] * 1.4426950408889634f;
@@ -505,7 +539,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     }
                 };
                 if constexpr (EPI == HG_GRAD) {
-                    uint32_t large[kUnit / 32];   // the columns to list
+                    uint32_t large[kUnit / 32], any = 0;   // the columns to list
 #pragma unroll
                     for (int q = 0; q < kUnit; q += 32) {
                         const int e0 = cb + q;
@@ -538,6 +572,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                             for (int j = 0; j < 32; ++j)
                                 large[q / 32] |= keep && fabsf(acc[q + j]) >= kLarge ? 1u << j : 0u;
                         }
+                        any |= large[q / 32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
                         if (q & 32) {
@@ -546,10 +581,12 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                             put(&tmOut, xc + q - 32);
                         }
                     }
-                    if (__any_sync(0xffffffffu, (large[0] | large[1] | large[2] | large[3]) != 0)) {
+                    if (__any_sync(0xffffffffu, any != 0)) {
                         int n = 0;
-                        if (large[0] | large[1] | large[2] | large[3]) {
-                            n = atomicAdd(&a.cnt[row], __popc(large[0]) + __popc(large[1]) + __popc(large[2]) + __popc(large[3]));
+                        if (any) {
+#pragma unroll
+                            for (int q = 0; q < kUnit / 32; ++q) n += __popc(large[q]);
+                            n = atomicAdd(&a.cnt[row], n);
                             if (a.fl) a.fl[(int64_t)((cb - a.n0) / kListRows) * a.fs + (row >> 7)] = 1;
                         }
 #pragma unroll
@@ -592,9 +629,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         if (EPI != HG_FWD && lane == 0) store_wait_all();
     } else {
         if constexpr (kEpi == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLo ? 72 : 40));
-        if (warp == 0) {
-            // ---------------- producer (the whole warp; lane 0 issues, and lanes
-            // 0-15 gather four rows of B each in an extra step)
+        if (warp == 0 || warp == 3) {
+            // ---------------- producers (whole warps): A, and B
+            const bool isA = warp == 0;
             uint32_t s = 0, ph = 1;   // stage, and the parity of its last release
             Item t;
             for (int i = first; ok && item_of(a, i, t); i += step) {
@@ -615,45 +652,46 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     const uint32_t sb = s0 + s * stage_bytes, sa = sb + kOpBytes;
                     const bool main = !kLo || k < k1;
                     const int st = ex.x + k - k1;   // an extra step's list
-                    int4 r = make_int4(0, 0, 0, 0);
-                    if (kLo && !main && lane < 16) r = *(const int4 *)(a.lidx + (int64_t)st * 64 + lane * 4);
+                    int4 r = make_int4(0, 0, 0, 0);   // its rows of B: lanes 0-15 gather four each
+                    if (kLo && !main && !isA && lane < 16) r = *(const int4 *)(a.lidx + (int64_t)st * 64 + lane * 4);
                     ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ph, a.err, 1, tc::kWaitNs));
                     if (!ok) break;
-                    if (lane == 0) {
-                        if (rank == 0) mbar_expect_tx(full(s), main ? bytes : CTAS * 2 * kOpBytes);
-                        const int ka = k * kBK, kb = a.kb0 + k * kBK;
+                    if (isA) {
+                        if (rank == 0) expect_tx_warp(full(s), main ? bytes : CTAS * 2 * kOpBytes);
+                        const int ka = k * kBK;
                         if (main) {
                             if constexpr (kAMn) {
-                                load_2d<CTAS>(sa, &tmA, ma, ka, fb);
-                                load_2d<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
+                                load_2d_warp<CTAS>(sa, &tmA, ma, ka, fb);
+                                load_2d_warp<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
                             } else if (mine) {
-                                load_2d<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka, ma, fb);
-                            }
-                            if constexpr (kBMn) {
-                                load_2d<CTAS>(sb, &tmB, nb, kb, fb);
-                                load_2d<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);
-                            } else {
-                                load_2d<CTAS>(sb, &tmB, kb, nb, fb);
+                                load_2d_warp<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka, ma, fb);
                             }
                         } else if constexpr (kAMn) {   // remainders [step][64][256 rows]
-                            load_2d<CTAS>(sa, &tmLoA, ma % kListRows, st * 64, fb);
-                            load_2d<CTAS>(sa + 8192, &tmLoA, ma % kListRows + 64, st * 64, fb);
+                            load_2d_warp<CTAS>(sa, &tmLoA, ma % kListRows, st * 64, fb);
+                            load_2d_warp<CTAS>(sa + 8192, &tmLoA, ma % kListRows + 64, st * 64, fb);
                         } else {                       // [step][256 rows][64]
-                            load_2d<CTAS>(sa, &tmLoA, 0, st * kListRows + ma % kListRows, fb);
+                            load_2d_warp<CTAS>(sa, &tmLoA, 0, st * kListRows + ma % kListRows, fb);
                         }
-                    }
-                    __syncwarp();
-                    if (kLo && !main && lane < 16) {
+                    } else if (main) {
+                        const int kb = a.kb0 + k * kBK;
+                        if constexpr (kBMn) {
+                            load_2d_warp<CTAS>(sb, &tmB, nb, kb, fb);
+                            load_2d_warp<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);
+                        } else {
+                            load_2d_warp<CTAS>(sb, &tmB, kb, nb, fb);
+                        }
+                    } else if (kLo && lane < 16) {
                         r.x += a.lb0, r.y += a.lb0, r.z += a.lb0, r.w += a.lb0;
                         gather4<CTAS>(sb + lane * 512, &tmLoB, nb, r, fb);
                         gather4<CTAS>(sb + 8192 + lane * 512, &tmLoB, nb + 64, r, fb);
                     }
+                    __syncwarp();
                     if (++s == stages) s = 0, ph ^= 1;
                 }
             }
         } else if (warp == 1) {
             // ---------------- MMA issuer
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
                 const uint32_t idesc = tc::idesc_bf16(CTAS * 128, BN, kAMn) | ((uint32_t)kBMn << 16);
                 constexpr uint32_t kAStep = kAMn ? 2048 >> 4 : 32 >> 4;   // 16 k
                 constexpr uint32_t kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
@@ -665,21 +703,21 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     const int2 ex = extra(t);
                     for (int c0 = k0; ok && c0 < k1; c0 += kChunk, ++gc) {
                         const uint32_t b = gc & 1;
-                        if (!(ok = mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs))) break;
+                        // (every lane waits; the outcome is made uniform)
+                        ok = __all_sync(0xffffffffu, mbar_wait(tempty(b), ((gc >> 1) & 1) ^ 1, a.err, 2, tc::kWaitNs));
+                        if (!ok) break;
                         tc_fence_after();
                         int c1 = c0 + kChunk;
                         if (c1 >= k1) c1 = k1 + ex.y;   // (the extra steps join the last chunk)
                         for (int k = c0; k < c1; ++k) {
-                            if (!(ok = mbar_wait(full(s), ph, a.err, 3, tc::kWaitNs))) break;
+                            ok = __all_sync(0xffffffffu, mbar_wait(full(s), ph, a.err, 3, tc::kWaitNs));
+                            if (!ok) break;
                             tc_fence_after();
                             const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                mma<CTAS>(tmem + b * BN, da + j * kAStep, db + j * kBStep, idesc, k > c0 || j > 0);
-                            commit<CTAS>(empty(s));
+                            mma_step_warp<CTAS>(tmem + b * BN, da, db, kAStep, kBStep, idesc, k > c0, empty(s));
                             if (++s == stages) s = 0, ph ^= 1;
                         }
-                        if (ok) commit<CTAS>(tfull(b));
+                        if (ok) commit_warp<CTAS>(tfull(b));
                     }
                 }
             }
