@@ -616,6 +616,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.M = vc;
             a.N = h.d;
             a.ksteps = (int)cdiv(h.T, kBK);
+            a.beside = dX != nullptr;
             a.lists = w.lists[1];
             a.lidx = w.lidx[1];
             const Operand lo{w.lo[1], kListRows, (int64_t)w.max_steps[1] * 64, true};

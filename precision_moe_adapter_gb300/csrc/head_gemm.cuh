@@ -117,6 +117,7 @@ struct Args {
     const int2 *lists;       // DX, DW: per 256 rows (first step, number of steps) of remainders
     const int32_t *lidx;     // DX, DW: [step][64] row of B
     int lb0;                 // DX, DW: offset of these rows
+    int beside;              // DW: launched right behind DX
     int accumulate;          // DX: add to the FP32 partials
     int bf16_out;            // DX: the output map is the BF16 dX itself
     DevErr *err;
@@ -393,14 +394,16 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
 
-    grid_wait();
+    // DW after DX: its inputs were complete when DX started, so it runs beside
+    // DX and waits for it at the end only (whatever comes next waits for both)
+    if (EPI != HG_DW || !a.beside) grid_wait();
     grid_go();
     // DX, DW: the item's extra K steps on remainders (with a tile's first K step)
     constexpr bool kLo = EPI == HG_DX || EPI == HG_DW;
     constexpr int kChunk = chunk_of(EPI);
     auto extra = [&](const Item &t) {
         if constexpr (kLo)
-            if (t.k0 == 0) return a.lists[t.m * CTAS * 128 / kListRows];
+            if (t.k0 == 0) return __ldcg(a.lists + t.m * CTAS * 128 / kListRows);
         return make_int2(0, 0);
     };
     bool ok = true;
@@ -647,32 +650,33 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 };
                 const uint32_t bytes = CTAS * kOpBytes + (arows(0) + (CTAS == 2 ? arows(1) : 0)) * 128u;
                 const int mine = arows(rank);
-                for (int k = k0; k < k1 + ex.y; ++k) {
+                auto slot_free = [&]() {
+                    return ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ph, a.err, 1, tc::kWaitNs));
+                };
+                auto next = [&]() {
+                    __syncwarp();
+                    if (++s == stages) s = 0, ph ^= 1;
+                };
+                // an extra step's rows of B: lanes 0-15 gather four each, fetched a step ahead
+                auto rows_of = [&](int e) {
+                    return kLo && !isA && lane < 16 && e < ex.y
+                               ? __ldcg((const int4 *)(a.lidx + (int64_t)(ex.x + e) * 64 + lane * 4))
+                               : make_int4(0, 0, 0, 0);
+                };
+                for (int k = k0; k < k1; ++k) {
                     const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
                     const uint32_t sb = s0 + s * stage_bytes, sa = sb + kOpBytes;
-                    const bool main = !kLo || k < k1;
-                    const int st = ex.x + k - k1;   // an extra step's list
-                    int4 r = make_int4(0, 0, 0, 0);   // its rows of B: lanes 0-15 gather four each
-                    if (kLo && !main && !isA && lane < 16) r = *(const int4 *)(a.lidx + (int64_t)st * 64 + lane * 4);
-                    ok = __all_sync(0xffffffffu, mbar_wait(empty(s), ph, a.err, 1, tc::kWaitNs));
-                    if (!ok) break;
+                    if (!slot_free()) break;
                     if (isA) {
-                        if (rank == 0) expect_tx_warp(full(s), main ? bytes : CTAS * 2 * kOpBytes);
+                        if (rank == 0) expect_tx_warp(full(s), bytes);
                         const int ka = k * kBK;
-                        if (main) {
-                            if constexpr (kAMn) {
-                                load_2d_warp<CTAS>(sa, &tmA, ma, ka, fb);
-                                load_2d_warp<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
-                            } else if (mine) {
-                                load_2d_warp<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka, ma, fb);
-                            }
-                        } else if constexpr (kAMn) {   // remainders [step][64][256 rows]
-                            load_2d_warp<CTAS>(sa, &tmLoA, ma % kListRows, st * 64, fb);
-                            load_2d_warp<CTAS>(sa + 8192, &tmLoA, ma % kListRows + 64, st * 64, fb);
-                        } else {                       // [step][256 rows][64]
-                            load_2d_warp<CTAS>(sa, &tmLoA, 0, st * kListRows + ma % kListRows, fb);
+                        if constexpr (kAMn) {
+                            load_2d_warp<CTAS>(sa, &tmA, ma, ka, fb);
+                            load_2d_warp<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
+                        } else if (mine) {
+                            load_2d_warp<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka, ma, fb);
                         }
-                    } else if (main) {
+                    } else {
                         const int kb = a.kb0 + k * kBK;
                         if constexpr (kBMn) {
                             load_2d_warp<CTAS>(sb, &tmB, nb, kb, fb);
@@ -680,13 +684,31 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         } else {
                             load_2d_warp<CTAS>(sb, &tmB, kb, nb, fb);
                         }
-                    } else if (kLo && lane < 16) {
+                    }
+                    next();
+                }
+                int4 r = rows_of(0);
+                for (int e = 0; kLo && ok && e < ex.y; ++e) {
+                    const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
+                    const uint32_t sb = s0 + s * stage_bytes, sa = sb + kOpBytes;
+                    const int st = ex.x + e;
+                    const int4 rn = rows_of(e + 1);
+                    if (!slot_free()) break;
+                    if (isA) {
+                        if (rank == 0) expect_tx_warp(full(s), CTAS * 2 * kOpBytes);
+                        if constexpr (kAMn) {   // remainders [step][64][256 rows]
+                            load_2d_warp<CTAS>(sa, &tmLoA, ma % kListRows, st * 64, fb);
+                            load_2d_warp<CTAS>(sa + 8192, &tmLoA, ma % kListRows + 64, st * 64, fb);
+                        } else {                // [step][256 rows][64]
+                            load_2d_warp<CTAS>(sa, &tmLoA, 0, st * kListRows + ma % kListRows, fb);
+                        }
+                    } else if (lane < 16) {
                         r.x += a.lb0, r.y += a.lb0, r.z += a.lb0, r.w += a.lb0;
                         gather4<CTAS>(sb + lane * 512, &tmLoB, nb, r, fb);
                         gather4<CTAS>(sb + 8192 + lane * 512, &tmLoB, nb + 64, r, fb);
                     }
-                    __syncwarp();
-                    if (++s == stages) s = 0, ph ^= 1;
+                    r = rn;
+                    next();
                 }
             }
         } else if (warp == 1) {
@@ -729,6 +751,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
         const uint64_t t0 = tc::globaltimer();
         while (tc::globaltimer() - t0 < 1000000ull) __nanosleep(1000);
     }
+    if (EPI == HG_DW && a.beside) grid_wait();
     __syncwarp();
     tc_fence_before();
     __syncthreads();

@@ -20,14 +20,15 @@ _BF16 = (torch.bfloat16, torch.int16)
 
 
 def _check(name, t, dtypes, shape, device):
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 class DeviceHead:
