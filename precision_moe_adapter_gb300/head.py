@@ -15,20 +15,9 @@ from __future__ import annotations
 import torch
 
 from . import pmoe
+from .layer import check_tensor as _check
 
 _BF16 = (torch.bfloat16, torch.int16)
-
-
-def _check(name, t, dtypes, shape, device):
-    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
-        return
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    raise ValueError(f"{name}: must be contiguous")
 
 
 class DeviceHead:

@@ -6,6 +6,8 @@ the workspaces, and runs one step of the layer:
 
     moe_route -> moe_permute -> moe_chunked_forward -> moe_backward_data
 
+and the router's training side: moe_balance_forward, moe_route_backward.
+
 Every computation happens in libpmoe's kernels; this module only allocates
 and passes pointers.
 """
@@ -18,6 +20,20 @@ import torch
 
 from . import pmoe
 from .inputs import LayerConfig
+
+
+def check_tensor(name, t, dtypes, shape, device):
+    """Raises unless t is a dense tensor of one of the dtypes, of the shape, on
+    the device (the C ABI sees bare pointers)."""
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _dev(a, device) -> torch.Tensor:
@@ -45,6 +61,15 @@ class Routing:
                             self.active, self.num_active)
 
 
+@dataclass
+class Balance:
+    """The balance loss of each packed sequence and what its gradient needs."""
+    counts: torch.Tensor      # int32 [nseq, E]
+    ntok: torch.Tensor        # int32 [nseq]
+    pmean: torch.Tensor       # f32 [nseq, E]
+    loss: torch.Tensor        # f32 [nseq]
+
+
 class DeviceLayer:
     """Frozen experts + router + adapter of one layer on a CUDA device.
 
@@ -57,6 +82,8 @@ class DeviceLayer:
                  S_down=None, R_up=None, R_down=None, device="cuda"):
         self.cfg = cfg
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self.dims = pmoe.dims(cfg.T, cfg.d, cfg.E, cfg.k, cfg.I, cfg.b)
         self.w13, self.s13 = _dev(w13, self.device), _dev(s13, self.device)
         self.w2, self.s2 = _dev(w2, self.device), _dev(s2, self.device)
@@ -132,6 +159,58 @@ class DeviceLayer:
         ws = self.workspace(pmoe.OP_BACKWARD, C)
         pmoe.moe_backward_data(self.dims, self.wts, self.adp, rt.c(), X, dY, ctx, C, dX,
                                d_topk_w, dR_up, dR_down, ws)
+
+    def new_balance(self, nseq: int = 1) -> Balance:
+        E, dev = self.cfg.E, self.device
+        return Balance(counts=torch.zeros((nseq, E), dtype=torch.int32, device=dev),
+                       ntok=torch.zeros(nseq, dtype=torch.int32, device=dev),
+                       pmean=torch.zeros((nseq, E), dtype=torch.float32, device=dev),
+                       loss=torch.zeros(nseq, dtype=torch.float32, device=dev))
+
+    def _balance_ws(self, nseq: int) -> torch.Tensor:
+        key = ("balance", nseq)
+        if key not in self._ws:
+            n = pmoe.moe_balance_ws_bytes(self.dims, nseq)
+            if n == 0:
+                raise ValueError(f"unsupported number of sequences: {nseq}")
+            self._ws[key] = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return self._ws[key]
+
+    def _balance_args(self, logits, valid, seq, nseq):
+        cfg, dev = self.cfg, self.device
+        check_tensor("logits", logits, (torch.float32,), (cfg.T, cfg.E), dev)
+        if valid is not None:
+            check_tensor("valid", valid, (torch.uint8,), (cfg.T,), dev)
+        if seq is not None:
+            check_tensor("seq", seq, (torch.int32,), (nseq + 1,), dev)
+
+    def balance(self, logits, rt: Routing, bal: Balance, valid=None, seq=None):
+        """Counts, mean probabilities and balance loss of the routing ``rt`` of
+        ``logits`` (f32 [T, E], as ``route`` writes them); ``valid`` uint8 [T]
+        or None, ``seq`` int32 [nseq + 1] bounds or None (one sequence)."""
+        nseq = bal.loss.shape[0]
+        self._balance_args(logits, valid, seq, nseq)
+        pmoe.moe_balance_forward(self.dims, logits, rt.idx, valid, seq, nseq, bal.counts, bal.ntok,
+                                 bal.pmean, bal.loss, self._balance_ws(nseq))
+
+    def route_backward(self, logits, rt: Routing, dlogits, d_topk_w=None, bal: Balance | None = None,
+                       g_loss=None, valid=None, seq=None):
+        """dlogits (f32 [T, E]) from the routing weights' gradient (``d_topk_w``
+        of ``backward``) and from the balance losses (upstream ``g_loss``
+        f32 [nseq], ``bal`` from ``balance``); either may be left out."""
+        cfg, dev = self.cfg, self.device
+        nseq = 1 if bal is None else bal.loss.shape[0]
+        if (g_loss is None) != (bal is None):
+            raise ValueError("bal and g_loss go together")
+        self._balance_args(logits, valid, seq, nseq)
+        check_tensor("dlogits", dlogits, (torch.float32,), (cfg.T, cfg.E), dev)
+        if d_topk_w is not None:
+            check_tensor("d_topk_w", d_topk_w, (torch.float32,), (cfg.T, cfg.k), dev)
+        if g_loss is not None:
+            check_tensor("g_loss", g_loss, (torch.float32,), (nseq,), dev)
+        pmoe.moe_route_backward(self.dims, logits, rt.idx, rt.w, d_topk_w, valid, seq, nseq,
+                                bal.counts if bal else None, bal.ntok if bal else None, g_loss,
+                                dlogits, self._balance_ws(nseq))
 
     def grads(self):
         """Fresh (dR_up, dR_down) buffers shaped like the rotations."""
