@@ -41,7 +41,9 @@ static Ws carve(void *base, int T, int E, int nseq)
         return p;
     };
     Ws w;
-    w.L = (int)std::max<int64_t>(16, cdiv(cdiv(T, 2 * 152), 16) * 16);
+    // (16 warps share a slab; slabs of short sequences hold about two of them)
+    const int64_t least = std::min<int64_t>(16, std::max<int64_t>(1, 2ll * T / nseq));
+    w.L = (int)std::max<int64_t>(least, T > 16 * 2 * 152 ? cdiv(cdiv(T, 2 * 152), 16) * 16 : 0);
     w.slots = (int)cdiv(std::max(T, 1), w.L) + nseq;
     w.Ep = (E + 3) & ~3;
     w.err = (DevErr *)take(kHdrBytes);
@@ -59,14 +61,20 @@ __device__ __forceinline__ int seq_at(const int32_t *seq, int s, int nseq, int T
     return min(max(seq[s], 0), T);
 }
 // The sequence that holds token t: the last s with seq[s] <= t (nseq if t is
-// past the last sequence's end, -1 before the first)
+// past the last sequence's end, -1 before the first).  By a whole warp, 32
+// bounds at a time: a search in halves would wait for a load at every step.
 __device__ __forceinline__ int seq_of(const int32_t *seq, int nseq, int T, int t)
 {
-    int lo = 0, hi = nseq + 1;   // first s in [0, nseq + 1) with seq[s] > t
-    while (lo < hi) {
-        const int m = (lo + hi) >> 1;
-        if (seq_at(seq, m, nseq, T) > t) hi = m;
-        else lo = m + 1;
+    if (!seq) return t < T ? 0 : 1;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = nseq + 1;   // the first bound > t is in [lo, lo + len], known > t at lo + len
+    while (len > 0) {
+        const int stride = (len + 31) >> 5, i = lo + (lane + 1) * stride - 1;
+        const unsigned b = __ballot_sync(0xffffffffu, i >= lo + len || seq_at(seq, i, nseq, T) > t);
+        const int f = b ? __ffs(b) - 1 : 32;   // the first stride whose last bound is > t
+        const int end = lo + len;
+        lo = min(lo + f * stride, end);
+        len = stride > 1 ? min(stride - 1, end - lo) : 0;
     }
     return lo - 1;
 }
