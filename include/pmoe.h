@@ -394,7 +394,8 @@ pmoe_status adapter_cayley_grad(int32_t nblk, int32_t b, const float *S, const f
  * with X bf16 [T, d] hidden states and W bf16 [V, d] the head.  The logits
  * are never stored: the forward keeps one (max, sum) pair per token and 128
  * vocabulary entries, the backward recomputes z in pieces of the vocabulary
- * and holds G = dL/dz of one piece (at most 512 MiB) in the workspace.
+ * and holds G = dL/dz of one piece in the workspace (at most 512 MiB, or 256
+ * entries of the vocabulary).
  *   T >= 0 tokens, d % 64 == 0, d <= 8192, 1 <= V <= 2^24, T <= 2^24
  *   K  teacher entries per token (distillation), <= 256; ignored otherwise
  *   scale  factor of every logit, 1 / temperature: finite and > 0
@@ -416,8 +417,9 @@ size_t head_workspace_bytes(pmoe_head_dims dims, int op);
  * head_logprob_forward -- logp_t = scale z_{t, y_t} - lse_t (the negative
  * softmax cross entropy) of the token's target y_t.
  *   target int32 [T]; a negative target is an ignored token: logp = 0, no
- *          gradient.  A target >= V is ignored and recorded as
- *          PMOE_ERR_BAD_INDEX in the error word.
+ *          gradient (its row of dX is zero whatever X holds there).  A
+ *          target >= V is ignored and recorded as PMOE_ERR_BAD_INDEX in the
+ *          error word.
  *   logp   f32 [T] (out)          lse f32 [T] (out; the backward's input)
  *   ws     >= head_workspace_bytes(dims, PMOE_HEAD_FORWARD)
  */

@@ -578,6 +578,11 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         any |= large[q / 32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
+                        // a row without gradient stays zero, whatever its hidden state holds
+                        if (__any_sync(0xffffffffu, cf == 0.f)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) acc[q + j] = cf == 0.f ? 0.f : acc[q + j];
+                        }
                         if (q & 32) {
                             reuse();
                             stage16(q - 32);

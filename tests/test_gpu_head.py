@@ -238,3 +238,32 @@ def test_large_entries_of_the_gradient_keep_16_bits(T, d, V):
     for got, ref in ((dX, rdX), (dW, rdW)):
         best = (ref.to(torch.bfloat16).to(D) - ref).norm()
         assert (got.to(D) - ref).norm() <= 1.05 * best
+
+
+def test_ignored_tokens_may_hold_anything():
+    """NaN and infinities in the hidden states of ignored tokens reach neither
+    the other tokens nor their own rows of dX."""
+    T, d, V, K = 300, 128, 1003, 4
+    X, W, y, up, g = make(T, d, V)
+    off = torch.rand(T, generator=g, device="cuda") < 0.3
+    y = torch.where(off, torch.full_like(y, -1), y)
+    Xn = X.clone()
+    Xn[off] = float("nan")
+    Xn[off.nonzero()[0, 0], ::2] = float("inf")
+    upn = torch.where(off, torch.full_like(up, float("nan")), up)
+    ref = run_logprob(X, W, y, up, 1.0, dW=False)
+    got = run_logprob(Xn, W, y, upn, 1.0, dW=False)
+    assert torch.equal(got[1], ref[1]) and torch.equal(got[2][~off], ref[2][~off])
+    assert torch.equal(got[3], ref[3]) and torch.all(got[3][off] == 0)
+    ids = torch.randint(0, V, (T, K), generator=g, device="cuda").to(torch.int32)
+    ids[off] = -1
+    t = torch.randn((T, K), generator=g, device="cuda")
+    out = []
+    for x, u in ((X, up), (Xn, upn)):
+        h = DeviceHead(W, T, K=K)
+        loss, lse, dX = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(X)
+        h.distill(x, ids, t, loss, lse)
+        h.distill_backward(x, ids, t, lse, u, dX)
+        out.append((loss, dX))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert torch.all(out[1][0][off] == 0) and torch.all(out[1][1][off] == 0)
