@@ -13,7 +13,6 @@ namespace pmoe {
 namespace hg {
 
 constexpr int kMaxK = 256;                    // teacher entries per token
-constexpr uint16_t kNone = 0xFFFF;
 constexpr int kSms = 152;                     // SMs of a GB300
 constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece
 
@@ -24,79 +23,141 @@ __device__ __forceinline__ void clear(int *p, int n)
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) p[i] = 0;
 }
 
-// Distillation: one warp per token turns the teacher's K entries into a
-// probability each, q = softmax(scale t) over the entries present, ordered
-// by vocabulary id (missing ones last, id kNoId, q = 0).  The place of an
-// entry is the number of entries before it in (id, slot) order.  first[u] is
-// the place of the first entry of the 128 vocabulary entries u (kNone: it has
-// none), so that the GEMM's epilogue finds a unit's entries with one load.
+// Distillation: the teacher's K entries of a token as probabilities, q =
+// softmax(scale t) over the entries present.  Entries with one id become one:
+// q is their sum and h their sum of q log q.  They are placed in vocabulary
+// order (the place of an entry is the number of ids below its own), and for
+// every unit of 128 vocabulary entries that has some, tab holds 256 + the
+// place of its first and mask its columns, so that the GEMM's epilogue takes
+// a unit's entries one after the other.
+// Every entry looks at all K ids in shared memory, so the chain is K long: a
+// warp per token up to 32 entries, else a CTA (128 threads, so at most 2
+// entries each).
+template <int TPT>
 __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float scale, const int32_t *__restrict__ t_idx,
                                                       const float *__restrict__ t_logits, const float *__restrict__ g,
-                                                      int32_t *__restrict__ ids, float *__restrict__ q,
-                                                      float *__restrict__ lq, uint16_t *__restrict__ first, int NU,
-                                                      float *__restrict__ coef, int *__restrict__ zero, int nzero,
-                                                      DevErr *err)
+                                                      float *__restrict__ q, float *__restrict__ h,
+                                                      int *__restrict__ nent, uint16_t *__restrict__ tab,
+                                                      uint4 *__restrict__ mask, int NU, float *__restrict__ coef,
+                                                      int *__restrict__ zero, int nzero, DevErr *err)
 {
-    __shared__ int32_t skey[4][kMaxK];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * 4 + warp;
+    constexpr int kMax = TPT == 32 ? 32 : kMaxK, kN = kMax / TPT, kTok = 128 / TPT;
+    __shared__ int32_t skey[kTok][kMax];
+    __shared__ float2 sq[kTok][kMax];            // (q, q log q)
+    __shared__ uint32_t smask[kTok][kMax][4];    // by the place of a unit's first entry
+    __shared__ float sred[4];
+    const int grp = threadIdx.x / TPT, tid = threadIdx.x % TPT, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kTok + grp;
     grid_wait();
     grid_go();
     clear(zero, nzero);
-    if (t >= T) return;
-    const float inf = __int_as_float(0x7f800000);
-    float x[kMaxK / 32];
-    float m = -inf;
-    bool any = false;
+    if (t >= T) return;   // (a whole group)
+    auto sync = [&]() {
+        if constexpr (TPT == 32) __syncwarp();
+        else __syncthreads();
+    };
+    auto reduce = [&](float v, auto op) {   // over the group
 #pragma unroll
-    for (int i = 0; i < kMaxK / 32; ++i) {
-        const int k = i * 32 + lane;
+        for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if constexpr (TPT > 32) {
+            __syncthreads();
+            if (lane == 0) sred[threadIdx.x >> 5] = v;
+            __syncthreads();
+            v = op(op(sred[0], sred[1]), op(sred[2], sred[3]));
+        }
+        return v;
+    };
+    const float inf = __int_as_float(0x7f800000);
+    int32_t key[kN];
+    float x[kN], m = -inf;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const int k = i * TPT + tid;
+        key[i] = kNoId;
         x[i] = -inf;
         if (k >= K) continue;
         const int id = t_idx[(int64_t)t * K + k];
         const float l = t_logits[(int64_t)t * K + k] * scale;
         if (id >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, id);
-        const bool has = id >= 0 && id < V && l != -inf;   // (a logit of -inf has probability zero)
-        skey[warp][k] = has ? id : kNoId;
-        if (has) {
+        if (id >= 0 && id < V && l != -inf) {   // (a logit of -inf has probability zero)
+            key[i] = id;
             x[i] = l;
             m = fmaxf(m, l);
-            any = true;
         }
+        skey[grp][k] = key[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) smask[grp][k][e] = 0;
     }
-    any = __any_sync(0xffffffffu, any);
+    for (int u = tid; u < NU; u += TPT) tab[(int64_t)t * NU + u] = 0;
+    m = reduce(m, [](float a, float b) { return fmaxf(a, b); });
     float s = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll
-    for (int i = 0; i < kMaxK / 32; ++i)
-        if (any) s += expf(x[i] - m);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int i = 0; i < kN; ++i) s += key[i] != kNoId ? expf(x[i] - m) : 0.f;
+    s = reduce(s, [](float a, float b) { return a + b; });
     const float ls = logf(s);
-    for (int u = lane; u < NU; u += 32) first[(int64_t)t * NU + u] = kNone;
-    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kMaxK / 32; ++i) {
-        const int k = i * 32 + lane;
+    for (int i = 0; i < kN; ++i) {
+        const int k = i * TPT + tid;
         if (k >= K) continue;
-        const int32_t key = skey[warp][k];
-        int r = 0;
-        bool lead = true;   // no entry of its unit comes before it
-        for (int j = 0; j < K; ++j) {
-            const int32_t o = skey[warp][j];
-            const bool before = o < key || (o == key && j < k);
-            r += before;
-            lead &= !(before && o / kUnit == key / kUnit);
-        }
-        const bool has = key != kNoId;
-        const int64_t at = (int64_t)t * K + r;
-        ids[at] = key;
-        q[at] = has ? expf(x[i] - m) / s : 0.f;
-        if (lq) lq[at] = has ? x[i] - m - ls : 0.f;
-        if (has && lead) first[(int64_t)t * NU + key / kUnit] = (uint16_t)r;
+        const float qk = key[i] != kNoId ? expf(x[i] - m) / s : 0.f;
+        sq[grp][k] = make_float2(qk, qk > 0.f ? qk * (x[i] - m - ls) : 0.f);
     }
-    if (coef && lane == 0) coef[t] = any ? g[t] * scale : 0.f;
+    sync();
+    // entries that repeat an earlier one's id join it (its thread adds them, in order)
+    float2 v[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        v[i] = make_float2(0.f, 0.f);
+        if (key[i] == kNoId) continue;
+        bool again = false;
+#pragma unroll 8
+        for (int j = 0; j < K; ++j) {
+            const bool same = skey[grp][j] == key[i];
+            const float2 o = sq[grp][j];
+            v[i].x += same ? o.x : 0.f;
+            v[i].y += same ? o.y : 0.f;
+            again |= same && j < i * TPT + tid;
+        }
+        if (again) key[i] = kNoId;
+    }
+    sync();
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (i * TPT + tid < K) skey[grp][i * TPT + tid] = key[i];
+    sync();
+    int place[kN], first[kN];   // ids below its own; ids in units below its own
+    float n = 0.f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        place[i] = first[i] = 0;
+        if (key[i] == kNoId) continue;
+        n += 1.f;
+#pragma unroll 8
+        for (int j = 0; j < K; ++j) {
+            const int32_t o = skey[grp][j];
+            place[i] += o < key[i];
+            first[i] += o / kUnit < key[i] / kUnit;
+        }
+        atomicOr(&smask[grp][first[i]][key[i] % kUnit / 32], 1u << (key[i] & 31));
+    }
+    sync();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        if (key[i] == kNoId) continue;
+        const int64_t at = (int64_t)t * K + place[i], u = (int64_t)t * NU + key[i] / kUnit;
+        q[at] = v[i].x;
+        if (h) h[at] = v[i].y;
+        if (place[i] == first[i]) {
+            const uint32_t *b = smask[grp][first[i]];
+            tab[u] = (uint16_t)(256 + place[i]);
+            mask[u] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+    }
+    if (nent) {
+        n = reduce(n, [](float a, float b) { return a + b; });
+        if (tid == 0) nent[t] = (int)n;
+    }
+    if (coef && tid == 0) coef[t] = m > -inf ? g[t] * scale : 0.f;
 }
 
 // Log-probability: the row's factor of dz = g s (onehot - p) = coef (p - onehot)
@@ -120,11 +181,11 @@ __global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, co
 // to the largest logit m, in base 2: a log-probability is ln 2 (c z - m -
 // log2 sum), with c z - m in one rounding, so that the value of a confident
 // token keeps its relative accuracy although its logit and lse cancel.
-__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float c, bool distill,
+__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float c,
                                                       const float2 *__restrict__ part, const float *__restrict__ zt,
-                                                      const int32_t *__restrict__ ids, const float *__restrict__ q,
-                                                      const float *__restrict__ lq, float *__restrict__ value,
-                                                      float *__restrict__ lse, DevErr *err)
+                                                      const int32_t *__restrict__ target, const int *__restrict__ nent,
+                                                      const float *__restrict__ q, const float *__restrict__ h,
+                                                      float *__restrict__ value, float *__restrict__ lse, DevErr *err)
 {
     __shared__ float2 sw[4];
     const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -162,15 +223,16 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     const float ls = log2f(s);
     auto logp = [&](float z) { return kLn2 * (fmaf(z, c, -m) - ls); };
     float v = 0.f;
-    if (distill) {
-        for (int k = lane; k < K; k += 32) {
+    if (!target) {
+        const int n = nent[t];
+        for (int k = lane; k < n; k += 32) {
             const int64_t at = (int64_t)t * K + k;
-            if (ids[at] != kNoId) v += q[at] * (lq[at] - logp(zt[at]));
+            v += h[at] - q[at] * logp(zt[at]);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     } else {
-        const int y = ids[t];
+        const int y = target[t];
         if (y >= 0 && y < V) v = logp(zt[t]);
         else if (y >= V && lane == 0) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
     }
@@ -401,9 +463,10 @@ static Tiling dx_tiling(const pmoe_head_dims &h)
 
 struct Ws {
     DevErr *err;
-    int32_t *ids;            // [T][K] sorted teacher ids
-    float *q, *lq;           // [T][K]
-    uint16_t *first;         // [T][NU]
+    float *q, *h;            // teacher entries [T][K]: q, q log q
+    int *nent;               // [T] their number
+    uint16_t *tab;           // [T][NU]
+    uint4 *mask;             // [T][NU]
     float *zt;               // [T][max(K, 1)]
     float2 *part;            // [T][NU]
     float *coef;             // [T]
@@ -433,11 +496,12 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
     Ws w{};
     const size_t T = h.T, K = h.K;
     w.err = (DevErr *)take(kHdrBytes);
-    w.ids = (int32_t *)take(T * K * 4);
     w.q = (float *)take(T * K * 4);
-    w.first = (uint16_t *)take(K ? T * cdiv(h.V, kUnit) * 2 : 0);
+    w.tab = (uint16_t *)take(K ? T * cdiv(h.V, kUnit) * 2 : 0);
+    w.mask = (uint4 *)take(K ? T * cdiv(h.V, kUnit) * 16 : 0);
     if (op == PMOE_HEAD_FORWARD) {
-        w.lq = (float *)take(T * K * 4);
+        w.h = (float *)take(T * K * 4);
+        w.nent = (int *)take(K ? T * 4 : 0);
         w.zt = (float *)take(T * std::max<size_t>(K, 1) * 4);
         w.part = (float2 *)take(T * cdiv(h.V, kUnit) * 8);
     } else {
@@ -520,16 +584,21 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
 }
 
 // ------------------------------------------------------------------ passes
+static bool launch_teacher(const pmoe_head_dims &h, float scale, const int32_t *idx, const float *t_logits, const float *g,
+                           const Ws &w, int *zero, int nzero, cudaStream_t st)
+{
+    const int tpt = h.K <= 32 ? 32 : 128;
+    return launch_chained(tpt == 32 ? k_head_teacher<32> : k_head_teacher<128>, (unsigned)cdiv(h.T, 128 / tpt), 128, 0, 1, st,
+                          h.T, h.V, h.K, scale, idx, t_logits, g, w.q, w.h, w.nent, w.tab, w.mask, (int)cdiv(h.V, kUnit),
+                          w.coef, zero, nzero, w.err);
+}
+
 static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W, float scale, const int32_t *idx,
                            const float *t_logits, bool distill, float *value, float *lse, const Ws &w, cudaStream_t st)
 {
     const int K = distill ? h.K : 1;
-    const int32_t *ids = idx;
     if (distill) {
-        if (!launch_chained(k_head_teacher, (unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, K, scale, idx, t_logits,
-                            nullptr, w.ids, w.q, w.lq, w.first, (int)cdiv(h.V, kUnit), nullptr, nullptr, 0, w.err))
-            return PMOE_ERR_CUDA;
-        ids = w.ids;
+        if (!launch_teacher(h, scale, idx, t_logits, nullptr, w, nullptr, 0, st)) return PMOE_ERR_CUDA;
     }
     Args a{};
     a.M = h.T;
@@ -540,15 +609,16 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     a.NU = (int)cdiv(h.V, kUnit);
     a.part = w.part;
     a.zt = w.zt;
-    a.ids = ids;
-    a.first = distill ? w.first : nullptr;
+    a.target = distill ? nullptr : idx;
+    a.tab = w.tab;
+    a.mask = w.mask;
     a.K = K;
     a.err = w.err;
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
-    return launch_chained(k_head_combine, (unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, a.c, distill, w.part, w.zt, ids, w.q,
-                          w.lq, value, lse, w.err)
+    return launch_chained(k_head_combine, (unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, a.c, w.part, w.zt, a.target, w.nent, w.q,
+                          w.h, value, lse, w.err)
                ? PMOE_OK
                : PMOE_ERR_CUDA;
 }
@@ -560,8 +630,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     const int K = distill ? h.K : 1;
     const int nzero = (int)(w.zero_bytes / 4);
     const bool made =
-        distill ? launch_chained(k_head_teacher, (unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, K, scale, idx, t_logits, g,
-                                 w.ids, w.q, nullptr, w.first, (int)cdiv(h.V, kUnit), w.coef, w.cnt, nzero, w.err)
+        distill ? launch_teacher(h, scale, idx, t_logits, g, w, w.cnt, nzero, st)
                 : launch_chained(k_head_coef, (unsigned)cdiv(h.T, 256), 256, 0, 1, st, h.T, h.V, scale, idx, g, w.coef,
                                  w.cnt, nzero, w.err);
     if (!made) return PMOE_ERR_CUDA;
@@ -586,9 +655,10 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.V = h.V;
             a.ksteps = h.d / kBK;
             a.c = scale * 1.4426950408889634f;
-            a.ids = distill ? w.ids : idx;
-            a.q = distill ? w.q : nullptr;
-            a.first = distill ? w.first : nullptr;
+            a.target = distill ? nullptr : idx;
+            a.tab = w.tab;
+            a.mask = w.mask;
+            a.q = w.q;
             a.NU = (int)cdiv(h.V, kUnit);
             a.K = K;
             a.lse = lse;

@@ -102,11 +102,13 @@ struct Args {
     float c;                 // FWD, GRAD: scale * log2(e)
     int NU;                  // FWD, GRAD: units of the vocabulary
     float2 *part;            // FWD: [T][NU] (max, sum) in base 2
-    float *zt;               // FWD: [T][K] raw logits of the target entries
-    const int32_t *ids;      // FWD, GRAD: [T][K] target entries, ascending, kNoId last
-    const uint16_t *first;   // FWD, GRAD: [T][NU] place of a unit's first entry (>= K: none),
-                             // or NULL: K is 1
-    const float *q;          // GRAD: [T][K] their probabilities, or NULL: 1
+    // the target entries of FWD and GRAD: one per token with probability 1
+    // (target), or up to K per token, in vocabulary order
+    const int32_t *target;   // [T], or NULL
+    const uint16_t *tab;     // [T][NU]: 0 where the unit has none, else 256 + place of its first
+    const uint4 *mask;       // [T][NU]: the unit's columns that have one (where tab is not 0)
+    const float *q;          // GRAD: [T][K] probabilities
+    float *zt;               // FWD: [T][K] raw logits of the entries (out)
     int K;
     const float *lse;        // GRAD: [T]
     const float *coef;       // GRAD: [T] factor of the row (0: no gradient)
@@ -428,17 +430,27 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             const int cb = a.n0 + t.n * BN + half * kUnit;   // first column
             const int nv = min(kUnit, a.V - cb);             // FWD, GRAD: valid columns (may be <= 0)
             const bool live = row < a.M && nv > 0;
-            // the row's first target entry among the columns (kNoId: none), its
-            // normaliser and factor: fetched while the tensor cores work
-            const int32_t *ids = a.ids + (int64_t)row * a.K;
-            int pos = 0, id = kNoId;
-            float qv = 1.f, l2 = 0.f, cf = 0.f;
+            // the row's target entries among the columns (a bit each) and the place
+            // of the first, its normaliser and factor: fetched while the tensor
+            // cores work
+            uint32_t mw[kUnit / 32] = {0, 0, 0, 0};
+            int64_t pos = (int64_t)row * a.K;
+            float l2 = 0.f, cf = 0.f;
             if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
-                if (live) {
-                    if (a.first) pos = a.first[(int64_t)row * a.NU + cb / kUnit];
-                    if (pos < a.K) id = ids[pos];
-                    if (id < cb || id >= a.V) id = kNoId;   // (K = 1: no target among the columns before)
-                    if (EPI == HG_GRAD && a.q && pos < a.K) qv = a.q[(int64_t)row * a.K + pos];
+                if (live && a.target) {
+                    const int j = a.target[row] - cb;
+                    if (j >= 0 && j < nv) {
+#pragma unroll
+                        for (int e = 0; e < kUnit / 32; ++e) mw[e] = j >> 5 == e ? 1u << (j & 31) : 0u;
+                    }
+                } else if (live) {
+                    const int64_t at = (int64_t)row * a.NU + cb / kUnit;
+                    const int e = a.tab[at];
+                    if (e) {
+                        const uint4 m = a.mask[at];
+                        mw[0] = m.x, mw[1] = m.y, mw[2] = m.z, mw[3] = m.w;
+                        pos += e - 256;
+                    }
                 }
                 if (EPI == HG_GRAD && row < a.M) {
                     l2 = a.lse[row] * 1.4426950408889634f;
@@ -490,18 +502,10 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             if constexpr (EPI == HG_FWD) {
 #pragma unroll
                 for (int q = 0; q < kUnit; q += 32) {
-                    const int e0 = cb + q;   // entries of columns e0 .. e0 + 31
-                    while (__any_sync(0xffffffffu, id < e0 + 32)) {
-                        const int j0 = id - e0;   // (kNoId is beyond every column)
-                        float z = 0.f;
+                    if (!__any_sync(0xffffffffu, mw[q / 32] != 0)) continue;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) z = j == j0 ? acc[q + j] : z;
-                        if (id < e0 + 32) {
-                            a.zt[(int64_t)row * a.K + pos] = z;
-                            ++pos;
-                            id = pos < a.K ? ids[pos] : kNoId;
-                        }
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (mw[q / 32] >> j & 1u) a.zt[pos++] = acc[q + j];
                 }
                 if (nv < kUnit) {
 #pragma unroll
@@ -545,18 +549,23 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     uint32_t large[kUnit / 32], any = 0;   // the columns to list
 #pragma unroll
                     for (int q = 0; q < kUnit; q += 32) {
-                        const int e0 = cb + q;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) acc[q + j] = ex2(fmaf(acc[q + j], a.c, -l2));
-                        while (__any_sync(0xffffffffu, id < e0 + 32)) {
-                            const int j0 = id - e0;
+                        if (__any_sync(0xffffffffu, mw[q / 32] != 0)) {
+                            if (a.target) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) acc[q + j] -= j == j0 ? qv : 0.f;
-                            if (id < e0 + 32) {
-                                id = kNoId;
-                                if (++pos < a.K) {
-                                    id = ids[pos];
-                                    qv = a.q[(int64_t)row * a.K + pos];   // (K > 1: q is given)
+                                for (int j = 0; j < 32; ++j) acc[q + j] -= mw[q / 32] >> j & 1u ? 1.f : 0.f;
+                            } else {
+#pragma unroll
+                                for (int j0 = 0; j0 < 32; j0 += 8) {   // (eight loads on their way at once)
+                                    float v[8];
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        v[j] = 0.f;
+                                        if (mw[q / 32] >> (j0 + j) & 1u) v[j] = a.q[pos++];
+                                    }
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) acc[q + j0 + j] -= v[j];
                                 }
                             }
                         }
