@@ -484,11 +484,11 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
     bool ok = true;
     if (dims.T > 0)
         bal::by_experts(dims.E, [&](auto tpt, auto v, auto ni) {
-            auto kern = bal::k_balance_partial<tpt.value, v.value, ni.value>;
+            constexpr auto kern = bal::k_balance_partial<tpt.value, v.value, ni.value>;
             const size_t sm = (size_t)(bal::fwd_threads(tpt.value) / tpt.value + 1) * w.Ep * 4;
             static const bool attr =   // up to 17 rows of 1024 floats (69 KB)
                 cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 17 * 4096) == cudaSuccess;
-            ok = attr && launch_chained(kern, (unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
+            ok = attr && launch_chained<kern>((unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
                                 w.L, w.Ep, logits, idx, valid, seq, nseq, w.psum, w.cnt, w.ntok, w.err);
         });
     // CTAs per sequence: 32 experts each up to 8 CTAs, then more experts each
@@ -496,7 +496,7 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
     // few slots a sequence: smaller CTAs start sooner (37 sequences of 16384 tokens: 8.5 us with 1024
     // threads); one long sequence: more strands (8192 tokens, 6.3 us with 1024, 8.5 with 512)
     const unsigned threads = w.slots / nseq >= 64 ? bal::kRedThreads : std::max(256, cols);
-    ok = ok && launch_chained(bal::k_balance_reduce, (unsigned)(nseq * C), threads, 0, C, stream, dims.T, dims.E,
+    ok = ok && launch_chained<bal::k_balance_reduce>((unsigned)(nseq * C), threads, 0, C, stream, dims.T, dims.E,
                               dims.k, w.L, w.Ep, cols, C, seq, nseq, w.psum, w.cnt, w.ntok, counts, ntok, pmean, loss,
                               w.err);
     return ok ? PMOE_OK : PMOE_ERR_CUDA;
@@ -518,7 +518,7 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
     bool ok = true;
     bal::by_experts(dims.E, [&](auto tpt, auto v, auto ni) {
         const unsigned groups = bal::kThreads / tpt.value;   // (rows of at most 32 KB in all)
-        ok = launch_chained(bal::k_route_backward<tpt.value, v.value, ni.value>, (unsigned)cdiv(dims.T, groups),
+        ok = launch_chained<bal::k_route_backward<tpt.value, v.value, ni.value>>((unsigned)cdiv(dims.T, groups),
                             bal::kThreads, (size_t)groups * b.Ep * 4, 1, stream, dims.T, dims.E, dims.k, logits, idx, w, d_topk_w, valid, seq,
                             nseq, counts, ntok, g_loss, dlogits, b.err);
     });

@@ -245,118 +245,143 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
 // ------------------------------------------------------------------ large entries
 // The extra K steps of one product, one CTA per 256 output rows.  The
 // entries of the rows take consecutive columns of A, in (token, vocabulary
-// id) order whatever order GRAD's threads listed them in; a block's steps
-// are taken from a counter, so blocks may come in any order, but a block's
-// own columns, and with them its sums, are fixed.
-//   DX (kDw 0): rows are tokens, a column's row of B is its vocabulary entry
+// id) order whatever order GRAD's threads listed them in.
+//   DX (kDw 0): rows are tokens, a column's row of B is its vocabulary entry;
+//   a block's entries have their own place (kMaxLarge steps of 64 each 256
+//   tokens at most)
 //   DW (kDw 1): rows are vocabulary entries, the row of B is the token; `fl`
-//   names the blocks of 128 tokens to look at
+//   names the blocks of 128 tokens to look at, four tokens a thread.  A
+//   block's steps are taken from a counter, so blocks may come in any order,
+//   but a block's own columns, and with them its sums, are fixed.
+// The entries found are kept in shared memory while there is room, else the
+// tokens are read again once the block's steps are known.
+constexpr int kLargeThreads = 1024, kLargeKept = 1024;   // (threads: at most)
+constexpr int kLargeSteps = kListRows * kMaxLarge / 64;   // of a block of tokens
+struct LargeShared {
+    int warp[kLargeThreads / 32], base;
+    int3 kept[kLargeKept];   // (token - t0, vocabulary entry, remainder)
+};
+
+// Exclusive sum of n over the CTA's threads, and the total
+__device__ __forceinline__ int large_scan(LargeShared &sh, int n, int &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp[warp] = x;
+    __syncthreads();
+    int s = lane < warps ? sh.warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    const int before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+    total = __shfl_sync(0xffffffffu, s, 31);
+    return (warp ? before : 0) + x - n;
+}
+
 template <int kDw>
-__device__ void large_steps(int blk, int T, const int *__restrict__ cnt, const int2 *__restrict__ large,
+__device__ void large_steps(LargeShared &sh, int blk, int T, const int *__restrict__ cnt, const int2 *__restrict__ large,
                             const uint8_t *__restrict__ fl, int fs, int *__restrict__ steps, int2 *__restrict__ lists,
                             int32_t *__restrict__ lidx, uint16_t *__restrict__ lo)
 {
-    __shared__ int sw[8], s_base;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int2 e[kMaxLarge];
-    int n = 0;
-    // this thread's entries of token t, ascending by vocabulary id
-    auto fetch = [&](int t) {
-        n = 0;
-        if (t >= T) return;
-        const int c = min(cnt[t], kMaxLarge);
-        int last = -1;
-        for (int i = 0; i < c; ++i) {
-            int2 best = make_int2(kNoId, 0);
-            for (int j = 0; j < c; ++j) {
-                const int2 v = large[(int64_t)t * kMaxLarge + j];
-                if (v.x > last && v.x < best.x) best = v;
-            }
-            last = best.x;
-            if (!kDw || best.x / kListRows == blk) {
+    constexpr int R = kDw ? 4 : 1;   // tokens a thread
+    const int tid = threadIdx.x, t0 = kDw ? 0 : blk * kListRows, t1 = kDw ? T : min(T, t0 + kListRows);
+    int64_t first = -1;              // the block's first step, once it is known
+    auto put = [&](int at, int t, int v, int rem) {
+        if (first < 0) {
+            if (at < kLargeKept) sh.kept[at] = make_int3(t - t0, v, rem);
+            return;
+        }
+        const int64_t st = first + at / 64;
+        const int c = at % 64;
+        lidx[st * 64 + c] = kDw ? t : v;
+        lo[st * 64 * kListRows + (kDw ? c * kListRows + v % kListRows : (t - t0) * 64 + c)] = (uint16_t)rem;
+    };
+    auto ours = [&](int id) { return !kDw || id / kListRows == blk; };
+    // all entries of the block, each with its column; returns their number.
+    // (Most tokens have one or two; loops over a token's entries stay loops:
+    // unrolled, the code's own fetches took longer than its work.)
+    auto walk = [&]() {
+        int total = 0;
+        for (int b = t0; b < t1; b += blockDim.x * R) {
+            const int t = b + tid * R;
+            int c[R], n[R], sum = 0;
+            int2 f[R];
 #pragma unroll
-                for (int j = 0; j < kMaxLarge; ++j)
-                    if (j == n) e[j] = best;
-                ++n;
+            for (int r = 0; r < R; ++r) {   // (all first loads at once)
+                c[r] = t + r < t1 ? min(cnt[t + r], kMaxLarge) : 0;
+                f[r] = t + r < t1 ? large[(int64_t)(t + r) * kMaxLarge] : make_int2(0, 0);
+            }
+            const bool look = t < t1 && (!kDw || fl[(int64_t)blk * fs + (t >> 7)] != 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                n[r] = look && c[r] > 0 && ours(f[r].x);
+                if (look)
+#pragma unroll 1
+                    for (int j = 1; j < c[r]; ++j) n[r] += ours(large[(int64_t)(t + r) * kMaxLarge + j].x);
+                sum += n[r];
+            }
+            int all, at = total + large_scan(sh, sum, all);
+            total += all;
+            if (sum) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int2 *x = large + (int64_t)(t + r) * kMaxLarge;
+                    if (n[r]) {
+#pragma unroll 1
+                        for (int j = 0; j < c[r]; ++j) {
+                            const int2 v = x[j];
+                            if (!ours(v.x)) continue;
+                            int place = 0;   // ascending by vocabulary id
+#pragma unroll 1
+                            for (int i = 0; i < c[r] && c[r] > 1; ++i) place += ours(x[i].x) && x[i].x < v.x;
+                            put(at + place, t + r, v.x, v.y);
+                        }
+                    }
+                    at += n[r];
+                }
             }
         }
+        return total;
     };
-    // exclusive sum of n over the CTA's threads, and the total
-    auto scan = [&](int &total) {
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) sw[warp] = x;
-        __syncthreads();
-        int base = 0;
-        total = 0;
-        for (int i = 0; i < 8; ++i) {
-            if (i < warp) base += sw[i];
-            total += sw[i];
-        }
-        return base + x - n;
-    };
-    auto put = [&](int at, int t) {   // the thread's entries from column `at` of the block's steps
-#pragma unroll
-        for (int j = 0; j < kMaxLarge; ++j)
-            if (j < n) {
-                const int64_t st = s_base + (at + j) / 64;
-                const int c = (at + j) % 64;
-                lidx[st * 64 + c] = kDw ? t : e[j].x;
-                lo[st * 64 * kListRows + (kDw ? c * kListRows + e[j].x % kListRows : (t % kListRows) * 64 + c)] =
-                    (uint16_t)e[j].y;
-            }
-    };
-    // tokens 256 at a time; for DW only where a flag is set
-    const int t0 = kDw ? 0 : blk * kListRows, t1 = kDw ? T : min(T, t0 + kListRows);
-    auto wanted = [&](int t) {
-        if (!kDw) return true;
-        const uint8_t *f = fl + (int64_t)blk * fs + (t >> 7);
-        return f[0] != 0 || ((t >> 7) + 1 < fs && f[1] != 0);
-    };
-    int total = 0;
-    for (int t = t0; t < t1; t += 256) {
-        if (!wanted(t)) continue;
-        int c;
-        fetch(t + tid);
-        scan(c);
-        total += c;
-    }
-    const int ns = (total + 63) / 64;
+    const int total = walk(), ns = (total + 63) / 64;
     if (tid == 0) {
-        s_base = ns ? atomicAdd(steps, ns) : 0;
-        lists[blk] = make_int2(s_base, ns);
+        sh.base = !kDw ? blk * kLargeSteps : ns ? atomicAdd(steps, ns) : 0;
+        lists[blk] = make_int2(sh.base, ns);
     }
     __syncthreads();
     if (!ns) return;
-    uint4 *z = (uint4 *)(lo + (int64_t)s_base * 64 * kListRows);
-    for (int i = tid; i < ns * 64 * kListRows / 8; i += 256) z[i] = make_uint4(0, 0, 0, 0);
-    for (int i = total + tid; i < ns * 64; i += 256) lidx[(int64_t)s_base * 64 + i] = 0;   // (its column of A is zero)
+    first = sh.base;
+    uint4 *z = (uint4 *)(lo + first * 64 * kListRows);
+    for (int i = tid; i < ns * 64 * kListRows / 8; i += blockDim.x) z[i] = make_uint4(0, 0, 0, 0);
+    for (int i = total + tid; i < ns * 64; i += blockDim.x) lidx[first * 64 + i] = 0;   // (its column of A is zero)
     __syncthreads();
-    int at = 0;
-    for (int t = t0; t < t1; t += 256) {
-        if (!wanted(t)) continue;
-        int c;
-        if (kDw) fetch(t + tid);   // (DX: the only batch is still in registers)
-        const int off = scan(c);
-        put(at + off, t + tid);
-        at += c;
+    if (total <= kLargeKept) {
+        for (int i = tid; i < total; i += blockDim.x)
+            put(i, t0 + sh.kept[i].x, sh.kept[i].y, sh.kept[i].z);
+    } else {
+        walk();
     }
 }
 
 // CTAs 0 .. nx-1: DX's blocks, the others DW's
-__global__ void __launch_bounds__(256) k_head_large(int nx, int T, const int *cnt, const int2 *large, const uint8_t *fl,
-                                                    int fs, int *steps, int2 *lists0, int32_t *lidx0, uint16_t *lo0,
-                                                    int2 *lists1, int32_t *lidx1, uint16_t *lo1)
+__global__ void __launch_bounds__(kLargeThreads) k_head_large(int nx, int T, const int *cnt, const int2 *large,
+                                                              const uint8_t *fl, int fs, int *steps, int2 *lists0,
+                                                              int32_t *lidx0, uint16_t *lo0, int2 *lists1,
+                                                              int32_t *lidx1, uint16_t *lo1)
 {
+    __shared__ LargeShared sh;
     grid_wait();
     grid_go();
-    if ((int)blockIdx.x < nx) large_steps<0>(blockIdx.x, T, cnt, large, fl, fs, steps, lists0, lidx0, lo0);
-    else large_steps<1>(blockIdx.x - nx, T, cnt, large, fl, fs, steps + 1, lists1, lidx1, lo1);
+    if ((int)blockIdx.x < nx) large_steps<0>(sh, blockIdx.x, T, cnt, large, fl, fs, steps, lists0, lidx0, lo0);
+    else large_steps<1>(sh, blockIdx.x - nx, T, cnt, large, fl, fs, steps, lists1, lidx1, lo1);
 }
 
 struct Parts {
@@ -472,9 +497,9 @@ struct Ws {
     float *coef;             // [T]
     uint16_t *G;             // [T][piece]
     // G's large entries: per token, then as the extra K steps of DX and DW
-    int *cnt;                // [T], then the flags and two step counters: zeroed per piece
+    int *cnt;                // [T], then the step counter and the flags: zeroed per piece
     uint8_t *fl;             // [piece / 256][fs]
-    int *steps;              // [2]
+    int *steps;              // DW's steps taken so far
     size_t zero_bytes;
     int fs;
     int2 *large;             // [T][kMaxLarge]
@@ -511,14 +536,14 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
         w.G = (uint16_t *)take(T * piece * 2);
         const int blocks[2] = {(int)cdiv(h.T, kListRows), piece / kListRows};
         w.fs = (int)cdiv(h.T, 128);
-        w.zero_bytes = (T * 4 + 8 + (size_t)blocks[1] * w.fs + 3) & ~(size_t)3;
+        w.zero_bytes = (T * 4 + 4 + (size_t)blocks[1] * w.fs + 3) & ~(size_t)3;
         uint8_t *z = take(w.zero_bytes);
         w.cnt = (int *)z;
         w.steps = w.cnt + T;
-        w.fl = (uint8_t *)(w.steps + 2);
+        w.fl = (uint8_t *)(w.steps + 1);
         w.large = (int2 *)take(T * kMaxLarge * 8);
         for (int i = 0; i < 2; ++i) {
-            w.max_steps[i] = (int)(cdiv((int64_t)h.T * kMaxLarge, 64) + blocks[i]);
+            w.max_steps[i] = i == 0 ? blocks[0] * kLargeSteps : (int)(cdiv((int64_t)h.T * kMaxLarge, 64) + blocks[1]);
             w.lists[i] = (int2 *)take((size_t)blocks[i] * 8);
             w.lidx[i] = (int32_t *)take((size_t)w.max_steps[i] * 64 * 4);
             w.lo[i] = (uint16_t *)take((size_t)w.max_steps[i] * 64 * kListRows * 2);
@@ -544,13 +569,13 @@ template <int CTAS, int BN, int EPI>
 static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap (&ml)[2],
                       const Args &a, cudaStream_t st)
 {
-    auto kern = k_head_gemm<CTAS, BN, EPI>;
+    constexpr auto kern = k_head_gemm<CTAS, BN, EPI>;
     static const bool attr =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(BN)) == cudaSuccess;
     if (!attr) return false;
     const int64_t items = a.whole + ((int64_t)a.mt * a.nt - a.whole) * a.splits;
     const int64_t clusters = std::min<int64_t>(items, tc::num_sms() / CTAS);
-    return launch_chained(kern, (unsigned)(clusters * CTAS), threads_of(BN),
+    return launch_chained<kern>((unsigned)(clusters * CTAS), threads_of(BN),
                           smem_of(BN), CTAS, st, ma, mt, mb, mo, ml[0], ml[1], a);
 }
 
@@ -584,13 +609,19 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
 }
 
 // ------------------------------------------------------------------ passes
+template <auto K>
+using Kernel = std::integral_constant<decltype(K), K>;
+
 static bool launch_teacher(const pmoe_head_dims &h, float scale, const int32_t *idx, const float *t_logits, const float *g,
                            const Ws &w, int *zero, int nzero, cudaStream_t st)
 {
     const int tpt = h.K <= 32 ? 32 : 128;
-    return launch_chained(tpt == 32 ? k_head_teacher<32> : k_head_teacher<128>, (unsigned)cdiv(h.T, 128 / tpt), 128, 0, 1, st,
-                          h.T, h.V, h.K, scale, idx, t_logits, g, w.q, w.h, w.nent, w.tab, w.mask, (int)cdiv(h.V, kUnit),
-                          w.coef, zero, nzero, w.err);
+    auto launch = [&](auto kern) {
+        return launch_chained<decltype(kern)::value>((unsigned)cdiv(h.T, 128 / tpt), 128, 0, 1, st, h.T, h.V, h.K, scale, idx,
+                                                     t_logits, g, w.q, w.h, w.nent, w.tab, w.mask, (int)cdiv(h.V, kUnit),
+                                                     w.coef, zero, nzero, w.err);
+    };
+    return tpt == 32 ? launch(Kernel<k_head_teacher<32>>()) : launch(Kernel<k_head_teacher<128>>());
 }
 
 static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W, float scale, const int32_t *idx,
@@ -617,7 +648,7 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
-    return launch_chained(k_head_combine, (unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, a.c, w.part, w.zt, a.target, w.nent, w.q,
+    return launch_chained<k_head_combine>((unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, a.c, w.part, w.zt, a.target, w.nent, w.q,
                           w.h, value, lse, w.err)
                ? PMOE_OK
                : PMOE_ERR_CUDA;
@@ -631,7 +662,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     const int nzero = (int)(w.zero_bytes / 4);
     const bool made =
         distill ? launch_teacher(h, scale, idx, t_logits, g, w, w.cnt, nzero, st)
-                : launch_chained(k_head_coef, (unsigned)cdiv(h.T, 256), 256, 0, 1, st, h.T, h.V, scale, idx, g, w.coef,
+                : launch_chained<k_head_coef>((unsigned)cdiv(h.T, 256), 256, 0, 1, st, h.T, h.V, scale, idx, g, w.coef,
                                  w.cnt, nzero, w.err);
     if (!made) return PMOE_ERR_CUDA;
     const int piece = piece_of(h.T, h.V);
@@ -669,7 +700,9 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
                 return PMOE_ERR_CUDA;
         }
         const int nx = dX ? (int)cdiv(h.T, kListRows) : 0, nw = dW ? (int)cdiv(vc, kListRows) : 0;
-        if (!launch_chained(k_head_large, (unsigned)(nx + nw), 256, 0, 1, st, nx, h.T, w.cnt, w.large, w.fl, w.fs, w.steps,
+        // a block of tokens takes 256 threads; blocks of the vocabulary look at all tokens, four a thread
+        const unsigned threads = nw == 0 || h.T <= 4 * kListRows ? kListRows : kLargeThreads;
+        if (!launch_chained<k_head_large>((unsigned)(nx + nw), threads, 0, 1, st, nx, h.T, w.cnt, w.large, w.fl, w.fs, w.steps,
                             w.lists[0], w.lidx[0], w.lo[0], w.lists[1], w.lidx[1], w.lo[1]))
             return PMOE_ERR_CUDA;
         if (dX) {
@@ -710,7 +743,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     }
     if (dX && w.dx) {
         const int64_t n = (int64_t)h.T * h.d;
-        if (!launch_chained(k_head_sum, (unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, 1, st, h.T, h.d,
+        if (!launch_chained<k_head_sum>((unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, 1, st, h.T, h.d,
                             Parts{tx.mt, tx.nt, tx.gm, tx.whole, tx.bn, tx.splits}, w.dx, (uint16_t *)dX))
             return PMOE_ERR_CUDA;
     }

@@ -16,11 +16,17 @@ namespace pmoe {
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Launches a kernel that begins with grid_wait(), in clusters of `cluster` CTAs
-template <class... P, class... A>
-bool launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st,
-                    A... args)
+// Launches kernel K, which begins with grid_wait(), in clusters of `cluster`
+// CTAs.  Every kernel of a chain asks for the SM's memory to be all shared
+// memory, as the GEMMs need it: an SM that has to change the split between
+// two kernels waits until it is empty (13 us over the 8 launches of a small
+// distillation step).
+template <auto K, class... A>
+bool launch_chained(unsigned grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st, A... args)
 {
+    static const bool split = cudaFuncSetAttribute(K, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+    if (!split) return false;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
@@ -34,7 +40,7 @@ bool launch_chained(void (*kern)(P...), unsigned grid, unsigned block, size_t sm
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kern, (P)args...) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, K, args...) != cudaSuccess) return false;
     note_launch();
     return true;
 }
