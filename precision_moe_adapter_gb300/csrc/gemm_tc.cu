@@ -86,22 +86,6 @@ bool make_slots_tmap(CUtensorMap *m, const void *base, int64_t slots, int64_t ro
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_tmap3(CUtensorMap *m, const void *base, bool f32, int64_t cols, int64_t rows, int64_t planes,
-                int box_cols, int box_rows)
-{
-    EncodeTiled enc = encoder();
-    if (!enc) return false;
-    const cuuint64_t e = f32 ? 4 : 2;
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    cuuint64_t strides[2] = {(cuuint64_t)cols * e, (cuuint64_t)rows * cols * e};
-    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2,
-               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // One-shot test hook (pmoe_debug_expire_gemm_wait): the wait limit of the
 // next grouped-GEMM launch, 0 when none is armed.
 static std::atomic<uint64_t> g_expire_wait_ns{0};

@@ -19,10 +19,6 @@ bool make_bytes_tmap(CUtensorMap *m, const void *base, int64_t rows, int64_t row
 // BF16 scratch slots [slots][rows][cols], box 64 cols x box_rows, 128-byte swizzle
 bool make_slots_tmap(CUtensorMap *m, const void *base, int64_t slots, int64_t rows, int64_t cols,
                      int64_t slot_bytes, int box_rows);
-// BF16 or FP32 row-major [planes][rows][cols] (planes 0: a 2-D map [rows][cols]),
-// 128-byte swizzle, boxes of box_rows x box_cols (128 bytes)
-bool make_tmap3(CUtensorMap *m, const void *base, bool f32, int64_t cols, int64_t rows, int64_t planes,
-                int box_cols, int box_rows);
 int num_sms();
 // The bounded-wait limit and withheld item of the next launch: the armed test
 // hook (once), else the default limit and none.

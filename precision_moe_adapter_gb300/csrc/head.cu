@@ -5,8 +5,8 @@
 // layout, the choice of tiles and the entry points.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
-#include "gemm_tc_host.cuh"
 #include "head_gemm.cuh"
 
 namespace pmoe {
@@ -555,6 +555,30 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
 }
 
 // ------------------------------------------------------------------ launch
+// BF16 or FP32 row-major [planes][rows][cols] (planes 0: a 2-D map [rows][cols]),
+// 128-byte swizzle, boxes of box_rows x box_cols (128 bytes), zeros past the end
+static bool make_map(CUtensorMap *m, const void *base, bool f32, int64_t cols, int64_t rows, int64_t planes, int box_cols,
+                     int box_rows)
+{
+    // (through the runtime's driver entry point: the library does not link libcuda)
+    static const decltype(&cuTensorMapEncodeTiled) encode = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return (decltype(&cuTensorMapEncodeTiled))(ok ? p : nullptr);
+    }();
+    if (!encode) return false;
+    const cuuint64_t e = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * e, (cuuint64_t)rows * cols * e};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2,
+                  const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 struct Operand {
     const void *base;
     int64_t cols, rows;
@@ -562,7 +586,7 @@ struct Operand {
 };
 static bool map_operand(CUtensorMap *m, const Operand &o)
 {
-    return tc::make_tmap3(m, o.base, false, o.cols, o.rows, 0, kBK, o.mn ? 64 : 128);
+    return make_map(m, o.base, false, o.cols, o.rows, 0, kBK, o.mn ? 64 : 128);
 }
 
 template <int CTAS, int BN, int EPI>
@@ -574,7 +598,7 @@ static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtens
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(BN)) == cudaSuccess;
     if (!attr) return false;
     const int64_t items = a.whole + ((int64_t)a.mt * a.nt - a.whole) * a.splits;
-    const int64_t clusters = std::min<int64_t>(items, tc::num_sms() / CTAS);
+    const int64_t clusters = std::min<int64_t>(items, gemm_num_sms() / CTAS);
     return launch_chained<kern>((unsigned)(clusters * CTAS), threads_of(BN),
                           smem_of(BN), CTAS, st, ma, mt, mb, mo, ml[0], ml[1], a);
 }
@@ -593,12 +617,12 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
     if ((EPI == HG_FWD || EPI == HG_GRAD) && A.rows < 128) a.abytes = (int)cdiv(a.tail, 8) * 1024;
     a.stages = std::min(kMaxStages, kRingBytes / (kOpBytes + a.abytes));
     memset(&mt, 0, sizeof mt);
-    if (!A.mn && a.tail && !tc::make_tmap3(&mt, A.base, false, A.cols, A.rows, 0, kBK, a.tail)) return false;
+    if (!A.mn && a.tail && !make_map(&mt, A.base, false, A.cols, A.rows, 0, kBK, a.tail)) return false;
     memset(&mo, 0, sizeof mo);
     memset(ml, 0, sizeof ml);
     if (out) mo = *out;
     // (rows of B are gathered one by one: boxes of one row)
-    if (lo && (!map_operand(&ml[0], *lo) || !tc::make_tmap3(&ml[1], B.base, false, B.cols, B.rows, 0, kBK, 1))) return false;
+    if (lo && (!map_operand(&ml[0], *lo) || !make_map(&ml[1], B.base, false, B.cols, B.rows, 0, kBK, 1))) return false;
     a.mt = t.mt;
     a.nt = t.nt;
     a.splits = t.splits;
@@ -694,7 +718,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.K = K;
             a.lse = lse;
             a.coef = w.coef;
-            if (!tc::make_tmap3(&mo, w.G, false, ldg, h.T, 1, 64, 32) ||
+            if (!make_map(&mo, w.G, false, ldg, h.T, 1, 64, 32) ||
                 !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo,
                                  nullptr, a, st))
                 return PMOE_ERR_CUDA;
@@ -714,8 +738,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.bf16_out = w.dx == nullptr;
             a.accumulate = v0 > 0;
             Tiling t = tx;
-            const bool made = w.dx ? tc::make_tmap3(&mo, w.dx, true, h.d, h.T, tx.splits, 32, 32)
-                                   : tc::make_tmap3(&mo, dX, false, h.d, h.T, 1, 64, 32);
+            const bool made = w.dx ? make_map(&mo, w.dx, true, h.d, h.T, tx.splits, 32, 32)
+                                   : make_map(&mo, dX, false, h.d, h.T, 1, 64, 32);
             // (a last, shorter piece: shorter parts, perhaps fewer; the other sums then stand)
             t.kper = (int)cdiv(a.ksteps, tx.splits);
             t.splits = (int)cdiv(a.ksteps, t.kper);
@@ -735,7 +759,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.lists = w.lists[1];
             a.lidx = w.lidx[1];
             const Operand lo{w.lo[1], kListRows, (int64_t)w.max_steps[1] * 64, true};
-            if (!tc::make_tmap3(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 32) ||
+            if (!make_map(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 32) ||
                 !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {X, h.d, h.T, true}, &mo, &lo, a,
                                st))
                 return PMOE_ERR_CUDA;
