@@ -396,7 +396,7 @@ pmoe_status adapter_cayley_grad(int32_t nblk, int32_t b, const float *S, const f
  * vocabulary entries, the backward recomputes z in pieces of the vocabulary
  * and holds G = dL/dz of one piece in the workspace (at most 512 MiB, or 256
  * entries of the vocabulary).
- *   T >= 0 tokens, d % 64 == 0, d <= 8192, 1 <= V <= 2^24, T <= 2^24
+ *   T >= 0 tokens, d % 64 == 0, d <= 8192, 1 <= V < 2^24, T <= 2^24
  *   K  teacher entries per token (distillation), <= 256; ignored otherwise
  *   scale  factor of every logit, 1 / temperature: finite and > 0
  * A token's forward results do not depend on the other tokens of the call

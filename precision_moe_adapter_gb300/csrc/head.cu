@@ -26,14 +26,15 @@ __device__ __forceinline__ void clear(int *p, int n)
 // Distillation: the teacher's K entries of a token as probabilities, q =
 // softmax(scale t) over the entries present.  Entries with one id become one:
 // q is their sum and h their sum of q log q.  They are placed in vocabulary
-// order (the place of an entry is the number of ids below its own), and for
-// every unit of 128 vocabulary entries that has some, tab holds 256 + the
-// place of its first and mask its columns, so that the GEMM's epilogue takes
-// a unit's entries one after the other.
-// Every entry looks at all K ids in shared memory, so the chain is K long: a
-// warp per token up to 32 entries, else a CTA (128 threads, so at most 2
-// entries each).
-template <int TPT>
+// order, and for every unit of 128 vocabulary entries that has some, tab
+// holds 256 + the place of its first and mask its columns, so that the GEMM's
+// epilogue takes a unit's entries one after the other.
+// A warp per token sorts 32 kN words (id << 8 | slot; kGone last) in its
+// registers, word i of a lane being element 32 i + lane, by a bitonic network:
+// comparing every entry with every other one took 17 us at T = 4096, K = 64,
+// against 5.
+constexpr uint32_t kGone = 0xFFFFFFFFu;   // (V < 2^24: no id reaches it)
+template <int kN>
 __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float scale, const int32_t *__restrict__ t_idx,
                                                       const float *__restrict__ t_logits, const float *__restrict__ g,
                                                       float *__restrict__ q, float *__restrict__ h,
@@ -41,123 +42,114 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
                                                       uint4 *__restrict__ mask, int NU, float *__restrict__ coef,
                                                       int *__restrict__ zero, int nzero, DevErr *err)
 {
-    constexpr int kMax = TPT == 32 ? 32 : kMaxK, kN = kMax / TPT, kTok = 128 / TPT;
-    __shared__ int32_t skey[kTok][kMax];
-    __shared__ float2 sq[kTok][kMax];            // (q, q log q)
-    __shared__ uint32_t smask[kTok][kMax][4];    // by the place of a unit's first entry
-    __shared__ float sred[4];
-    const int grp = threadIdx.x / TPT, tid = threadIdx.x % TPT, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kTok + grp;
+    constexpr int kAll = 32 * kN;
+    __shared__ float2 sq[4][kAll];            // (q, q log q) by slot
+    __shared__ uint32_t sk[4][kAll];          // the sorted words
+    __shared__ __align__(16) uint32_t smask[4][kAll][4];   // by the place of a unit's first entry
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * 4 + warp;
     grid_wait();
     grid_go();
     clear(zero, nzero);
-    if (t >= T) return;   // (a whole group)
-    auto sync = [&]() {
-        if constexpr (TPT == 32) __syncwarp();
-        else __syncthreads();
-    };
-    auto reduce = [&](float v, auto op) {   // over the group
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if constexpr (TPT > 32) {
-            __syncthreads();
-            if (lane == 0) sred[threadIdx.x >> 5] = v;
-            __syncthreads();
-            v = op(op(sred[0], sred[1]), op(sred[2], sred[3]));
-        }
-        return v;
-    };
+    if (t >= T) return;
     const float inf = __int_as_float(0x7f800000);
-    int32_t key[kN];
+    uint32_t w[kN];
     float x[kN], m = -inf;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-        const int k = i * TPT + tid;
-        key[i] = kNoId;
+        const int k = i * 32 + lane;
+        w[i] = kGone;
         x[i] = -inf;
-        if (k >= K) continue;
-        const int id = t_idx[(int64_t)t * K + k];
-        const float l = t_logits[(int64_t)t * K + k] * scale;
-        if (id >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, id);
-        if (id >= 0 && id < V && l != -inf) {   // (a logit of -inf has probability zero)
-            key[i] = id;
-            x[i] = l;
-            m = fmaxf(m, l);
+        if (k < K) {
+            const int id = t_idx[(int64_t)t * K + k];
+            const float l = t_logits[(int64_t)t * K + k] * scale;
+            if (id >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, id);
+            if (id >= 0 && id < V && l != -inf) {   // (a logit of -inf has probability zero)
+                w[i] = (uint32_t)id << 8 | k;
+                x[i] = l;
+                m = fmaxf(m, l);
+            }
         }
-        skey[grp][k] = key[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) smask[grp][k][e] = 0;
+        *(uint4 *)smask[warp][k] = make_uint4(0, 0, 0, 0);
     }
-    for (int u = tid; u < NU; u += TPT) tab[(int64_t)t * NU + u] = 0;
-    m = reduce(m, [](float a, float b) { return fmaxf(a, b); });
+    for (int u = lane; u < NU; u += 32) tab[(int64_t)t * NU + u] = 0;
     float s = 0.f;
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) s += key[i] != kNoId ? expf(x[i] - m) : 0.f;
-    s = reduce(s, [](float a, float b) { return a + b; });
+    for (int i = 0; i < kN; ++i) any |= w[i] != kGone;
+    any = __any_sync(0xffffffffu, any);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s += w[i] != kGone ? expf(x[i] - m) : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float ls = logf(s);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-        const int k = i * TPT + tid;
-        if (k >= K) continue;
-        const float qk = key[i] != kNoId ? expf(x[i] - m) / s : 0.f;
-        sq[grp][k] = make_float2(qk, qk > 0.f ? qk * (x[i] - m - ls) : 0.f);
+        const float qk = w[i] != kGone ? expf(x[i] - m) / s : 0.f;
+        sq[warp][i * 32 + lane] = make_float2(qk, qk > 0.f ? qk * (x[i] - m - ls) : 0.f);
     }
-    sync();
-    // entries that repeat an earlier one's id join it (its thread adds them, in order)
-    float2 v[kN];
+#pragma unroll
+    for (int k = 2; k <= kAll; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j; j /= 2) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const bool up = ((i * 32 + lane) & k) == 0;
+                if (j < 32) {
+                    const uint32_t o = __shfl_xor_sync(0xffffffffu, w[i], j);
+                    w[i] = ((lane & j) == 0) == up ? min(w[i], o) : max(w[i], o);
+                } else if ((i & (j / 32)) == 0) {   // (the pair lies in this lane)
+                    const int e = i | (j / 32);
+                    const uint32_t lo = min(w[i], w[e]), hi = max(w[i], w[e]);
+                    w[i] = up ? lo : hi;
+                    w[e] = up ? hi : lo;
+                }
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) sk[warp][i * 32 + lane] = w[i];
+    __syncwarp();
+    int n = 0, f0 = 0;   // ids so far; place of the first id of the current unit
+    int place[kN], first[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-        v[i] = make_float2(0.f, 0.f);
-        if (key[i] == kNoId) continue;
-        bool again = false;
-#pragma unroll 8
-        for (int j = 0; j < K; ++j) {
-            const bool same = skey[grp][j] == key[i];
-            const float2 o = sq[grp][j];
-            v[i].x += same ? o.x : 0.f;
-            v[i].y += same ? o.y : 0.f;
-            again |= same && j < i * TPT + tid;
+        const int e = i * 32 + lane;
+        const uint32_t before = e ? sk[warp][e - 1] : kGone;
+        const bool has = w[i] != kGone, lead = has && (e == 0 || before >> 8 != w[i] >> 8);
+        const bool opens = lead && (e == 0 || (before >> 8) / kUnit != (w[i] >> 8) / kUnit);
+        const unsigned bl = __ballot_sync(0xffffffffu, lead), bo = __ballot_sync(0xffffffffu, opens);
+        const unsigned below = (1u << lane) - 1u, upto = below | 1u << lane;
+        place[i] = lead ? n + __popc(bl & below) : -1;
+        const int src = 31 - __clz(bo & upto);   // the lane that opens this entry's unit (-1: an earlier word)
+        first[i] = src >= 0 ? n + __popc(bl & ((1u << src) - 1u)) : f0;
+        const int last = 31 - __clz(bo);
+        if (last >= 0) f0 = n + __popc(bl & ((1u << last) - 1u));
+        n += __popc(bl);
+        if (!lead) continue;
+        const uint32_t id = w[i] >> 8;
+        float2 v = sq[warp][w[i] & 255];
+        for (int j = e + 1; j < kAll && sk[warp][j] >> 8 == id && sk[warp][j] != kGone; ++j) {   // the same id, slots ascending
+            const float2 o = sq[warp][sk[warp][j] & 255];
+            v.x += o.x;
+            v.y += o.y;
         }
-        if (again) key[i] = kNoId;
+        const int64_t at = (int64_t)t * K + place[i];
+        q[at] = v.x;
+        if (h) h[at] = v.y;
+        atomicOr(&smask[warp][first[i]][id % kUnit / 32], 1u << (id & 31));
     }
-    sync();
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-        if (i * TPT + tid < K) skey[grp][i * TPT + tid] = key[i];
-    sync();
-    int place[kN], first[kN];   // ids below its own; ids in units below its own
-    float n = 0.f;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        place[i] = first[i] = 0;
-        if (key[i] == kNoId) continue;
-        n += 1.f;
-#pragma unroll 8
-        for (int j = 0; j < K; ++j) {
-            const int32_t o = skey[grp][j];
-            place[i] += o < key[i];
-            first[i] += o / kUnit < key[i] / kUnit;
-        }
-        atomicOr(&smask[grp][first[i]][key[i] % kUnit / 32], 1u << (key[i] & 31));
-    }
-    sync();
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        if (key[i] == kNoId) continue;
-        const int64_t at = (int64_t)t * K + place[i], u = (int64_t)t * NU + key[i] / kUnit;
-        q[at] = v[i].x;
-        if (h) h[at] = v[i].y;
-        if (place[i] == first[i]) {
-            const uint32_t *b = smask[grp][first[i]];
+        if (place[i] >= 0 && place[i] == first[i]) {
+            const int64_t u = (int64_t)t * NU + (w[i] >> 8) / kUnit;
             tab[u] = (uint16_t)(256 + place[i]);
-            mask[u] = make_uint4(b[0], b[1], b[2], b[3]);
+            mask[u] = *(const uint4 *)smask[warp][first[i]];
         }
-    }
-    if (nent) {
-        n = reduce(n, [](float a, float b) { return a + b; });
-        if (tid == 0) nent[t] = (int)n;
-    }
-    if (coef && tid == 0) coef[t] = m > -inf ? g[t] * scale : 0.f;
+    if (nent && lane == 0) nent[t] = n;
+    if (coef && lane == 0) coef[t] = any ? g[t] * scale : 0.f;
 }
 
 // Log-probability: the row's factor of dz = g s (onehot - p) = coef (p - onehot)
@@ -387,33 +379,47 @@ __global__ void __launch_bounds__(kLargeThreads) k_head_large(int nx, int T, con
 struct Parts {
     int mt, nt, gm, whole, tile, splits;   // the tiling of DX (tile: rows and columns)
 };
-// dX = bf16(sum of the FP32 parts, in order): one part where the tile was
-// taken whole.  T x d, a thread 8 columns of a row (d % 64 == 0).
+// dX = bf16(sum of the FP32 parts): one part where the tile was taken whole.
+// T x d (d % 64 == 0), a thread 4 columns of a row; kS threads share the parts
+// of the same columns, and their sums are added in order.
+template <int kS>
 __global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const float *__restrict__ part,
                                                   uint16_t *__restrict__ out)
 {
+    __shared__ float4 sh[kS > 1 ? 256 : 1];
+    constexpr int kCols = 256 / kS;
+    const int64_t n = (int64_t)T * d, i = (blockIdx.x * (int64_t)kCols + threadIdx.x % kCols) * 4;
+    const int strand = threadIdx.x / kCols;
     grid_wait();
     grid_go();
-    const int64_t n = (int64_t)T * d;
-    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ll) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) {
         const int m = (int)(i / d) / p.tile, c = (int)(i % d) / p.tile, g = m / p.gm;
         const int item = g * p.gm * p.nt + c * min(p.gm, p.mt - g * p.gm) + m - g * p.gm;
         const int parts = item < p.whole ? 1 : p.splits;
-        float4 a = *(const float4 *)(part + i), b = *(const float4 *)(part + i + 4);
 #pragma unroll 4
-        for (int s = 1; s < parts; ++s) {
-            const float4 x = *(const float4 *)(part + s * n + i), y = *(const float4 *)(part + s * n + i + 4);
+        for (int s = strand; s < parts; s += kS) {
+            const float4 x = *(const float4 *)(part + s * n + i);
             a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-            b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
         }
-        *(uint4 *)(out + i) = make_uint4(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w), pack_bf2(b.x, b.y), pack_bf2(b.z, b.w));
     }
+    if constexpr (kS > 1) {
+        sh[threadIdx.x] = a;
+        __syncthreads();
+        if (strand) return;
+#pragma unroll
+        for (int s = 1; s < kS; ++s) {
+            const float4 x = sh[s * kCols + threadIdx.x];
+            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+        }
+    }
+    if (i < n) *(uint2 *)(out + i) = make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
 }
 
 // ------------------------------------------------------------------ plan
 static bool head_ok(const pmoe_head_dims &h)
 {
-    return h.T >= 0 && h.d > 0 && h.d % 64 == 0 && h.d <= 8192 && h.V > 0 && h.V <= (1 << 24) && h.K >= 0 &&
+    return h.T >= 0 && h.d > 0 && h.d % 64 == 0 && h.d <= 8192 && h.V > 0 && h.V < (1 << 24) && h.K >= 0 &&
            h.K <= kMaxK && h.T <= (1 << 24);
 }
 
@@ -468,7 +474,7 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
     if (split && cut) {
         const double part = 2.0 * 128 * t.ctas * t.bn * 4 / 6e6;   // us
         double least = 0;
-        for (int64_t s = 1; s <= std::min<int64_t>(ksteps, 64); ++s) {
+        for (int64_t s = 1; s <= std::min<int64_t>(ksteps, 2 * kSms); ++s) {
             const double us = cdiv(cut * s, slots) * (cdiv(ksteps, s) * 0.28 + 2) + (s > 1 ? cut * s * part + 4 : 0);
             if (s == 1 || us < least) {
                 least = us;
@@ -639,13 +645,15 @@ using Kernel = std::integral_constant<decltype(K), K>;
 static bool launch_teacher(const pmoe_head_dims &h, float scale, const int32_t *idx, const float *t_logits, const float *g,
                            const Ws &w, int *zero, int nzero, cudaStream_t st)
 {
-    const int tpt = h.K <= 32 ? 32 : 128;
     auto launch = [&](auto kern) {
-        return launch_chained<decltype(kern)::value>((unsigned)cdiv(h.T, 128 / tpt), 128, 0, 1, st, h.T, h.V, h.K, scale, idx,
+        return launch_chained<decltype(kern)::value>((unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, h.K, scale, idx,
                                                      t_logits, g, w.q, w.h, w.nent, w.tab, w.mask, (int)cdiv(h.V, kUnit),
                                                      w.coef, zero, nzero, w.err);
     };
-    return tpt == 32 ? launch(Kernel<k_head_teacher<32>>()) : launch(Kernel<k_head_teacher<128>>());
+    return h.K <= 32    ? launch(Kernel<k_head_teacher<1>>())
+           : h.K <= 64  ? launch(Kernel<k_head_teacher<2>>())
+           : h.K <= 128 ? launch(Kernel<k_head_teacher<4>>())
+                        : launch(Kernel<k_head_teacher<8>>());
 }
 
 static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W, float scale, const int32_t *idx,
@@ -767,9 +775,14 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     }
     if (dX && w.dx) {
         const int64_t n = (int64_t)h.T * h.d;
-        if (!launch_chained<k_head_sum>((unsigned)std::min<int64_t>(cdiv(n, 2048), kSms * 8), 256, 0, 1, st, h.T, h.d,
-                            Parts{tx.mt, tx.nt, tx.gm, tx.whole, tx.bn, tx.splits}, w.dx, (uint16_t *)dX))
-            return PMOE_ERR_CUDA;
+        const Parts parts{tx.mt, tx.nt, tx.gm, tx.whole, tx.bn, tx.splits};
+        // (64 parts of 60 x 64: one thread for all parts of its columns takes 10 us)
+        const bool ok = tx.splits >= 16
+                            ? launch_chained<k_head_sum<16>>((unsigned)cdiv(n, 64), 256, 0, 1, st, h.T, h.d, parts, w.dx,
+                                                             (uint16_t *)dX)
+                            : launch_chained<k_head_sum<1>>((unsigned)cdiv(n, 1024), 256, 0, 1, st, h.T, h.d, parts, w.dx,
+                                                            (uint16_t *)dX);
+        if (!ok) return PMOE_ERR_CUDA;
     }
     return PMOE_OK;
 }
