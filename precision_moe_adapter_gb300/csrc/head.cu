@@ -169,11 +169,12 @@ __global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, co
 
 // ------------------------------------------------------------------ combine
 // One CTA per token joins the NU softmax partials in one fixed order, and
-// forms the token's value from the target logits.  Everything stays relative
-// to the largest logit m, in base 2: a log-probability is ln 2 (c z - m -
-// log2 sum), with c z - m in one rounding, so that the value of a confident
-// token keeps its relative accuracy although its logit and lse cancel.
-__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float c,
+// forms the token's value from the target logits.  A partial (m, s) stands for
+// s 2^M with M = c m as rounded; lse = scale m + ln 2 (log2 s + M - c m), whose
+// second term is exact to its own size, and a log-probability is scale z - lse
+// with this lse, the one that the backward is given (scale z as rounded in
+// all three places).
+__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float scale, float c,
                                                       const float2 *__restrict__ part, const float *__restrict__ zt,
                                                       const int32_t *__restrict__ target, const int *__restrict__ nent,
                                                       const float *__restrict__ q, const float *__restrict__ h,
@@ -185,21 +186,16 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     grid_wait();
     grid_go();
     const float2 *p = part + (int64_t)t * NU;
-    float m = ninf, s = 0.f;   // base 2
-#pragma unroll 4
-    for (int i = threadIdx.x; i < NU; i += 128) {
-        const float2 v = p[i];
-        const float n = fmaxf(m, v.x);
-        s = s * exp2f(m - n) + v.y * exp2f(v.x - n);
+    float m = ninf, s = 0.f;
+    auto join = [&](float om, float os) {   // (no partials yet: m = -inf, s = 0)
+        const float n = fmaxf(m, om), N = __fmul_rn(n, c);
+        const float x = m == ninf ? 0.f : s * exp2f(__fmul_rn(m, c) - N);
+        const float y = om == ninf ? 0.f : os * exp2f(__fmul_rn(om, c) - N);
         m = n;
-    }
-    // (a thread without partials has m = -inf, s = 0)
-    auto join = [&](float om, float os) {
-        const float n = fmaxf(m, om);
-        const float a = m == ninf ? 0.f : s * exp2f(m - n), b = om == ninf ? 0.f : os * exp2f(om - n);
-        m = n;
-        s = a + b;
+        s = x + y;
     };
+#pragma unroll 4
+    for (int i = threadIdx.x; i < NU; i += 128) join(p[i].x, p[i].y);
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
@@ -211,9 +207,9 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     m = sw[0].x;
     s = sw[0].y;
     for (int i = 1; i < 4; ++i) join(sw[i].x, sw[i].y);
-    constexpr float kLn2 = 0.6931471805599453f;
-    const float ls = log2f(s);
-    auto logp = [&](float z) { return kLn2 * (fmaf(z, c, -m) - ls); };
+    const float ls = 0.6931471805599453f * (log2f(s) - fmaf(m, c, -__fmul_rn(m, c)));
+    const float l = __fadd_rn(__fmul_rn(m, scale), ls);
+    auto logp = [&](float z) { return __fmul_rn(z, scale) - l; };
     float v = 0.f;
     if (!target) {
         const int n = nent[t];
@@ -230,7 +226,7 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     }
     if (lane == 0) {
         value[t] = v;
-        lse[t] = fmaf(m, kLn2, kLn2 * ls);
+        lse[t] = l;
     }
 }
 
@@ -680,7 +676,7 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
-    return launch_chained<k_head_combine>((unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, a.c, w.part, w.zt, a.target, w.nent, w.q,
+    return launch_chained<k_head_combine>((unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, scale, a.c, w.part, w.zt, a.target, w.nent, w.q,
                           w.h, value, lse, w.err)
                ? PMOE_OK
                : PMOE_ERR_CUDA;
@@ -717,7 +713,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.n0 = v0;
             a.V = h.V;
             a.ksteps = h.d / kBK;
-            a.c = scale * 1.4426950408889634f;
+            a.scale = scale;
             a.target = distill ? nullptr : idx;
             a.tab = w.tab;
             a.mask = w.mask;

@@ -26,8 +26,10 @@
 // run of chunk_of(EPI) K steps is therefore summed in its own TMEM buffer and
 // added to the tile's FP32 sum in registers (round to nearest), which bounds
 // the error at any length.  The forward's values are FP32 outputs: chunks of
-// 512 columns, relative error about 5e-7.  The other results are rounded to
-// BF16, so longer chunks do.  The two buffers alternate, so the tensor cores
+// 512 columns, relative error about 5e-7; GRAD takes the same chunks, so that
+// its logits are the forward's bit for bit and p - 1 of a confident token
+// does not see their error.  The other results are rounded to BF16, so longer
+// chunks do.  The two buffers alternate, so the tensor cores
 // work on the next chunk while one is drained, and on the next tile's first
 // two chunks during the epilogue proper.
 //
@@ -75,7 +77,7 @@ constexpr int kMaxStages = 11;
 static_assert(kMaxStages * (kOpBytes + 1024) <= kRingBytes, "deepest ring");
 constexpr int kWarpOut = 32 * 128;       // a warp's staged output box: 32 rows of 128 bytes
 // K steps summed in one TMEM buffer
-constexpr int chunk_of(int epi) { return epi == HG_FWD ? 8 : epi == HG_GRAD ? 16 : 32; }
+constexpr int chunk_of(int epi) { return epi == HG_FWD || epi == HG_GRAD ? 8 : 32; }
 constexpr int32_t kNoId = 0x7fffffff;
 constexpr float kLarge = 0.25f;          // entries of |p - q| that keep their remainder
 constexpr int kMaxLarge = 8;             // of a token
@@ -99,9 +101,9 @@ struct Args {
     int tail;                // FWD, GRAD, DX: rows of tmAt's boxes, the M % 128 last rows of A
                              // (a box with rows past the tensor's end loads slowly)
     int V;                   // FWD, GRAD: number of vocabulary entries
-    float c;                 // FWD, GRAD: scale * log2(e)
+    float scale, c;          // GRAD: the logits' factor; FWD: that times log2(e)
     int NU;                  // FWD, GRAD: units of the vocabulary
-    float2 *part;            // FWD: [T][NU] (max, sum) in base 2
+    float2 *part;            // FWD: [T][NU] (largest z, sum of 2^(c z - its c z))
     // the target entries of FWD and GRAD: one per token with probability 1
     // (target), or up to K per token, in vocabulary order
     const int32_t *target;   // [T], or NULL
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             // cores work
             uint32_t mw[kUnit / 32] = {0, 0, 0, 0};
             int64_t pos = (int64_t)row * a.K;
-            float l2 = 0.f, cf = 0.f;
+            float lse = 0.f, cf = 0.f;
             if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
                 if (live && a.target) {
                     const int j = a.target[row] - cb;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     }
                 }
                 if (EPI == HG_GRAD && row < a.M) {
-                    l2 = a.lse[row] * 1.4426950408889634f;
+                    lse = a.lse[row];
                     cf = a.coef[row];
                 }
             }
@@ -517,12 +519,12 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 for (int e = 0; e < 4; ++e) mx[e] = acc[e];
 #pragma unroll
                 for (int j = 4; j < kUnit; ++j) mx[j & 3] = fmaxf(mx[j & 3], acc[j]);
-                const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m2 = m * a.c;
                 float sm[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < kUnit; ++j) sm[j & 3] += ex2(fmaf(acc[j], a.c, -m2));
                 if (live)
-                    a.part[(int64_t)row * a.NU + cb / kUnit] = make_float2(m2, (sm[0] + sm[1]) + (sm[2] + sm[3]));
+                    a.part[(int64_t)row * a.NU + cb / kUnit] = make_float2(m, (sm[0] + sm[1]) + (sm[2] + sm[3]));
             } else {
                 // through shared memory (the warp's 32 rows of 128 bytes, 128-byte
                 // swizzle) to TMA stores, which clip rows and columns past the end
@@ -550,11 +552,12 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
 #pragma unroll
                     for (int q = 0; q < kUnit; q += 32) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[q + j] = ex2(fmaf(acc[q + j], a.c, -l2));
+                        for (int j = 0; j < 32; ++j)   // (the difference is exact near p = 1)
+                            acc[q + j] = ex2((__fmul_rn(acc[q + j], a.scale) - lse) * 1.4426950408889634f) * cf;
                         if (__any_sync(0xffffffffu, mw[q / 32] != 0)) {
                             if (a.target) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) acc[q + j] -= mw[q / 32] >> j & 1u ? 1.f : 0.f;
+                                for (int j = 0; j < 32; ++j) acc[q + j] -= mw[q / 32] >> j & 1u ? cf : 0.f;
                             } else {
 #pragma unroll
                                 for (int j0 = 0; j0 < 32; j0 += 8) {   // (eight loads on their way at once)
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                                         if (mw[q / 32] >> (j0 + j) & 1u) v[j] = a.q[pos++];
                                     }
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) acc[q + j0 + j] -= v[j];
+                                    for (int j = 0; j < 8; ++j) acc[q + j0 + j] = fmaf(v[j], -cf, acc[q + j0 + j]);
                                 }
                             }
                         }
@@ -577,16 +580,15 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         float big = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(acc[q + j]));
-                        const bool keep = big >= kLarge && cf != 0.f;
+                        const float least = kLarge * fabsf(cf);
+                        const bool keep = big >= least && cf != 0.f;
                         large[q / 32] = 0;
                         if (__any_sync(0xffffffffu, keep)) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                large[q / 32] |= keep && fabsf(acc[q + j]) >= kLarge ? 1u << j : 0u;
+                                large[q / 32] |= keep && fabsf(acc[q + j]) >= least ? 1u << j : 0u;
                         }
                         any |= large[q / 32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[q + j] *= cf;
                         // a row without gradient stays zero, whatever its hidden state holds
                         if (__any_sync(0xffffffffu, cf == 0.f)) {
 #pragma unroll
