@@ -401,7 +401,8 @@ pmoe_status adapter_cayley_grad(int32_t nblk, int32_t b, const float *S, const f
  *   scale  factor of every logit, 1 / temperature: finite and > 0
  * A token's forward results do not depend on the other tokens of the call
  * (bit-identical across T), and every result is run-to-run identical.
- * The sums over d run in FP32 chunks of 512 columns added in FP32.
+ * The sums over d run in FP32 chunks of 512 columns added in FP32; the logits
+ * of the target, or of teacher entries with q >= 1/4, are FP32 dot products.
  */
 typedef struct {
     int32_t T, d, V, K;
@@ -430,8 +431,8 @@ pmoe_status head_logprob_forward(pmoe_head_dims dims, const void *X, const void 
 /*
  * head_logprob_backward -- for upstream gradients g_t = dL/dlogp_t:
  *   G_tv = g_t scale ([v = y_t] - p_tv);  dX = bf16(G W);  dW = bf16(G^T X)
- * G enters both products in BF16, its large entries (|[v = y] - p| >= 1/4)
- * as two BF16 terms (16 bits); the sums are FP32.
+ * G enters both products in BF16, its large entries (|[v = y] - p| >=
+ * (1 - p_y) / 4) as two BF16 terms (16 bits); the sums are FP32.
  *   lse    f32 [T] from the forward       g   f32 [T] (in)
  *   dX     bf16 [T, d] or NULL (out)      dW  bf16 [V, d] or NULL (out,
  *          overwritten; NULL: the head is frozen); one of them is needed
@@ -462,7 +463,8 @@ pmoe_status head_distill_forward(pmoe_head_dims dims, const void *X, const void 
 /*
  * head_distill_backward -- for upstream gradients g_t = dL/dloss_t:
  *   G_tv = g_t scale (p_tv - sum_{k: idx_k = v} q_k)   (0 without entries)
- * and dX, dW as in head_logprob_backward.
+ * and dX, dW as in head_logprob_backward (entries of G with |p - q| >= 1/4 in
+ * 16 bits).
  */
 pmoe_status head_distill_backward(pmoe_head_dims dims, const void *X, const void *W, float scale,
                                   const int32_t *t_idx, const float *t_logits, const float *lse,

@@ -16,6 +16,48 @@ constexpr int kMaxK = 256;                    // teacher entries per token
 constexpr int kSms = 152;                     // SMs of a GB300
 constexpr int64_t kPieceBytes = 512ll << 20;  // most bytes of G of a vocabulary piece
 
+constexpr int kAnchors = 4;
+constexpr float kAnchorQ = 0.25f;
+// A token's anchors, [T][kAnchors]: vocabulary id (-1: none), place among the
+// token's entries, entry of G
+struct Anchors {
+    int32_t *id;
+    int *place;
+    float *g;
+};
+// What k_head_teacher needs in the backward (coef NULL: forward)
+struct TeacherGrad {
+    const uint16_t *X, *W;
+    int d;
+    const float *lse, *g;
+    float2 *coef;            // [T] factor of G, and least |G| of an entry that keeps its remainder
+};
+
+// x . w over d columns by a warp: exact products of BF16 rows, 8 columns a lane
+// at a time, then a tree.  The order is fixed, so forward and backward agree.
+__device__ __forceinline__ float row_dot(const uint16_t *__restrict__ x, const uint16_t *__restrict__ w, int d)
+{
+    float a = 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < d / 8; i += 32) {
+        const uint4 u = ((const uint4 *)x)[i], v = ((const uint4 *)w)[i];
+        const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a = fmaf(bf2f((uint16_t)us[j]), bf2f((uint16_t)vs[j]), a);
+            a = fmaf(bf2f((uint16_t)(us[j] >> 16)), bf2f((uint16_t)(vs[j] >> 16)), a);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+}
+// p - q of an entry with logit z
+__device__ __forceinline__ float p_minus_q(float z, float scale, float lse, float q)
+{
+    return expm1f(__fmul_rn(z, scale) - lse) + (1.f - q);
+}
+
 // ------------------------------------------------------------------ targets
 // The backward's first kernel also clears the counters of its first piece.
 __device__ __forceinline__ void clear(int *p, int n)
@@ -36,10 +78,10 @@ __device__ __forceinline__ void clear(int *p, int n)
 constexpr uint32_t kGone = 0xFFFFFFFFu;   // (V < 2^24: no id reaches it)
 template <int kN>
 __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float scale, const int32_t *__restrict__ t_idx,
-                                                      const float *__restrict__ t_logits, const float *__restrict__ g,
+                                                      const float *__restrict__ t_logits,
                                                       float *__restrict__ q, float *__restrict__ h,
                                                       int *__restrict__ nent, uint16_t *__restrict__ tab,
-                                                      uint4 *__restrict__ mask, int NU, float *__restrict__ coef,
+                                                      uint4 *__restrict__ mask, int NU, Anchors an, TeacherGrad b,
                                                       int *__restrict__ zero, int nzero, DevErr *err)
 {
     constexpr int kAll = 32 * kN;
@@ -74,10 +116,6 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
     }
     for (int u = lane; u < NU; u += 32) tab[(int64_t)t * NU + u] = 0;
     float s = 0.f;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) any |= w[i] != kGone;
-    any = __any_sync(0xffffffffu, any);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
@@ -112,6 +150,7 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
     for (int i = 0; i < kN; ++i) sk[warp][i * 32 + lane] = w[i];
     __syncwarp();
     int n = 0, f0 = 0;   // ids so far; place of the first id of the current unit
+    int na = 0;          // anchors so far
     int place[kN], first[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -127,19 +166,36 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
         const int last = 31 - __clz(bo);
         if (last >= 0) f0 = n + __popc(bl & ((1u << last) - 1u));
         n += __popc(bl);
-        if (!lead) continue;
         const uint32_t id = w[i] >> 8;
-        float2 v = sq[warp][w[i] & 255];
-        for (int j = e + 1; j < kAll && sk[warp][j] >> 8 == id && sk[warp][j] != kGone; ++j) {   // the same id, slots ascending
-            const float2 o = sq[warp][sk[warp][j] & 255];
-            v.x += o.x;
-            v.y += o.y;
+        float2 v = make_float2(0.f, 0.f);
+        if (lead) {
+            v = sq[warp][w[i] & 255];
+            for (int j = e + 1; j < kAll && sk[warp][j] >> 8 == id && sk[warp][j] != kGone; ++j) {   // the same id, slots ascending
+                const float2 o = sq[warp][sk[warp][j] & 255];
+                v.x += o.x;
+                v.y += o.y;
+            }
+            const int64_t at = (int64_t)t * K + place[i];
+            q[at] = v.x;
+            if (h) h[at] = v.y;
+            atomicOr(&smask[warp][first[i]][id % kUnit / 32], 1u << (id & 31));
         }
-        const int64_t at = (int64_t)t * K + place[i];
-        q[at] = v.x;
-        if (h) h[at] = v.y;
-        atomicOr(&smask[warp][first[i]][id % kUnit / 32], 1u << (id & 31));
+        const unsigned ba = __ballot_sync(0xffffffffu, v.x >= kAnchorQ);
+        const int slot = na + __popc(ba & below);
+        if (v.x >= kAnchorQ && slot < kAnchors) {
+            an.id[t * kAnchors + slot] = (int32_t)id;
+            an.place[t * kAnchors + slot] = place[i];
+        }
+        for (unsigned m2 = b.coef ? ba : 0u; m2; m2 &= m2 - 1) {   // backward: the anchors' entries of G
+            const int src = __ffs(m2) - 1, sl = na + __popc(ba & ((1u << src) - 1u));
+            const int aid = __shfl_sync(0xffffffffu, (int)id, src);
+            const float aq = __shfl_sync(0xffffffffu, v.x, src);
+            const float z = row_dot(b.X + (int64_t)t * b.d, b.W + (int64_t)aid * b.d, b.d);
+            if (lane == 0 && sl < kAnchors) an.g[t * kAnchors + sl] = b.g[t] * scale * p_minus_q(z, scale, b.lse[t], aq);
+        }
+        na += __popc(ba);
     }
+    if (lane >= na && lane < kAnchors) an.id[t * kAnchors + lane] = -1;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kN; ++i)
@@ -148,23 +204,40 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
             tab[u] = (uint16_t)(256 + place[i]);
             mask[u] = *(const uint4 *)smask[warp][first[i]];
         }
-    if (nent && lane == 0) nent[t] = n;
-    if (coef && lane == 0) coef[t] = any ? g[t] * scale : 0.f;
+    if (lane == 0) {
+        nent[t] = n;
+        if (b.coef) {
+            const float cf = n ? b.g[t] * scale : 0.f;
+            b.coef[t] = make_float2(cf, kLarge * fabsf(cf));
+        }
+    }
 }
 
-// Log-probability: the row's factor of dz = g s (onehot - p) = coef (p - onehot)
-__global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, const int32_t *__restrict__ target,
-                                                   const float *__restrict__ g, float *__restrict__ coef,
-                                                   int *__restrict__ zero, int nzero, DevErr *err)
+// Log-probability, backward, a warp per token: G = coef (p - onehot) with coef =
+// -g s (0: no target), its entry at the target, and the least entry that keeps
+// its remainder.
+__global__ void __launch_bounds__(128) k_head_target(int T, int V, int d, float scale, const uint16_t *__restrict__ X,
+                                                     const uint16_t *__restrict__ W, const int32_t *__restrict__ target,
+                                                     const float *__restrict__ lse, const float *__restrict__ g,
+                                                     float2 *__restrict__ coef, Anchors an, int *__restrict__ zero,
+                                                     int nzero, DevErr *err)
 {
-    const int t = blockIdx.x * 256 + threadIdx.x;
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     grid_wait();
     grid_go();
     clear(zero, nzero);
     if (t >= T) return;
     const int y = target[t];
-    if (y >= V) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
-    coef[t] = y >= 0 && y < V ? -g[t] * scale : 0.f;
+    const bool has = y >= 0 && y < V;
+    const float z = has ? row_dot(X + (int64_t)t * d, W + (int64_t)y * d, d) : 0.f;
+    if (y >= V && lane == 0) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
+    const float cf = has ? -g[t] * scale : 0.f, e = has ? p_minus_q(z, scale, lse[t], 1.f) : 0.f;
+    if (lane < kAnchors) {
+        an.id[t * kAnchors + lane] = lane == 0 && has ? y : -1;
+        an.g[t * kAnchors + lane] = lane == 0 ? cf * e : 0.f;
+    }
+    // (not below 1e-4, where 1 - p_y is no longer a bound for the other entries as computed)
+    if (lane == 0) coef[t] = make_float2(cf, kLarge * fminf(fmaxf(fabsf(e), 1e-4f), 1.f) * fabsf(cf));
 }
 
 // ------------------------------------------------------------------ combine
@@ -173,19 +246,43 @@ __global__ void __launch_bounds__(256) k_head_coef(int T, int V, float scale, co
 // s 2^M with M = c m as rounded; lse = scale m + ln 2 (log2 s + M - c m), whose
 // second term is exact to its own size, and a log-probability is scale z - lse
 // with this lse, the one that the backward is given (scale z as rounded in
-// all three places).
-__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, float scale, float c,
+// all three places).  The anchors' terms of the sum are replaced by those of
+// their logits computed again.
+__global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, int d, float scale, float c,
+                                                      const uint16_t *__restrict__ X, const uint16_t *__restrict__ W,
                                                       const float2 *__restrict__ part, const float *__restrict__ zt,
                                                       const int32_t *__restrict__ target, const int *__restrict__ nent,
                                                       const float *__restrict__ q, const float *__restrict__ h,
-                                                      float *__restrict__ value, float *__restrict__ lse, DevErr *err)
+                                                      Anchors an, float *__restrict__ value, float *__restrict__ lse,
+                                                      DevErr *err)
 {
     __shared__ float2 sw[4];
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float sz[kAnchors];
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float ninf = -__int_as_float(0x7f800000);
+    // (before the wait: all of this was complete when the GEMM before started)
+    int id[kAnchors] = {-1, -1, -1, -1}, place[kAnchors] = {0, 0, 0, 0};
+    if (target) {
+        const int y = target[t];
+        if (y >= V && threadIdx.x == 0) record_error(err, PMOE_ERR_BAD_INDEX, (int)t, y);
+        if (y >= 0 && y < V) id[0] = y;
+    } else {
+#pragma unroll
+        for (int n = 0; n < kAnchors; ++n) {
+            id[n] = __ldcg(an.id + t * kAnchors + n);
+            if (id[n] >= 0) place[n] = __ldcg(an.place + t * kAnchors + n);
+        }
+    }
+    static_assert(kAnchors == 4, "an anchor for each of the CTA's warps");
+    const int mine = warp == 0 ? id[0] : warp == 1 ? id[1] : warp == 2 ? id[2] : id[3];
+    if (mine >= 0) {
+        const float z = row_dot(X + t * d, W + (int64_t)mine * d, d);
+        if (lane == 0) sz[warp] = z;
+    }
     grid_wait();
     grid_go();
-    const float2 *p = part + (int64_t)t * NU;
+    const float2 *p = part + t * NU;
     float m = ninf, s = 0.f;
     auto join = [&](float om, float os) {   // (no partials yet: m = -inf, s = 0)
         const float n = fmaxf(m, om), N = __fmul_rn(n, c);
@@ -204,9 +301,27 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     if (lane == 0) sw[warp] = make_float2(m, s);
     __syncthreads();
     if (warp) return;
+    const float za[kAnchors] = {sz[0], sz[1], sz[2], sz[3]};   // (only where id >= 0)
     m = sw[0].x;
     s = sw[0].y;
     for (int i = 1; i < 4; ++i) join(sw[i].x, sw[i].y);
+    if (id[0] >= 0) {   // (where an anchor has the largest logit, the sum is taken relative to its new one)
+        const float M = __fmul_rn(m, c);
+        float rest = s, top = m;
+#pragma unroll
+        for (int n = 0; n < kAnchors; ++n)
+            if (id[n] >= 0) {
+                const float z = zt[t * K + place[n]];
+                rest -= exp2f(fmaf(z, c, -M));
+                if (z == m) top = za[n];
+            }
+        const float N = __fmul_rn(top, c);
+        s = fmaxf(rest, 0.f) * exp2f(M - N);
+#pragma unroll
+        for (int n = 0; n < kAnchors; ++n)
+            if (id[n] >= 0) s += exp2f(fmaf(za[n], c, -N));
+        m = top;
+    }
     const float ls = 0.6931471805599453f * (log2f(s) - fmaf(m, c, -__fmul_rn(m, c)));
     const float l = __fadd_rn(__fmul_rn(m, scale), ls);
     auto logp = [&](float z) { return __fmul_rn(z, scale) - l; };
@@ -214,15 +329,17 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, floa
     if (!target) {
         const int n = nent[t];
         for (int k = lane; k < n; k += 32) {
-            const int64_t at = (int64_t)t * K + k;
-            v += h[at] - q[at] * logp(zt[at]);
+            const int64_t at = t * K + k;
+            float z = zt[at];
+#pragma unroll
+            for (int e = 0; e < kAnchors; ++e)
+                if (id[e] >= 0 && place[e] == k) z = za[e];
+            v += h[at] - q[at] * logp(z);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    } else {
-        const int y = target[t];
-        if (y >= 0 && y < V) v = logp(zt[t]);
-        else if (y >= V && lane == 0) record_error(err, PMOE_ERR_BAD_INDEX, t, y);
+    } else if (id[0] >= 0) {
+        v = logp(za[0]);
     }
     if (lane == 0) {
         value[t] = v;
@@ -496,7 +613,8 @@ struct Ws {
     uint4 *mask;             // [T][NU]
     float *zt;               // [T][max(K, 1)]
     float2 *part;            // [T][NU]
-    float *coef;             // [T]
+    Anchors an;
+    float2 *coef;            // [T] factor and least large entry of G
     uint16_t *G;             // [T][piece]
     // G's large entries: per token, then as the extra K steps of DX and DW
     int *cnt;                // [T], then the step counter and the flags: zeroed per piece
@@ -526,15 +644,18 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
     w.q = (float *)take(T * K * 4);
     w.tab = (uint16_t *)take(K ? T * cdiv(h.V, kUnit) * 2 : 0);
     w.mask = (uint4 *)take(K ? T * cdiv(h.V, kUnit) * 16 : 0);
+    w.nent = (int *)take(K ? T * 4 : 0);
+    w.an.id = (int32_t *)take(T * kAnchors * 4);
+    w.an.place = (int *)take(T * kAnchors * 4);
     if (op == PMOE_HEAD_FORWARD) {
         w.h = (float *)take(T * K * 4);
-        w.nent = (int *)take(K ? T * 4 : 0);
         w.zt = (float *)take(T * std::max<size_t>(K, 1) * 4);
         w.part = (float2 *)take(T * cdiv(h.V, kUnit) * 8);
     } else {
         const int piece = piece_of(h.T, h.V);
         const Tiling t = dx_tiling(h);
-        w.coef = (float *)take(T * 4);
+        w.coef = (float2 *)take(T * 8);
+        w.an.g = (float *)take(T * kAnchors * 4);
         w.G = (uint16_t *)take(T * piece * 2);
         const int blocks[2] = {(int)cdiv(h.T, kListRows), piece / kListRows};
         w.fs = (int)cdiv(h.T, 128);
@@ -638,13 +759,13 @@ static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CU
 template <auto K>
 using Kernel = std::integral_constant<decltype(K), K>;
 
-static bool launch_teacher(const pmoe_head_dims &h, float scale, const int32_t *idx, const float *t_logits, const float *g,
-                           const Ws &w, int *zero, int nzero, cudaStream_t st)
+static bool launch_teacher(const pmoe_head_dims &h, float scale, const int32_t *idx, const float *t_logits, const Ws &w,
+                           const TeacherGrad &b, int *zero, int nzero, cudaStream_t st)
 {
     auto launch = [&](auto kern) {
         return launch_chained<decltype(kern)::value>((unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, h.K, scale, idx,
-                                                     t_logits, g, w.q, w.h, w.nent, w.tab, w.mask, (int)cdiv(h.V, kUnit),
-                                                     w.coef, zero, nzero, w.err);
+                                                     t_logits, w.q, w.h, w.nent, w.tab, w.mask, (int)cdiv(h.V, kUnit),
+                                                     w.an, b, zero, nzero, w.err);
     };
     return h.K <= 32    ? launch(Kernel<k_head_teacher<1>>())
            : h.K <= 64  ? launch(Kernel<k_head_teacher<2>>())
@@ -657,7 +778,7 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
 {
     const int K = distill ? h.K : 1;
     if (distill) {
-        if (!launch_teacher(h, scale, idx, t_logits, nullptr, w, nullptr, 0, st)) return PMOE_ERR_CUDA;
+        if (!launch_teacher(h, scale, idx, t_logits, w, TeacherGrad{}, nullptr, 0, st)) return PMOE_ERR_CUDA;
     }
     Args a{};
     a.M = h.T;
@@ -676,8 +797,8 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
-    return launch_chained<k_head_combine>((unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, scale, a.c, w.part, w.zt, a.target, w.nent, w.q,
-                          w.h, value, lse, w.err)
+    return launch_chained<k_head_combine>((unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, h.d, scale, a.c, (const uint16_t *)X,
+                          (const uint16_t *)W, w.part, w.zt, a.target, w.nent, w.q, w.h, w.an, value, lse, w.err)
                ? PMOE_OK
                : PMOE_ERR_CUDA;
 }
@@ -688,10 +809,12 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
 {
     const int K = distill ? h.K : 1;
     const int nzero = (int)(w.zero_bytes / 4);
+    // (this kernel clears the counters of the first piece)
+    const uint16_t *x = (const uint16_t *)X, *wt = (const uint16_t *)W;
     const bool made =
-        distill ? launch_teacher(h, scale, idx, t_logits, g, w, w.cnt, nzero, st)
-                : launch_chained<k_head_coef>((unsigned)cdiv(h.T, 256), 256, 0, 1, st, h.T, h.V, scale, idx, g, w.coef,
-                                 w.cnt, nzero, w.err);
+        distill ? launch_teacher(h, scale, idx, t_logits, w, TeacherGrad{x, wt, h.d, lse, g, w.coef}, w.cnt, nzero, st)
+                : launch_chained<k_head_target>((unsigned)cdiv(h.T, 4), 128, 0, 1, st, h.T, h.V, h.d, scale, x, wt, idx, lse, g,
+                                                w.coef, w.an, w.cnt, nzero, w.err);
     if (!made) return PMOE_ERR_CUDA;
     const int piece = piece_of(h.T, h.V);
     const Tiling tx = dx_tiling(h);
@@ -722,6 +845,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.K = K;
             a.lse = lse;
             a.coef = w.coef;
+            a.anchor = (const int4 *)w.an.id;
+            a.anchor_g = (const float4 *)w.an.g;
             if (!make_map(&mo, w.G, false, ldg, h.T, 1, 64, 32) ||
                 !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo,
                                  nullptr, a, st))

@@ -36,13 +36,21 @@
 // G is the BF16 operand of two products.  Where a token's distribution is
 // concentrated, a few large entries of G carry the whole gradient, and their
 // rounding to 8 bits would be its error.  GRAD lists the entries with
-// |p - q| >= kLarge (a token has at most 8, as sum |p - q| <= 2), and the
-// products run extra K steps of 64 such entries each on the roundings'
+// |p - q| >= kLarge (a token has at most 8, as sum |p - q| <= 2; with a single
+// target y, |p - q| >= kLarge (1 - p_y): at most 5), and the products run
+// extra K steps of 64 such entries each on the roundings'
 // remainders (a second BF16, 16 bits together): A holds one remainder per
 // column (built by head.cu, one list per 256 output rows), B the matching
 // rows of W or X, gathered by TMA.  That is one or two steps per tile of the
 // hundreds the product has; remainders of whole tiles would double the
 // steps of every tile that holds a large entry.
+//
+// Anchors: where a token's target (or an entry of the teacher) holds much of
+// the probability, the value and G there are differences of nearly equal
+// numbers, and the tensor cores' error of z (5e-7 relative, biased) would be
+// 1e-6 and more of them.  The logits of the target, or of teacher entries
+// with q >= 1/4 (at most 4), are therefore computed again in FP32 by head.cu,
+// which corrects the sums of the forward and gives GRAD these entries of G.
 //
 // Every element's sum runs over k in the same order whatever the tile shape,
 // and the softmax partials cover 128 aligned columns: the results do not
@@ -113,7 +121,10 @@ struct Args {
     float *zt;               // FWD: [T][K] raw logits of the entries (out)
     int K;
     const float *lse;        // GRAD: [T]
-    const float *coef;       // GRAD: [T] factor of the row (0: no gradient)
+    const float2 *coef;      // GRAD: [T] factor of the row (0: no gradient) and least |G| of an
+                             // entry that keeps its remainder
+    const int4 *anchor;      // GRAD: [T] vocabulary ids of the row's anchors (-1: none) and
+    const float4 *anchor_g;  // their entries of G
     int *cnt;                // GRAD: [T] large entries of each token, listed in
     int2 *large;             // [T][kMaxLarge] as (vocabulary column - n0, remainder)
     uint8_t *fl;             // GRAD: [vocabulary block of 256][fs] 1 where a block of 128
@@ -437,10 +448,13 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             // cores work
             uint32_t mw[kUnit / 32] = {0, 0, 0, 0};
             int64_t pos = (int64_t)row * a.K;
-            float lse = 0.f, cf = 0.f;
+            float lse = 0.f;
+            float2 cf = make_float2(0.f, 0.f);   // factor, least large entry
+            int an[4] = {-1, -1, -1, -1};        // anchors and their entries of G
+            float ag[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
-                if (live && a.target) {
-                    const int j = a.target[row] - cb;
+                if (live && a.target) {   // (GRAD: an anchor)
+                    const int j = EPI == HG_FWD ? a.target[row] - cb : -1;
                     if (j >= 0 && j < nv) {
 #pragma unroll
                         for (int e = 0; e < kUnit / 32; ++e) mw[e] = j >> 5 == e ? 1u << (j & 31) : 0u;
@@ -457,6 +471,10 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 if (EPI == HG_GRAD && row < a.M) {
                     lse = a.lse[row];
                     cf = a.coef[row];
+                    const int4 i4 = a.anchor[row];
+                    const float4 g4 = a.anchor_g[row];
+                    an[0] = i4.x, an[1] = i4.y, an[2] = i4.z, an[3] = i4.w;
+                    ag[0] = g4.x, ag[1] = g4.y, ag[2] = g4.z, ag[3] = g4.w;
                 }
             }
             float acc[kUnit];
@@ -553,23 +571,29 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     for (int q = 0; q < kUnit; q += 32) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)   // (the difference is exact near p = 1)
-                            acc[q + j] = ex2((__fmul_rn(acc[q + j], a.scale) - lse) * 1.4426950408889634f) * cf;
+                            acc[q + j] = ex2((__fmul_rn(acc[q + j], a.scale) - lse) * 1.4426950408889634f) * cf.x;
                         if (__any_sync(0xffffffffu, mw[q / 32] != 0)) {
-                            if (a.target) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) acc[q + j] -= mw[q / 32] >> j & 1u ? cf : 0.f;
-                            } else {
+                            for (int j0 = 0; j0 < 32; j0 += 8) {   // (eight loads on their way at once)
+                                float v[8];
 #pragma unroll
-                                for (int j0 = 0; j0 < 32; j0 += 8) {   // (eight loads on their way at once)
-                                    float v[8];
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) {
-                                        v[j] = 0.f;
-                                        if (mw[q / 32] >> (j0 + j) & 1u) v[j] = a.q[pos++];
-                                    }
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) acc[q + j0 + j] = fmaf(v[j], -cf, acc[q + j0 + j]);
+                                for (int j = 0; j < 8; ++j) {
+                                    v[j] = 0.f;
+                                    if (mw[q / 32] >> (j0 + j) & 1u) v[j] = a.q[pos++];
                                 }
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) acc[q + j0 + j] = fmaf(v[j], -cf.x, acc[q + j0 + j]);
+                            }
+                        }
+                        const int e0 = cb + q;
+                        auto in = [&](int id) { return (unsigned)(id - e0) < 32u; };
+                        if (__any_sync(0xffffffffu, in(an[0]) || in(an[1]) || in(an[2]) || in(an[3]))) {
+#pragma unroll 1
+                            for (int n = 0; n < 4; ++n) {
+                                const int j0 = (n == 0 ? an[0] : n == 1 ? an[1] : n == 2 ? an[2] : an[3]) - e0;
+                                const float gv = n == 0 ? ag[0] : n == 1 ? ag[1] : n == 2 ? ag[2] : ag[3];
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) acc[q + j] = j == j0 ? gv : acc[q + j];
                             }
                         }
                         if (nv < kUnit) {
@@ -580,19 +604,18 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         float big = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(acc[q + j]));
-                        const float least = kLarge * fabsf(cf);
-                        const bool keep = big >= least && cf != 0.f;
+                        const bool keep = big >= cf.y && cf.x != 0.f;
                         large[q / 32] = 0;
                         if (__any_sync(0xffffffffu, keep)) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                large[q / 32] |= keep && fabsf(acc[q + j]) >= least ? 1u << j : 0u;
+                                large[q / 32] |= keep && fabsf(acc[q + j]) >= cf.y ? 1u << j : 0u;
                         }
                         any |= large[q / 32];
                         // a row without gradient stays zero, whatever its hidden state holds
-                        if (__any_sync(0xffffffffu, cf == 0.f)) {
+                        if (__any_sync(0xffffffffu, cf.x == 0.f)) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) acc[q + j] = cf == 0.f ? 0.f : acc[q + j];
+                            for (int j = 0; j < 32; ++j) acc[q + j] = cf.x == 0.f ? 0.f : acc[q + j];
                         }
                         if (q & 32) {
                             reuse();

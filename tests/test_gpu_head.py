@@ -267,3 +267,38 @@ def test_ignored_tokens_may_hold_anything():
         out.append((loss, dX))
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
     assert torch.all(out[1][0][off] == 0) and torch.all(out[1][1][off] == 0)
+
+
+@pytest.mark.parametrize("T,d,V,K", [(1, 2048, 4000, 0), (40, 7168, 300, 0), (300, 512, 5003, 0), (33, 2048, 1003, 5)])
+def test_confident_tokens_keep_fp32_accuracy(T, d, V, K):
+    """Where the target holds most of the probability its logit is 10 to 20,
+    and the tensor cores' biased sums would be off by 1e-5 of it.  The value
+    is the difference of two FP32 numbers of that size (half a unit each, and
+    the FP32 dot product's few units): within 2^-21 (1 + |lse|).  p - 1 has
+    the same absolute error, so a token's row of dX is within 2^-21 (1 + |lse|)
+    of |g s| times the rows of W that carry it, besides the BF16 rounding."""
+    X, W, y, up, g = make(T, d, V, seed=5, lean=0.0)
+    X = (0.05 * X.float() + (10 + 10 * torch.rand((T, 1), generator=g, device="cuda")) * W[y.long()].float()
+         / W[y.long()].float().square().sum(1, keepdim=True)).to(torch.bfloat16)
+    Q = torch.zeros((T, V), dtype=D, device="cuda")
+    if K:
+        ids = torch.cat([y[:, None], torch.randint(0, V, (T, K - 1), generator=g, device="cuda")], 1).to(torch.int32).contiguous()
+        t = torch.randn((T, K), generator=g, device="cuda")
+        t[:, 0] += 9
+        q = torch.softmax(t.to(D), 1)
+        Q.scatter_add_(1, ids.long(), q)
+        h = DeviceHead(W, T, K=K)
+        val, lse, dX = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(X)
+        h.distill(X, ids, t, val, lse)
+        h.distill_backward(X, ids, t, lse, up, dX)
+        rlse, rv, rdX, _ = reference(X, W, 1.0, Q, torch.xlogy(q, q).sum(1), up, 1.0)
+    else:
+        _, val, lse, dX, _ = run_logprob(X, W, y, up, 1.0, dW=False)
+        Q[torch.arange(T, device="cuda"), y.long()] = 1
+        rlse, rv, rdX, _ = reference(X, W, 1.0, Q, 0.0, up, -1.0)
+    tol = 2.0 ** -21 * (1 + rlse.abs())
+    assert torch.all((lse.to(D) - rlse).abs() <= tol), ((lse.to(D) - rlse).abs() / tol).max()
+    assert torch.all((val.to(D) - rv).abs() <= tol), ((val.to(D) - rv).abs() / tol).max()
+    err = (dX.to(D) - rdX).norm(dim=1)
+    row = up.to(D).abs() * W.to(D).norm(dim=1).max()
+    assert torch.all(err <= 2.0 ** -8 * rdX.norm(dim=1) + 2 * tol * row), (err / row).max()
