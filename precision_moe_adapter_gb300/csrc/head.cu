@@ -549,6 +549,21 @@ static int piece_of(int T, int V)
     return (int)(cdiv(cdiv(V, np), 256) * 256);
 }
 
+// Whether G's remainders are kept in whole (2 terms) instead of in lists: for
+// small vocabularies, where a block of 256 entries has long lists.  With about
+// 2.5 large entries a token, the lists lengthen K by 640 / V and DW's take one
+// CTA 0.33 us for every 64 entries of its block; two terms double K and write G
+// twice.  (Forward and both gradients, two terms against lists: T = 4013, d = 192,
+// V = 263 45 against 151 us; T = 8000, d = 128, V = 1500 86 against 131.)
+static int terms_of(const pmoe_head_dims &h)
+{
+    const int piece = piece_of(h.T, h.V);
+    if (piece < h.V || 4ll * h.T * piece > kPieceBytes) return 1;
+    const double tv = (double)h.T * h.V, mma = 4 * tv * h.d / 1.5e9;   // us
+    const double lists = 0.33 * h.T * 2.5 * 256 / (64.0 * h.V) + mma * 640 / h.V, twice = mma + tv * 2 / 5e6;
+    return twice < lists ? 2 : 1;
+}
+
 struct Tiling {
     int ctas, bn;
     int mt, nt, gm;      // gm: m tiles that run together
@@ -602,7 +617,7 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
 }
 static Tiling dx_tiling(const pmoe_head_dims &h)
 {
-    return tiling(h.T, h.d, cdiv(std::min(piece_of(h.T, h.V), h.V), kBK), true);
+    return tiling(h.T, h.d, cdiv(std::min(piece_of(h.T, h.V), h.V), kBK) * terms_of(h), true);
 }
 
 struct Ws {
@@ -615,7 +630,8 @@ struct Ws {
     float2 *part;            // [T][NU]
     Anchors an;
     float2 *coef;            // [T] factor and least large entry of G
-    uint16_t *G;             // [T][piece]
+    int terms;
+    uint16_t *G;             // [T][terms][piece]
     // G's large entries: per token, then as the extra K steps of DX and DW
     int *cnt;                // [T], then the step counter and the flags: zeroed per piece
     uint8_t *fl;             // [piece / 256][fs]
@@ -656,7 +672,8 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
         const Tiling t = dx_tiling(h);
         w.coef = (float2 *)take(T * 8);
         w.an.g = (float *)take(T * kAnchors * 4);
-        w.G = (uint16_t *)take(T * piece * 2);
+        w.terms = terms_of(h);
+        w.G = (uint16_t *)take(T * piece * w.terms * 2);
         const int blocks[2] = {(int)cdiv(h.T, kListRows), piece / kListRows};
         w.fs = (int)cdiv(h.T, 128);
         w.zero_bytes = (T * 4 + 4 + (size_t)blocks[1] * w.fs + 3) & ~(size_t)3;
@@ -820,9 +837,11 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     const Tiling tx = dx_tiling(h);
     for (int v0 = 0; v0 < h.V; v0 += piece) {
         const int vc = std::min(piece, h.V - v0);
-        const int64_t ldg = piece;
+        const int64_t ldg = (int64_t)piece * w.terms;
         CUtensorMap mo;
         Args b{};   // what the piece's products share
+        b.terms = w.terms;
+        b.aoff = piece;
         b.cnt = w.cnt;
         b.large = w.large;
         b.fl = dW ? w.fl : nullptr;
@@ -832,7 +851,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
         {   // G = coef (softmax(Z) - q) of this piece
             Args a = b;
             a.M = h.T;
-            a.N = (int)ldg;
+            a.N = piece;
             a.n0 = v0;
             a.V = h.V;
             a.ksteps = h.d / kBK;
@@ -855,14 +874,16 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
         const int nx = dX ? (int)cdiv(h.T, kListRows) : 0, nw = dW ? (int)cdiv(vc, kListRows) : 0;
         // a block of tokens takes 256 threads; blocks of the vocabulary look at all tokens, four a thread
         const unsigned threads = nw == 0 || h.T <= 4 * kListRows ? kListRows : kLargeThreads;
-        if (!launch_chained<k_head_large>((unsigned)(nx + nw), threads, 0, 1, st, nx, h.T, w.cnt, w.large, w.fl, w.fs, w.steps,
+        if (w.terms == 1 &&
+            !launch_chained<k_head_large>((unsigned)(nx + nw), threads, 0, 1, st, nx, h.T, w.cnt, w.large, w.fl, w.fs, w.steps,
                             w.lists[0], w.lidx[0], w.lo[0], w.lists[1], w.lidx[1], w.lo[1]))
             return PMOE_ERR_CUDA;
         if (dX) {
             Args a = b;
             a.M = h.T;
             a.N = h.d;
-            a.ksteps = (int)cdiv(vc, kBK);
+            a.kone = (int)cdiv(vc, kBK);
+            a.ksteps = a.kone * w.terms;
             a.kb0 = v0;
             a.bf16_out = w.dx == nullptr;
             a.accumulate = v0 > 0;
@@ -883,7 +904,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             Args a = b;
             a.M = vc;
             a.N = h.d;
-            a.ksteps = (int)cdiv(h.T, kBK);
+            a.kone = (int)cdiv(h.T, kBK);
+            a.ksteps = a.kone * w.terms;
             a.beside = dX != nullptr;
             a.lists = w.lists[1];
             a.lidx = w.lidx[1];

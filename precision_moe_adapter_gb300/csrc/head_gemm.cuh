@@ -43,7 +43,9 @@
 // column (built by head.cu, one list per 256 output rows), B the matching
 // rows of W or X, gathered by TMA.  That is one or two steps per tile of the
 // hundreds the product has; remainders of whole tiles would double the
-// steps of every tile that holds a large entry.
+// steps of every tile that holds a large entry.  (Where the vocabulary is so
+// small that the lists would be long, all remainders are kept beside G and
+// the products run over both: head.cu, `terms`.)
 //
 // Anchors: where a token's target (or an entry of the teacher) holds much of
 // the probability, the value and G there are differences of nearly equal
@@ -125,6 +127,9 @@ struct Args {
                              // entry that keeps its remainder
     const int4 *anchor;      // GRAD: [T] vocabulary ids of the row's anchors (-1: none) and
     const float4 *anchor_g;  // their entries of G
+    int terms;               // 2: G's remainders are kept in whole, aoff columns to the right of
+    int aoff;                // G, and no entries are listed; DX, DW: K runs over both, kone
+    int kone;                // steps each
     int *cnt;                // GRAD: [T] large entries of each token, listed in
     int2 *large;             // [T][kMaxLarge] as (vocabulary column - n0, remainder)
     uint8_t *fl;             // GRAD: [vocabulary block of 256][fs] 1 where a block of 128
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
     constexpr int kChunk = chunk_of(EPI);
     auto extra = [&](const Item &t) {
         if constexpr (kLo)
-            if (t.k0 == 0) return __ldcg(a.lists + t.m * CTAS * 128 / kListRows);
+            if (t.k0 == 0 && a.terms == 1) return __ldcg(a.lists + t.m * CTAS * 128 / kListRows);
         return make_int2(0, 0);
     };
     bool ok = true;
@@ -547,10 +552,10 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 // through shared memory (the warp's 32 rows of 128 bytes, 128-byte
                 // swizzle) to TMA stores, which clip rows and columns past the end
                 const int xc = t.n * BN + half * kUnit, yr = mrow + quad * 32;
-                auto put = [&](const CUtensorMap *tm, int x) {   // the staged box goes out at column x
+                auto put = [&](int x, int xoff = 0) {   // the staged box goes out at column x (+ xoff)
                     tc::fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0 && x < a.N && yr < a.M) store_3d(tm, ob, x, yr, t.s, a.accumulate != 0);
+                    if (lane == 0 && x < a.N && yr < a.M) store_3d(&tmOut, ob, x + xoff, yr, t.s, a.accumulate != 0);
                 };
                 auto reuse = [&]() {                             // the previous box has been read
                     if (lane == 0) store_wait_read();
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         float big = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(acc[q + j]));
-                        const bool keep = big >= cf.y && cf.x != 0.f;
+                        const bool keep = big >= cf.y && cf.x != 0.f && a.terms == 1;
                         large[q / 32] = 0;
                         if (__any_sync(0xffffffffu, keep)) {
 #pragma unroll
@@ -620,7 +625,17 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                         if (q & 32) {
                             reuse();
                             stage16(q - 32);
-                            put(&tmOut, xc + q - 32);
+                            put(xc + q - 32);
+                        }
+                    }
+                    if (a.terms == 2) {
+#pragma unroll
+                        for (int q = 0; q < kUnit; q += 64) {
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) acc[q + j] -= bf2f(f2bf(acc[q + j]));   // exact
+                            reuse();
+                            stage16(q);
+                            put(xc + q, a.aoff);
                         }
                     }
                     if (__any_sync(0xffffffffu, any != 0)) {
@@ -656,14 +671,14 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                                              make_uint4(__float_as_uint(acc[e]), __float_as_uint(acc[e + 1]),
                                                         __float_as_uint(acc[e + 2]), __float_as_uint(acc[e + 3])));
                         }
-                        put(&tmOut, xc + q);
+                        put(xc + q);
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < kUnit; q += 64) {
                         reuse();
                         stage16(q);
-                        put(&tmOut, xc + q);
+                        put(xc + q);
                     }
                 }
             }
@@ -706,17 +721,19 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                     const uint32_t fb = CTAS == 2 ? map_leader(full(s)) : full(s);
                     const uint32_t sb = s0 + s * stage_bytes, sa = sb + kOpBytes;
                     if (!slot_free()) break;
+                    const int second = kLo && a.terms == 2 && k >= a.kone;   // the remainders' turn
+                    const int kk = second ? k - a.kone : k, xo = second ? a.aoff : 0;
                     if (isA) {
                         if (rank == 0) expect_tx_warp(full(s), bytes);
-                        const int ka = k * kBK;
+                        const int ka = kk * kBK;
                         if constexpr (kAMn) {
-                            load_2d_warp<CTAS>(sa, &tmA, ma, ka, fb);
-                            load_2d_warp<CTAS>(sa + 8192, &tmA, ma + 64, ka, fb);
+                            load_2d_warp<CTAS>(sa, &tmA, ma + xo, ka, fb);
+                            load_2d_warp<CTAS>(sa + 8192, &tmA, ma + xo + 64, ka, fb);
                         } else if (mine) {
-                            load_2d_warp<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka, ma, fb);
+                            load_2d_warp<CTAS>(sa, mine == 128 ? &tmA : &tmAt, ka + xo, ma, fb);
                         }
                     } else {
-                        const int kb = a.kb0 + k * kBK;
+                        const int kb = a.kb0 + kk * kBK;
                         if constexpr (kBMn) {
                             load_2d_warp<CTAS>(sb, &tmB, nb, kb, fb);
                             load_2d_warp<CTAS>(sb + 8192, &tmB, nb + 64, kb, fb);

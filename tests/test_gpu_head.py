@@ -219,7 +219,8 @@ def test_no_tokens_and_ids_out_of_range():
     assert loss[3] == 0 and np.isfinite(loss.cpu().numpy()).all()
 
 
-@pytest.mark.parametrize("T,d,V", [(64, 64, 40), (300, 256, 5003), (2570, 2048, 2700)])
+@pytest.mark.parametrize("T,d,V", [(64, 64, 40), (300, 256, 5003), (2570, 2048, 2700), (2001, 192, 263),
+                                   (4100, 1024, 600)])
 def test_large_entries_of_the_gradient_keep_16_bits(T, d, V):
     """Confident tokens whose target is another one: G is about +g at one
     entry and -g at the target, next to nothing elsewhere (1 - p <= 2%).
