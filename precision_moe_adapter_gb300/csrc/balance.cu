@@ -250,6 +250,9 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, in
     __shared__ float sw[kRedThreads / 32], sl[8];   // sl: the CTAs' shares (CTA 0)
     __shared__ int sn;
     const int s = blockIdx.x / C, r = blockIdx.x % C;
+    // CTA 0's shared memory may be written once CTA 0 has started: every CTA
+    // arrives here and waits just before its store
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     grid_wait();
     grid_go();
     const int a = seq_at(seq, s, nseq, T), b = seq_at(seq, s + 1, nseq, T);
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(kRedThreads) k_balance_reduce(int T, int E, in
     for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if ((threadIdx.x & 31) == 0) sw[threadIdx.x >> 5] = part;
     __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (threadIdx.x == 0) {
         float t = 0.f;
         for (int i = 0; i < (int)blockDim.x / 32; ++i) t += sw[i];

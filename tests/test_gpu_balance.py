@@ -128,6 +128,25 @@ def test_packed_sequences_with_padding(T, E, k, bounds):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,S", [(60, 33, 2000), (60, 250, 1500), (200, 4096, 300)])
+def test_clusters_of_mostly_empty_sequences(T, E, S):
+    """A CTA of an empty sequence has its share of the loss almost at once and
+    hands it to the first CTA of its cluster, which must have started: many
+    such clusters, the few tokens spread among them."""
+    logits, idx, w, dw, g = make(T, E, 4, seed=S)
+    cuts = torch.sort(torch.randint(0, T + 1, (9,), generator=g, device="cuda")).values.tolist()
+    bounds = [0] * (S // 2) + [cuts[i * 9 // (S - S // 2)] for i in range(S - S // 2)] + [T]
+    seq = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    gl = torch.rand(S, generator=g, device="cuda") + 0.1
+    got = call(logits, idx, w, dw, None, seq, S, gl)
+    assert got[5] == pmoe.PMOE_OK
+    check(got, reference(logits, idx, w, dw, None, bounds, gl))
+    for _ in range(5):
+        for a, b in zip(got[:5], call(logits, idx, w, dw, None, seq, S, gl)[:5]):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_disabled_experts_and_bad_ids():
     logits, idx, w, dw, g = make(40, 24, 2)
     logits[:, 5] = -float("inf")
