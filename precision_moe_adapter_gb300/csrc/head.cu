@@ -52,6 +52,13 @@ __device__ __forceinline__ float row_dot(const uint16_t *__restrict__ x, const u
     for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     return a;
 }
+// Least |G| of an entry that keeps its remainder: `share` of the factor's size,
+// and not below the least normal number, as a threshold that underflows to
+// zero would list every column, those past the vocabulary's end among them
+__device__ __forceinline__ float least_large(float cf, float share)
+{
+    return fmaxf(kLarge * share * fabsf(cf), 1.17549435e-38f);
+}
 // p - q of an entry with logit z
 __device__ __forceinline__ float p_minus_q(float z, float scale, float lse, float q)
 {
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float
         nent[t] = n;
         if (b.coef) {
             const float cf = n ? b.g[t] * scale : 0.f;
-            b.coef[t] = make_float2(cf, kLarge * fabsf(cf));
+            b.coef[t] = make_float2(cf, least_large(cf, 1.f));
         }
     }
 }
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(128) k_head_target(int T, int V, int d, float 
         an.g[t * kAnchors + lane] = lane == 0 ? cf * e : 0.f;
     }
     // (not below 1e-4, where 1 - p_y is no longer a bound for the other entries as computed)
-    if (lane == 0) coef[t] = make_float2(cf, kLarge * fminf(fmaxf(fabsf(e), 1e-4f), 1.f) * fabsf(cf));
+    if (lane == 0) coef[t] = make_float2(cf, least_large(cf, fminf(fmaxf(fabsf(e), 1e-4f), 1.f)));
 }
 
 // ------------------------------------------------------------------ combine

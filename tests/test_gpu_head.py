@@ -303,3 +303,35 @@ def test_confident_tokens_keep_fp32_accuracy(T, d, V, K):
     err = (dX.to(D) - rdX).norm(dim=1)
     row = up.to(D).abs() * W.to(D).norm(dim=1).max()
     assert torch.all(err <= 2.0 ** -8 * rdX.norm(dim=1) + 2 * tol * row), (err / row).max()
+
+
+@pytest.mark.parametrize("K", [0, 3])
+def test_upstream_coefficients_that_underflow(K):
+    """Tokens whose factor is so small that a share of it is no FP32 number
+    have no large entries; the other tokens' gradients are what they are with
+    a zero there, and runs are identical."""
+    T, d, V = 300, 512, 5003
+    X, W, y, up, g = make(T, d, V)
+    tiny = torch.rand(T, generator=g, device="cuda") < 0.3
+    up = torch.where(tiny, torch.full_like(up, 1.4e-45), up)
+    up[tiny.nonzero()[::2, 0]] *= -3
+    zero = torch.where(tiny, torch.zeros_like(up), up)
+    ids = torch.randint(0, V, (T, max(K, 1)), generator=g, device="cuda").to(torch.int32)
+    t = torch.randn((T, max(K, 1)), generator=g, device="cuda")
+    h = DeviceHead(W, T, K=K)
+    val, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    out = []
+    for u in (up, zero, up):
+        dX, dW = torch.full_like(X, float("nan")), torch.full_like(W, float("nan"))
+        if K:
+            h.distill(X, ids, t, val, lse)
+            h.distill_backward(X, ids, t, lse, u, dX, dW)
+        else:
+            h.logprob(X, y, val, lse)
+            h.logprob_backward(X, y, lse, u, dX, dW)
+        out.append((dX, dW))
+    assert h.status() == pmoe.PMOE_OK
+    assert torch.equal(out[0][0], out[2][0]) and torch.equal(out[0][1], out[2][1])
+    assert torch.equal(out[0][0][~tiny], out[1][0][~tiny])
+    assert torch.all(out[0][0][tiny].float().abs() < 1e-38)
+    assert torch.equal(out[0][1].float(), out[1][1].float())
