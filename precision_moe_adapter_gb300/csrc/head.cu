@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, int 
     grid_go();
     const float2 *p = part + t * NU;
     float m = ninf, s = 0.f;
-    auto join = [&](float om, float os) {   // (no partials yet: m = -inf, s = 0)
+    auto join = [&](float om, float os) {   // (no partials yet: m = -inf, s = 0; a NaN stays one)
         const float n = fmaxf(m, om), N = __fmul_rn(n, c);
-        const float x = m == ninf ? 0.f : s * exp2f(__fmul_rn(m, c) - N);
-        const float y = om == ninf ? 0.f : os * exp2f(__fmul_rn(om, c) - N);
+        const float x = m == ninf ? s : s * exp2f(__fmul_rn(m, c) - N);
+        const float y = om == ninf ? os : os * exp2f(__fmul_rn(om, c) - N);
         m = n;
         s = x + y;
     };
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, int 
                 if (z == m) top = za[n];
             }
         const float N = __fmul_rn(top, c);
-        s = fmaxf(rest, 0.f) * exp2f(M - N);
+        s = (rest < 0.f ? 0.f : rest) * exp2f(M - N);   // (a NaN stays one)
 #pragma unroll
         for (int n = 0; n < kAnchors; ++n)
             if (id[n] >= 0) s += exp2f(fmaf(za[n], c, -N));

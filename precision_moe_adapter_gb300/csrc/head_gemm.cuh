@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 for (int e = 0; e < 4; ++e) mx[e] = acc[e];
 #pragma unroll
                 for (int j = 4; j < kUnit; ++j) mx[j & 3] = fmaxf(mx[j & 3], acc[j]);
-                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m2 = m * a.c;
+                // (logits of -inf only sum to zero, and a NaN among them to NaN)
+                const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m2 = m == -inf ? 0.f : m * a.c;
                 float sm[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < kUnit; ++j) sm[j & 3] += ex2(fmaf(acc[j], a.c, -m2));

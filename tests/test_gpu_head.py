@@ -335,3 +335,23 @@ def test_upstream_coefficients_that_underflow(K):
     assert torch.equal(out[0][0][~tiny], out[1][0][~tiny])
     assert torch.all(out[0][0][tiny].float().abs() < 1e-38)
     assert torch.equal(out[0][1].float(), out[1][1].float())
+
+
+@pytest.mark.parametrize("V,bad", [(1003, 500), (1025, 1024), (5003, 0)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_a_vocabulary_row_that_is_not_a_number_shows(V, bad, what):
+    """A NaN (or infinite) row of the head makes every token's sum NaN (or
+    infinite): no token's value or lse may look like a number then, its own
+    target's logit being finite, whether or not the row shares its unit of
+    128 with others."""
+    T, d = 70, 128
+    X, W, y, up, g = make(T, d, V)
+    y = torch.where(y == bad, (y + 7) % V, y)
+    W[bad] = what
+    logp, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    h = DeviceHead(W, T, K=2)
+    h.logprob(X, y, logp, lse)
+    assert not torch.isfinite(logp).any() and not torch.isfinite(lse).any()
+    ids = torch.stack([y, (y + 1 + (y + 1 == bad)) % V], 1).to(torch.int32).contiguous()
+    h.distill(X, ids, torch.tensor([[3.0, 0.0]], device="cuda").repeat(T, 1), logp, lse)
+    assert not torch.isfinite(logp).any() and not torch.isfinite(lse).any()
