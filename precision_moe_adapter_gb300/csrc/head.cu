@@ -248,13 +248,12 @@ __global__ void __launch_bounds__(128) k_head_target(int T, int V, int d, float 
 }
 
 // ------------------------------------------------------------------ combine
-// One CTA per token joins the NU softmax partials in one fixed order, and
-// forms the token's value from the target logits.  A partial (m, s) stands for
-// s 2^M with M = c m as rounded; lse = scale m + ln 2 (log2 s + M - c m), whose
-// second term is exact to its own size, and a log-probability is scale z - lse
-// with this lse, the one that the backward is given (scale z as rounded in
-// all three places).  The anchors' terms of the sum are replaced by those of
-// their logits computed again.
+// One CTA per token joins the NU softmax partials in one fixed order, adds the
+// anchors, which the partials leave out, and forms the token's value.  A partial
+// (m, s) stands for s 2^M with M = c m as rounded.  With `top` the largest
+// logit and L = ln sum_v exp(scale (z_v - top)), lse = scale top + L (scale z as
+// rounded in the backward too) and a log-probability is scale (z - top) - L:
+// where an anchor is the largest, L = log1p(the others) however small they are.
 __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, int d, float scale, float c,
                                                       const uint16_t *__restrict__ X, const uint16_t *__restrict__ W,
                                                       const float2 *__restrict__ part, const float *__restrict__ zt,
@@ -312,26 +311,23 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, int 
     m = sw[0].x;
     s = sw[0].y;
     for (int i = 1; i < 4; ++i) join(sw[i].x, sw[i].y);
-    if (id[0] >= 0) {   // (where an anchor has the largest logit, the sum is taken relative to its new one)
-        const float M = __fmul_rn(m, c);
-        float rest = s, top = m;
+    float top = m;
+    int lead = -1;   // the anchor that is the largest, if one is
 #pragma unroll
-        for (int n = 0; n < kAnchors; ++n)
-            if (id[n] >= 0) {
-                const float z = zt[t * K + place[n]];
-                rest -= exp2f(fmaf(z, c, -M));
-                if (z == m) top = za[n];
-            }
-        const float N = __fmul_rn(top, c);
-        s = (rest < 0.f ? 0.f : rest) * exp2f(M - N);   // (a NaN stays one)
+    for (int n = 0; n < kAnchors; ++n)
+        if (id[n] >= 0 && za[n] >= top) {
+            if (lead < 0 || za[n] > top) lead = n;
+            top = za[n];
+        }
+    // sums relative to c top, which the partials' M differs from by its rounding
+    const float off = fmaf(top, c, -__fmul_rn(m, c));
+    float rest = m == ninf ? s : s * exp2f(-off);
 #pragma unroll
-        for (int n = 0; n < kAnchors; ++n)
-            if (id[n] >= 0) s += exp2f(fmaf(za[n], c, -N));
-        m = top;
-    }
-    const float ls = 0.6931471805599453f * (log2f(s) - fmaf(m, c, -__fmul_rn(m, c)));
-    const float l = __fadd_rn(__fmul_rn(m, scale), ls);
-    auto logp = [&](float z) { return __fmul_rn(z, scale) - l; };
+    for (int n = 0; n < kAnchors; ++n)
+        if (id[n] >= 0 && n != lead) rest += exp2f((za[n] - top) * c);
+    const float L = lead >= 0 ? log1pf(rest) : 0.6931471805599453f * log2f(rest);
+    const float l = __fadd_rn(__fmul_rn(top, scale), L);
+    auto logp = [&](float z) { return (z - top) * scale - L; };
     float v = 0.f;
     if (!target) {
         const int n = nent[t];
@@ -633,7 +629,7 @@ struct Ws {
     int *nent;               // [T] their number
     uint16_t *tab;           // [T][NU]
     uint4 *mask;             // [T][NU]
-    float *zt;               // [T][max(K, 1)]
+    float *zt;               // [T][K]
     float2 *part;            // [T][NU]
     Anchors an;
     float2 *coef;            // [T] factor and least large entry of G
@@ -672,7 +668,7 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
     w.an.place = (int *)take(T * kAnchors * 4);
     if (op == PMOE_HEAD_FORWARD) {
         w.h = (float *)take(T * K * 4);
-        w.zt = (float *)take(T * std::max<size_t>(K, 1) * 4);
+        w.zt = (float *)take(T * K * 4);
         w.part = (float2 *)take(T * cdiv(h.V, kUnit) * 8);
     } else {
         const int piece = piece_of(h.T, h.V);
@@ -814,6 +810,7 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     a.part = w.part;
     a.zt = w.zt;
     a.target = distill ? nullptr : idx;
+    a.anchor = (const int4 *)w.an.id;
     a.tab = w.tab;
     a.mask = w.mask;
     a.K = K;

@@ -117,19 +117,19 @@ struct Args {
     float scale, c;          // GRAD: the logits' factor; FWD: that times log2(e)
     int NU;                  // FWD, GRAD: units of the vocabulary
     float2 *part;            // FWD: [T][NU] (largest z, sum of 2^(c z - its c z))
-    // the target entries of FWD and GRAD: one per token with probability 1
-    // (target), or up to K per token, in vocabulary order
+    // the target entries of FWD and GRAD: one per token with probability 1 (an
+    // anchor), or up to K per token, in vocabulary order
     const int32_t *target;   // [T], or NULL
     const uint16_t *tab;     // [T][NU]: 0 where the unit has none, else 256 + place of its first
     const uint4 *mask;       // [T][NU]: the unit's columns that have one (where tab is not 0)
     const float *q;          // GRAD: [T][K] probabilities
-    float *zt;               // FWD: [T][K] raw logits of the entries (out)
+    float *zt;               // FWD: [T][K] raw logits of a teacher's entries (out)
     int K;
     const float *lse;        // GRAD: [T]
     const float2 *coef;      // GRAD: [T] factor of the row (0: no gradient) and least |G| of an
                              // entry that keeps its remainder
-    const int4 *anchor;      // GRAD: [T] vocabulary ids of the row's anchors (-1: none) and
-    const float4 *anchor_g;  // their entries of G
+    const int4 *anchor;      // [T] vocabulary ids of the row's anchors (-1: none; FWD: without
+    const float4 *anchor_g;  // targets) and, GRAD, their entries of G
     int terms;               // 2: G's remainders are kept in whole, aoff columns to the right of
     int aoff;                // G, and no entries are listed; DX, DW: K runs over both, kone
     int kone;                // steps each
@@ -461,13 +461,15 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             int an[4] = {-1, -1, -1, -1};        // anchors and their entries of G
             float ag[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (EPI == HG_FWD || EPI == HG_GRAD) {
-                if (live && a.target) {   // (GRAD: an anchor)
-                    const int j = EPI == HG_FWD ? a.target[row] - cb : -1;
-                    if (j >= 0 && j < nv) {
-#pragma unroll
-                        for (int e = 0; e < kUnit / 32; ++e) mw[e] = j >> 5 == e ? 1u << (j & 31) : 0u;
+                if (EPI == HG_FWD && live) {
+                    if (a.target) {
+                        an[0] = a.target[row];
+                    } else {
+                        const int4 i4 = a.anchor[row];
+                        an[0] = i4.x, an[1] = i4.y, an[2] = i4.z, an[3] = i4.w;
                     }
-                } else if (live) {
+                }
+                if (live && !a.target) {
                     const int64_t at = (int64_t)row * a.NU + cb / kUnit;
                     const int e = a.tab[at];
                     if (e) {
@@ -530,10 +532,23 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
             if constexpr (EPI == HG_FWD) {
 #pragma unroll
                 for (int q = 0; q < kUnit; q += 32) {
-                    if (!__any_sync(0xffffffffu, mw[q / 32] != 0)) continue;
+                    if (__any_sync(0xffffffffu, mw[q / 32] != 0)) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (mw[q / 32] >> j & 1u) a.zt[pos++] = acc[q + j];
+                        for (int j = 0; j < 32; ++j)
+                            if (mw[q / 32] >> j & 1u) a.zt[pos++] = acc[q + j];
+                    }
+                    // the anchors stay out of the sum: the combine adds them
+                    uint32_t out = 0;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint32_t j = (uint32_t)an[n] - (uint32_t)(cb + q);
+                        out |= j < 32u ? 1u << j : 0u;
+                    }
+                    if (__any_sync(0xffffffffu, out != 0)) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (out >> j & 1u) acc[q + j] = -inf;
+                    }
                 }
                 if (nv < kUnit) {
 #pragma unroll

@@ -355,3 +355,30 @@ def test_a_vocabulary_row_that_is_not_a_number_shows(V, bad, what):
     ids = torch.stack([y, (y + 1 + (y + 1 == bad)) % V], 1).to(torch.int32).contiguous()
     h.distill(X, ids, torch.tensor([[3.0, 0.0]], device="cuda").repeat(T, 1), logp, lse)
     assert not torch.isfinite(logp).any() and not torch.isfinite(lse).any()
+
+
+@pytest.mark.parametrize("T,d,V,K,scale", [(40, 2048, 4000, 0, 1.0), (33, 512, 1003, 0, 1 / 0.7), (300, 7168, 640, 0, 1.0),
+                                           (64, 256, 129, 0, 2.0), (50, 2048, 1003, 1, 1.0)])
+def test_confident_values_are_accurate_relative_to_themselves(T, d, V, K, scale):
+    """-log p = log1p(sum over the others of exp(s (z_v - z_y))).  Each
+    exponent is off by at most the errors of its two logits and a unit in 2^24
+    of its size (here under 40); exp2, the sums and log1p add some units in
+    2^24.  All are relative errors of the sum, so of the value however small
+    it is: from about e^-2 down to e^-30."""
+    X, W, y, up, g = make(T, d, V, seed=11, lean=0.0)
+    Wy = W[y.long()].float()
+    X = (0.05 * X.float() + (6 + 26 * torch.rand((T, 1), generator=g, device="cuda")) / scale * Wy
+         / Wy.square().sum(1, keepdim=True)).to(torch.bfloat16)
+    h = DeviceHead(W, T, K=K, scale=scale, backward=False)
+    val, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    if K:
+        h.distill(X, y[:, None].contiguous(), torch.zeros((T, 1), device="cuda"), val, lse)
+    else:
+        h.logprob(X, y, val, lse)
+        val = -val
+    z = scale * (X.to(D) @ W.to(D).T)
+    rest = z.scatter(1, y[:, None].long(), -math.inf) - z.gather(1, y[:, None].long())
+    ref = torch.log1p(rest.exp().sum(1))
+    tol = 2 * logit_bound(X, W, scale) + 64 * 2.0 ** -24
+    err = (val.to(D) - ref).abs() / ref
+    assert torch.all(err <= tol), (err / tol).max()
