@@ -418,7 +418,8 @@ size_t head_workspace_bytes(pmoe_head_dims dims, int op);
  * head_logprob_forward -- logp_t = scale z_{t, y_t} - lse_t (the negative
  * softmax cross entropy) of the token's target y_t.
  *   target int32 [T]; a negative target is an ignored token: logp = 0, no
- *          gradient (its row of dX is zero whatever X holds there).  A
+ *          gradient (its row of dX is zero, and dW takes nothing from it,
+ *          whatever X holds there).  A
  *          target >= V is ignored and recorded as PMOE_ERR_BAD_INDEX in the
  *          error word.
  *   logp   f32 [T] (out)          lse f32 [T] (out; the backward's input)

@@ -382,3 +382,55 @@ def test_confident_values_are_accurate_relative_to_themselves(T, d, V, K, scale)
     tol = 2 * logit_bound(X, W, scale) + 64 * 2.0 ** -24
     err = (val.to(D) - ref).abs() / ref
     assert torch.all(err <= tol), (err / tol).max()
+
+
+@pytest.mark.parametrize("T,d,V,K", [(300, 128, 1003, 0), (700, 192, 9001, 0), (300, 256, 5003, 4), (40, 64, 300, 4)])
+def test_ignored_tokens_do_not_reach_the_heads_gradient(T, d, V, K):
+    """NaN and infinities in the hidden states of ignored tokens, the first one
+    among them, leave dW what it is with zeros there."""
+    X, W, y, up, g = make(T, d, V)
+    off = torch.rand(T, generator=g, device="cuda") < 0.3
+    off[0] = True
+    y = torch.where(off, torch.full_like(y, -1), y)
+    ids = torch.randint(0, V, (T, max(K, 1)), generator=g, device="cuda").to(torch.int32)
+    ids[off] = -1
+    t = torch.randn((T, max(K, 1)), generator=g, device="cuda")
+    h = DeviceHead(W, T, K=K)
+    val, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    out = []
+    for fill in (0.0, math.nan, math.inf):
+        Xf = X.clone()
+        Xf[off] = fill
+        dX, dW = torch.full_like(X, float("nan")), torch.full_like(W, float("nan"))
+        if K:
+            h.distill(Xf, ids, t, val, lse)
+            h.distill_backward(Xf, ids, t, lse, up, dX, dW)
+        else:
+            h.logprob(Xf, y, val, lse)
+            h.logprob_backward(Xf, y, lse, up, dX, dW)
+        out.append((dX, dW))
+    assert torch.isfinite(out[0][1].float()).all()
+    for dX, dW in out[1:]:
+        assert torch.equal(dX, out[0][0]) and torch.equal(dW, out[0][1])
+
+
+@pytest.mark.parametrize("T,d,V,K", [(300, 256, 5003, 0), (1100, 512, 9001, 0), (64, 64, 40, 0), (600, 256, 9001, 6)])
+def test_gradient_of_the_head_alone(T, d, V, K):
+    """dW without dX (hidden states that take no gradient) is the dW of both."""
+    X, W, y, up, g = make(T, d, V)
+    y = torch.where(torch.rand(T, generator=g, device="cuda") < 0.2, torch.full_like(y, -1), y)
+    ids = torch.randint(0, V, (T, max(K, 1)), generator=g, device="cuda").to(torch.int32)
+    t = 3 * torch.randn((T, max(K, 1)), generator=g, device="cuda")
+    h = DeviceHead(W, T, K=K)
+    val, lse, dX = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(X)
+    both, alone = torch.full_like(W, float("nan")), torch.full_like(W, float("nan"))
+    if K:
+        h.distill(X, ids, t, val, lse)
+        h.distill_backward(X, ids, t, lse, up, dX, both)
+        h.distill_backward(X, ids, t, lse, up, None, alone)
+    else:
+        h.logprob(X, y, val, lse)
+        h.logprob_backward(X, y, lse, up, dX, both)
+        h.logprob_backward(X, y, lse, up, None, alone)
+    assert h.status() == pmoe.PMOE_OK
+    assert torch.isfinite(alone.float()).all() and torch.equal(both, alone)
