@@ -25,11 +25,15 @@
 // with the number of K steps (about one part in 2^24 per 16 columns).  Every
 // run of chunk_of(EPI) K steps is therefore summed in its own TMEM buffer and
 // added to the tile's FP32 sum in registers (round to nearest), which bounds
-// the error at any length.  The forward's values are FP32 outputs: chunks of
-// 512 columns, relative error about 5e-7; GRAD takes the same chunks, so that
-// its logits are the forward's bit for bit and p - 1 of a confident token
+// the error at any length.  (DX and DW end with the extra steps described below
+// in their last run.  At most T / 8 of them meet in one tile, and the four MMAs of
+// each lose up to 2^-24 of that run's sum: 6e-5 of dW at any T, should all tokens
+// have all their 8 entries in one block of the vocabulary, for results that are
+// rounded to 2^-9.)  The forward's values are FP32 outputs:
+// runs of 512 columns, relative error about 5e-7; GRAD takes the same runs, so
+// that its logits are the forward's bit for bit and p - 1 of a confident token
 // does not see their error.  The other results are rounded to BF16, so longer
-// chunks do.  (Chunks of 256 columns in FWD and GRAD cost a policy step 4%.)
+// runs do.  (Runs of 256 columns in FWD and GRAD cost a policy step 4%.)
 // The two buffers alternate, so the tensor cores work on the next chunk while
 // one is drained, and on the next tile's first two chunks during the epilogue
 // proper: 91 to 97% of the tensor pipe's cycles are busy at T = 4096, d = 2048,
@@ -57,9 +61,11 @@
 // with q >= 1/4 (at most 4), are therefore computed again in FP32 by head.cu,
 // which corrects the sums of the forward and gives GRAD these entries of G.
 //
-// Every element's sum runs over k in the same order whatever the tile shape,
-// and the softmax partials cover 128 aligned columns: the results do not
-// depend on the number of tokens in the call.
+// Every logit's sum runs over k in the same order whatever the tile shape, and
+// the softmax partials cover 128 aligned columns: the forward's results do not
+// depend on the number of tokens in the call.  (A row of dX may, in its last
+// bits: the pieces of the vocabulary, the cuts along K and the choice between
+// lists and whole remainders go by T.)
 #pragma once
 
 #include "gemm_tc.cuh"

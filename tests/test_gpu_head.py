@@ -434,3 +434,30 @@ def test_gradient_of_the_head_alone(T, d, V, K):
         h.logprob_backward(X, y, lse, up, None, alone)
     assert h.status() == pmoe.PMOE_OK
     assert torch.isfinite(alone.float()).all() and torch.equal(both, alone)
+
+
+def test_targets_in_one_block_of_the_vocabulary():
+    """Every token has the same target, so that one row of dW takes a remainder
+    from each of them: 1024 extra K steps, from a list that does not fit its
+    builder's shared memory.  The sums are of one sign, so what the tensor cores
+    truncate would add up: at most 128 MMAs a run lose 2^-24 of it each, and the
+    4096 of the extra steps the same of the last of 32 runs, which is 2^-17 of
+    the whole each.  The mean over d elements of their BF16 rounding (at most 2^-9
+    each; the columns' factors of 1 to 2 spread the sums over many BF16 steps)
+    has a standard deviation of 2^-9 / sqrt(3 d), of which 5 are allowed."""
+    T, d, V = 65536, 8192, 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    X = torch.randn((T, d), generator=g, device="cuda", dtype=torch.bfloat16).abs_() + 0.5
+    X *= torch.exp2(torch.arange(d, device="cuda") / d).to(torch.bfloat16)
+    W = torch.randn((V, d), generator=g, device="cuda", dtype=torch.bfloat16).mul_(0.002)
+    y = torch.full((T,), 300, dtype=torch.int32, device="cuda")
+    up = 0.5 + torch.rand(T, generator=g, device="cuda")
+    h, logp, lse, _, dW = run_logprob(X, W, y, up, 1.0)
+    assert h.status() == pmoe.PMOE_OK
+    ref = torch.zeros(d, dtype=D, device="cuda")
+    for a in range(0, T, 4096):
+        r = slice(a, a + 4096)
+        ref += (up[r].to(D) * (1 - logp[r].to(D).exp())) @ X[r].to(D)
+    bias = ((dW[300].to(D) - ref) / ref).mean().abs()
+    assert bias <= 2 * 2.0 ** -17 + 5 * 2.0 ** -9 / math.sqrt(3 * d), bias
