@@ -461,3 +461,59 @@ def test_targets_in_one_block_of_the_vocabulary():
         ref += (up[r].to(D) * (1 - logp[r].to(D).exp())) @ X[r].to(D)
     bias = ((dW[300].to(D) - ref) / ref).mean().abs()
     assert bias <= 2 * 2.0 ** -17 + 5 * 2.0 ** -9 / math.sqrt(3 * d), bias
+
+
+def _distill_in_parts(X, W, ids, t, up, scale, dW):
+    T, V = X.shape[0], W.shape[0]
+    h = DeviceHead(W, T, K=ids.shape[1], scale=scale)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dX = torch.full_like(X, float("nan"))
+    dWt = torch.full_like(W, float("nan")) if dW else None
+    h.distill(X, ids, t, loss, lse)
+    h.distill_backward(X, ids, t, lse, up, dX, dWt)
+    assert h.status() == pmoe.PMOE_OK
+    rdW = torch.zeros((V, W.shape[1]), dtype=D, device="cuda")
+    for a in range(0, T, 512):
+        r = slice(a, min(a + 512, T))
+        q = torch.nan_to_num(torch.softmax((scale * t[r].to(D)).masked_fill(ids[r] < 0, -math.inf), 1))
+        Q = torch.zeros((r.stop - a, V), dtype=D, device="cuda").scatter_add_(1, ids[r].clamp(min=0).long(), q)
+        rlse, rv, rdX, w = reference(X[r], W, scale, Q, torch.xlogy(q, q).sum(1), up[r], 1.0)
+        rdW += w
+        check_values(X[r], W, scale, lse[r], loss[r], rlse, rv)
+        check_grad(dX[r], rdX, "dX")
+    if dW:
+        check_grad(dWt, rdW, "dW")
+
+
+@pytest.mark.parametrize("T,d,V,K,top,dW", [
+    (700, 256, 8009, 16, 0.0, True), (1030, 128, 10007, 40, 6.0, True),          # pairs of CTAs, lists
+    (8192, 64, 70001, 9, 4.0, True), (4100, 320, 66001, 64, 3.0, False)])        # several pieces
+def test_distill_as_training_runs_it(T, d, V, K, top, dW):
+    """Entries and anchors anywhere in the vocabulary, so in every piece and in
+    both halves of a pair's tile; some tokens have one confident entry, some
+    none, some repeat an id."""
+    X, W, y, up, g = make(T, d, V, seed=K)
+    ids = torch.randint(0, V, (T, K), generator=g, device="cuda").to(torch.int32)
+    ids[:, 0] = y
+    ids[::7, 1] = ids[::7, 2]
+    ids[::11, K // 2:] = -1
+    ids[5::50] = -1
+    t = torch.randn((T, K), generator=g, device="cuda")
+    t[:, 0] += top
+    _distill_in_parts(X, W, ids.contiguous(), t, up, 0.7, dW)
+
+
+def test_distill_of_a_token_does_not_depend_on_the_batch():
+    T, d, V, K = 700, 512, 20011, 12
+    X, W, y, up, g = make(T, d, V)
+    ids = torch.randint(0, V, (T, K), generator=g, device="cuda").to(torch.int32)
+    ids[:, 0] = y
+    t = 2 * torch.randn((T, K), generator=g, device="cuda")
+    t[::2, 0] += 6
+    out = []
+    for n in (T, 1, 7, 128, 129, 300):
+        h = DeviceHead(W, n, K=K, backward=False)
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        h.distill(X[:n].clone(), ids[:n].clone(), t[:n].clone(), loss, lse)
+        assert torch.equal(loss, (out or [loss])[0][:n]) and torch.equal(lse, (out or [0, lse])[1][:n]), n
+        out = out or [loss, lse]
