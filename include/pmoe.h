@@ -571,7 +571,9 @@ pmoe_status pmoe_kernel_time(int which, double *ms_total, int *launches);
  * then gives up after wait_ns, records PMOE_ERR_TIMEOUT in the call's error
  * word, and every role of that CTA leaves its loop after its own bounded
  * wait and frees its tensor memory; the call's outputs are incomplete.
- * One-shot: the launch consumes the hook.  wait_ns in [1e5, 2e9] (the
+ * A head_* call takes the hook for all of its products: in each of them the
+ * first work item's signals are withheld (for both CTAs of a pair).
+ * One-shot: the launch or head_* call consumes the hook.  wait_ns in [1e5, 2e9] (the
  * bound keeps every issued copy and MMA long finished before a role gives
  * up), else PMOE_ERR_INVALID_ARG.  Process-wide state: not for use while
  * other threads launch layer work.

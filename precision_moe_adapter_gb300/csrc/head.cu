@@ -10,6 +10,11 @@
 #include "head_gemm.cuh"
 
 namespace pmoe {
+namespace tc {
+// gemm_tc.cu: the bounded-wait limit and withheld item of the next products: the
+// armed test hook (once), else the default limit and none
+void take_wait_hook(uint64_t &wait_ns, int &skip_item);
+}  // namespace tc
 namespace hg {
 
 constexpr int kMaxK = 256;                    // teacher entries per token
@@ -828,6 +833,7 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     a.mask = w.mask;
     a.K = K;
     a.err = w.err;
+    tc::take_wait_hook(a.wait_ns, a.skip_item);
     if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
                         st))
         return PMOE_ERR_CUDA;
@@ -853,6 +859,9 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     if (!made) return PMOE_ERR_CUDA;
     const int piece = piece_of(h.T, h.V);
     const Tiling tx = dx_tiling(h);
+    uint64_t wait_ns;
+    int skip_item;
+    tc::take_wait_hook(wait_ns, skip_item);
     for (int v0 = 0; v0 < h.V; v0 += piece) {
         const int vc = std::min(piece, h.V - v0);
         const int64_t ldg = (int64_t)piece * w.terms;
@@ -864,6 +873,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
         b.large = w.large;
         b.fl = dW ? w.fl : nullptr;
         b.fs = w.fs;
+        b.wait_ns = wait_ns;
+        b.skip_item = skip_item;
         b.err = w.err;
         if (v0 > 0 && cudaMemsetAsync(w.cnt, 0, w.zero_bytes, st) != cudaSuccess) return PMOE_ERR_CUDA;
         {   // G = coef (softmax(Z) - q) of this piece

@@ -517,3 +517,28 @@ def test_distill_of_a_token_does_not_depend_on_the_batch():
         h.distill(X[:n].clone(), ids[:n].clone(), t[:n].clone(), loss, lse)
         assert torch.equal(loss, (out or [loss])[0][:n]) and torch.equal(lse, (out or [0, lse])[1][:n]), n
         out = out or [loss, lse]
+
+
+@pytest.mark.parametrize("T,d,V", [(40, 256, 300), (300, 512, 5003), (700, 256, 8009)])
+def test_a_wait_that_runs_out_is_reported(T, d, V):
+    """One accumulator-full signal of every product is withheld and waits end
+    after 2 ms: the call ends, reports PMOE_ERR_TIMEOUT, and the next one is
+    what it was.  Single CTAs with whole remainders, with lists, and pairs."""
+    X, W, y, up, g = make(T, d, V)
+    ref = run_logprob(X, W, y, up, 1.0)
+    h, (logp, lse, dX, dW) = ref[0], [torch.empty_like(t) for t in ref[1:]]
+    assert h.status() == pmoe.PMOE_OK
+    pmoe.pmoe_debug_expire_gemm_wait(2_000_000)
+    h.logprob(X, y, logp, lse)
+    assert h.status() == pmoe.PMOE_ERR_TIMEOUT
+    h.logprob(X, y, logp, lse)
+    assert h.status() == pmoe.PMOE_OK
+    assert torch.equal(logp, ref[1]) and torch.equal(lse, ref[2])
+    for x, w in ((dX, dW), (dX, None), (None, dW)):
+        pmoe.pmoe_debug_expire_gemm_wait(2_000_000)
+        h.logprob_backward(X, y, lse, up, x, w)
+        assert h.status() == pmoe.PMOE_ERR_TIMEOUT
+        h.logprob_backward(X, y, lse, up, x, w)
+        assert h.status() == pmoe.PMOE_OK
+        assert x is None or torch.equal(x, ref[3])
+        assert w is None or torch.equal(w, ref[4])
