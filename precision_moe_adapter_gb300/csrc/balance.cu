@@ -490,9 +490,8 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
         bal::by_experts(dims.E, [&](auto tpt, auto v, auto ni) {
             constexpr auto kern = bal::k_balance_partial<tpt.value, v.value, ni.value>;
             const size_t sm = (size_t)(bal::fwd_threads(tpt.value) / tpt.value + 1) * w.Ep * 4;
-            static const bool attr =   // up to 17 rows of 1024 floats (69 KB)
-                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 17 * 4096) == cudaSuccess;
-            ok = attr && launch_chained<kern>((unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
+            // (up to 17 rows of 1024 floats: 69 KB)
+            ok = set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(17 * 4096) && launch_chained<kern>((unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
                                 w.L, w.Ep, logits, idx, valid, seq, nseq, w.psum, w.cnt, w.ntok, w.err);
         });
     // CTAs per sequence: 32 experts each up to 8 CTAs, then more experts each

@@ -755,9 +755,7 @@ static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtens
                       const Args &a, cudaStream_t st)
 {
     constexpr auto kern = k_head_gemm<CTAS, BN, EPI>;
-    static const bool attr =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(BN)) == cudaSuccess;
-    if (!attr) return false;
+    if (!set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(smem_of(BN))) return false;
     const int64_t items = a.whole + ((int64_t)a.mt * a.nt - a.whole) * a.splits;
     const int64_t clusters = std::min<int64_t>(items, gemm_num_sms() / CTAS);
     return launch_chained<kern>((unsigned)(clusters * CTAS), threads_of(BN),

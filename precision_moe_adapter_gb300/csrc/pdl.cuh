@@ -9,12 +9,29 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace pmoe {
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Sets attribute A of kernel K, once on each device (attributes are a device's
+// own); a failure is not kept, the next call tries again.
+template <auto K, cudaFuncAttribute A>
+bool set_attribute(int value)
+{
+    static std::atomic<uint64_t> done{0};   // a bit per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(K, A, value) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // Launches kernel K, which begins with grid_wait(), in clusters of `cluster`
 // CTAs.  Every kernel of a chain asks for the SM's memory to be all shared
@@ -24,9 +41,7 @@ __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_
 template <auto K, class... A>
 bool launch_chained(unsigned grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st, A... args)
 {
-    static const bool split = cudaFuncSetAttribute(K, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                   cudaSharedmemCarveoutMaxShared) == cudaSuccess;
-    if (!split) return false;
+    if (!set_attribute<K, cudaFuncAttributePreferredSharedMemoryCarveout>(cudaSharedmemCarveoutMaxShared)) return false;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
