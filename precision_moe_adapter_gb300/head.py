@@ -15,6 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import pmoe
+from .layer import check_current
 from .layer import check_tensor as _check
 
 _BF16 = (torch.bfloat16, torch.int16)
@@ -26,13 +27,15 @@ class DeviceHead:
     ``K`` is the number of teacher entries per token (distillation), ``scale``
     the factor of every logit (1 / temperature).  ``backward=False`` leaves
     out the backward's workspace.  Calls on one head share its workspaces and
-    must be ordered (one stream, or events)."""
+    must be ordered (one stream, or events); they are made on torch's current
+    device, which must be W's."""
 
     def __init__(self, W: torch.Tensor, T: int, K: int = 0, scale: float = 1.0,
                  backward: bool = True):
         if W.dim() != 2:
             raise ValueError(f"W: shape {tuple(W.shape)}, expected [V, d]")
         _check("W", W, _BF16, W.shape, W.device)
+        check_current(W.device)
         self.W, self.scale, self.device = W, float(scale), W.device
         V, d = W.shape
         self.dims = pmoe.head_dims(T, d, V, K)
@@ -46,6 +49,7 @@ class DeviceHead:
 
     def _in(self, X, **f32):
         h = self.dims
+        check_current(self.device)
         _check("X", X, _BF16, (h.T, h.d), self.device)
         for name, t in f32.items():
             _check(name, t, (torch.float32,), (h.T,), self.device)
@@ -99,6 +103,7 @@ class DeviceHead:
 
     def status(self) -> int:
         """First device error recorded by the calls so far (synchronizes)."""
+        check_current(self.device)
         s = pmoe.PMOE_OK
         for ws in self._ws.values():
             s = s or pmoe.moe_query_status(ws)

@@ -36,6 +36,14 @@ def check_tensor(name, t, dtypes, shape, device):
     raise ValueError(f"{name}: must be contiguous")
 
 
+def check_current(device):
+    """Raises unless the CUDA device is torch's current one, on which (and on
+    whose stream) the library launches."""
+    if device.type == "cuda" and torch.cuda.current_device() != device.index:
+        raise RuntimeError(f"the current device is cuda:{torch.cuda.current_device()}, the tensors are "
+                           f"on {device}: call under torch.cuda.device({device.index})")
+
+
 def _dev(a, device) -> torch.Tensor:
     if isinstance(a, torch.Tensor):   # already a tensor (e.g. drawn on the device)
         return a.to(device)
@@ -178,6 +186,7 @@ class DeviceLayer:
 
     def _balance_args(self, logits, valid, seq, nseq):
         cfg, dev = self.cfg, self.device
+        check_current(dev)
         check_tensor("logits", logits, (torch.float32,), (cfg.T, cfg.E), dev)
         if valid is not None:
             check_tensor("valid", valid, (torch.uint8,), (cfg.T,), dev)

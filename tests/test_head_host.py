@@ -81,3 +81,27 @@ def test_device_head_checks(monkeypatch):
         h.distill(X, torch.zeros((4, 3), dtype=torch.int32), torch.zeros((4, 3)), f, f)
     with pytest.raises(RuntimeError):
         h.logprob_backward(X, y, f, f, X)
+
+
+def test_calls_on_another_device_are_refused(monkeypatch):
+    """The library launches on the current device: a head (or a layer's router)
+    whose tensors are on another one says so before it looks at anything else."""
+    from precision_moe_adapter_gb300 import layer
+    monkeypatch.setattr(pmoe, "moe_clear_status", lambda ws, stream=None: None)
+    h = head.DeviceHead(torch.zeros((100, 64), dtype=BF16), 4, K=2)
+    h.device = torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for call in (lambda: h.logprob(None, None, None, None), lambda: h.distill(None, None, None, None, None),
+                 lambda: h.logprob_backward(None, None, None, None, None),
+                 lambda: h.distill_backward(None, None, None, None, None, None), h.status):
+        with pytest.raises(RuntimeError, match="cuda:1"):
+            call()
+    with pytest.raises(RuntimeError, match="cuda:1"):
+        layer.check_current(torch.device("cuda", 1))
+    L = layer.DeviceLayer.__new__(layer.DeviceLayer)
+    L.cfg, L.device = None, torch.device("cuda", 1)
+    with pytest.raises(RuntimeError, match="cuda:1"):
+        L._balance_args(None, None, None, 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    layer.check_current(torch.device("cuda", 1))
+    layer.check_current(torch.device("cpu"))
