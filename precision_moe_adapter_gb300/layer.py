@@ -39,9 +39,10 @@ def check_tensor(name, t, dtypes, shape, device):
 def check_current(device):
     """Raises unless the CUDA device is torch's current one, on which (and on
     whose stream) the library launches."""
-    if device.type == "cuda" and torch.cuda.current_device() != device.index:
+    index = device.index   # (None on the CPU)
+    if index is not None and torch.cuda.current_device() != index:
         raise RuntimeError(f"the current device is cuda:{torch.cuda.current_device()}, the tensors are "
-                           f"on {device}: call under torch.cuda.device({device.index})")
+                           f"on {device}: call under torch.cuda.device({index})")
 
 
 def _dev(a, device) -> torch.Tensor:
