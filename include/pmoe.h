@@ -395,7 +395,10 @@ pmoe_status adapter_cayley_grad(int32_t nblk, int32_t b, const float *S, const f
  * are never stored: the forward keeps one (max, sum) pair per token and 128
  * vocabulary entries, the backward recomputes z in pieces of the vocabulary
  * and holds G = dL/dz of one piece in the workspace (at most 512 MiB, or 256
- * entries of the vocabulary).
+ * entries of the vocabulary).  Beside G the backward's workspace holds 6 bytes
+ * for each of the T d hidden values (dX's FP32 sums and a copy of X), the parts
+ * of the tiles that are cut among the SMs (some tens of MB) and about 8 KB a
+ * token of lists; for a teacher, 18 bytes per token and 128 vocabulary entries.
  *   T >= 0 tokens, d % 64 == 0, d <= 8192, 1 <= V < 2^24, T <= 2^24
  *   K  teacher entries per token (distillation), <= 256; ignored otherwise
  *   scale  factor of every logit, 1 / temperature: finite and > 0

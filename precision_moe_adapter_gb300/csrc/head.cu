@@ -510,13 +510,15 @@ __global__ void __launch_bounds__(kLargeThreads) k_head_large(int nx, int T, con
 
 struct Parts {
     int mt, nt, gm, whole, tile, splits;   // the tiling of DX (tile: rows and columns)
+    int cut, rows, cols;                   // cut tiles, and what is kept of one
 };
-// dX = bf16(sum of the FP32 parts): one part where the tile was taken whole.
+// dX = bf16(sum of the FP32 parts): `first` holds every tile's first part, `rest`
+// [splits - 1][cut][rows][cols] the further ones of the tiles that were cut.
 // T x d (d % 64 == 0), a thread 4 columns of a row; kS threads share the parts
 // of the same columns, and their sums are added in order.
 template <int kS>
-__global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const float *__restrict__ part,
-                                                  uint16_t *__restrict__ out)
+__global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const float *__restrict__ first,
+                                                  const float *__restrict__ rest, uint16_t *__restrict__ out)
 {
     __shared__ float4 sh[kS > 1 ? 256 : 1];
     constexpr int kCols = 256 / kS;
@@ -526,12 +528,14 @@ __global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const f
     grid_go();
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < n) {
-        const int m = (int)(i / d) / p.tile, c = (int)(i % d) / p.tile, g = m / p.gm;
+        const int row = (int)(i / d), col = (int)(i % d), m = row / p.tile, c = col / p.tile, g = m / p.gm;
         const int item = g * p.gm * p.nt + c * min(p.gm, p.mt - g * p.gm) + m - g * p.gm;
         const int parts = item < p.whole ? 1 : p.splits;
+        const float *x1 = rest + ((int64_t)(item - p.whole) * p.rows + row - m * p.tile) * p.cols + col - c * p.tile;
+        const int64_t step = (int64_t)p.cut * p.rows * p.cols;
 #pragma unroll 4
         for (int s = strand; s < parts; s += kS) {
-            const float4 x = *(const float4 *)(part + s * n + i);
+            const float4 x = *(const float4 *)(s == 0 ? first + i : x1 + (s - 1) * step);
             a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
         }
     }
@@ -663,7 +667,8 @@ struct Ws {
     int32_t *lidx[2];        // [steps][64]
     uint16_t *lo[2];         // [steps] remainders: DX [256 tokens][64], DW [64][256 entries]
     int max_steps[2];
-    float *dx;               // [splits][T][d]
+    float *dx, *dxp;         // FP32 parts of dX: [T][d], and those of the cut tiles beyond the first
+    Parts parts;
     size_t bytes;
 };
 static Ws carve(void *base, const pmoe_head_dims &h, int op)
@@ -709,7 +714,11 @@ static Ws carve(void *base, const pmoe_head_dims &h, int op)
             w.lidx[i] = (int32_t *)take((size_t)w.max_steps[i] * 64 * 4);
             w.lo[i] = (uint16_t *)take((size_t)w.max_steps[i] * 64 * kListRows * 2);
         }
-        if (t.splits > 1 || piece < h.V) w.dx = (float *)take((size_t)t.splits * T * h.d * 4);
+        // (few tokens: only their rows of a tile are kept; T = 1 writes its row and no more)
+        w.parts = {t.mt, t.nt, t.gm, t.whole, t.bn, t.splits, t.mt * t.nt - t.whole, std::min(t.bn, h.T), std::min(t.bn, h.d)};
+        if (t.splits > 1 || piece < h.V) w.dx = (float *)take(T * h.d * 4);
+        if (t.splits > 1)
+            w.dxp = (float *)take((size_t)(t.splits - 1) * w.parts.cut * w.parts.rows * w.parts.cols * 4);
     }
     w.bytes = off;
     return w;
@@ -751,35 +760,39 @@ static bool map_operand(CUtensorMap *m, const Operand &o)
 }
 
 template <int CTAS, int BN, int EPI>
-static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtensorMap &mb, const CUtensorMap &mo, const CUtensorMap (&ml)[2],
-                      const Args &a, cudaStream_t st)
+static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtensorMap &mb, const CUtensorMap (&mo)[2],
+                      const CUtensorMap (&ml)[2], const Args &a, cudaStream_t st)
 {
     constexpr auto kern = k_head_gemm<CTAS, BN, EPI>;
     if (!set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(smem_of(BN))) return false;
     const int64_t items = a.whole + ((int64_t)a.mt * a.nt - a.whole) * a.splits;
     const int64_t clusters = std::min<int64_t>(items, gemm_num_sms() / CTAS);
     return launch_chained<kern>((unsigned)(clusters * CTAS), threads_of(BN),
-                          smem_of(BN), CTAS, st, ma, mt, mb, mo, ml[0], ml[1], a);
+                          smem_of(BN), CTAS, st, ma, mt, mb, mo[0], mo[1], ml[0], ml[1], a);
 }
 
-// One product: M x N outputs over ksteps K steps, with the tiles of `t`;
+// One product: M x N outputs over ksteps K steps, with the tiles of `t`; `out`,
+// `part`: the maps of the outputs and of the cut tiles' further parts (or NULL);
 // `lo`: DX, DW: the remainders of G's large entries
 template <int EPI>
-static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CUtensorMap *out, const Operand *lo, Args a,
-                   cudaStream_t st)
+static bool launch(const Tiling &t, const Operand &A, const Operand &B, const CUtensorMap *out, const CUtensorMap *part,
+                   const Operand *lo, Args a, cudaStream_t st)
 {
-    CUtensorMap ma, mt, mb, mo, ml[2];
-    if (!map_operand(&ma, A) || !map_operand(&mb, B)) return false;
+    CUtensorMap ma, mt, mb, mo[2], ml[2];
     a.tail = (int)(A.rows % 128);
+    // (fewer than 128 rows: A's only boxes are the tail's)
+    memset(&ma, 0, sizeof ma);
+    if (((A.mn || A.rows >= 128) && !map_operand(&ma, A)) || !map_operand(&mb, B)) return false;
     a.abytes = kOpBytes;
     // (with extra K steps A's tiles are always whole)
     if ((EPI == HG_FWD || EPI == HG_GRAD) && A.rows < 128) a.abytes = (int)cdiv(a.tail, 8) * 1024;
     a.stages = std::min(kMaxStages, kRingBytes / (kOpBytes + a.abytes));
     memset(&mt, 0, sizeof mt);
     if (!A.mn && a.tail && !make_map(&mt, A.base, false, A.cols, A.rows, 0, kBK, a.tail)) return false;
-    memset(&mo, 0, sizeof mo);
+    memset(mo, 0, sizeof mo);
     memset(ml, 0, sizeof ml);
-    if (out) mo = *out;
+    if (out) mo[0] = *out;
+    if (part) mo[1] = *part;
     // (rows of B are gathered one by one: boxes of one row)
     if (lo && (!map_operand(&ml[0], *lo) || !make_map(&ml[1], B.base, false, B.cols, B.rows, 0, kBK, 1))) return false;
     a.mt = t.mt;
@@ -832,8 +845,8 @@ static pmoe_status forward(const pmoe_head_dims &h, const void *X, const void *W
     a.K = K;
     a.err = w.err;
     tc::take_wait_hook(a.wait_ns, a.skip_item);
-    if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr, a,
-                        st))
+    if (!launch<HG_FWD>(tiling(h.T, h.V, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, nullptr, nullptr,
+                        nullptr, a, st))
         return PMOE_ERR_CUDA;
     return launch_chained<k_head_combine>((unsigned)h.T, 128, 0, 1, st, h.V, K, a.NU, h.d, scale, a.c, (const uint16_t *)X,
                           (const uint16_t *)W, w.part, w.zt, a.target, w.nent, w.q, w.h, w.an, value, lse, w.err)
@@ -895,7 +908,7 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.anchor_g = (const float4 *)w.an.g;
             if (!make_map(&mo, w.G, false, ldg, h.T, 1, 64, 32) ||
                 !launch<HG_GRAD>(tiling(h.T, vc, a.ksteps, false), {X, h.d, h.T, false}, {W, h.d, h.V, false}, &mo,
-                                 nullptr, a, st))
+                                 nullptr, nullptr, a, st))
                 return PMOE_ERR_CUDA;
         }
         const int nx = dX ? (int)cdiv(h.T, kListRows) : 0, nw = dW ? (int)cdiv(vc, kListRows) : 0;
@@ -915,8 +928,11 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.bf16_out = w.dx == nullptr;
             a.accumulate = v0 > 0;
             Tiling t = tx;
-            const bool made = w.dx ? make_map(&mo, w.dx, true, h.d, h.T, tx.splits, 32, 32)
-                                   : make_map(&mo, dX, false, h.d, h.T, 1, 64, 32);
+            CUtensorMap mp;
+            const Parts &p = w.parts;
+            const bool made =
+                (w.dx ? make_map(&mo, w.dx, true, h.d, h.T, 1, 32, 32) : make_map(&mo, dX, false, h.d, h.T, 1, 64, 32)) &&
+                (!w.dxp || make_map(&mp, w.dxp, true, p.cols, p.rows, (int64_t)(p.splits - 1) * p.cut, 32, 32));
             // (a last, shorter piece: shorter parts, perhaps fewer; the other sums then stand)
             t.kper = (int)cdiv(a.ksteps, tx.splits);
             t.splits = (int)cdiv(a.ksteps, t.kper);
@@ -924,7 +940,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.lidx = w.lidx[0];
             a.lb0 = v0;
             const Operand lo{w.lo[0], 64, (int64_t)w.max_steps[0] * kListRows, false};
-            if (!made || !launch<HG_DX>(t, {w.G, ldg, h.T, false}, {W, h.d, h.V, true}, &mo, &lo, a, st))
+            if (!made ||
+                !launch<HG_DX>(t, {w.G, ldg, h.T, false}, {W, h.d, h.V, true}, &mo, w.dxp ? &mp : nullptr, &lo, a, st))
                 return PMOE_ERR_CUDA;
         }
         if (dW) {
@@ -938,20 +955,19 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
             a.lidx = w.lidx[1];
             const Operand lo{w.lo[1], kListRows, (int64_t)w.max_steps[1] * 64, true};
             if (!make_map(&mo, (uint16_t *)dW + (int64_t)v0 * h.d, false, h.d, vc, 1, 64, 32) ||
-                !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {xz, h.d, h.T, true}, &mo, &lo, a,
-                               st))
+                !launch<HG_DW>(tiling(vc, h.d, a.ksteps, false), {w.G, ldg, h.T, true}, {xz, h.d, h.T, true}, &mo, nullptr,
+                               &lo, a, st))
                 return PMOE_ERR_CUDA;
         }
     }
     if (dX && w.dx) {
         const int64_t n = (int64_t)h.T * h.d;
-        const Parts parts{tx.mt, tx.nt, tx.gm, tx.whole, tx.bn, tx.splits};
         // (64 parts of 60 x 64: one thread for all parts of its columns takes 10 us)
         const bool ok = tx.splits >= 16
-                            ? launch_chained<k_head_sum<16>>((unsigned)cdiv(n, 64), 256, 0, 1, st, h.T, h.d, parts, w.dx,
-                                                             (uint16_t *)dX)
-                            : launch_chained<k_head_sum<1>>((unsigned)cdiv(n, 1024), 256, 0, 1, st, h.T, h.d, parts, w.dx,
-                                                            (uint16_t *)dX);
+                            ? launch_chained<k_head_sum<16>>((unsigned)cdiv(n, 64), 256, 0, 1, st, h.T, h.d, w.parts, w.dx,
+                                                             w.dxp, (uint16_t *)dX)
+                            : launch_chained<k_head_sum<1>>((unsigned)cdiv(n, 1024), 256, 0, 1, st, h.T, h.d, w.parts, w.dx,
+                                                            w.dxp, (uint16_t *)dX);
         if (!ok) return PMOE_ERR_CUDA;
     }
     return PMOE_OK;

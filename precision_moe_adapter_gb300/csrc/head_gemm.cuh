@@ -338,6 +338,7 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi)
 
 struct Item {
     int m, n, s;   // m tile, n tile, split
+    int part;      // s > 0: place among the further parts of the cut tiles
     int k0, k1;    // K steps
 };
 // Work item i (the whole tiles, then the others' first parts, their second
@@ -352,6 +353,7 @@ __device__ __forceinline__ bool item_of(const Args &a, int i, Item &t)
         if (i - a.whole >= cut * a.splits) return false;
         t.s = (i - a.whole) / cut;
         i -= t.s * cut;
+        t.part = (t.s - 1) * cut + i - a.whole;
         t.k0 = t.s * a.kper;
         t.k1 = min(t.k0 + a.kper, a.ksteps);
     }
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                                                                  const __grid_constant__ CUtensorMap tmAt,
                                                                  const __grid_constant__ CUtensorMap tmB,
                                                                  const __grid_constant__ CUtensorMap tmOut,
+                                                                 const __grid_constant__ CUtensorMap tmPart,
                                                                  const __grid_constant__ CUtensorMap tmLoA,
                                                                  const __grid_constant__ CUtensorMap tmLoB,
                                                                  const Args a)
@@ -582,7 +585,11 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_head_gemm(const __grid_co
                 auto put = [&](int x, int xoff = 0) {   // the staged box goes out at column x (+ xoff)
                     tc::fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0 && x < a.N && yr < a.M) store_3d(&tmOut, ob, x + xoff, yr, t.s, a.accumulate != 0);
+                    if (lane == 0 && x < a.N && yr < a.M) {
+                        if (EPI == HG_DX && t.s > 0)    // a tile of its own
+                            store_3d(&tmPart, ob, x - t.n * BN, yr - t.m * CTAS * 128, t.part, a.accumulate != 0);
+                        else store_3d(&tmOut, ob, x + xoff, yr, 0, a.accumulate != 0);
+                    }
                 };
                 auto reuse = [&]() {                             // the previous box has been read
                     if (lane == 0) store_wait_read();

@@ -105,3 +105,14 @@ def test_calls_on_another_device_are_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     layer.check_current(torch.device("cuda", 1))
     layer.check_current(torch.device("cpu"))
+
+
+@pytest.mark.parametrize("T,d,V", [(32768, 7168, 163840), (20000, 7168, 131072), (8192, 7168, 163840), (4096, 2048, 131072),
+                                   (1, 8192, 131072), (64, 2048, 32000), (100000, 512, 163840)])
+def test_backward_workspace_is_what_the_header_says(L, T, d, V):
+    """G of a piece, 6 bytes per hidden value, the parts of the cut tiles (fewer
+    than 152 tiles of 64 KB, or 76 of 256 KB, times at most a few tens), about
+    8 KB a token: not a whole FP32 dX for every part of a cut tile."""
+    G = max(512 << 20, T * 512)
+    n = pmoe.head_workspace_bytes(pmoe.head_dims(T, d, V), pmoe.HEAD_BACKWARD)
+    assert n <= G + 6 * T * d + (192 << 20) + 8600 * T
