@@ -507,7 +507,8 @@ pmoe_status head_distill_backward(pmoe_head_dims dims, const void *X, const void
  *   dlogits f32 [T, E] (out, overwritten); its column sums are the gradient of
  *           the router bias
  *   ws      >= moe_balance_ws_bytes(dims, nseq)
- * dims: T, E and k are used; 1 <= nseq <= 2^20.  Fixed summation order.
+ * dims: T, E and k are used (E <= 4096, k <= 32), the others may be anything;
+ * 1 <= nseq <= 2^20.  Fixed summation order.
  */
 size_t moe_balance_ws_bytes(pmoe_dims dims, int32_t nseq);
 pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32_t *idx,

@@ -456,6 +456,13 @@ static void by_experts(int E, F f)
     else by_width<1>(E, f);
 }
 
+// T, E and k alone: a router needs no layer behind it
+static bool sizes_ok(const pmoe_dims &d, int nseq)
+{
+    return d.T >= 0 && d.E > 0 && d.E <= 4096 && d.k > 0 && d.k <= 32 && d.k <= d.E &&
+           (int64_t)d.T * d.k <= INT32_MAX / 2 && nseq >= 1 && nseq <= (1 << 20);
+}
+
 static bool aligned(std::initializer_list<const void *> ps)
 {
     for (const void *p : ps)
@@ -472,7 +479,7 @@ extern "C" {
 
 size_t moe_balance_ws_bytes(pmoe_dims dims, int32_t nseq)
 {
-    if (!dims_ok(dims) || nseq < 1 || nseq > (1 << 20)) return 0;
+    if (!bal::sizes_ok(dims, nseq)) return 0;
     return bal::carve(nullptr, dims.T, dims.E, nseq).bytes;
 }
 
@@ -480,7 +487,7 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
                                 const int32_t *seq, int32_t nseq, int32_t *counts, int32_t *ntok, float *pmean,
                                 float *loss, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
-    if (!dims_ok(dims) || nseq < 1 || nseq > (1 << 20) || (!seq && nseq != 1)) return PMOE_ERR_INVALID_ARG;
+    if (!bal::sizes_ok(dims, nseq) || (!seq && nseq != 1)) return PMOE_ERR_INVALID_ARG;
     if ((dims.T > 0 && (!logits || !idx)) || !counts || !ntok || !pmean || !loss) return PMOE_ERR_INVALID_ARG;
     if (!bal::aligned({logits, idx, valid, seq, counts, ntok, pmean, loss})) return PMOE_ERR_INVALID_ARG;
     const bal::Ws w = bal::carve(ws, dims.T, dims.E, nseq);
@@ -510,7 +517,7 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
                                const int32_t *counts, const int32_t *ntok, const float *g_loss, float *dlogits, void *ws,
                                size_t ws_bytes, cudaStream_t stream)
 {
-    if (!dims_ok(dims) || nseq < 1 || nseq > (1 << 20) || (!seq && nseq != 1)) return PMOE_ERR_INVALID_ARG;
+    if (!bal::sizes_ok(dims, nseq) || (!seq && nseq != 1)) return PMOE_ERR_INVALID_ARG;
     if (!d_topk_w && !g_loss) return PMOE_ERR_INVALID_ARG;
     if (dims.T > 0 && (!dlogits || (d_topk_w && (!idx || !w)) || (g_loss && (!logits || !counts || !ntok))))
         return PMOE_ERR_INVALID_ARG;

@@ -248,3 +248,18 @@ def test_refusals():
         assert bwd(*(good[:i] + [v] + good[i + 1:])) == INV, (i, v)
     assert bwd(*(good[:4] + [None] + good[5:10] + [None] + good[11:])) == INV     # neither term
     assert bwd(*(good[:12] + [None] + good[13:])) == WS
+
+
+def test_a_router_without_a_layer():
+    """The sizes that the operators do not use are not looked at; those that
+    they use are."""
+    bare, full = pmoe.dims(64, 0, 8, 2, 0, 0), pmoe.dims(64, 64, 8, 2, 64, 16)
+    assert pmoe.moe_balance_ws_bytes(bare, 3) == pmoe.moe_balance_ws_bytes(full, 3) > 256
+    assert pmoe.moe_balance_ws_bytes(pmoe.dims(64, 100, 8, 2, 100, 7), 1) > 256
+    for bad in ((-1, 8, 2), (64, 0, 2), (64, 4097, 2), (64, 8, 0), (64, 40, 33), (64, 8, 9), (1 << 28, 8, 5)):
+        assert pmoe.moe_balance_ws_bytes(pmoe.dims(bad[0], 0, bad[1], bad[2], 0, 0), 1) == 0, bad
+    L, buf = pmoe.lib(), ctypes.create_string_buffer(64)
+    p = ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 16
+    WS = pmoe.PMOE_ERR_WORKSPACE                          # (past the checks of the sizes)
+    assert L.moe_balance_forward(bare, p, p, None, None, 1, p, p, p, p, p, 256, None) == WS
+    assert L.moe_route_backward(bare, p, p, p, p, None, None, 1, p, p, p, p, p, 256, None) == WS
