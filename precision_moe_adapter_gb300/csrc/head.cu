@@ -41,12 +41,13 @@ struct TeacherGrad {
 
 // x . w over d columns by a warp: exact products of BF16 rows, 8 columns a lane
 // at a time, then a tree.  The order is fixed, so forward and backward agree.
-__device__ __forceinline__ float row_dot(const uint16_t *__restrict__ x, const uint16_t *__restrict__ w, int d)
+// (Read past L1: the forward's call comes before its kernel's wait.)
+__device__ __forceinline__ float row_dot(const uint16_t *x, const uint16_t *w, int d)
 {
     float a = 0.f;
 #pragma unroll 4
     for (int i = threadIdx.x & 31; i < d / 8; i += 32) {
-        const uint4 u = ((const uint4 *)x)[i], v = ((const uint4 *)w)[i];
+        const uint4 u = __ldcg((const uint4 *)x + i), v = __ldcg((const uint4 *)w + i);
         const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(128) k_head_combine(int V, int K, int NU, int 
     // (before the wait: all of this was complete when the GEMM before started)
     int id[kAnchors] = {-1, -1, -1, -1}, place[kAnchors] = {0, 0, 0, 0};
     if (target) {
-        const int y = target[t];
+        const int y = __ldcg(target + t);
         if (y >= V && threadIdx.x == 0) record_error(err, PMOE_ERR_BAD_INDEX, (int)t, y);
         if (y >= 0 && y < V) id[0] = y;
     } else {

@@ -1,10 +1,17 @@
 // pdl.cuh -- programmatic dependent launch: a kernel of a chain starts (its
 // launch latency and set-up) while the kernel before it in the stream still
-// runs.  Every kernel launched this way calls grid_wait() before it reads or
-// writes anything in global memory: it returns once the kernel before has
-// completed and its writes are visible, and as that kernel waited in turn,
-// so has everything earlier in the stream.  grid_go() lets the next kernel's
-// CTAs be placed as soon as all of this kernel's have started.
+// runs.  Every kernel launched this way calls grid_wait(): it returns once the
+// kernel before has completed and its writes are visible, and as that kernel
+// waited in turn, so has everything earlier in the stream.  grid_go() lets the
+// next kernel's CTAs be placed as soon as all of this kernel's have called it.
+//
+// Before its wait a kernel touches global memory in two places only:
+// k_head_combine reads the tokens' targets, anchors and rows of X and W, and
+// k_head_gemm<DW> behind DX reads G and its lists and writes dW.  Both rest on
+// this: the kernel before calls grid_go() after its own wait, so when the one
+// behind it starts, everything before that kernel is complete.  What is touched
+// early is nothing that the kernel before writes (nor, for dW, reads), and it is
+// read past L1 (__ldcg, TMA), which may hold lines of an earlier call.
 #pragma once
 
 #include <cuda_runtime.h>

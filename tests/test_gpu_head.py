@@ -542,3 +542,25 @@ def test_a_wait_that_runs_out_is_reported(T, d, V):
         assert h.status() == pmoe.PMOE_OK
         assert x is None or torch.equal(x, ref[3])
         assert w is None or torch.equal(w, ref[4])
+
+
+def test_inputs_rewritten_between_calls():
+    """Calls behind one another on a stream, each behind kernels that have just
+    rewritten the hidden states, the targets and the head in place: every call
+    sees its own."""
+    T, d, V = 130, 256, 1003
+    sets = [make(T, d, V, seed=i)[:4] for i in range(4)]
+    want = [run_logprob(*s, 1.0)[1:] for s in sets]
+    X, W, y, up = (t.clone() for t in sets[0])
+    h = DeviceHead(W, T)
+    got = []
+    for i in range(24):
+        for t, new in zip((X, W, y, up), sets[i % 4]):
+            t.copy_(new)
+        logp, lse, dX, dW = (torch.empty_like(t) for t in want[0])
+        h.logprob(X, y, logp, lse)
+        h.logprob_backward(X, y, lse, up, dX, dW)
+        got.append((logp, lse, dX, dW))
+    for i, g in enumerate(got):
+        for a, b in zip(g, want[i % 4]):
+            assert torch.equal(a, b), i
