@@ -11,7 +11,6 @@
 #include <cmath>
 
 #include "common.cuh"
-#include "launch.h"
 #include "pdl.cuh"
 
 namespace pmoe {

@@ -40,15 +40,10 @@ bool set_attribute(int value)
     return true;
 }
 
-// Launches kernel K, which begins with grid_wait(), in clusters of `cluster`
-// CTAs.  Every kernel of a chain asks for the SM's memory to be all shared
-// memory, as the GEMMs need it: an SM that has to change the split between
-// two kernels waits until it is empty (13 us over the 8 launches of a small
-// distillation step).
+// Launches kernel K, which calls grid_wait(), in clusters of `cluster` CTAs
 template <auto K, class... A>
 bool launch_chained(unsigned grid, unsigned block, size_t smem, unsigned cluster, cudaStream_t st, A... args)
 {
-    if (!set_attribute<K, cudaFuncAttributePreferredSharedMemoryCarveout>(cudaSharedmemCarveoutMaxShared)) return false;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
