@@ -497,13 +497,15 @@ pmoe_status moe_balance_forward(pmoe_dims dims, const float *logits, const int32
             constexpr auto kern = bal::k_balance_partial<tpt.value, v.value, ni.value>;
             const size_t sm = (size_t)(bal::fwd_threads(tpt.value) / tpt.value + 1) * w.Ep * 4;
             // (up to 17 rows of 1024 floats: 69 KB)
-            ok = set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(17 * 4096) && launch_chained<kern>((unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E, dims.k,
-                                w.L, w.Ep, logits, idx, valid, seq, nseq, w.psum, w.cnt, w.ntok, w.err);
+            ok = set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(17 * 4096) &&
+                 launch_chained<kern>((unsigned)cdiv(dims.T, w.L), bal::fwd_threads(tpt.value), sm, 1, stream, dims.T, dims.E,
+                                dims.k, w.L, w.Ep, logits, idx, valid, seq, nseq, w.psum, w.cnt, w.ntok, w.err);
         });
     // CTAs per sequence: 32 experts each up to 8 CTAs, then more experts each
     const int cols = (int)(cdiv(dims.E, 256) * 32), C = (int)cdiv(dims.E, cols);
-    // few slots a sequence: smaller CTAs start sooner (37 sequences of 16384 tokens: 8.5 us with 1024
-    // threads); one long sequence: more strands (8192 tokens, 6.3 us with 1024, 8.5 with 512)
+    // few slots a sequence: smaller CTAs start sooner (forward of 37 sequences of 16384 tokens, E = 256:
+    // 12.6 us with 256 threads, 15.0 with 1024); one long sequence: more strands (8192 tokens, E = 384:
+    // 8.9 us with 1024, 11.8 with 256)
     const unsigned threads = w.slots / nseq >= 64 ? bal::kRedThreads : std::max(256, cols);
     ok = ok && launch_chained<bal::k_balance_reduce>((unsigned)(nseq * C), threads, 0, C, stream, dims.T, dims.E,
                               dims.k, w.L, w.Ep, cols, C, seq, nseq, w.psum, w.cnt, w.ntok, counts, ntok, pmean, loss,

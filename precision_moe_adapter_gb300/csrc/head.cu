@@ -62,7 +62,7 @@ __device__ __forceinline__ float row_dot(const uint16_t *x, const uint16_t *w, i
 // dW = G^T X would take 0 * NaN from a row of X that has no gradient, whatever
 // it holds: DW reads a copy in which such rows are zero, made by the warp that
 // knows the row's factor.  (T = 4096, d = 2048, V = 32000, forward and both
-// gradients: 1352 us with the copy, 1341 without.)
+// gradients: 1351 us with the copy, 1343 without.)
 __device__ __forceinline__ void copy_row(uint16_t *__restrict__ out, const uint16_t *__restrict__ x, int d, float cf)
 {
 #pragma unroll 4
@@ -96,9 +96,9 @@ __device__ __forceinline__ void clear(int *p, int n)
 // holds 256 + the place of its first and mask its columns, so that the GEMM's
 // epilogue takes a unit's entries one after the other.
 // A warp per token sorts 32 kN words (id << 8 | slot; kGone last) in its
-// registers, word i of a lane being element 32 i + lane, by a bitonic network:
-// comparing every entry with every other one took 17 us at T = 4096, K = 64,
-// against 5.
+// registers, word i of a lane being element 32 i + lane, by a bitonic network
+// (comparing every entry with every other one takes K / 32 times as many steps
+// as there are words).
 constexpr uint32_t kGone = 0xFFFFFFFFu;   // (V < 2^24: no id reaches it)
 template <int kN>
 __global__ void __launch_bounds__(128) k_head_teacher(int T, int V, int K, float scale, const int32_t *__restrict__ t_idx,
@@ -563,8 +563,8 @@ static bool head_ok(const pmoe_head_dims &h)
 // Vocabulary entries per piece of the backward: G of one piece is at most
 // kPieceBytes; pieces of equal size, multiples of 256.  Every further piece
 // adds dX's FP32 sums to memory once more: T = 4096, d = 2048, V = 131072 runs
-// its backward in 2713 us with pieces of 128 MB, 2564 with 256, 2497 with 512,
-// 2463 with 1024.
+// its backward in 2826 us with pieces of 128 MB, 2701 with 256, 2675 with 512,
+// 2645 with 1024.
 static int piece_of(int T, int V)
 {
     int64_t most = kPieceBytes / (2ll * std::max(T, 1)) / 256 * 256;
@@ -578,7 +578,8 @@ static int piece_of(int T, int V)
 // 2.5 large entries a token, the lists lengthen K by 640 / V and DW's take one
 // CTA 0.33 us for every 64 entries of its block; two terms double K and write G
 // twice.  (Forward and both gradients, two terms against lists: T = 4013, d = 192,
-// V = 263 45 against 151 us; T = 8000, d = 128, V = 1500 86 against 131.)
+// V = 263 46 against 145 us; T = 8000, d = 128, V = 1500 84 against 129; at T = 4000,
+// d = 512, V = 3000 both take 91.)
 static int terms_of(const pmoe_head_dims &h)
 {
     const int piece = piece_of(h.T, h.V);
@@ -596,8 +597,8 @@ struct Tiling {
 };
 // Tiles of an M x N product over ksteps K steps.  `split`: tiles of the last,
 // partly filled round may be cut along K, their parts then being added up.
-// (T = 4096, d = 2048, V = 131072: backward 2591 us without, 2497 with; T = 64,
-// V = 32000: 117 us without, 54 with.)
+// (T = 4096, d = 2048, V = 131072: backward 2692 us without, 2675 with; T = 64,
+// V = 32000: 127 us without, 57 with.)
 // The number of parts is the one of least time by this estimate: a K step of
 // a tile takes 0.28 us (the tensor cores' rate at 1.8 GHz), each round 2 us
 // to fill and to drain, each part's FP32 tile goes to memory and back, and
@@ -607,17 +608,18 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool split)
     Tiling t;
     // A pair of CTAs on a 256 x 256 tile reads each operand half as often as
     // single CTAs on 128 x 128; single CTAs fill the GPU with smaller products.
-    // Forward and backward at d = 2048, singles against pairs: 38 tiles of 256
-    // (T = 512, V = 4864) 53.6 against 57.8 us, 76 tiles (T = 1024) 68 against
-    // 72, 152 tiles 103 against 101; policy-sized products 44.8 against 31.9 ms.
+    // Forward and backward at d = 2048, V = 4864, singles for all products against
+    // pairs for all: 38 tiles of 256 (T = 512) 53.8 against 59.6 us, 76 tiles
+    // (T = 1024) 74 against 76 (71 by this rule: dX has fewer), 152 tiles
+    // (T = 2048) 123 against 104 (115 by this rule, dX's 64 tiles as singles).
     t.ctas = cdiv(M, 256) * cdiv(N, 256) >= kSms / 2 && M > 128 ? 2 : 1;
     t.bn = 128 * t.ctas;
     t.mt = (int)cdiv(M, 128 * t.ctas);
     t.nt = (int)cdiv(N, t.bn);
     // m tiles that run together: their rows of A stay in L2 while the n tiles
     // pass; groups of equal size.  T = 8192, d = 7168, V = 32768, forward and
-    // backward: 6.36 ms with groups of 8 tiles, 6.41 with 48 MB, 6.85 with 96 MB
-    // or all tiles; at T = 4096, d = 2048 all are within 2%.
+    // backward: 6.78 ms by this rule, 6.82 with groups of 8 tiles, 6.99 with 48 MB
+    // alone, 6.96 with 96 MB, 7.39 with all tiles in one group.
     const int64_t stripe = 2ll * 128 * t.ctas * ksteps * kBK;
     const int64_t most = std::max<int64_t>(8, (48ll << 20) / std::max<int64_t>(stripe, 1));
     t.gm = (int)cdiv(t.mt, cdiv(t.mt, most));
@@ -963,7 +965,8 @@ static pmoe_status backward(const pmoe_head_dims &h, const void *X, const void *
     }
     if (dX && w.dx) {
         const int64_t n = (int64_t)h.T * h.d;
-        // (64 parts of 60 x 64: one thread for all parts of its columns takes 10 us)
+        // (T = 60, d = 64, V = 38592, a tile in 64 parts: the backward takes 29.4 us with 16 threads for
+        // the parts of a column, 29.9 with one)
         const bool ok = tx.splits >= 16
                             ? launch_chained<k_head_sum<16>>((unsigned)cdiv(n, 64), 256, 0, 1, st, h.T, h.d, w.parts, w.dx,
                                                              w.dxp, (uint16_t *)dX)

@@ -14,8 +14,8 @@
 // Roles (CTAS CTAs of one cluster work on one CTAS*128 x BN tile; persistent
 // over the tiles):
 //   warps 0, 3  TMA producers of this CTA's 128 rows of A, and of its BN/CTAS
-//               rows of B (a warp issues a copy every 150 clocks or so: one
-//               for both would bound the smaller tiles)
+//               rows of B (one warp for both would bound the
+//               smaller tiles by the rate at which it issues copies)
 //   warp 1      MMA issuer (CTA 0 of the cluster only), K steps of 64
 //   warp 2      TMEM allocator
 //   warps 4..   epilogue, one warp per 32 TMEM lanes and 128 columns: a
@@ -33,12 +33,15 @@
 // runs of 512 columns, relative error about 5e-7; GRAD takes the same runs, so
 // that its logits are the forward's bit for bit and p - 1 of a confident token
 // does not see their error.  The other results are rounded to BF16, so longer
-// runs do.  (Runs of 256 columns in FWD and GRAD cost a policy step 4%.)
+// runs do.  (Runs of 256 columns in FWD and GRAD cost a step at
+// T = 4096, d = 2048, V = 131072 1 to 2%.)
 // The two buffers alternate, so the tensor cores work on the next chunk while
 // one is drained, and on the next tile's first two chunks during the epilogue
 // proper: 91 to 97% of the tensor pipe's cycles are busy at T = 4096, d = 2048,
 // V = 32768, and a step at T = 8192, d = 7168, V = 131072 runs its three
-// products at 1.67 PFLOP/s (27.7 ms), the card's sustained rate.
+// products at 1.65 to 1.72 PFLOP/s (27 to 28 ms), the card's sustained rate.
+// Exponentials are ex2.approx, whose relative error PTX bounds by about 2^-22;
+// their arguments are rounded once, 2^-24 of their size.
 //
 // G is the BF16 operand of two products.  Where a token's distribution is
 // concentrated, a few large entries of G carry the whole gradient, and their
@@ -50,16 +53,22 @@
 // one list per 256 output rows), B the matching rows of W or X, gathered by
 // TMA.  That is a few steps per tile of the hundreds the product has;
 // remainders of whole tiles would double the steps of every tile that holds a
-// large entry.  (Where the vocabulary is so
-// small that the lists would be long, all remainders are kept beside G and
-// the products run over both: head.cu, `terms`.)
+// large entry.  (Where the vocabulary is so small that the lists would be long,
+// all remainders are kept beside G and the products run over both: head.cu,
+// `terms`.)  A teacher that is spread over many entries has none that large, and
+// its gradient takes the rounding of G's entries to 8 bits beside its own: dX at
+// T = 4096, d = 2048, V = 131072, K = 64 (the largest q about 0.16) is 1.95e-3 from
+// FP64, 1.66e-3 being dX's own rounding.  Listing from 1/16 (up to 32 entries a
+// token) gives 1.78e-3 and from 1/32 1.72e-3, for 0 and 3% of that step but 26 and
+// 94% of one at T = 1024, d = 512, V = 32000, K = 16 with both gradients.
 //
 // Anchors: where a token's target (or an entry of the teacher) holds much of
 // the probability, the value and G there are differences of nearly equal
 // numbers, and the tensor cores' error of z (5e-7 relative, biased) would be
 // 1e-6 and more of them.  The logits of the target, or of teacher entries
-// with q >= 1/4 (at most 4), are therefore computed again in FP32 by head.cu,
-// which corrects the sums of the forward and gives GRAD these entries of G.
+// with q >= 1/4 (at most 4), are therefore computed in FP32 by head.cu: FWD leaves
+// these columns out of its sums, so that what is left of the probability keeps
+// its own relative accuracy, and GRAD is given these entries of G.
 //
 // Every logit's sum runs over k in the same order whatever the tile shape, and
 // the softmax partials cover 128 aligned columns: the forward's results do not
@@ -173,7 +182,7 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // (what it orders are TMEM reads, which tcgen05's own fence covers; a release
-// at cluster scope would also wait for the warp's global stores, 2300 clocks)
+// at cluster scope would also wait for the warp's global stores)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -181,7 +190,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 // The calls named *_warp are made by a whole converged warp, so that their
 // operands stay in uniform registers; one elected lane issues.  (Issued from
 // a branch on the lane, each MMA or copy first moves its operands there: a K
-// step's four MMAs then take 590 clocks whatever their size.)
+// step then takes the same time whatever the tile's size.)
 template <int CTAS>
 __device__ __forceinline__ void load_2d_warp(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar)
 {
