@@ -531,13 +531,17 @@ __global__ void __launch_bounds__(256) k_head_sum(int T, int d, Parts p, const f
     if (i < n) {
         const int row = (int)(i / d), col = (int)(i % d), m = row / p.tile, c = col / p.tile, g = m / p.gm;
         const int item = g * p.gm * p.nt + c * min(p.gm, p.mt - g * p.gm) + m - g * p.gm;
-        const int parts = item < p.whole ? 1 : p.splits;
-        const float *x1 = rest + ((int64_t)(item - p.whole) * p.rows + row - m * p.tile) * p.cols + col - c * p.tile;
-        const int64_t step = (int64_t)p.cut * p.rows * p.cols;
+        if (strand == 0) a = *(const float4 *)(first + i);
+        if (item >= p.whole) {
+            const int64_t step = (int64_t)p.cut * p.rows * p.cols;
+            const int s0 = strand ? strand : kS;
+            const float *x1 = rest + ((int64_t)(item - p.whole) * p.rows + row - m * p.tile) * p.cols + col - c * p.tile +
+                              (s0 - 1) * step;
 #pragma unroll 4
-        for (int s = strand; s < parts; s += kS) {
-            const float4 x = *(const float4 *)(s == 0 ? first + i : x1 + (s - 1) * step);
-            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+            for (int s = s0; s < p.splits; s += kS, x1 += kS * step) {
+                const float4 x = *(const float4 *)x1;
+                a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+            }
         }
     }
     if constexpr (kS > 1) {
