@@ -564,3 +564,28 @@ def test_inputs_rewritten_between_calls():
     for i, g in enumerate(got):
         for a, b in zip(g, want[i % 4]):
             assert torch.equal(a, b), i
+
+
+def test_absent_teacher_entries_may_hold_anything():
+    """The logits of absent entries are not looked at, whatever they hold."""
+    T, d, V, K = 70, 128, 1003, 9
+    X, W, y, up, g = make(T, d, V)
+    ids = torch.randint(0, V, (T, K), generator=g, device="cuda").to(torch.int32)
+    gone = torch.rand((T, K), generator=g, device="cuda") < 0.4
+    gone[3] = True
+    ids[gone] = -1
+    t = 2 * torch.randn((T, K), generator=g, device="cuda")
+    out = []
+    for fill in (0.0, math.nan, math.inf, -math.inf, 3e38):
+        tf = torch.where(gone, torch.full_like(t, fill), t)
+        h = DeviceHead(W, T, K=K, scale=2.0)
+        loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        dX, dW = torch.empty_like(X), torch.empty_like(W)
+        h.distill(X, ids, tf, loss, lse)
+        h.distill_backward(X, ids, tf, lse, up, dX, dW)
+        out.append((loss, lse, dX, dW))
+        assert h.status() == pmoe.PMOE_OK
+    assert torch.isfinite(out[0][0]).all() and out[0][0][3] == 0
+    for o in out[1:]:
+        for a, b in zip(o, out[0]):
+            assert torch.equal(a, b)
