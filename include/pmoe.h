@@ -406,6 +406,8 @@ pmoe_status adapter_cayley_grad(int32_t nblk, int32_t b, const float *S, const f
  * (bit-identical across T), and every result is run-to-run identical.
  * The sums over d run in FP32 chunks of 512 columns added in FP32; the logits
  * of the target, or of teacher entries with q >= 1/4, are FP32 dot products.
+ * A log-probability is accurate relative to itself, however near to 0; the
+ * backward takes p from the FP32 lse, so 1 - p is off by up to half a unit of it.
  */
 typedef struct {
     int32_t T, d, V, K;
