@@ -523,6 +523,161 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
                                const int32_t *ntok, const float *g_loss, float *dlogits,
                                void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * moe_gate_forward / moe_gate_backward -- the gate of a layer that routes by
+ * scores, a sibling of moe_route's softmax over the chosen logits (the pages
+ * leave the router's form open; this is the form of the DeepSeek-V3 and Kimi-K2
+ * layers whose shapes the configurations have):
+ *   s = sigmoid(logits), or softmax(logits) over all E experts
+ *   c = s + bias            (the balancing bias takes part in the choice alone)
+ *   the experts lie in `groups` consecutive groups; a group counts by the sum of
+ *   its group_sum (1 or 2) largest c, the best topk_groups groups stay
+ *   idx = the k experts of these groups with the largest c, in descending order
+ *   w_j = factor s_j / (sum_i s_i + 1e-20)          (renorm; else factor s_j)
+ * Ties go to the lower group or expert.  The choice is that of the exact c: where
+ * FP32 cannot tell two of them apart they are formed in FP64 (of equal c in FP64
+ * the lower id is taken).  Without a bias the order is that of the logits.
+ * A logit of -inf is an expert that is chosen only where fewer than k others are
+ * left (with the weight 0), and adds nothing to its group; other logits and the
+ * bias are finite.
+ *   logits f32 [T, E] (as moe_router_logits writes them)   bias f32 [E] or NULL
+ *   idx    int32 [T, k] (out)      w f32 [T, k] (out): as moe_permute and
+ *          moe_chunked_forward take them
+ * Gradient, for dw = d_topk_w (of moe_backward_data) and D the denominator of w (1
+ * without renorm):
+ *   ds_j = factor / D (dw_j - [renorm] sum_i dw_i s_i / D)
+ *   sigmoid: dlogits_tj = ds_j s_j (1 - s_j) for the chosen experts, else 0
+ *   softmax: dlogits_te = s_e ([e chosen] ds_e - sum_j ds_j s_j)
+ *   idx    from the forward (an id outside [0, E) takes no part)
+ *   accumulate  nonzero: added to dlogits (for instance to the balance loss's
+ *          part of moe_route_backward), else written
+ * Requires 1 <= E <= 4096, 1 <= k <= 32, groups <= 32, E % groups == 0,
+ * k <= topk_groups E / groups, factor finite.  No workspace; a token's results do
+ * not depend on the other tokens.
+ */
+enum { PMOE_SCORE_SIGMOID = 0, PMOE_SCORE_SOFTMAX = 1 };
+typedef struct {
+    int32_t T, E, k;
+    int32_t groups, topk_groups, group_sum;   /* 1, 1, 1: no groups */
+    int32_t score;                            /* PMOE_SCORE_* */
+    int32_t renorm;
+    float factor;
+} pmoe_gate;
+pmoe_status moe_gate_forward(pmoe_gate gate, const float *logits, const float *bias, int32_t *idx,
+                             float *w, cudaStream_t stream);
+pmoe_status moe_gate_backward(pmoe_gate gate, const float *logits, const int32_t *idx,
+                              const float *d_topk_w, int accumulate, float *dlogits,
+                              cudaStream_t stream);
+
+/*
+ * moe_router_logits -- the logits of moe_route (same modes, same values) before its
+ * bias, without the choice: for moe_gate_forward.
+ *   logits f32 [T, E] (out)      the other arguments as moe_route
+ */
+pmoe_status moe_router_logits(pmoe_dims dims, const void *X, const float *Wr, float *logits,
+                              int mode, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * fp8_quantize, fp8_transpose, fp8_gemm -- 8-bit linear layers with both operands
+ * in E4M3 and FP32 scales per block (NeMo RL FP8 article, section "RL 中线性层的
+ * FP8", Table 1: weights per [128, 128], activations per [1, 128]).
+ *
+ * fp8_quantize: per row and 128 columns (the last block may be shorter)
+ *   a = max(max |x|, 2^-100);  s = a / 448, or with pow2 the least power of two
+ *   >= a / 448;  q = e4m3(x / s), the exact quotient (448 x / a) rounded to nearest, ties
+ *   to even.  A block with an infinity or a NaN becomes NaN.
+ *   X bf16 [rows, K]     q u8 [rows, K] (out)     K % 16 == 0
+ *   s f32 [ceil(K/128), rows] (out): the blocks of a column range are consecutive
+ * fp8_transpose: qt [K, N] = q^T and st [ceil(K/128), ceil(N/128)] = s^T of a weight
+ *   q u8 [N, K], s f32 [ceil(N/128), ceil(K/128)] (PMOE_W_FP8_B128_F32 with shorter
+ *   blocks at the ends): what the gradient's product reads, laid out once.
+ *   N % 16 == 0, K % 16 == 0
+ * fp8_gemm: Y[r, n] = bf16(sum_b As[b, r] Ws[n / 128, b] sum_{k in block b} A[r, k] W[n, k])
+ *   A u8 [rows, K], As f32 [ceil(K/128), rows]     (as fp8_quantize writes them)
+ *   W u8 [N, K], Ws f32 [ceil(N/128), ceil(K/128)]
+ *   Y bf16 [rows, N] (out)     N % 16 == 0, K % 16 == 0
+ *   The sum over a block runs on the tensor cores, the sum over blocks in FP32.
+ *   For few rows the blocks are shared among several CTAs, whose FP32 sums are
+ *   added in order: a row's result may differ in its last bit with the number of
+ *   rows in the call, not between runs.
+ *   ws >= fp8_gemm_ws_bytes(rows, N, K) (the error word; the shared sums)
+ * rows, N, K <= 2^20 (rows 2^24).  q, qt, A and W are E4M3 codes.
+ */
+pmoe_status fp8_quantize(int32_t rows, int32_t K, const void *X, int pow2, void *q, float *s,
+                         cudaStream_t stream);
+pmoe_status fp8_transpose(int32_t N, int32_t K, const void *q, const float *s, void *qt, float *st,
+                          cudaStream_t stream);
+size_t fp8_gemm_ws_bytes(int32_t rows, int32_t N, int32_t K);
+pmoe_status fp8_gemm(int32_t rows, int32_t N, int32_t K, const void *A, const float *As,
+                     const void *W, const float *Ws, void *Y, void *ws, size_t ws_bytes,
+                     cudaStream_t stream);
+
+/*
+ * dense_w8a8_forward / dense_w8a8_backward -- dense_linear_* with the activations
+ * in 8 bits too: a frozen FP8 projection with the orthogonal adapter on its input.
+ *   forward:  x~ = bf16(X blockdiag(R));  Y = bf16(Q(x~) W^T)
+ *   backward: dx~ = Q(dY) W;  dR = sum_rows x_blk^T dx~_blk (FP32);
+ *             dX = bf16(dx~ blockdiag(R)^T)      (R NULL: dX = bf16(Q(dY) W))
+ * with Q = fp8_quantize (along K in the forward, along N in the backward); Q's
+ * rounding is passed straight through.
+ *   q, s    W as fp8_gemm has it      qt, st   its fp8_transpose
+ *   R       bf16 [K/block, block, block] or NULL (no adapter; block is then not
+ *           looked at); block in {16, 32, 64, 128}, K % block == 0, K % 64 == 0
+ *   X       bf16 [rows, K] (in; backward: only looked at with an adapter)
+ *   Y, dY   bf16 [rows, N]    dX bf16 [rows, K]    dR f32 shaped like R (iff R)
+ *   ws      >= dense_w8a8_ws_bytes(rows, N, K, adapter), which does not fall as
+ *           rows grow: one of the largest batch serves smaller ones
+ */
+size_t dense_w8a8_ws_bytes(int32_t rows, int32_t N, int32_t K, int adapter);
+pmoe_status dense_w8a8_forward(const void *q, const float *s, int32_t N, int32_t K, int32_t block,
+                               const void *R, int32_t rows, const void *X, int pow2, void *Y,
+                               void *ws, size_t ws_bytes, cudaStream_t stream);
+pmoe_status dense_w8a8_backward(const void *qt, const float *st, int32_t N, int32_t K,
+                                int32_t block, const void *R, int32_t rows, const void *X,
+                                const void *dY, int pow2, void *dX, float *dR, void *ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * grad_norm / grad_clip -- the global norm of a list of gradients (the adapter's dS
+ * or dR of every layer, a head's dW) and clipping by it:
+ *   norm = sqrt(sum of the squares of all elements)
+ *   coef = min(1, max_norm / (norm + 1e-6));  dst = src coef, rounded to its type
+ * A NaN among the gradients makes norm and every dst NaN; an infinity makes the
+ * norm infinite, coef 0 (and its own element NaN): the caller looks at norm.
+ * The list lies on the device, made once for buffers that stay:
+ *   grad_list_fill  (host) checks n gradients and writes their table to `table`, a
+ *           host buffer of grad_list_bytes(n) bytes; the caller copies that to the
+ *           device (16-byte aligned) and sets list->table to the copy
+ *   pmoe_grad  src, dst device pointers, 16-byte aligned (dst == src: in place),
+ *           n elements (0 allowed), dtype PMOE_GRAD_*.  No dst may overlap another
+ *           entry's src or dst, nor its own src but in whole
+ *   norm    f32 [1] (out)
+ *   ws      >= grad_ws_bytes() bytes
+ * max_norm > 0 and finite.  The squares are summed in FP64 (of at most 8 in FP32),
+ * in a fixed order: results are run-to-run identical.  Where coef is 1, gradients
+ * in place are not written.
+ */
+enum { PMOE_GRAD_F32 = 0, PMOE_GRAD_BF16 = 1 };
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t n;
+    int32_t dtype;
+} pmoe_grad;
+typedef struct {
+    const void *table;   /* device */
+    int64_t chunks;      /* as grad_list_fill sets them */
+    int32_t n;
+} pmoe_grad_list;
+size_t grad_list_bytes(int32_t n);
+pmoe_status grad_list_fill(int32_t n, const pmoe_grad *grads, void *table, size_t bytes,
+                           pmoe_grad_list *list);
+size_t grad_ws_bytes(void);
+pmoe_status grad_norm(pmoe_grad_list list, float *norm, void *ws, size_t ws_bytes,
+                      cudaStream_t stream);
+pmoe_status grad_clip(pmoe_grad_list list, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                      cudaStream_t stream);
+
 /* Bytes of device workspace an op needs (op = PMOE_OP_*).  Includes the
  * 256-byte error word at the start.  In SCRATCH mode this includes the
  * C-expert BF16 dequant buffer, reported separately by

@@ -219,6 +219,45 @@ static PermWs carve_perm(void *ws, const pmoe_dims &d, size_t *bytes)
     return w;
 }
 
+// FP32 logits of the router, before its bias
+static pmoe_status router_logits(const pmoe_dims &dims, const void *X, const float *Wr, int mode, const PermWs &pw,
+                                 float *logits, cudaStream_t stream)
+{
+    if (mode == PMOE_ROUTE_EXACT) {
+        ScopedTimer tm(PMOE_KT_ROUTER, stream);
+        launch_router_exact(dims.T, dims.d, dims.E, (const uint16_t *)X, Wr, logits, stream);
+    } else {
+        ScopedTimer tm(PMOE_KT_ROUTER, stream);
+        // K splits (a function of d alone): every split is one matrix of
+        // [E, 3d / splits] and writes its own partial logits
+        const int splits = router_splits(dims.d);
+        const int ks = 3 * dims.d / splits;
+        const int rows = router_tile_rows(dims.T, dims.E, splits, gemm_num_sms());
+        launch_router_prep(dims.T, dims.d, dims.E, Wr, pw.wr3, pw.rtiles, pw.rchunk, rows, stream);
+        GemmArgs g{};
+        g.kind = GK_ROUTER;
+        g.fmt = kFmtBF16;
+        g.wq = (const uint8_t *)pw.wr3;
+        g.wq_stride = (int64_t)dims.E * ks * 2;
+        g.Nst = dims.E;
+        g.Kst = ks;
+        g.nmat = splits;
+        g.A = (const uint16_t *)X;
+        g.K = ks;
+        g.Kb = dims.d;
+        g.Nout = dims.E;
+        g.tiles = pw.rtiles;
+        g.chunk_tiles = pw.rchunk;
+        g.c0 = 0;
+        g.c1 = 1;
+        g.outf = pw.rpart;
+        g.outf_split = (int64_t)dims.T * dims.E;
+        if (!launch_gemm_tc(g, dims.T, pw.err, stream)) return PMOE_ERR_CUDA;
+        launch_router_reduce(dims.T, dims.E, splits, pw.rpart, logits, stream);
+    }
+    return PMOE_OK;
+}
+
 static pmoe_status launched(cudaStream_t st)
 {
     (void)st;
@@ -329,40 +368,25 @@ pmoe_status moe_route(pmoe_dims dims, const void *X, const float *Wr, const floa
     PermWs pw = carve_perm(ws, dims, &need);
     if (!ws || ws_bytes < need || !aligned16(ws)) return PMOE_ERR_WORKSPACE;
     if (dims.T == 0) return PMOE_OK;
-    if (mode == PMOE_ROUTE_EXACT) {
-        ScopedTimer tm(PMOE_KT_ROUTER, stream);
-        launch_router_exact(dims.T, dims.d, dims.E, (const uint16_t *)X, Wr, pw.logits, stream);
-    } else {
-        ScopedTimer tm(PMOE_KT_ROUTER, stream);
-        // K splits (a function of d alone): every split is one matrix of
-        // [E, 3d / splits] and writes its own partial logits
-        const int splits = router_splits(dims.d);
-        const int ks = 3 * dims.d / splits;
-        const int rows = router_tile_rows(dims.T, dims.E, splits, gemm_num_sms());
-        launch_router_prep(dims.T, dims.d, dims.E, Wr, pw.wr3, pw.rtiles, pw.rchunk, rows, stream);
-        GemmArgs g{};
-        g.kind = GK_ROUTER;
-        g.fmt = kFmtBF16;
-        g.wq = (const uint8_t *)pw.wr3;
-        g.wq_stride = (int64_t)dims.E * ks * 2;
-        g.Nst = dims.E;
-        g.Kst = ks;
-        g.nmat = splits;
-        g.A = (const uint16_t *)X;
-        g.K = ks;
-        g.Kb = dims.d;
-        g.Nout = dims.E;
-        g.tiles = pw.rtiles;
-        g.chunk_tiles = pw.rchunk;
-        g.c0 = 0;
-        g.c1 = 1;
-        g.outf = pw.rpart;
-        g.outf_split = (int64_t)dims.T * dims.E;
-        if (!launch_gemm_tc(g, dims.T, pw.err, stream)) return PMOE_ERR_CUDA;
-        launch_router_reduce(dims.T, dims.E, splits, pw.rpart, pw.logits, stream);
-    }
+    const pmoe_status s = router_logits(dims, X, Wr, mode, pw, pw.logits, stream);
+    if (s != PMOE_OK) return s;
     launch_route_topk(dims.T, dims.E, dims.k, pw.logits, bias, idx, w, logits, stream);
     return launched(stream);
+}
+
+pmoe_status moe_router_logits(pmoe_dims dims, const void *X, const float *Wr, float *logits, int mode,
+                              void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!dims_ok(dims) || (mode != PMOE_ROUTE_FAST && mode != PMOE_ROUTE_EXACT))
+        return PMOE_ERR_INVALID_ARG;
+    if (dims.T > 0 && (!X || !Wr || !logits)) return PMOE_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(Wr) || !aligned16(logits)) return PMOE_ERR_INVALID_ARG;
+    size_t need;
+    PermWs pw = carve_perm(ws, dims, &need);
+    if (!ws || ws_bytes < need || !aligned16(ws)) return PMOE_ERR_WORKSPACE;
+    if (dims.T == 0) return PMOE_OK;
+    const pmoe_status s = router_logits(dims, X, Wr, mode, pw, logits, stream);
+    return s != PMOE_OK ? s : launched(stream);
 }
 
 pmoe_status moe_permute(pmoe_dims dims, const int32_t *idx, const pmoe_routing *out, void *ws,

@@ -1,0 +1,554 @@
+// gate.cu -- the gate of a layer that routes by scores: sigmoid or softmax of
+// the logits, a balancing bias that takes part in the choice alone, groups of
+// experts, the top k, weights renormalised; and its gradient.
+//
+// The choice is the one of the exact scores.  Without a bias the order of the
+// experts is that of their logits, and keys of the logits decide.  With one, c =
+// score + bias is formed in FP32 first; where two experts that the choice has to
+// tell apart (neighbours among the best k + 1) lie within the error of their c,
+// the candidates' c are formed again in FP64, one candidate a lane.  The same
+// holds for the last group in and the first one out; then all of the token's c
+// are formed in FP64.  Of 16384 tokens with 256 experts some 30 take the first
+// of these ways and one or two the second.
+#include <cmath>
+#include <initializer_list>
+
+#include "common.cuh"
+#include "launch.h"
+#include "pdl.cuh"
+
+namespace pmoe {
+namespace gate {
+
+constexpr int kMaxGroups = 32;
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct Args {
+    int T, E, k, G, top, gsum, gsize;   // gsize: experts of a group
+    int softmax, renorm, has_bias, grouped;
+    float factor;
+    const float *logits, *bias;
+    int32_t *idx;
+    float *w;
+};
+
+// Keys in the order of the values: 0 is an expert that is taken or out, 1 a NaN
+__device__ __forceinline__ uint32_t key_of(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return v != v ? 1u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k)
+{
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ uint64_t key_of(double v)
+{
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return v != v ? 1ull : (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double of_key(uint64_t k)
+{
+    return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kAll, k); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t k)
+{
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(k >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ float warp_fmax(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+template <class F>
+__device__ __forceinline__ F warp_sum(F v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// exp(l - m) for l <= m, with the rounding of the difference taken back
+__device__ __forceinline__ float exp_below(float l, float m)
+{
+    const float d = l - m;
+    if (!(d > -200.f)) return d != d ? d : 0.f;          // (also l = -inf)
+    const float t = d + m, err = (l - t) - (m - (t - d));   // l - m = d + err
+    return expf(d) * (1.f + err);
+}
+__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+
+// Where the row's softmax stands: its largest logit and 1 / sum
+struct Norm {
+    float m, inv;
+};
+
+// The factor of the lane's expert: s, or with renorm s / (sum of s + 1e-20).  The
+// quotient is formed from scores relative to the largest chosen one, so that it
+// keeps its accuracy where all of them are below FP32's range.
+constexpr float kLnEps = -46.0517019f;   // ln(1e-20)
+__device__ __forceinline__ float share(bool softmax, bool renorm, float l, bool live, Norm n)
+{
+    float s = 0.f, eps = 1e-20f;
+    if (!renorm) return !live ? 0.f : softmax ? exp_below(l, n.m) * n.inv : sigmoid(l);
+    const float base = of_key(warp_max(key_of(live ? l : -INFINITY)));
+    if (base == -INFINITY) return 0.f;
+    if (softmax) {
+        if (live) s = exp_below(l, base);
+        eps = expf(n.m - base + kLnEps) / n.inv;
+    } else if (base > -40.f) {
+        if (live) s = sigmoid(l);
+    } else {
+        if (live) s = exp_below(l, base) * sigmoid(-l);
+        eps = expf(kLnEps - base);
+    }
+    return s / (warp_sum(s) + eps);
+}
+
+// The two largest keys among `n` consecutive ones, joined over `sub` lanes
+template <class Key>
+__device__ __forceinline__ void top2(Key &a, Key &b, Key x)
+{
+    const Key lo = x < a ? x : a;
+    a = x < a ? a : x;
+    b = lo > b ? lo : b;
+}
+
+// Keeps the best `top` of G groups: lane g < G gives its group's score; the kept
+// ones as a mask (ties to the lower group), and through `in`, `out` the least
+// score kept and the largest not kept.
+template <class Key>
+__device__ __forceinline__ uint32_t keep_groups(Key score, int G, int top, Key &in, Key &out)
+{
+    const int lane = threadIdx.x & 31;
+    int rank = 0;
+    for (int g = 0; g < G; ++g) {
+        const Key s = __shfl_sync(kAll, score, g);
+        rank += s > score || (s == score && g < lane);
+    }
+    const bool kept = lane < G && rank < top;
+    in = ~warp_max(kept ? ~score : (Key)0);
+    out = warp_max(lane < G && !kept ? score : (Key)0);
+    return __ballot_sync(kAll, kept);
+}
+
+// Key of each group's score in lane g < G, from the keys of its experts in shared
+// memory (expert e at e + e / 32): `val` makes it of the two best ones' (0: none).
+template <class Key, class V>
+__device__ __forceinline__ auto group_score(const Key *buf, const Args &a, V val)
+{
+    const int lane = threadIdx.x & 31;
+    int sub = 1;   // lanes of a group, a power of two
+    while (sub * 2 * a.G <= 32) sub *= 2;
+    const int g = lane / sub, j = lane - g * sub, per = (a.gsize + sub - 1) / sub;
+    Key x = 0, y = 0;
+    if (g < a.G) {
+        const int e1 = min((j + 1) * per, a.gsize);
+        for (int e = j * per; e < e1; ++e) {
+            const int at = g * a.gsize + e;
+            top2(x, y, buf[at + (at >> 5)]);
+        }
+    }
+    for (int o = 1; o < sub; o *= 2) {
+        const Key x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
+        top2(x, y, x2);
+        top2(x, y, y2);
+    }
+    return __shfl_sync(kAll, val(x, y), min(lane * sub, 31));
+}
+// The key of a group's score from those of its two best c: experts that cannot
+// be chosen (-inf) add nothing
+template <class Key>
+__device__ __forceinline__ Key sum_of(const Args &a, Key x, Key y)
+{
+    if (a.gsum == 1 || y <= 1 || of_key(y) == -INFINITY) return x;
+    return key_of(of_key(x) + of_key(y));
+}
+
+__device__ __forceinline__ double exact_c(const Args &a, const float *row, int e, Norm n, double zinv)
+{
+    const double l = (double)row[e];
+    const double s = a.softmax ? exp(l - (double)n.m) * zinv : 1. / (1. + exp(-l));
+    return l == -INFINITY ? -INFINITY : s + (a.has_bias ? (double)a.bias[e] : 0.);
+}
+__device__ __forceinline__ double exact_zinv(const Args &a, const float *row, Norm n)
+{
+    if (!a.softmax) return 1.;
+    double z = 0.;
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) z += exp((double)row[e] - (double)n.m);
+    return 1. / warp_sum(z);
+}
+
+// The whole choice in FP64: lane j < k returns the j-th expert
+__device__ __noinline__ int choose_exact(const Args &a, const float *row, Norm n, uint64_t *buf)
+{
+    const int lane = threadIdx.x & 31;
+    const double zinv = exact_zinv(a, row, n);
+    for (int e = lane; e < a.E; e += 32) buf[e + (e >> 5)] = key_of(exact_c(a, row, e, n, zinv));
+    __syncwarp();
+    if (a.grouped) {
+        uint64_t in, out;
+        const uint64_t s = group_score(buf, a, [&](uint64_t x, uint64_t y) { return sum_of(a, x, y); });
+        const uint32_t kept = keep_groups(s, a.G, a.top, in, out);
+        __syncwarp();
+        for (int e = lane; e < a.E; e += 32)
+            if (!(kept >> (e / a.gsize) & 1u)) buf[e + (e >> 5)] = 0;
+        __syncwarp();
+    }
+    int mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = 0;
+        int id = 0x7fffffff;
+        for (int e = lane; e < a.E; e += 32) {
+            const uint64_t v = buf[e + (e >> 5)];
+            if (v > best) best = v, id = e;
+        }
+        const uint64_t m = warp_max(best);
+        const int e = (int)__reduce_min_sync(kAll, best == m ? (uint32_t)id : 0x7fffffffu);
+        if (e < a.E && e % 32 == lane) buf[e + (e >> 5)] = 0;
+        __syncwarp();
+        if (lane == j) mine = e;
+    }
+    return mine;
+}
+
+// One warp a token, experts 32 i + lane in a lane's registers
+template <int kN, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) k_gate(const Args a)
+{
+    extern __shared__ uint64_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *buf = smem + (size_t)warp * (a.E + a.E / 32 + 1);   // (used by the cases that need it)
+    __shared__ int cand[kWarps][32];
+    grid_wait();
+    grid_go();
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+        const float *row = a.logits + t * a.E;
+        uint32_t key[kN];
+        Norm n{0.f, 1.f};
+        {
+            float v[kN];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int e = i * 32 + lane;
+                v[i] = e < a.E ? row[e] : -INFINITY;
+            }
+            if (a.softmax) {
+                float m = v[0];
+#pragma unroll
+                for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
+                m = warp_fmax(m);
+                n.m = m == -INFINITY ? 0.f : m;   // (no expert can be chosen: all scores are zero)
+                if (a.has_bias || a.grouped || !a.renorm) {
+                    float z = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) z += exp_below(v[i], n.m);
+                    z = warp_sum(z);
+                    n.inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+                }
+            }
+            if (a.has_bias) {
+                constexpr float L = 1.4426950408889634f;
+                const float ml = n.m * L;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    const int e = i * 32 + lane;
+                    const float s = a.softmax ? ex2(fmaf(v[i], L, -ml)) * n.inv : rcp(1.f + ex2(v[i] * -L));
+                    if (v[i] != -INFINITY) v[i] = s + a.bias[e];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) key[i] = i * 32 + lane < a.E ? key_of(v[i]) : 0u;
+        }
+        // error of a c beside its own rounding: 2^-21 of the largest score
+        const float terr = 1.9073486e-6f * (a.softmax ? n.inv : 1.f);
+        auto near = [&](float x, float y) {   // x >= y
+            return y != -INFINITY && !(x - y > terr + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
+        };
+        bool whole = false;   // the groups are too close to call in FP32
+        if (a.grouped) {
+            uint32_t *kb = (uint32_t *)buf;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int e = i * 32 + lane;
+                if (e < a.E) kb[e + (e >> 5)] = key[i];
+            }
+            __syncwarp();
+            uint32_t in, out, kept;
+            if (a.has_bias || a.gsum == 1) {
+                const uint32_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) { return sum_of(a, x, y); });
+                kept = keep_groups(s, a.G, a.top, in, out);
+                if (a.has_bias && a.top < a.G) {
+                    const float x = of_key(in), y = of_key(out);
+                    whole = a.gsum == 1 ? near(x, y) : near(0.5f * x, 0.5f * y);
+                }
+            } else {   // sums of two scores, from the logits, in FP64 at once
+                const uint64_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) {
+                    auto score = [&](uint32_t k) {
+                        const double l = of_key(k);
+                        return k <= 1u || l == -INFINITY ? 0. : a.softmax ? exp(l - (double)n.m) : 1. / (1. + exp(-l));
+                    };
+                    if (x <= 1u || of_key(x) == -INFINITY) return key_of(-(double)INFINITY);
+                    return key_of(score(x) + score(y));
+                });
+                uint64_t i64, o64;
+                kept = keep_groups(s, a.G, a.top, i64, o64);
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int e = i * 32 + lane;
+                if (e < a.E && !(kept >> (e / a.gsize) & 1u)) key[i] = 0u;
+            }
+            __syncwarp();
+        }
+        // the best k (k + 1 where c decides): lane j keeps the j-th
+        int mine = 0;
+        if (!whole) {
+            uint32_t mk = 0;
+            const int rounds = a.has_bias ? min(a.k + 1, 32) : a.k;
+            for (int j = 0; j < rounds; ++j) {
+                uint32_t best = key[0];
+#pragma unroll
+                for (int i = 1; i < kN; ++i) best = max(best, key[i]);
+                const uint32_t m = warp_max(best);
+                if (m == 0) break;   // (fewer than k + 1 experts)
+                uint32_t id = 0x7fffffffu;
+#pragma unroll
+                for (int i = kN - 1; i >= 0; --i)
+                    if (key[i] == m) id = (uint32_t)(i * 32 + lane);
+                const uint32_t e = __reduce_min_sync(kAll, id);
+#pragma unroll
+                for (int i = 0; i < kN; ++i)
+                    if (e == (uint32_t)(i * 32 + lane)) key[i] = 0u;
+                if (lane == j) mine = (int)e, mk = m;
+            }
+            if (a.has_bias) {
+                const uint32_t nk = __shfl_down_sync(kAll, mk, 1);
+                bool close = lane < 31 && lane < a.k && mk > 1 && nk > 1 && near(of_key(mk), of_key(nk));
+                const uint32_t lowest = __shfl_sync(kAll, mk, a.k - 1);
+                if (a.k == 32) close = true;   // (the 33rd is not known)
+                if (__any_sync(kAll, close)) {
+                    // every expert that may be among the best k
+                    const float c0 = of_key(lowest), edge = c0 - 2.f * (terr + 4.7683716e-7f * fabsf(c0));
+                    int cnt = 0;
+                    for (int j = 0; j < rounds; ++j) {   // those taken come back
+                        const uint32_t m = __shfl_sync(kAll, mk, j);
+                        const int e = __shfl_sync(kAll, mine, j);
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            if (m != 0 && e == i * 32 + lane) key[i] = m;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {
+                        const bool in = key[i] > 1u && !(of_key(key[i]) < edge);
+                        const uint32_t b = __ballot_sync(kAll, in);
+                        const int at = cnt + __popc(b & ((1u << lane) - 1u));
+                        if (in && at < 32) cand[warp][at] = i * 32 + lane;
+                        cnt += __popc(b);
+                    }
+                    __syncwarp();
+                    if (lowest <= 1u || cnt > 32) {
+                        whole = true;
+                    } else {
+                        const double zinv = exact_zinv(a, row, n);
+                        const int e = lane < cnt ? cand[warp][lane] : 0;
+                        const uint64_t c = lane < cnt ? key_of(exact_c(a, row, e, n, zinv)) : 0ull;
+                        int rank = 0;   // (candidates are in the order of their ids)
+                        for (int j = 0; j < cnt; ++j) {
+                            const uint64_t o = __shfl_sync(kAll, c, j);
+                            const int oe = __shfl_sync(kAll, e, j);
+                            rank += o > c || (o == c && oe < e);
+                        }
+                        __syncwarp();
+                        if (lane < cnt && rank < a.k) cand[warp][rank] = e;
+                        __syncwarp();
+                        mine = lane < a.k ? cand[warp][lane] : 0;
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (whole) mine = choose_exact(a, row, n, buf);
+        // the weights: the scores without the bias
+        const bool live = lane < a.k;
+        const float l = live ? row[mine] : 0.f;
+        const float w = a.factor * share(a.softmax, a.renorm, l, live, n);
+        if (live) {
+            a.idx[t * a.k + lane] = mine;
+            a.w[t * a.k + lane] = w;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+// With D = sum of the chosen scores + 1e-20 (or 1), the gradient of score j is
+//   ds_j = factor / D (dw_j - [renorm] sum_i dw_i s_i / D)
+// and that of the logits
+//   sigmoid: dl_j = ds_j s_j (1 - s_j) of the chosen experts, else 0
+//   softmax: dl_e = s_e ([chosen] ds_e - sum_j ds_j s_j)
+// A warp a token; an expert that idx names twice takes both parts.
+struct BwdArgs {
+    int T, E, k;
+    int softmax, renorm, accumulate;
+    float factor;
+    const float *logits;
+    const int32_t *idx;
+    const float *dw;
+    float *dl;
+};
+
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) k_gate_backward(const BwdArgs a)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_wait();
+    grid_go();
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+        const float *row = a.logits + t * a.E;
+        float *out = a.dl + t * a.E;
+        const int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
+        const bool live = e >= 0 && e < a.E;
+        const float dw = live ? a.dw[t * a.k + lane] : 0.f;
+        const float l = live ? row[e] : 0.f;
+        float m = 0.f, inv = 1.f;
+        if (a.softmax) {
+            m = -INFINITY;
+            for (int i = lane; i < a.E; i += 32) m = fmaxf(m, row[i]);
+            m = warp_fmax(m);
+            if (m == -INFINITY) m = 0.f;
+            float z = 0.f;
+            for (int i = lane; i < a.E; i += 32) z += exp_below(row[i], m);
+            z = warp_sum(z);
+            inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+        }
+        // ds_j s_j = factor (dw_j - mean) p_j with p_j the weight before its factor
+        const float p = share(a.softmax, a.renorm, l, live, Norm{m, inv});
+        const float mean = a.renorm ? warp_sum(dw * p) : 0.f;
+        float g = a.factor * (dw - mean) * p;
+        // (1 - s as the score of the opposite logit: it keeps its accuracy near 0)
+        if (!a.softmax) g *= sigmoid(-l);
+        if (!live) g = 0.f;
+        const float dot = a.softmax ? warp_sum(g) : 0.f;
+        float sum = 0.f;   // parts of the same expert, in order
+        bool first = true;
+        for (int j = 0; j < a.k; ++j) {
+            const float o = __shfl_sync(kAll, g, j);
+            if (__shfl_sync(kAll, e, j) == e) {
+                sum += o;
+                if (j < lane) first = false;
+            }
+        }
+        if (a.softmax) {
+            for (int i = lane; i < a.E; i += 32) {
+                const float v = -(exp_below(row[i], m) * inv) * dot;
+                out[i] = a.accumulate ? out[i] + v : v;
+            }
+        } else if (!a.accumulate) {
+            for (int i = lane; i < a.E; i += 32) out[i] = 0.f;
+        }
+        __syncwarp();   // (orders the row's stores before what is added to them)
+        if (live && first) out[e] = a.softmax || a.accumulate ? out[e] + sum : sum;
+        __syncwarp();
+    }
+}
+
+static bool ok(const pmoe_gate &g)
+{
+    if (g.T < 0 || g.E < 1 || g.E > 4096 || g.k < 1 || g.k > 32 || g.k > g.E) return false;
+    if (g.groups < 1 || g.groups > kMaxGroups || g.E % g.groups || g.topk_groups < 1 || g.topk_groups > g.groups) return false;
+    if (g.k > g.topk_groups * (g.E / g.groups)) return false;
+    if (g.group_sum != 1 && g.group_sum != 2) return false;
+    if (g.score != PMOE_SCORE_SIGMOID && g.score != PMOE_SCORE_SOFTMAX) return false;
+    if (!std::isfinite(g.factor)) return false;
+    return (int64_t)g.T * g.k <= (int64_t)INT32_MAX / 2;
+}
+static bool aligned(std::initializer_list<const void *> ps)
+{
+    for (const void *p : ps)
+        if ((uintptr_t)p & 15) return false;
+    return true;
+}
+
+template <int kN, int kWarps>
+static bool launch_as(const Args &a, cudaStream_t st)
+{
+    // keys of a token: of FP32 values for the groups, of FP64 ones for a close call
+    const size_t smem = a.has_bias || a.grouped ? (size_t)kWarps * (a.E + a.E / 32 + 1) * 8 : 0;
+    if (smem > 40 * 1024 && !set_attribute<k_gate<kN, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize>(
+                                (int)(kWarps * (32 * kN + kN + 1) * 8)))
+        return false;
+    const int64_t ctas = std::min<int64_t>(cdiv(a.T, kWarps), (int64_t)gemm_num_sms() * 16);
+    return launch_chained<k_gate<kN, kWarps>>((unsigned)ctas, 32 * kWarps, smem, 1, st, a);
+}
+
+}  // namespace gate
+}  // namespace pmoe
+
+using namespace pmoe;
+
+extern "C" {
+
+pmoe_status moe_gate_forward(pmoe_gate g, const float *logits, const float *bias, int32_t *idx, float *w,
+                             cudaStream_t stream)
+{
+    if (!gate::ok(g) || (g.T > 0 && (!logits || !idx || !w)) || !gate::aligned({logits, bias, idx, w}))
+        return PMOE_ERR_INVALID_ARG;
+    if (g.T == 0) return PMOE_OK;
+    gate::Args a{};
+    a.T = g.T;
+    a.E = g.E;
+    a.k = g.k;
+    a.G = g.groups;
+    a.top = g.topk_groups;
+    a.gsum = g.group_sum;
+    a.gsize = g.E / g.groups;
+    a.softmax = g.score == PMOE_SCORE_SOFTMAX;
+    a.renorm = g.renorm != 0;
+    a.has_bias = bias != nullptr;
+    a.grouped = g.topk_groups < g.groups;
+    a.factor = g.factor;
+    a.logits = logits;
+    a.bias = bias;
+    a.idx = idx;
+    a.w = w;
+    const int n = (int)cdiv(g.E, 32);
+    const bool done = n <= 1    ? gate::launch_as<1, 8>(a, stream)
+                      : n <= 2  ? gate::launch_as<2, 8>(a, stream)
+                      : n <= 4  ? gate::launch_as<4, 8>(a, stream)
+                      : n <= 8  ? gate::launch_as<8, 8>(a, stream)
+                      : n <= 12 ? gate::launch_as<12, 8>(a, stream)
+                      : n <= 16 ? gate::launch_as<16, 8>(a, stream)
+                      : n <= 32 ? gate::launch_as<32, 8>(a, stream)
+                                : gate::launch_as<128, 4>(a, stream);
+    return done ? PMOE_OK : PMOE_ERR_CUDA;
+}
+
+pmoe_status moe_gate_backward(pmoe_gate g, const float *logits, const int32_t *idx, const float *d_topk_w,
+                              int accumulate, float *dlogits, cudaStream_t stream)
+{
+    if (!gate::ok(g) || (g.T > 0 && (!logits || !idx || !d_topk_w || !dlogits)) ||
+        !gate::aligned({logits, idx, d_topk_w, dlogits}))
+        return PMOE_ERR_INVALID_ARG;
+    if (g.T == 0) return PMOE_OK;
+    gate::BwdArgs a{g.T, g.E, g.k, g.score == PMOE_SCORE_SOFTMAX, g.renorm != 0, accumulate != 0, g.factor,
+                    logits, idx, d_topk_w, dlogits};
+    const int64_t ctas = std::min<int64_t>(cdiv(g.T, 8), (int64_t)gemm_num_sms() * 16);
+    return launch_chained<gate::k_gate_backward<8>>((unsigned)ctas, 256, 0, 1, stream, a) ? PMOE_OK : PMOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -6,7 +6,9 @@ the workspaces, and runs one step of the layer:
 
     moe_route -> moe_permute -> moe_chunked_forward -> moe_backward_data
 
-and the router's training side: moe_balance_forward, moe_route_backward.
+and the router's training side: moe_balance_forward, moe_route_backward.  A layer
+that routes by scores takes moe_router_logits -> moe_gate_forward in moe_route's
+place, and moe_gate_backward.
 
 Every computation happens in libpmoe's kernels; this module only allocates
 and passes pointers.
@@ -148,6 +150,34 @@ class DeviceLayer:
               mode: int = pmoe.ROUTE_FAST):
         ws = self.workspace(pmoe.OP_PERMUTE)
         pmoe.moe_route(self.dims, X, self.Wr, self.bias, logits, rt.idx, rt.w, ws, mode=mode)
+
+    def router_logits(self, X: torch.Tensor, logits: torch.Tensor, mode: int = pmoe.ROUTE_FAST):
+        """logits (f32 [T, E]) of the router before its bias."""
+        ws = self.workspace(pmoe.OP_PERMUTE)
+        pmoe.moe_router_logits(self.dims, X, self.Wr, logits, ws, mode=mode)
+
+    def _gate_args(self, g: pmoe.Gate, logits):
+        cfg = self.cfg
+        check_current(self.device)
+        if (g.T, g.E, g.k) != (cfg.T, cfg.E, cfg.k):
+            raise ValueError(f"gate of T={g.T}, E={g.E}, k={g.k} on a layer of T={cfg.T}, E={cfg.E}, k={cfg.k}")
+        check_tensor("logits", logits, (torch.float32,), (cfg.T, cfg.E), self.device)
+
+    def gate(self, g: pmoe.Gate, logits, rt: Routing, bias=None):
+        """The choice and the weights of ``rt`` by scores (``pmoe.gate``) of
+        ``logits``; ``bias`` (f32 [E]) takes part in the choice alone."""
+        self._gate_args(g, logits)
+        if bias is not None:
+            check_tensor("bias", bias, (torch.float32,), (self.cfg.E,), self.device)
+        pmoe.moe_gate_forward(g, logits, bias, rt.idx, rt.w)
+
+    def gate_backward(self, g: pmoe.Gate, logits, rt: Routing, d_topk_w, dlogits, accumulate=False):
+        """dlogits (f32 [T, E]) of the gate's weights, written or (``accumulate``)
+        added to what ``route_backward`` left there of the balance loss."""
+        self._gate_args(g, logits)
+        check_tensor("d_topk_w", d_topk_w, (torch.float32,), (self.cfg.T, self.cfg.k), self.device)
+        check_tensor("dlogits", dlogits, (torch.float32,), (self.cfg.T, self.cfg.E), self.device)
+        pmoe.moe_gate_backward(g, logits, rt.idx, d_topk_w, dlogits, accumulate)
 
     def permute(self, rt: Routing):
         pmoe.moe_permute(self.dims, rt.idx, rt.c(), self.workspace(pmoe.OP_PERMUTE))

@@ -22,6 +22,8 @@ MODE_FUSED, MODE_SCRATCH = 0, 1
 ROUTE_FAST, ROUTE_EXACT = 0, 1
 OP_PERMUTE, OP_FORWARD, OP_BACKWARD = 0, 1, 2
 HEAD_FORWARD, HEAD_BACKWARD = 0, 1
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+GRAD_F32, GRAD_BF16 = 0, 1
 
 EXPORTS = ("moe_route", "moe_permute", "moe_chunked_forward", "moe_backward_data", "moe_dequant",
            "adapter_apply", "adapter_grad", "adapter_cayley", "adapter_cayley_grad",
@@ -33,7 +35,11 @@ EXPORTS = ("moe_route", "moe_permute", "moe_chunked_forward", "moe_backward_data
            "moe_adapter_publish", "moe_chunked_forward_slots", "pmoe_debug_expire_gemm_wait",
            "head_workspace_bytes", "head_logprob_forward", "head_logprob_backward",
            "head_distill_forward", "head_distill_backward",
-           "moe_balance_ws_bytes", "moe_balance_forward", "moe_route_backward")
+           "moe_balance_ws_bytes", "moe_balance_forward", "moe_route_backward",
+           "moe_router_logits", "moe_gate_forward", "moe_gate_backward",
+           "fp8_quantize", "fp8_transpose", "fp8_gemm_ws_bytes", "fp8_gemm",
+           "dense_w8a8_ws_bytes", "dense_w8a8_forward", "dense_w8a8_backward",
+           "grad_list_bytes", "grad_list_fill", "grad_ws_bytes", "grad_norm", "grad_clip")
 PERMUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 KT_GEMM_GATE_UP, KT_GEMM_DOWN, KT_GEMM_BWD_G, KT_GEMM_BWD_DX, KT_ROUTER = 0, 1, 2, 3, 4
 
@@ -52,6 +58,21 @@ class Dims(ctypes.Structure):
 class HeadDims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("V", ctypes.c_int32),
                 ("K", ctypes.c_int32)]
+
+
+class Gate(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "E", "k", "groups", "topk_groups", "group_sum", "score", "renorm")] + [
+                    ("factor", ctypes.c_float)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class GradListC(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("chunks", ctypes.c_int64), ("n", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):
@@ -123,6 +144,17 @@ def _declare(L):
         "head_distill_backward": [H, p, p, f32, p, p, p, p, p, p, p, sz, p],
         "moe_balance_forward": [D, p, p, p, p, i32, p, p, p, p, p, sz, p],
         "moe_route_backward": [D, p, p, p, p, p, p, i32, p, p, p, p, p, sz, p],
+        "moe_router_logits": [D, p, p, p, ctypes.c_int, p, sz, p],
+        "moe_gate_forward": [Gate, p, p, p, p, p],
+        "moe_gate_backward": [Gate, p, p, p, ctypes.c_int, p, p],
+        "fp8_quantize": [i32, i32, p, ctypes.c_int, p, p, p],
+        "fp8_transpose": [i32, i32, p, p, p, p, p],
+        "fp8_gemm": [i32, i32, i32, p, p, p, p, p, p, sz, p],
+        "dense_w8a8_forward": [p, p, i32, i32, i32, p, i32, p, ctypes.c_int, p, p, sz, p],
+        "dense_w8a8_backward": [p, p, i32, i32, i32, p, i32, p, p, ctypes.c_int, p, p, p, sz, p],
+        "grad_list_fill": [i32, ctypes.POINTER(Grad), p, sz, ctypes.POINTER(GradListC)],
+        "grad_norm": [GradListC, p, p, sz, p],
+        "grad_clip": [GradListC, f32, p, p, sz, p],
         "moe_clear_status": [p, p],
         "moe_query_status": [p, p],
     }
@@ -142,6 +174,14 @@ def _declare(L):
     L.moe_balance_ws_bytes.restype = sz
     L.head_workspace_bytes.argtypes = [H, ctypes.c_int]
     L.head_workspace_bytes.restype = sz
+    L.fp8_gemm_ws_bytes.argtypes = [i32, i32, i32]
+    L.fp8_gemm_ws_bytes.restype = sz
+    L.dense_w8a8_ws_bytes.argtypes = [i32, i32, i32, ctypes.c_int]
+    L.dense_w8a8_ws_bytes.restype = sz
+    L.grad_list_bytes.argtypes = [i32]
+    L.grad_list_bytes.restype = sz
+    L.grad_ws_bytes.argtypes = []
+    L.grad_ws_bytes.restype = sz
     L.moe_ctx_bytes.argtypes = [D]
     L.moe_ctx_bytes.restype = sz
     L.pmoe_debug_expire_gemm_wait.argtypes = [ctypes.c_uint64]
@@ -381,6 +421,90 @@ def head_distill_backward(hd, X, W, scale, t_idx, t_logits, lse, g, dX, dW, ws, 
     _check(lib().head_distill_backward(hd, _ptr(X), _ptr(W), scale, _ptr(t_idx), _ptr(t_logits),
                                        _ptr(lse), _ptr(g), _ptr(dX), _ptr(dW), _ptr(ws),
                                        _nbytes(ws), _stream(stream)), "head_distill_backward")
+
+
+def moe_router_logits(dm, X, Wr, logits, ws, mode=ROUTE_FAST, stream=None):
+    _check(lib().moe_router_logits(dm, _ptr(X), _ptr(Wr), _ptr(logits), mode, _ptr(ws), _nbytes(ws),
+                                   _stream(stream)), "moe_router_logits")
+
+
+def gate(T, E, k, score="sigmoid", groups=1, topk_groups=1, group_sum=2, renorm=True,
+         factor=1.0) -> Gate:
+    """A gate's shape and form; ``score`` is "sigmoid" or "softmax"."""
+    scores = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
+    if score not in scores:
+        raise ValueError(f"score: {score!r}, expected one of {sorted(scores)}")
+    return Gate(T, E, k, groups, topk_groups, group_sum, scores[score], int(bool(renorm)), factor)
+
+
+def moe_gate_forward(g: Gate, logits, bias, idx, w, stream=None):
+    _check(lib().moe_gate_forward(g, _ptr(logits), _ptr(bias), _ptr(idx), _ptr(w), _stream(stream)),
+           "moe_gate_forward")
+
+
+def moe_gate_backward(g: Gate, logits, idx, d_topk_w, dlogits, accumulate=False, stream=None):
+    _check(lib().moe_gate_backward(g, _ptr(logits), _ptr(idx), _ptr(d_topk_w), int(accumulate),
+                                   _ptr(dlogits), _stream(stream)), "moe_gate_backward")
+
+
+def fp8_quantize(rows, K, X, q, s, pow2=False, stream=None):
+    _check(lib().fp8_quantize(rows, K, _ptr(X), int(pow2), _ptr(q), _ptr(s), _stream(stream)),
+           "fp8_quantize")
+
+
+def fp8_transpose(N, K, q, s, qt, st, stream=None):
+    _check(lib().fp8_transpose(N, K, _ptr(q), _ptr(s), _ptr(qt), _ptr(st), _stream(stream)),
+           "fp8_transpose")
+
+
+def fp8_gemm_ws_bytes(rows, N, K) -> int:
+    return int(lib().fp8_gemm_ws_bytes(rows, N, K))
+
+
+def fp8_gemm(rows, N, K, A, As, W, Ws, Y, ws, stream=None):
+    _check(lib().fp8_gemm(rows, N, K, _ptr(A), _ptr(As), _ptr(W), _ptr(Ws), _ptr(Y), _ptr(ws),
+                          _nbytes(ws), _stream(stream)), "fp8_gemm")
+
+
+def dense_w8a8_ws_bytes(rows, N, K, adapter=False) -> int:
+    return int(lib().dense_w8a8_ws_bytes(rows, N, K, int(adapter)))
+
+
+def dense_w8a8_forward(q, s, N, K, block, R, rows, X, Y, ws, pow2=False, stream=None):
+    _check(lib().dense_w8a8_forward(_ptr(q), _ptr(s), N, K, block, _ptr(R), rows, _ptr(X), int(pow2),
+                                    _ptr(Y), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "dense_w8a8_forward")
+
+
+def dense_w8a8_backward(qt, st, N, K, block, R, rows, X, dY, dX, dR, ws, pow2=False, stream=None):
+    _check(lib().dense_w8a8_backward(_ptr(qt), _ptr(st), N, K, block, _ptr(R), rows, _ptr(X), _ptr(dY),
+                                     int(pow2), _ptr(dX), _ptr(dR), _ptr(ws), _nbytes(ws),
+                                     _stream(stream)), "dense_w8a8_backward")
+
+
+def grad_ws_bytes() -> int:
+    return int(lib().grad_ws_bytes())
+
+
+def grad_list_fill(grads):
+    """(list, table bytes) of (src, dst, n, dtype) tuples; the caller copies the
+    table to the device and sets ``list.table``."""
+    n = len(grads)
+    arr = (Grad * max(n, 1))(*[Grad(*g) for g in grads])
+    nbytes = int(lib().grad_list_bytes(n))
+    table = ctypes.create_string_buffer(nbytes)
+    lst = GradListC()
+    _check(lib().grad_list_fill(n, arr, table, nbytes, ctypes.byref(lst)), "grad_list_fill")
+    return lst, table.raw
+
+
+def grad_norm(lst: GradListC, norm, ws, stream=None):
+    _check(lib().grad_norm(lst, _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream)), "grad_norm")
+
+
+def grad_clip(lst: GradListC, max_norm, norm, ws, stream=None):
+    _check(lib().grad_clip(lst, max_norm, _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "grad_clip")
 
 
 def moe_clear_status(ws, stream=None):
