@@ -111,7 +111,7 @@ __device__ __forceinline__ float share(bool softmax, bool renorm, float l, bool 
     if (softmax) {
         if (live) s = exp_below(l, base);
         eps = expf(n.m - base + kLnEps) / n.inv;
-    } else if (base > -40.f) {
+    } else if (base > 0.f) {
         if (live) s = sigmoid(l);
     } else {
         if (live) s = exp_below(l, base) * sigmoid(-l);
