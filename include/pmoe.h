@@ -600,7 +600,7 @@ pmoe_status moe_router_logits(pmoe_dims dims, const void *X, const float *Wr, fl
  *   For few rows the blocks are shared among several CTAs, whose FP32 sums are
  *   added in order: a row's result may differ in its last bit with the number of
  *   rows in the call, not between runs.
- *   ws >= fp8_gemm_ws_bytes(rows, N, K) (the error word; the shared sums)
+ *   ws >= fp8_gemm_ws_bytes(rows, N, K) (the error word)
  * rows, N, K <= 2^20 (rows 2^24).  q, qt, A and W are E4M3 codes.
  */
 pmoe_status fp8_quantize(int32_t rows, int32_t K, const void *X, int pow2, void *q, float *s,

@@ -12,6 +12,7 @@
 // of these ways and one or two the second.
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -32,11 +33,11 @@ struct Args {
     float *w;
 };
 
-// Keys in the order of the values: 0 is an expert that is taken or out, 1 a NaN
+// Keys in the order of the values; 0 is an expert that is taken or out
 __device__ __forceinline__ uint32_t key_of(float v)
 {
     const uint32_t u = __float_as_uint(v);
-    return v != v ? 1u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    return max(u ^ ((uint32_t)((int)u >> 31) | 0x80000000u), 1u);
 }
 __device__ __forceinline__ float of_key(uint32_t k)
 {
@@ -45,7 +46,8 @@ __device__ __forceinline__ float of_key(uint32_t k)
 __device__ __forceinline__ uint64_t key_of(double v)
 {
     const uint64_t u = (uint64_t)__double_as_longlong(v);
-    return v != v ? 1ull : (u >> 63) ? ~u : u | 0x8000000000000000ull;
+    const uint64_t k = (u >> 63) ? ~u : u | 0x8000000000000000ull;
+    return k ? k : 1ull;
 }
 __device__ __forceinline__ double of_key(uint64_t k)
 {
@@ -91,6 +93,8 @@ __device__ __forceinline__ float exp_below(float l, float m)
     const float t = d + m, err = (l - t) - (m - (t - d));   // l - m = d + err
     return expf(d) * (1.f + err);
 }
+// The same where 2^-22 and the difference's rounding (2^-24 of it) will do
+__device__ __forceinline__ float exp_below_fast(float l, float m) { return ex2((l - m) * 1.4426950408889634f); }
 __device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
 
 // Where the row's softmax stands: its largest logit and 1 / sum
@@ -194,7 +198,29 @@ __device__ __forceinline__ double exact_zinv(const Args &a, const float *row, No
     return 1. / warp_sum(z);
 }
 
-// The whole choice in FP64: lane j < k returns the j-th expert
+// The k largest keys in shared memory (expert e at e + e / 32), in order: lane j < k
+// returns the j-th expert
+template <class Key>
+__device__ __forceinline__ int choose(const Args &a, Key *buf)
+{
+    const int lane = threadIdx.x & 31;
+    int mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+        Key best = 0;
+        int id = 0x7fffffff;
+        for (int e = lane; e < a.E; e += 32) {
+            const Key v = buf[e + (e >> 5)];
+            if (v > best) best = v, id = e;
+        }
+        const Key m = warp_max(best);
+        const int e = (int)__reduce_min_sync(kAll, best == m ? (uint32_t)id : 0x7fffffffu);
+        if (e < a.E && e % 32 == lane) buf[e + (e >> 5)] = 0;
+        __syncwarp();
+        if (lane == j && e < a.E) mine = e;
+    }
+    return mine;
+}
+// The whole choice in FP64
 __device__ __noinline__ int choose_exact(const Args &a, const float *row, Norm n, uint64_t *buf)
 {
     const int lane = threadIdx.x & 31;
@@ -210,31 +236,42 @@ __device__ __noinline__ int choose_exact(const Args &a, const float *row, Norm n
             if (!(kept >> (e / a.gsize) & 1u)) buf[e + (e >> 5)] = 0;
         __syncwarp();
     }
-    int mine = 0;
-    for (int j = 0; j < a.k; ++j) {
-        uint64_t best = 0;
-        int id = 0x7fffffff;
-        for (int e = lane; e < a.E; e += 32) {
-            const uint64_t v = buf[e + (e >> 5)];
-            if (v > best) best = v, id = e;
-        }
-        const uint64_t m = warp_max(best);
-        const int e = (int)__reduce_min_sync(kAll, best == m ? (uint32_t)id : 0x7fffffffu);
-        if (e < a.E && e % 32 == lane) buf[e + (e >> 5)] = 0;
-        __syncwarp();
-        if (lane == j) mine = e;
+    return choose(a, buf);
+}
+// The FP64 order of a few candidates (lane < cnt has one): lane j < k returns the j-th
+__device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n, int e, int cnt, int *slot)
+{
+    const int lane = threadIdx.x & 31;
+    const double zinv = exact_zinv(a, row, n);
+    const uint64_t c = lane < cnt ? key_of(exact_c(a, row, e, n, zinv)) : 0ull;
+    int rank = 0;
+    for (int j = 0; j < cnt; ++j) {
+        const uint64_t o = __shfl_sync(kAll, c, j);
+        const int oe = __shfl_sync(kAll, e, j);
+        rank += o > c || (o == c && oe < e);
     }
-    return mine;
+    __syncwarp();
+    if (lane < cnt) slot[rank] = e;
+    __syncwarp();
+    return slot[lane];
 }
 
 // One warp a token, experts 32 i + lane in a lane's registers
+//
+// The best k are found among few candidates: the (k + 2)-th largest of the lanes' own
+// largest keys bounds the (k + 2)-th largest of all from below, and the keys from there
+// up (some 11 for k = 8, E = 384) are gathered, one a lane, and ranked.  (Taking the
+// largest k times over, each time looking through all keys again, took 1280 instructions a
+// token at k = 8, E = 384 and 23.7 us for 8192 tokens.)
 template <int kN, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) k_gate(const Args a)
+__global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Args a)
 {
     extern __shared__ uint64_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint64_t *buf = smem + (size_t)warp * (a.E + a.E / 32 + 1);   // (used by the cases that need it)
-    __shared__ int cand[kWarps][32];
+    // keys of a token: FP32 ones, of FP64 values for a close call
+    uint64_t *buf = (uint64_t *)((uint8_t *)smem + (size_t)warp * (((a.E + a.E / 32 + 1) * (a.has_bias ? 8 : 4) + 7) & ~7));
+    __shared__ int cand_id[kWarps][32];
+    __shared__ uint32_t cand_key[kWarps][32];
     grid_wait();
     grid_go();
     for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
@@ -257,18 +294,16 @@ __global__ void __launch_bounds__(32 * kWarps) k_gate(const Args a)
                 if (a.has_bias || a.grouped || !a.renorm) {
                     float z = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kN; ++i) z += exp_below(v[i], n.m);
+                    for (int i = 0; i < kN; ++i) z += exp_below_fast(v[i], n.m);
                     z = warp_sum(z);
                     n.inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
                 }
             }
             if (a.has_bias) {
-                constexpr float L = 1.4426950408889634f;
-                const float ml = n.m * L;
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
                     const int e = i * 32 + lane;
-                    const float s = a.softmax ? ex2(fmaf(v[i], L, -ml)) * n.inv : rcp(1.f + ex2(v[i] * -L));
+                    const float s = a.softmax ? exp_below_fast(v[i], n.m) * n.inv : rcp(1.f + ex2(v[i] * -1.4426950408889634f));
                     if (v[i] != -INFINITY) v[i] = s + a.bias[e];
                 }
             }
@@ -316,71 +351,69 @@ __global__ void __launch_bounds__(32 * kWarps) k_gate(const Args a)
             }
             __syncwarp();
         }
-        // the best k (k + 1 where c decides): lane j keeps the j-th
-        int mine = 0;
+        // the candidates, in the order of their ids
+        int mine = 0, cnt = 0;
         if (!whole) {
-            uint32_t mk = 0;
-            const int rounds = a.has_bias ? min(a.k + 1, 32) : a.k;
-            for (int j = 0; j < rounds; ++j) {
-                uint32_t best = key[0];
+            uint32_t best = key[0], least = 0;
 #pragma unroll
-                for (int i = 1; i < kN; ++i) best = max(best, key[i]);
-                const uint32_t m = warp_max(best);
-                if (m == 0) break;   // (fewer than k + 1 experts)
-                uint32_t id = 0x7fffffffu;
-#pragma unroll
-                for (int i = kN - 1; i >= 0; --i)
-                    if (key[i] == m) id = (uint32_t)(i * 32 + lane);
-                const uint32_t e = __reduce_min_sync(kAll, id);
-#pragma unroll
-                for (int i = 0; i < kN; ++i)
-                    if (e == (uint32_t)(i * 32 + lane)) key[i] = 0u;
-                if (lane == j) mine = (int)e, mk = m;
+            for (int i = 1; i < kN; ++i) best = max(best, key[i]);
+            for (int j = min(a.k + 2, 32); j > 0; --j) {
+                least = warp_max(best);
+                if (least == 0) break;          // fewer lanes have any: all keys are candidates
+                if (best == least) best = 0;    // (lanes with equal keys count as one)
             }
-            if (a.has_bias) {
-                const uint32_t nk = __shfl_down_sync(kAll, mk, 1);
-                bool close = lane < 31 && lane < a.k && mk > 1 && nk > 1 && near(of_key(mk), of_key(nk));
-                const uint32_t lowest = __shfl_sync(kAll, mk, a.k - 1);
-                if (a.k == 32) close = true;   // (the 33rd is not known)
-                if (__any_sync(kAll, close)) {
-                    // every expert that may be among the best k
-                    const float c0 = of_key(lowest), edge = c0 - 2.f * (terr + 4.7683716e-7f * fabsf(c0));
-                    int cnt = 0;
-                    for (int j = 0; j < rounds; ++j) {   // those taken come back
-                        const uint32_t m = __shfl_sync(kAll, mk, j);
-                        const int e = __shfl_sync(kAll, mine, j);
+            const uint32_t from = max(least, 1u);
+            uint32_t *ck = cand_key[warp];
+            int *ci = cand_id[warp];
 #pragma unroll
-                        for (int i = 0; i < kN; ++i)
-                            if (m != 0 && e == i * 32 + lane) key[i] = m;
-                    }
+            for (int i = 0; i < kN; ++i) {
+                const bool in = key[i] >= from;
+                const uint32_t b = __ballot_sync(kAll, in);
+                if (b) {
+                    const int at = cnt + __popc(b & ((1u << lane) - 1u));
+                    if (in && at < 32) ck[at] = key[i], ci[at] = i * 32 + lane;
+                    cnt += __popc(b);
+                }
+            }
+            __syncwarp();
+            if (cnt > 32) {
+                if (!a.has_bias) {
+                    uint32_t *kb = (uint32_t *)buf;
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
-                        const bool in = key[i] > 1u && !(of_key(key[i]) < edge);
-                        const uint32_t b = __ballot_sync(kAll, in);
-                        const int at = cnt + __popc(b & ((1u << lane) - 1u));
-                        if (in && at < 32) cand[warp][at] = i * 32 + lane;
-                        cnt += __popc(b);
+                        const int e = i * 32 + lane;
+                        if (e < a.E) kb[e + (e >> 5)] = key[i];
                     }
                     __syncwarp();
-                    if (lowest <= 1u || cnt > 32) {
-                        whole = true;
-                    } else {
-                        const double zinv = exact_zinv(a, row, n);
-                        const int e = lane < cnt ? cand[warp][lane] : 0;
-                        const uint64_t c = lane < cnt ? key_of(exact_c(a, row, e, n, zinv)) : 0ull;
-                        int rank = 0;   // (candidates are in the order of their ids)
-                        for (int j = 0; j < cnt; ++j) {
-                            const uint64_t o = __shfl_sync(kAll, c, j);
-                            const int oe = __shfl_sync(kAll, e, j);
-                            rank += o > c || (o == c && oe < e);
-                        }
-                        __syncwarp();
-                        if (lane < cnt && rank < a.k) cand[warp][rank] = e;
-                        __syncwarp();
-                        mine = lane < a.k ? cand[warp][lane] : 0;
-                        __syncwarp();
+                    mine = choose(a, kb);
+                }
+                whole = a.has_bias;
+            } else {
+                const uint32_t c = lane < cnt ? ck[lane] : 0u;
+                const int e = ci[lane];
+                int rank = 0;
+                for (int j = 0; j < cnt; ++j) {
+                    const uint32_t o = __shfl_sync(kAll, c, j);
+                    rank += o > c || (o == c && j < lane);
+                }
+                __syncwarp();
+                if (lane < cnt) ck[rank] = c, ci[rank] = e;
+                __syncwarp();
+                const uint32_t mk = lane < cnt ? ck[lane] : 0u;
+                mine = lane < cnt ? ci[lane] : 0;
+                if (a.has_bias) {
+                    const uint32_t nk = __shfl_down_sync(kAll, mk, 1);
+                    bool close = lane < a.k && lane + 1 < cnt && near(of_key(mk), of_key(nk));
+                    const float ck1 = of_key(__shfl_sync(kAll, mk, min(a.k, cnt) - 1));
+                    // everything that may be among the best k has to be a candidate
+                    const bool all = least == 0, short_by_one = cnt <= a.k && !all;
+                    if (__any_sync(kAll, close) || short_by_one) {
+                        const float edge = ck1 - 2.f * (terr + 4.7683716e-7f * fabsf(ck1));
+                        if (short_by_one || (!all && !(of_key(least) < edge))) whole = true;
+                        else mine = order_exact(a, row, n, mine, cnt, ci);
                     }
                 }
+                __syncwarp();
             }
         }
         if (whole) mine = choose_exact(a, row, n, buf);
@@ -412,7 +445,7 @@ struct BwdArgs {
     float *dl;
 };
 
-template <int kWarps>
+template <int kN, bool kSoftmax, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) k_gate_backward(const BwdArgs a)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -424,45 +457,59 @@ __global__ void __launch_bounds__(32 * kWarps) k_gate_backward(const BwdArgs a)
         const int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
         const bool live = e >= 0 && e < a.E;
         const float dw = live ? a.dw[t * a.k + lane] : 0.f;
-        const float l = live ? row[e] : 0.f;
-        float m = 0.f, inv = 1.f;
-        if (a.softmax) {
-            m = -INFINITY;
-            for (int i = lane; i < a.E; i += 32) m = fmaxf(m, row[i]);
+        float v[kN], m = 0.f, inv = 1.f;
+        if constexpr (kSoftmax) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = i * 32 + lane < a.E ? row[i * 32 + lane] : -INFINITY;
+            m = v[0];
+#pragma unroll
+            for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
             m = warp_fmax(m);
             if (m == -INFINITY) m = 0.f;
+        } else if (!a.accumulate) {   // zeros around the chosen experts
+            if (a.E % 4 == 0) {
+                for (int i = lane; i < a.E / 4; i += 32) ((float4 *)out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+                for (int i = lane; i < a.E; i += 32) out[i] = 0.f;
+            }
+        }
+        const float l = live ? row[e] : 0.f;
+        if constexpr (kSoftmax) {
             float z = 0.f;
-            for (int i = lane; i < a.E; i += 32) z += exp_below(row[i], m);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) z += v[i] = exp_below_fast(v[i], m);
             z = warp_sum(z);
             inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
         }
         // ds_j s_j = factor (dw_j - mean) p_j with p_j the weight before its factor
-        const float p = share(a.softmax, a.renorm, l, live, Norm{m, inv});
+        const float p = share(kSoftmax, a.renorm, l, live, Norm{m, inv});
         const float mean = a.renorm ? warp_sum(dw * p) : 0.f;
         float g = a.factor * (dw - mean) * p;
         // (1 - s as the score of the opposite logit: it keeps its accuracy near 0)
-        if (!a.softmax) g *= sigmoid(-l);
+        if constexpr (!kSoftmax) g *= sigmoid(-l);
         if (!live) g = 0.f;
-        const float dot = a.softmax ? warp_sum(g) : 0.f;
-        float sum = 0.f;   // parts of the same expert, in order
-        bool first = true;
-        for (int j = 0; j < a.k; ++j) {
-            const float o = __shfl_sync(kAll, g, j);
-            if (__shfl_sync(kAll, e, j) == e) {
-                sum += o;
-                if (j < lane) first = false;
+        const float dot = kSoftmax ? warp_sum(g) : 0.f;
+        // the parts of the same expert, in order, by the first lane that has it
+        const uint32_t same = __match_any_sync(kAll, live ? e : -1 - lane);
+        const bool first = live && (same & ((1u << lane) - 1u)) == 0;
+        float sum = g;
+        if (__any_sync(kAll, live && !first)) {
+            sum = 0.f;
+            for (int j = 0; j < a.k; ++j) {
+                const float o = __shfl_sync(kAll, g, j);
+                if (same >> j & 1u) sum += o;
             }
         }
-        if (a.softmax) {
-            for (int i = lane; i < a.E; i += 32) {
-                const float v = -(exp_below(row[i], m) * inv) * dot;
-                out[i] = a.accumulate ? out[i] + v : v;
+        if constexpr (kSoftmax) {
+            const float c = -inv * dot;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int j = i * 32 + lane;
+                if (j < a.E) out[j] = a.accumulate ? fmaf(v[i], c, out[j]) : v[i] * c;
             }
-        } else if (!a.accumulate) {
-            for (int i = lane; i < a.E; i += 32) out[i] = 0.f;
         }
         __syncwarp();   // (orders the row's stores before what is added to them)
-        if (live && first) out[e] = a.softmax || a.accumulate ? out[e] + sum : sum;
+        if (first) out[e] = kSoftmax || a.accumulate ? out[e] + sum : sum;
         __syncwarp();
     }
 }
@@ -484,16 +531,40 @@ static bool aligned(std::initializer_list<const void *> ps)
     return true;
 }
 
-template <int kN, int kWarps>
+// f(the experts a lane holds)
+template <class F>
+static bool by_size(int E, F f)
+{
+    const int n = (int)cdiv(E, 32);
+    return n <= 1    ? f(std::integral_constant<int, 1>())
+           : n <= 2  ? f(std::integral_constant<int, 2>())
+           : n <= 4  ? f(std::integral_constant<int, 4>())
+           : n <= 8  ? f(std::integral_constant<int, 8>())
+           : n <= 12 ? f(std::integral_constant<int, 12>())
+           : n <= 16 ? f(std::integral_constant<int, 16>())
+           : n <= 32 ? f(std::integral_constant<int, 32>())
+                     : f(std::integral_constant<int, 128>());
+}
+static unsigned ctas_of(int T, int warps)
+{
+    return (unsigned)std::min<int64_t>(cdiv(T, warps), (int64_t)gemm_num_sms() * 64);
+}
+
+template <int kN>
 static bool launch_as(const Args &a, cudaStream_t st)
 {
-    // keys of a token: of FP32 values for the groups, of FP64 ones for a close call
-    const size_t smem = a.has_bias || a.grouped ? (size_t)kWarps * (a.E + a.E / 32 + 1) * 8 : 0;
+    constexpr int kWarps = kN > 32 ? 4 : 8;
+    const size_t smem = (size_t)kWarps * (((a.E + a.E / 32 + 1) * (a.has_bias ? 8 : 4) + 7) & ~7);
     if (smem > 40 * 1024 && !set_attribute<k_gate<kN, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize>(
                                 (int)(kWarps * (32 * kN + kN + 1) * 8)))
         return false;
-    const int64_t ctas = std::min<int64_t>(cdiv(a.T, kWarps), (int64_t)gemm_num_sms() * 16);
-    return launch_chained<k_gate<kN, kWarps>>((unsigned)ctas, 32 * kWarps, smem, 1, st, a);
+    return launch_chained<k_gate<kN, kWarps>>(ctas_of(a.T, kWarps), 32 * kWarps, smem, 1, st, a);
+}
+template <int kN, bool kSoftmax>
+static bool launch_backward(const BwdArgs &a, cudaStream_t st)
+{
+    constexpr int kWarps = kN > 32 ? 4 : 8;
+    return launch_chained<k_gate_backward<kN, kSoftmax, kWarps>>(ctas_of(a.T, kWarps), 32 * kWarps, 0, 1, st, a);
 }
 
 }  // namespace gate
@@ -526,15 +597,7 @@ pmoe_status moe_gate_forward(pmoe_gate g, const float *logits, const float *bias
     a.bias = bias;
     a.idx = idx;
     a.w = w;
-    const int n = (int)cdiv(g.E, 32);
-    const bool done = n <= 1    ? gate::launch_as<1, 8>(a, stream)
-                      : n <= 2  ? gate::launch_as<2, 8>(a, stream)
-                      : n <= 4  ? gate::launch_as<4, 8>(a, stream)
-                      : n <= 8  ? gate::launch_as<8, 8>(a, stream)
-                      : n <= 12 ? gate::launch_as<12, 8>(a, stream)
-                      : n <= 16 ? gate::launch_as<16, 8>(a, stream)
-                      : n <= 32 ? gate::launch_as<32, 8>(a, stream)
-                                : gate::launch_as<128, 4>(a, stream);
+    const bool done = gate::by_size(g.E, [&](auto n) { return gate::launch_as<decltype(n)::value>(a, stream); });
     return done ? PMOE_OK : PMOE_ERR_CUDA;
 }
 
@@ -547,8 +610,9 @@ pmoe_status moe_gate_backward(pmoe_gate g, const float *logits, const int32_t *i
     if (g.T == 0) return PMOE_OK;
     gate::BwdArgs a{g.T, g.E, g.k, g.score == PMOE_SCORE_SOFTMAX, g.renorm != 0, accumulate != 0, g.factor,
                     logits, idx, d_topk_w, dlogits};
-    const int64_t ctas = std::min<int64_t>(cdiv(g.T, 8), (int64_t)gemm_num_sms() * 16);
-    return launch_chained<gate::k_gate_backward<8>>((unsigned)ctas, 256, 0, 1, stream, a) ? PMOE_OK : PMOE_ERR_CUDA;
+    const bool done = a.softmax ? gate::by_size(g.E, [&](auto n) { return gate::launch_backward<decltype(n)::value, true>(a, stream); })
+                                : gate::launch_backward<1, false>(a, stream);
+    return done ? PMOE_OK : PMOE_ERR_CUDA;
 }
 
 }  // extern "C"

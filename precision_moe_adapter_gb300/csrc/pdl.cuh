@@ -5,9 +5,10 @@
 // waited in turn, so has everything earlier in the stream.  grid_go() lets the
 // next kernel's CTAs be placed as soon as all of this kernel's have called it.
 //
-// Before its wait a kernel touches global memory in two places only:
-// k_head_combine reads the tokens' targets, anchors and rows of X and W, and
-// k_head_gemm<DW> behind DX reads G and its lists and writes dW.  Both rest on
+// Before its wait a kernel touches global memory in three places only:
+// k_head_combine reads the tokens' targets, anchors and rows of X and W,
+// k_head_gemm<DW> behind DX reads G and its lists and writes dW, and k_w8_gemm
+// behind k_fp8_quantize reads W.  All rest on
 // this: the kernel before calls grid_go() after its own wait, so when the one
 // behind it starts, everything before that kernel is complete.  What is touched
 // early is nothing that the kernel before writes (nor, for dW, reads), and it is

@@ -1,6 +1,7 @@
 // w8a8.cu -- 8-bit linear layers: quantisation per row and block of 128 columns,
 // the transposed weight of the gradient, the product's launches and the dense
 // layer with the orthogonal adapter around them (w8a8_gemm.cuh has the product).
+#include <atomic>
 #include <cstring>
 
 #include "w8a8_gemm.cuh"
@@ -15,7 +16,8 @@ void take_wait_hook(uint64_t &wait_ns, int &skip_item);
 }  // namespace tc
 namespace w8 {
 
-constexpr int kSms = 152;   // SMs of a GB300
+constexpr int kSms = 152;       // SMs of a GB300
+constexpr int kMaxSplits = 8;   // CTAs that share a tile: a portable cluster
 
 // ------------------------------------------------------------------ quantisation
 // Bound by HBM: 2 bytes read and 1 written per element.  A half-warp holds one
@@ -23,9 +25,9 @@ constexpr int kSms = 152;   // SMs of a GB300
 //
 // q is the exact quotient 448 x / a rounded to E4M3.  x and a are BF16 numbers, so a
 // quotient that is not one of E4M3's rounding midpoints is at least 2^-13 of itself
-// away from all of them (their products with a are integers of at most 12 bits on one
-// scale): the FP32 product with 448 / a, two roundings from it, is rounded to 16
-// bits first, which takes it back to a midpoint that it stands for, and across none.
+// away from all of them (their products with a are integers of at most 13 bits on one
+// scale): the FP32 product with an approximate 448 / a (2^-22) is rounded to 16 bits
+// first, which takes it back to a midpoint that it stands for, and across none.
 constexpr int kQThreads = 256;
 constexpr int kQBlocks = 4;   // blocks a half-warp has in flight
 
@@ -47,6 +49,16 @@ __device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x
     return (uint32_t)lo | (uint32_t)hi << 16;
 }
 
+// a / 448, correctly rounded: the remainder of a first quotient is exact, as a has 8
+// bits (checked for every BF16 number)
+__device__ __forceinline__ float over_448(float a)
+{
+    constexpr float r = 1.f / 448.f;
+    const float q = a * r;
+    return fmaf(fmaf(-q, 448.f, a), r, q);
+}
+
+// A half-warp takes kQBlocks consecutive blocks (of the row-major order of blocks)
 template <bool POW2>
 __global__ void __launch_bounds__(kQThreads) k_fp8_quantize(int rows, int K, int KB, const uint16_t *__restrict__ X,
                                                             uint8_t *__restrict__ q, float *__restrict__ s)
@@ -54,22 +66,22 @@ __global__ void __launch_bounds__(kQThreads) k_fp8_quantize(int rows, int K, int
     grid_wait();
     grid_go();
     const int lane = threadIdx.x & 15;
-    const uint32_t nblk = (uint32_t)rows * KB;   // (< 2^31: more would not fit the memory)
-    const uint32_t per = gridDim.x * (kQThreads / 16);
-    for (uint32_t b0 = blockIdx.x * (kQThreads / 16) + threadIdx.x / 16; b0 < ((nblk + 1) & ~1u);
-         b0 += per * kQBlocks) {
+    const uint32_t nblk = (uint32_t)rows * KB;   // (< 2^30)
+    const uint32_t per = gridDim.x * (kQThreads / 16) * kQBlocks;
+    // (both halves of a warp make the same turns)
+    for (uint32_t w0 = (blockIdx.x * (kQThreads / 16) + threadIdx.x / 32 * 2) * kQBlocks; w0 < nblk; w0 += per) {
+        const uint32_t b0 = w0 + (threadIdx.x / 16 & 1) * kQBlocks;
+        const uint32_t row0 = b0 / (uint32_t)KB, kb0 = b0 % (uint32_t)KB;
         uint4 u[kQBlocks];
-        int64_t row[kQBlocks];
-        int kb[kQBlocks];
+        uint32_t row = row0, kb = kb0;
 #pragma unroll
         for (int i = 0; i < kQBlocks; ++i) {
-            const uint32_t b = b0 + i * per;
-            row[i] = b / (uint32_t)KB;
-            kb[i] = (int)(b % (uint32_t)KB);
-            const int c = kb[i] * 128 + lane * 8;
+            const uint32_t c = kb * 128 + lane * 8;
             u[i] = make_uint4(0, 0, 0, 0);
-            if (b < nblk && c < K) u[i] = __ldcs((const uint4 *)(X + row[i] * K + c));
+            if (b0 + i < nblk && c < (uint32_t)K) u[i] = __ldcs((const uint4 *)(X + (int64_t)row * K + c));
+            if (++kb == (uint32_t)KB) kb = 0, ++row;
         }
+        row = row0, kb = kb0;
 #pragma unroll
         for (int i = 0; i < kQBlocks; ++i) {
             uint32_t m = absmax2(absmax2(u[i].x & 0x7FFF7FFFu, u[i].y), absmax2(u[i].z & 0x7FFF7FFFu, u[i].w));
@@ -78,14 +90,13 @@ __global__ void __launch_bounds__(kQThreads) k_fp8_quantize(int rows, int K, int
             m = absmax2(m, m >> 16 | m << 16);
             float a = __uint_as_float(m << 16);
             a = a < 7.8886091e-31f ? 7.8886091e-31f : a;   // 2^-100; a NaN stays
-            float sc = a / 448.f, r;
+            float sc = over_448(a), r;
             if constexpr (POW2) {
                 // (a / 448 in FP32 is a power of two only where the quotient is: 448 = 7 * 2^6)
-                const uint32_t e = (__float_as_uint(sc) + 0x7FFFFFu) & 0x7F800000u;
-                sc = a <= 3.4e38f ? __uint_as_float(e) : a;
-                r = 1.f / sc;
+                sc = __uint_as_float((__float_as_uint(sc) + 0x7FFFFFu) & 0x7F800000u);
+                r = __uint_as_float(0x7F000000u - __float_as_uint(sc));
             } else {
-                r = 448.f / a;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc));   // (sc and 1 / sc are normal numbers)
             }
             if (!(a <= 3.4e38f)) sc = __int_as_float(0x7fffffff);   // an infinity makes its block NaN too
             const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
@@ -95,12 +106,13 @@ __global__ void __launch_bounds__(kQThreads) k_fp8_quantize(int rows, int K, int
                 v[2 * j] = to_16_bits(__uint_as_float(w[j] << 16) * r);
                 v[2 * j + 1] = to_16_bits(__uint_as_float(w[j] & 0xFFFF0000u) * r);
             }
-            const uint32_t b = b0 + i * per;
-            const int c = kb[i] * 128 + lane * 8;
-            if (b < nblk && c < K) {
-                *(uint2 *)(q + row[i] * K + c) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
-                if (lane == 0) s[(int64_t)kb[i] * rows + row[i]] = sc;
+            const uint32_t c = kb * 128 + lane * 8;
+            if (b0 + i < nblk && c < (uint32_t)K) {
+                *(uint2 *)(q + (int64_t)row * K + c) =
+                    make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+                if (lane == 0) s[(int64_t)kb * rows + row] = sc;
             }
+            if (++kb == (uint32_t)KB) kb = 0, ++row;
         }
     }
 }
@@ -134,28 +146,32 @@ __global__ void __launch_bounds__(256) k_fp8_transpose(int N, int K, const uint8
 }
 
 // ------------------------------------------------------------------ product
-// out = sum of the splits' FP32 sums, in order; a thread 4 columns
-template <bool F32>
-__global__ void __launch_bounds__(256) k_w8_sum(int64_t n, int splits, const float *__restrict__ part,
-                                                void *__restrict__ out)
-{
-    grid_wait();
-    grid_go();
-    const int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 4;
-    if (i >= n) return;
-    float4 a = *(const float4 *)(part + i);
-#pragma unroll 4
-    for (int s = 1; s < splits; ++s) {
-        const float4 x = *(const float4 *)(part + s * n + i);
-        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-    }
-    if constexpr (F32) *(float4 *)((float *)out + i) = a;
-    else *(uint2 *)((uint16_t *)out + i) = make_uint2(hg::bf2(a.x, a.y), hg::bf2(a.z, a.w));
-}
-
 struct Tiling {
     int ctas, mt, nt, gm, splits, kper;
 };
+// Clusters of `size` CTAs of the product that run at once (they lie within a GPC, so
+// fewer than SMs / size)
+static int active_clusters(int size)
+{
+    static std::atomic<int> known[kMaxSplits + 1];
+    int n = known[size].load(std::memory_order_relaxed);
+    if (n) return n;
+    constexpr auto kern = k_w8_gemm<1, 128>;
+    if (!set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(kSmem)) return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+    if (n > 0) known[size].store(n, std::memory_order_relaxed);
+    return n;
+}
 static Tiling tiling(int64_t M, int64_t N, int64_t ksteps)
 {
     Tiling t;
@@ -166,35 +182,34 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps)
     const int64_t stripe = 128ll * t.ctas * ksteps * kStep;
     const int64_t most = std::max<int64_t>(8, (48ll << 20) / std::max<int64_t>(stripe, 1));
     t.gm = (int)cdiv(t.mt, cdiv(t.mt, most));
-    // few tiles: the blocks of K are shared out, so that every SM streams a part of W
+    // few tiles: the blocks of K are shared out, at least two a CTA, so that more SMs stream W
+    t.splits = 1;
+    t.kper = (int)ksteps;
     const int64_t tiles = (int64_t)t.mt * t.nt;
-    const int64_t want = std::max<int64_t>(1, std::min(kSms / t.ctas / tiles, cdiv(ksteps, 4)));
-    t.kper = (int)cdiv(ksteps, want);
-    t.splits = (int)cdiv(ksteps, t.kper);
+    for (int s = kMaxSplits; s > 1 && t.ctas == 1 && t.splits == 1; --s) {
+        const int64_t per = cdiv(ksteps, s);
+        if (tiles * s > kSms || per < 2 || cdiv(ksteps, per) != s || tiles > active_clusters(s)) continue;
+        t.splits = s;
+        t.kper = (int)per;
+    }
     return t;
 }
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-// Most FP32 values of the splits' sums, for up to `rows` rows: there are at most
-// kSms items of 128 x 128, and one for every four blocks of K
-static size_t part_elems(int64_t rows, int64_t N, int64_t K)
-{
-    const int64_t splits = std::min<int64_t>(kSms, cdiv(cdiv(K, kStep), 4));
-    return splits < 2 ? 0 : (size_t)std::min<int64_t>(splits * rows * N, (int64_t)kSms * 128 * 128);
-}
 
 template <int CTAS, int BN>
 static bool launch_as(const CUtensorMap &ma, const CUtensorMap &mt, const CUtensorMap &mb, const CUtensorMap &mo,
                       const Args &a, cudaStream_t st)
 {
     constexpr auto kern = k_w8_gemm<CTAS, BN>;
-    if (!set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(smem_of(BN))) return false;
+    if (!set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>(kSmem)) return false;
     const int64_t items = (int64_t)a.mt * a.nt * a.splits;
-    const int64_t clusters = std::min<int64_t>(items, gemm_num_sms() / CTAS);
-    return launch_chained<kern>((unsigned)(clusters * CTAS), threads_of(BN), smem_of(BN), CTAS, st, ma, mt, mb, mo, a);
+    const int64_t clusters = a.splits > 1 ? items : std::min<int64_t>(items, gemm_num_sms() / CTAS);
+    return launch_chained<kern>((unsigned)(clusters * CTAS), kThreads, kSmem, CTAS * a.splits, st, ma, mt, mb, mo,
+                                a);
 }
 
 static bool product(int rows, int N, int K, const void *A, const float *As, const void *W, const float *Ws, void *out,
-                    bool out_f32, float *part, DevErr *err, cudaStream_t st)
+                    bool out_f32, bool w_early, DevErr *err, cudaStream_t st)
 {
     const int ksteps = (int)cdiv(K, kStep);
     const Tiling t = tiling(rows, N, ksteps);
@@ -212,7 +227,9 @@ static bool product(int rows, int N, int K, const void *A, const float *As, cons
     a.stages = std::min(kMaxStages, kRingBytes / (kOpBytes + a.abytes));
     a.As = As;
     a.Ws = Ws;
-    a.f32_out = t.splits > 1 || out_f32;
+    a.f32_out = out_f32;
+    a.out = out;
+    a.w_early = w_early;
     a.err = err;
     tc::take_wait_hook(a.wait_ns, a.skip_item);
     CUtensorMap ma, mt, mb, mo;
@@ -221,15 +238,11 @@ static bool product(int rows, int N, int K, const void *A, const float *As, cons
     if (rows >= 128 && !tc::make_bytes_tmap(&ma, A, rows, K, kStep, 128, 128)) return false;
     if (a.tail && !tc::make_bytes_tmap(&mt, A, rows, K, kStep, a.tail, 128)) return false;
     if (!tc::make_bytes_tmap(&mb, W, N, K, kStep, 128, 128)) return false;
-    float *f32 = t.splits > 1 ? part : (float *)out;
-    if (a.f32_out ? !tc::make_f32_tmap(&mo, f32, t.splits, rows, N) : !tc::make_rows_tmap(&mo, out, rows, N, 32))
+    memset(&mo, 0, sizeof mo);
+    if (t.splits == 1 &&
+        !(out_f32 ? tc::make_f32_tmap(&mo, out, 1, rows, N) : tc::make_rows_tmap(&mo, out, rows, N, 32)))
         return false;
-    if (!(t.ctas == 2 ? launch_as<2, 256>(ma, mt, mb, mo, a, st) : launch_as<1, 128>(ma, mt, mb, mo, a, st))) return false;
-    if (t.splits == 1) return true;
-    const int64_t n = (int64_t)rows * N;
-    const unsigned grid = (unsigned)cdiv(n, 1024);
-    return out_f32 ? launch_chained<k_w8_sum<true>>(grid, 256, 0, 1, st, n, t.splits, (const float *)part, out)
-                   : launch_chained<k_w8_sum<false>>(grid, 256, 0, 1, st, n, t.splits, (const float *)part, out);
+    return t.ctas == 2 ? launch_as<2, 256>(ma, mt, mb, mo, a, st) : launch_as<1, 128>(ma, mt, mb, mo, a, st);
 }
 
 static bool quantize(int rows, int K, const void *X, bool pow2, void *q, float *s, cudaStream_t st)
@@ -255,11 +268,10 @@ struct Ws {
     DevErr *err;
     uint8_t *q;      // [rows][max(N, K)]
     float *s;        // [blocks][rows]
-    float *part;     // the splits' sums, of either direction
     float *buf;      // adapter: x~ (BF16) or dx~ (FP32), [rows][K]
     size_t bytes;
 };
-static Ws carve(void *ws, int64_t rows, int64_t N, int64_t K, bool dense, bool adapter)
+static Ws carve(void *ws, int64_t rows, int64_t N, int64_t K, bool adapter)
 {
     Ws w;
     uint8_t *base = (uint8_t *)ws;
@@ -271,11 +283,8 @@ static Ws carve(void *ws, int64_t rows, int64_t N, int64_t K, bool dense, bool a
     };
     w.err = (DevErr *)ws;
     const int64_t most = std::max(N, K);
-    w.q = dense ? take((size_t)rows * most) : nullptr;
-    w.s = dense ? (float *)take((size_t)rows * cdiv(most, 128) * 4) : nullptr;
-    size_t parts = part_elems(rows, N, K);
-    if (dense) parts = std::max(parts, part_elems(rows, K, N));
-    w.part = (float *)take(parts * 4);
+    w.q = take((size_t)rows * most);
+    w.s = (float *)take((size_t)rows * cdiv(most, 128) * 4);
     w.buf = adapter ? (float *)take((size_t)rows * K * 4) : nullptr;
     w.bytes = off;
     return w;
@@ -332,7 +341,7 @@ pmoe_status fp8_transpose(int32_t N, int32_t K, const void *q, const float *s, v
 
 size_t fp8_gemm_ws_bytes(int32_t rows, int32_t N, int32_t K)
 {
-    return w8::shape_ok(rows, N, K) ? w8::carve(nullptr, rows, N, K, false, false).bytes : 0;
+    return w8::shape_ok(rows, N, K) ? kHdrBytes : 0;
 }
 
 pmoe_status fp8_gemm(int32_t rows, int32_t N, int32_t K, const void *A, const float *As, const void *W, const float *Ws,
@@ -341,15 +350,14 @@ pmoe_status fp8_gemm(int32_t rows, int32_t N, int32_t K, const void *A, const fl
     if (!w8::shape_ok(rows, N, K) || !W || !Ws || (rows > 0 && (!A || !As || !Y)) || !w8::a16(A) || !w8::a16(As) ||
         !w8::a16(W) || !w8::a16(Ws) || !w8::a16(Y))
         return PMOE_ERR_INVALID_ARG;
-    const w8::Ws w = w8::carve(ws, rows, N, K, false, false);
-    if (!ws || ws_bytes < w.bytes || !w8::a16(ws)) return PMOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < kHdrBytes || !w8::a16(ws)) return PMOE_ERR_WORKSPACE;
     if (rows == 0) return PMOE_OK;
-    return w8::product(rows, N, K, A, As, W, Ws, Y, false, w.part, w.err, stream) ? PMOE_OK : PMOE_ERR_CUDA;
+    return w8::product(rows, N, K, A, As, W, Ws, Y, false, false, (DevErr *)ws, stream) ? PMOE_OK : PMOE_ERR_CUDA;
 }
 
 size_t dense_w8a8_ws_bytes(int32_t rows, int32_t N, int32_t K, int adapter)
 {
-    return w8::shape_ok(rows, N, K) ? w8::carve(nullptr, rows, N, K, true, adapter != 0).bytes : 0;
+    return w8::shape_ok(rows, N, K) ? w8::carve(nullptr, rows, N, K, adapter != 0).bytes : 0;
 }
 
 pmoe_status dense_w8a8_forward(const void *q, const float *s, int32_t N, int32_t K, int32_t block, const void *R,
@@ -359,7 +367,7 @@ pmoe_status dense_w8a8_forward(const void *q, const float *s, int32_t N, int32_t
     const pmoe_status e = w8::check_dense(q, s, N, K, block, R, rows);
     if (e != PMOE_OK) return e;
     if ((rows > 0 && (!X || !Y)) || !w8::a16(X) || !w8::a16(Y)) return PMOE_ERR_INVALID_ARG;
-    const w8::Ws w = w8::carve(ws, rows, N, K, true, R != nullptr);
+    const w8::Ws w = w8::carve(ws, rows, N, K, R != nullptr);
     if (!ws || ws_bytes < w.bytes || !w8::a16(ws)) return PMOE_ERR_WORKSPACE;
     if (rows == 0) return PMOE_OK;
     if (R) {
@@ -367,7 +375,7 @@ pmoe_status dense_w8a8_forward(const void *q, const float *s, int32_t N, int32_t
         X = w.buf;
     }
     return w8::quantize(rows, K, X, pow2 != 0, w.q, w.s, stream) &&
-                   w8::product(rows, N, K, w.q, w.s, q, s, Y, false, w.part, w.err, stream) &&
+                   w8::product(rows, N, K, w.q, w.s, q, s, Y, false, true, w.err, stream) &&
                    cudaPeekAtLastError() == cudaSuccess
                ? PMOE_OK
                : PMOE_ERR_CUDA;
@@ -382,14 +390,14 @@ pmoe_status dense_w8a8_backward(const void *qt, const float *st, int32_t N, int3
     if ((R && !dR) || (rows > 0 && (!dY || !dX || (R && !X))) || !w8::a16(X) || !w8::a16(dY) || !w8::a16(dX) ||
         !w8::a16(dR))
         return PMOE_ERR_INVALID_ARG;
-    const w8::Ws w = w8::carve(ws, rows, N, K, true, R != nullptr);
+    const w8::Ws w = w8::carve(ws, rows, N, K, R != nullptr);
     if (!ws || ws_bytes < w.bytes || !w8::a16(ws)) return PMOE_ERR_WORKSPACE;
     if (rows == 0)
         return !R || cudaMemsetAsync(dR, 0, (size_t)K * block * sizeof(float), stream) == cudaSuccess ? PMOE_OK
                                                                                                       : PMOE_ERR_CUDA;
     // dx~ in FP32 where an adapter follows, as in dense_linear_backward
     if (!w8::quantize(rows, N, dY, pow2 != 0, w.q, w.s, stream) ||
-        !w8::product(rows, K, N, w.q, w.s, qt, st, R ? (void *)w.buf : dX, R != nullptr, w.part, w.err, stream))
+        !w8::product(rows, K, N, w.q, w.s, qt, st, R ? (void *)w.buf : dX, R != nullptr, true, w.err, stream))
         return PMOE_ERR_CUDA;
     if (R) {
         launch_outer_tc(1, rows, K, block, (const uint16_t *)X, K, false, nullptr, 1, w.buf, true, K, nullptr, dR, stream);

@@ -6,8 +6,12 @@
 // Both operands are K-major; a K step is one block, 128 bytes of a row, one
 // 128-byte swizzle row.  The tensor cores sum one block into a TMEM buffer of its
 // own, the epilogue warps scale it and add it to the tile's FP32 sums, which stay in
-// registers: a thread owns a row's 128 columns, so that its scale is one number
-// a block, As[b][row] Ws[unit][b].
+// registers: a thread owns 128 (or 64) columns of a row, so that its scale is one
+// number a block, As[b][row] Ws[n / 128][b].
+//
+// Few tiles: a cluster of up to 8 CTAs shares a tile's blocks of K.  Their sums meet
+// through distributed shared memory and are added in order, each CTA a share of the
+// rows, so that neither a second kernel nor FP32 sums in memory are needed.
 //
 // Roles as in the head's products (head_gemm.cuh): warps 0 and 3 load A and W,
 // warp 1 issues the MMAs, warp 2 allocates TMEM, warps 4.. are the epilogue; CTAS CTAs
@@ -33,20 +37,23 @@ using tc::tc_fence_before;
 
 constexpr int kStep = 128;                     // K of a step: a block
 constexpr int kThreads0 = 128;
-constexpr int epi_warps(int BN) { return BN / kUnit * 4; }
-constexpr int threads_of(int BN) { return kThreads0 + 32 * epi_warps(BN); }
+// eight epilogue warps: each takes 32 rows and half of the tile's columns
+constexpr int kEpi = 8;
+constexpr int kThreads = kThreads0 + 32 * kEpi;
 constexpr int bufs_of(int BN) { return 512 / BN; }   // all of TMEM
-constexpr int smem_of(int BN) { return kRingBytes + epi_warps(BN) * kWarpOut + 512 + 1024; }
+constexpr int kSmem = kRingBytes + kEpi * kWarpOut + 512 + 1024;
 
 struct Args {
     int M, N;
     int mt, nt, gm;          // tiles, and m tiles that run together
-    int ksteps, splits, kper;   // K steps of a tile; items of kper steps
+    int ksteps, splits, kper;   // K steps of a tile; CTAs (of a cluster) that share it, kper each
     int stages, abytes;      // the ring: stages, and bytes of A in one
     int tail;                // rows of tmAt's boxes: the M % 128 last rows of A
     const float *As;         // [ksteps][M]
     const float *Ws;         // [ceil(N/128)][ksteps]
-    int f32_out;             // the output map is FP32, one plane a split
+    int f32_out;             // the output is FP32
+    void *out;               // splits > 1: [M][N]
+    int w_early;             // W was complete before the kernel before started
     uint64_t wait_ns;
     int skip_item;           // test hook (-1: none)
     DevErr *err;
@@ -57,18 +64,31 @@ struct Item {
 };
 __device__ __forceinline__ bool item_of(const Args &a, int i, Item &t)
 {
-    const int tiles = a.mt * a.nt;
-    t.s = i / tiles;
-    if (t.s >= a.splits) return false;
-    i -= t.s * tiles;
+    const int tile = i / a.splits;   // (shared tiles: one item a CTA, the cluster's ranks in order)
+    if (tile >= a.mt * a.nt) return false;
+    t.s = i - tile * a.splits;
     t.k0 = t.s * a.kper;
     t.k1 = min(t.k0 + a.kper, a.ksteps);
+    i = tile;
     const int gsz = a.gm * a.nt, g = i / gsz;
     i -= g * gsz;
     const int gm = min(a.gm, a.mt - g * a.gm);
     t.n = i / gm;
     t.m = g * a.gm + i - t.n * gm;
     return true;
+}
+// Place of 4 columns of a row among a CTA's sums of 128 x 128 (no bank conflicts by
+// rows or by columns)
+__device__ __forceinline__ uint32_t sum_at(int row, int j) { return (uint32_t)(row * 512 + ((j ^ (row & 31)) << 4)); }
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank)
+{
+    float4 v;
+    asm volatile("{ .reg .b32 r; mapa.shared::cluster.u32 r, %4, %5;\n"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r]; }"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
 }
 
 // A K step of 128: four MMAs of K = 32, the first one overwriting, and the
@@ -107,13 +127,56 @@ __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N)
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+__device__ __forceinline__ void tmem_issue16(uint32_t taddr, float *v)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+                   "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(float *v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
+}
+
+// Quads f0, f0 + 32 kEpi, ... < f1 of a shared tile: the sum over the cluster's CTAs
+// in their order, kU quads at a time
+template <int kS, int kU>
+__device__ __forceinline__ void join(const Args &a, const Item &t, uint32_t sums, int f0, int f1)
+{
+    for (; f0 < f1; f0 += kU * 32 * kEpi) {
+        float4 x[kU][kS];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int f = f0 + u * 32 * kEpi;
+#pragma unroll
+            for (int q = 0; q < kS; ++q)
+                if (f < f1 && q < a.splits) x[u][q] = ld_cluster(sums + sum_at(f >> 5, f & 31), (uint32_t)q);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int f = f0 + u * 32 * kEpi, c = t.n * 128 + (f & 31) * 4;
+            float4 v = x[u][0];
+#pragma unroll
+            for (int q = 1; q < kS; ++q)
+                if (q < a.splits) v.x += x[u][q].x, v.y += x[u][q].y, v.z += x[u][q].z, v.w += x[u][q].w;
+            if (f >= f1 || c >= a.N) continue;
+            const int64_t at = (int64_t)(t.m * 128 + (f >> 5)) * a.N + c;
+            if (a.f32_out) *(float4 *)((float *)a.out + at) = v;
+            else *(uint2 *)((uint16_t *)a.out + at) = make_uint2(hg::bf2(v.x, v.y), hg::bf2(v.z, v.w));
+        }
+    }
+}
+
 template <int CTAS, int BN>
-__global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_constant__ CUtensorMap tmA,
+__global__ void __launch_bounds__(kThreads, 1) k_w8_gemm(const __grid_constant__ CUtensorMap tmA,
                                                                const __grid_constant__ CUtensorMap tmAt,
                                                                const __grid_constant__ CUtensorMap tmB,
                                                                const __grid_constant__ CUtensorMap tmOut, const Args a)
 {
-    constexpr int kEpi = epi_warps(BN), kBufs = bufs_of(BN);
+    constexpr int kBufs = bufs_of(BN), kCols = BN / 2;   // (columns of an epilogue thread)
     static_assert(BN / CTAS == 128, "one 128-row operand tile of W per CTA");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -161,27 +224,31 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
 
-    grid_wait();
-    grid_go();
+    // W may be on its way before the wait (a.w_early): the kernel before neither writes
+    // it nor lets this one start before its own wait is over
+    if (warp != 3 || !a.w_early) {
+        grid_wait();
+        grid_go();
+    }
     bool ok = true;
     // registers: 384 x 168 = 128 x 40 + 256 x 232
     if (warp >= 4) {
         // ---------------- epilogue
-        if constexpr (kEpi == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int quad = warp & 3, half = (warp - 4) >> 2;
         const int rl = quad * 32 + lane;   // row of the CTA's 128
-        const uint32_t tld = tmem + ((uint32_t)(quad * 32) << 16) + half * kUnit;
+        const uint32_t tld = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
         const uint32_t ob = out0 + (warp - 4) * kWarpOut, orow = ob + lane * 128;
         const int NB = (int)cdiv(a.N, kUnit);
         uint32_t gc = 0;
         Item t;
         for (int i = first; ok && item_of(a, i, t); i += step) {
             const int mrow = (t.m * CTAS + (int)rank) * 128;
-            const int row = mrow + rl, unit = t.n * (BN / kUnit) + half;
+            const int row = mrow + rl, unit = (t.n * BN + half * kCols) / kUnit;
             const bool live = row < a.M && unit < NB;
             const float *ap = a.As + (live ? row : 0), *wp = a.Ws + (int64_t)(live ? unit : 0) * a.ksteps;
-            // the scales of four steps on their way
-            constexpr int kAhead = 4;
+            // the scales of two steps on their way
+            constexpr int kAhead = 2;
             float sa[kAhead], sw[kAhead];
             auto fetch = [&](int u, int k) {
                 if (k < t.k1) {
@@ -194,9 +261,9 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
                 sa[u] = sw[u] = 0.f;
                 fetch(u, t.k0 + u);
             }
-            float acc[kUnit];
+            float acc[kCols];
 #pragma unroll
-            for (int j = 0; j < kUnit; ++j) acc[j] = 0.f;
+            for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
 #pragma unroll 1
             for (int k = t.k0; ok && k < t.k1; k += kAhead) {
 #pragma unroll
@@ -210,31 +277,47 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
                     tc_fence_after();
                     const float s = sa[u] * sw[u];
                     fetch(u, k + u + kAhead);
+                    const uint32_t at = tld + b * BN;
+                    // 16 columns are on their way while the 16 before are added
+                    float v[2][16];
+                    tmem_issue16(at, v[0]);
 #pragma unroll
-                    for (int j = 0; j < kUnit; j += 32) {
-                        float v[32];
-                        hg::tmem_issue32(tld + b * BN + j, v);
-                        hg::tmem_wait(v);
+                    for (int j = 0; j < kCols / 16; ++j) {
+                        tmem_wait16(v[j & 1]);
+                        if (j + 1 < kCols / 16) {
+                            tmem_issue16(at + (j + 1) * 16, v[(j + 1) & 1]);
+                        } else {   // all of the buffer is in registers
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if constexpr (CTAS == 2) hg::arrive_cluster(hg::map_leader(tempty(b)));
+                                else mbar_arrive(tempty(b));
+                            }
+                        }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) acc[j + e] = fmaf(v[e], s, acc[j + e]);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CTAS == 2) hg::arrive_cluster(hg::map_leader(tempty(b)));
-                        else mbar_arrive(tempty(b));
+                        for (int e = 0; e < 16; ++e) acc[j * 16 + e] = fmaf(v[j & 1][e], s, acc[j * 16 + e]);
                     }
                     ++gc;
                 }
             }
             if (!ok) break;
+            if (CTAS == 1 && a.splits > 1) {   // (every MMA has read the ring: it holds the sums now)
+                if (row < a.M) {
+#pragma unroll
+                    for (int j = 0; j < kCols / 4; ++j)
+                        tc::st_shared_v4(s0 + sum_at(rl, half * (kCols / 4) + j),
+                                         make_uint4(__float_as_uint(acc[4 * j]), __float_as_uint(acc[4 * j + 1]),
+                                                    __float_as_uint(acc[4 * j + 2]), __float_as_uint(acc[4 * j + 3])));
+                }
+                continue;
+            }
             // through shared memory (the warp's 32 rows of 128 bytes, 128-byte swizzle)
             // to TMA stores, which clip rows and columns past the end
-            const int xc = t.n * BN + half * kUnit, yr = mrow + quad * 32;
+            const int xc = t.n * BN + half * kCols, yr = mrow + quad * 32;
             auto put = [&](int x) {
                 tc::fence_proxy_async();
                 __syncwarp();
-                if (lane == 0 && x < a.N && yr < a.M) hg::store_3d(&tmOut, ob, x, yr, t.s, false);
+                if (lane == 0 && x < a.N && yr < a.M) hg::store_3d(&tmOut, ob, x, yr, 0, false);
             };
             auto reuse = [&]() {   // the previous box has been read
                 if (lane == 0) hg::store_wait_read();
@@ -242,7 +325,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
             };
             if (a.f32_out) {
 #pragma unroll
-                for (int q = 0; q < kUnit; q += 32) {
+                for (int q = 0; q < kCols; q += 32) {
                     reuse();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -255,7 +338,7 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
                 }
             } else {
 #pragma unroll
-                for (int q = 0; q < kUnit; q += 64) {
+                for (int q = 0; q < kCols; q += 64) {
                     reuse();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -269,8 +352,19 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
             }
         }
         if (lane == 0) hg::store_wait_all();
+        if (CTAS == 1 && a.splits > 1) {
+            __syncwarp();
+            hg::cluster_sync();   // the cluster's sums are there
+            item_of(a, blockIdx.x, t);
+            const int n4 = min(128, a.M - t.m * 128) * 32;   // quads of the tile's rows
+            const int f0 = n4 * t.s / a.splits + threadIdx.x - kThreads0, f1 = n4 * (t.s + 1) / a.splits;
+            if (a.splits <= 4) join<4, 4>(a, t, s0, f0, f1);   // (as many loads on their way as registers allow)
+            else join<8, 2>(a, t, s0, f0, f1);
+            __syncwarp();
+            hg::cluster_sync();   // no CTA leaves while its sums are read
+        }
     } else {
-        if constexpr (kEpi == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 || warp == 3) {
             // ---------------- producers (whole warps): A, and W
             const bool isA = warp == 0;
@@ -322,6 +416,11 @@ __global__ void __launch_bounds__(threads_of(BN), 1) k_w8_gemm(const __grid_cons
                     }
                 }
             }
+        }
+        if (CTAS == 1 && a.splits > 1) {   // (the epilogue's two meetings)
+            __syncwarp();
+            hg::cluster_sync();
+            hg::cluster_sync();
         }
     }
     // After a wait that ran out, copies or MMAs may still be in flight: give
