@@ -26,6 +26,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 struct Args {
     int T, E, k, G, top, gsum, gsize;   // gsize: experts of a group
+    uint32_t gmagic;                    // e / gsize is the high half of e gmagic (0: e)
     int softmax, renorm, has_bias, grouped;
     float factor;
     const float *logits, *bias;
@@ -60,12 +61,6 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k)
     const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
 }
-__device__ __forceinline__ float warp_fmax(float v)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
-}
 template <class F>
 __device__ __forceinline__ F warp_sum(F v)
 {
@@ -78,6 +73,18 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float tanh_approx(float x)
+{
+    float y;
+    asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_fmax(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
 }
 __device__ __forceinline__ float rcp(float x)
 {
@@ -259,10 +266,12 @@ __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n,
 // One warp a token, experts 32 i + lane in a lane's registers
 //
 // The best k are found among few candidates: the (k + 2)-th largest of the lanes' own
-// largest keys bounds the (k + 2)-th largest of all from below, and the keys from there
-// up (some 11 for k = 8, E = 384) are gathered, one a lane, and ranked.  (Taking the
-// largest k times over, each time looking through all keys again, took 1280 instructions a
-// token at k = 8, E = 384 and 23.7 us for 8192 tokens.)
+// largest values bounds the (k + 2)-th largest of all from below, and the experts from
+// there up (some 11 for k = 8, E = 384) are gathered, one a lane, and ranked.  (Taking the
+// largest k times over, each time looking through all of them again, took 1280 instructions
+// a token at k = 8, E = 384 and 23.7 us for 8192 tokens.)  With sigmoid scores, a bias and
+// no groups the values of that search are c by tanh.approx (2^-11); only the
+// candidates' scores are computed in full.
 template <int kN, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Args a)
 {
@@ -271,64 +280,74 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
     // keys of a token: FP32 ones, of FP64 values for a close call
     uint64_t *buf = (uint64_t *)((uint8_t *)smem + (size_t)warp * (((a.E + a.E / 32 + 1) * (a.has_bias ? 8 : 4) + 7) & ~7));
     __shared__ int cand_id[kWarps][32];
-    __shared__ uint32_t cand_key[kWarps][32];
+    __shared__ float cand_c[kWarps][32], cand_s[kWarps][32];
+    int *ci = cand_id[warp];
+    float *cc = cand_c[warp], *cs = cand_s[warp];
     grid_wait();
     grid_go();
     for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
         const float *row = a.logits + t * a.E;
-        uint32_t key[kN];
+        float v[kN];   // -inf: no expert, or one that cannot be chosen
         Norm n{0.f, 1.f};
-        {
-            float v[kN];
+        const bool coarse = a.has_bias && !a.softmax && !a.grouped;
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int e = i * 32 + lane;
-                v[i] = e < a.E ? row[e] : -INFINITY;
-            }
-            if (a.softmax) {
-                float m = v[0];
+        for (int i = 0; i < kN; ++i) {
+            const int e = i * 32 + lane;
+            v[i] = e < a.E ? row[e] : -INFINITY;
+        }
+        if (a.softmax) {
+            float m = v[0];
 #pragma unroll
-                for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
-                m = warp_fmax(m);
-                n.m = m == -INFINITY ? 0.f : m;   // (no expert can be chosen: all scores are zero)
-                if (a.has_bias || a.grouped || !a.renorm) {
-                    float z = 0.f;
+            for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
+            m = warp_fmax(m);
+            n.m = m == -INFINITY ? 0.f : m;   // (no expert can be chosen: all scores are zero)
+            if (a.has_bias || a.grouped || !a.renorm) {
+                float z = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kN; ++i) z += exp_below_fast(v[i], n.m);
-                    z = warp_sum(z);
-                    n.inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+                for (int i = 0; i < kN; ++i) z += exp_below_fast(v[i], n.m);
+                if (a.has_bias) {   // (v is the exponential from here on; -inf stays)
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) v[i] = v[i] == -INFINITY ? v[i] : exp_below_fast(v[i], n.m);
                 }
+                z = warp_sum(z);
+                n.inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
             }
-            if (a.has_bias) {
+        }
+        if (a.has_bias) {
+            // (a loop for each form: a choice within one costs some 500 instructions a token)
+            auto form = [&](auto score) {
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
                     const int e = i * 32 + lane;
-                    const float s = a.softmax ? exp_below_fast(v[i], n.m) * n.inv : rcp(1.f + ex2(v[i] * -1.4426950408889634f));
-                    if (v[i] != -INFINITY) v[i] = s + a.bias[e];
+                    const float c = score(v[i], e < a.E ? __ldg(a.bias + e) : 0.f);
+                    v[i] = v[i] == -INFINITY ? -INFINITY : c;
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < kN; ++i) key[i] = i * 32 + lane < a.E ? key_of(v[i]) : 0u;
+            };
+            if (coarse) form([](float l, float b) { return fmaf(tanh_approx(0.5f * l), 0.5f, b + 0.5f); });
+            else if (a.softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
+            else form([](float l, float b) { return rcp(1.f + ex2(l * -1.4426950408889634f)) + b; });
         }
-        // error of a c beside its own rounding: 2^-21 of the largest score
-        const float terr = 1.9073486e-6f * (a.softmax ? n.inv : 1.f);
+        // error of the difference of two c beside their own rounding: their scores are
+        // off by less than 2^-21 of the largest one
+        const float terr = 9.5367432e-7f * (a.softmax ? n.inv : 1.f);
         auto near = [&](float x, float y) {   // x >= y
             return y != -INFINITY && !(x - y > terr + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
         };
+        int mine = 0, cnt = 0;
         bool whole = false;   // the groups are too close to call in FP32
         if (a.grouped) {
             uint32_t *kb = (uint32_t *)buf;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int e = i * 32 + lane;
-                if (e < a.E) kb[e + (e >> 5)] = key[i];
+                if (e < a.E) kb[e + (e >> 5)] = key_of(v[i]);
             }
             __syncwarp();
             uint32_t in, out, kept;
             if (a.has_bias || a.gsum == 1) {
                 const uint32_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) { return sum_of(a, x, y); });
                 kept = keep_groups(s, a.G, a.top, in, out);
-                if (a.has_bias && a.top < a.G) {
+                if (a.has_bias) {
                     const float x = of_key(in), y = of_key(out);
                     whole = a.gsum == 1 ? near(x, y) : near(0.5f * x, 0.5f * y);
                 }
@@ -346,85 +365,115 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
             }
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
-                const int e = i * 32 + lane;
-                if (e < a.E && !(kept >> (e / a.gsize) & 1u)) key[i] = 0u;
+                const uint32_t e = i * 32 + lane, g = a.gmagic ? __umulhi(e, a.gmagic) : e;
+                if (!(kept >> (g & 31u) & 1u)) v[i] = -INFINITY;
             }
-            __syncwarp();
-        }
-        // the candidates, in the order of their ids
-        int mine = 0, cnt = 0;
-        if (!whole) {
-            uint32_t best = key[0], least = 0;
+            if (!a.has_bias) {   // (for the search through keys, where it comes to that)
 #pragma unroll
-            for (int i = 1; i < kN; ++i) best = max(best, key[i]);
-            for (int j = min(a.k + 2, 32); j > 0; --j) {
-                least = warp_max(best);
-                if (least == 0) break;          // fewer lanes have any: all keys are candidates
-                if (best == least) best = 0;    // (lanes with equal keys count as one)
+                for (int i = 0; i < kN; ++i) {
+                    const uint32_t e = i * 32 + lane, g = a.gmagic ? __umulhi(e, a.gmagic) : e;
+                    if (e < (uint32_t)a.E && !(kept >> (g & 31u) & 1u)) kb[e + (e >> 5)] = 0u;
+                }
+                __syncwarp();
             }
-            const uint32_t from = max(least, 1u);
-            uint32_t *ck = cand_key[warp];
-            int *ci = cand_id[warp];
+        }
+        float s = 0.f;
+        bool scored = false;   // s is the lane's score
+        if (!whole) {
+            float best = v[0];
+#pragma unroll
+            for (int i = 1; i < kN; ++i) best = fmaxf(best, v[i]);
+            // the lanes' largest values sorted, descending (a bitonic network)
+#pragma unroll
+            for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+                for (int o = size / 2; o; o /= 2) {
+                    const float other = __shfl_xor_sync(kAll, best, o);
+                    const bool up = ((lane & o) == 0) == ((lane & size) == 0);
+                    best = up ? fmaxf(best, other) : fminf(best, other);
+                }
+            }
+            // (-inf: fewer lanes have any that can be chosen, all are candidates)
+            const float least = __shfl_sync(kAll, best, min(a.k + 2, 32) - 1);
+            const bool all = least == -INFINITY;
+            // (twice the error of the values: 2^-12 by tanh.approx, and roundings)
+            const float from = all          ? -3.402823466e38f
+                               : a.has_bias ? least - ((coarse ? 5.4e-4f : terr) + 4.8e-7f * fabsf(least))
+                                            : least;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
-                const bool in = key[i] >= from;
+                const bool in = v[i] >= from;
                 const uint32_t b = __ballot_sync(kAll, in);
                 if (b) {
                     const int at = cnt + __popc(b & ((1u << lane) - 1u));
-                    if (in && at < 32) ck[at] = key[i], ci[at] = i * 32 + lane;
+                    if (in && at < 32) ci[at] = i * 32 + lane;
                     cnt += __popc(b);
                 }
             }
             __syncwarp();
-            if (cnt > 32) {
-                if (!a.has_bias) {
-                    uint32_t *kb = (uint32_t *)buf;
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        const int e = i * 32 + lane;
-                        if (e < a.E) kb[e + (e >> 5)] = key[i];
-                    }
-                    __syncwarp();
-                    mine = choose(a, kb);
-                }
-                whole = a.has_bias;
+            if (cnt > 32 || cnt < a.k || (a.has_bias && cnt == a.k && !all)) {
+                whole = true;   // many equal ones, few that can be chosen, or k = 32
             } else {
-                const uint32_t c = lane < cnt ? ck[lane] : 0u;
-                const int e = ci[lane];
+                const int e = lane < cnt ? ci[lane] : 0;
+                const float l = lane < cnt ? row[e] : -INFINITY;
+                float c = l;
+                if (a.has_bias) {
+                    s = a.softmax ? exp_below(l, n.m) * n.inv : sigmoid(l);
+                    if (lane < cnt) c = s + a.bias[e];
+                }
                 int rank = 0;
                 for (int j = 0; j < cnt; ++j) {
-                    const uint32_t o = __shfl_sync(kAll, c, j);
+                    const float o = __shfl_sync(kAll, c, j);
                     rank += o > c || (o == c && j < lane);
                 }
                 __syncwarp();
-                if (lane < cnt) ck[rank] = c, ci[rank] = e;
+                if (lane < cnt) ci[rank] = e, cc[rank] = c, cs[rank] = s;
                 __syncwarp();
-                const uint32_t mk = lane < cnt ? ck[lane] : 0u;
                 mine = lane < cnt ? ci[lane] : 0;
+                c = lane < cnt ? cc[lane] : -INFINITY;
                 if (a.has_bias) {
-                    const uint32_t nk = __shfl_down_sync(kAll, mk, 1);
-                    bool close = lane < a.k && lane + 1 < cnt && near(of_key(mk), of_key(nk));
-                    const float ck1 = of_key(__shfl_sync(kAll, mk, min(a.k, cnt) - 1));
-                    // everything that may be among the best k has to be a candidate
-                    const bool all = least == 0, short_by_one = cnt <= a.k && !all;
-                    if (__any_sync(kAll, close) || short_by_one) {
-                        const float edge = ck1 - 2.f * (terr + 4.7683716e-7f * fabsf(ck1));
-                        if (short_by_one || (!all && !(of_key(least) < edge))) whole = true;
-                        else mine = order_exact(a, row, n, mine, cnt, ci);
-                    }
+                    s = cs[lane];
+                    const float nc = __shfl_down_sync(kAll, c, 1);
+                    scored = !__any_sync(kAll, lane < a.k && lane + 1 < cnt && near(c, nc));
+                    if (!scored) mine = order_exact(a, row, n, mine, cnt, ci);
+                } else {
+                    s = a.softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);
+                    scored = true;
                 }
-                __syncwarp();
+            }
+            __syncwarp();
+        }
+        if (whole) {
+            if (a.has_bias) {
+                mine = choose_exact(a, row, n, buf);
+            } else {
+                uint32_t *kb = (uint32_t *)buf;
+                if (!a.grouped) {
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {
+                        const int e = i * 32 + lane;
+                        if (e < a.E) kb[e + (e >> 5)] = key_of(v[i]);
+                    }
+                    __syncwarp();
+                }
+                mine = choose(a, kb);
             }
         }
-        if (whole) mine = choose_exact(a, row, n, buf);
         // the weights: the scores without the bias
         const bool live = lane < a.k;
-        const float l = live ? row[mine] : 0.f;
-        const float w = a.factor * share(a.softmax, a.renorm, l, live, n);
+        float w = 0.f;
+        if (scored) {
+            if (!live) s = 0.f;
+            const float D = a.renorm ? warp_sum(s) : 1.f;
+            w = a.renorm ? s / D : s;          // (1e-20 is below half a unit of D)
+            scored = D > 0.25f;
+        }
+        if (!scored) w = share(a.softmax, a.renorm, live ? row[mine] : 0.f, live, n);
         if (live) {
             a.idx[t * a.k + lane] = mine;
-            a.w[t * a.k + lane] = w;
+            a.w[t * a.k + lane] = a.factor * w;
         }
+        __syncwarp();
     }
 }
 
@@ -588,6 +637,7 @@ pmoe_status moe_gate_forward(pmoe_gate g, const float *logits, const float *bias
     a.top = g.topk_groups;
     a.gsum = g.group_sum;
     a.gsize = g.E / g.groups;
+    a.gmagic = a.gsize > 1 ? (uint32_t)(((1ull << 32) + a.gsize - 1) / a.gsize) : 0u;
     a.softmax = g.score == PMOE_SCORE_SOFTMAX;
     a.renorm = g.renorm != 0;
     a.has_bias = bias != nullptr;
