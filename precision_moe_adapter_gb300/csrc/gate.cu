@@ -7,9 +7,9 @@
 // score + bias is formed in FP32 first; where two experts that the choice has to
 // tell apart (neighbours among the best k + 1) lie within the error of their c,
 // the candidates' c are formed again in FP64, one candidate a lane.  The same
-// holds for the last group in and the first one out; then all of the token's c
-// are formed in FP64.  Of 16384 tokens with 256 experts some 30 take the first
-// of these ways and one or two the second.
+// holds for the last group in and the first one out, with the c of the experts that
+// count for their groups.  Where that does not settle it, all of the token's c are
+// formed in FP64.
 #include <cmath>
 #include <initializer_list>
 #include <type_traits>
@@ -205,6 +205,42 @@ __device__ __forceinline__ double exact_zinv(const Args &a, const float *row, No
     return 1. / warp_sum(z);
 }
 
+// The groups' choice from FP64 scores: of the experts that count in each group, by
+// their FP32 keys, FP64 values are formed.  `unsure` where those keys do not tell which ones count.
+template <class Near>
+__device__ __forceinline__ uint32_t keep_groups_exact(const Args &a, const float *row, Norm n, const uint32_t *buf, Near near,
+                                                      bool &unsure)
+{
+    const int lane = threadIdx.x & 31;
+    int sub = 1;
+    while (sub * 2 * a.G <= 32) sub *= 2;
+    const int g = lane / sub, j = lane - g * sub, per = (a.gsize + sub - 1) / sub;
+    uint32_t x = 0, y = 0, z = 0;   // the three largest keys, and the experts of the first two
+    int xi = 0, yi = 0;
+    auto put = [&](uint32_t k, int e) {
+        if (k > x) z = y, y = x, yi = xi, x = k, xi = e;
+        else if (k > y) z = y, y = k, yi = e;
+        else if (k > z) z = k;
+    };
+    if (g < a.G)
+        for (int e = g * a.gsize + j * per; e < g * a.gsize + min((j + 1) * per, a.gsize); ++e) put(buf[e + (e >> 5)], e);
+    for (int o = 1; o < sub; o *= 2) {
+        const uint32_t x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o), z2 = __shfl_xor_sync(kAll, z, o);
+        const int xi2 = __shfl_xor_sync(kAll, xi, o), yi2 = __shfl_xor_sync(kAll, yi, o);
+        put(x2, xi2);
+        put(y2, yi2);
+        put(z2, 0);   // (never among the first two of both)
+    }
+    const uint32_t last = a.gsum == 2 ? y : x, next = a.gsum == 2 ? z : y;
+    unsure = __any_sync(kAll, g < a.G && next > 1u && near(of_key(last), of_key(next)));
+    if (unsure) return 0;
+    const double zinv = exact_zinv(a, row, n);
+    double s = exact_c(a, row, xi, n, zinv);
+    if (a.gsum == 2 && y > 1u && of_key(y) != -INFINITY) s += exact_c(a, row, yi, n, zinv);
+    uint64_t in, out;
+    return keep_groups(__shfl_sync(kAll, key_of(s), min(lane * sub, 31)), a.G, a.top, in, out);
+}
+
 // The k largest keys in shared memory (expert e at e + e / 32), in order: lane j < k
 // returns the j-th expert
 template <class Key>
@@ -272,13 +308,16 @@ __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n,
 // a token at k = 8, E = 384 and 23.7 us for 8192 tokens.)  With sigmoid scores, a bias and
 // no groups the values of that search are c by tanh.approx (2^-11); only the
 // candidates' scores are computed in full.
-template <int kN, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Args a)
+enum Mode { kLogits = 0, kCoarse = 1, kAny = 2 };   // no bias or groups; sigmoid and bias, no groups; any
+template <int kN, int kWarps, int kMode>
+__global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gate(const Args a)
 {
+    const bool has_bias = kMode == kAny ? a.has_bias : kMode == kCoarse, softmax = kMode == kCoarse ? false : a.softmax;
+    const bool grouped = kMode == kAny && a.grouped;
     extern __shared__ uint64_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // keys of a token: FP32 ones, of FP64 values for a close call
-    uint64_t *buf = (uint64_t *)((uint8_t *)smem + (size_t)warp * (((a.E + a.E / 32 + 1) * (a.has_bias ? 8 : 4) + 7) & ~7));
+    uint64_t *buf = (uint64_t *)((uint8_t *)smem + (size_t)warp * (((a.E + a.E / 32 + 1) * (has_bias ? 8 : 4) + 7) & ~7));
     __shared__ int cand_id[kWarps][32];
     __shared__ float cand_c[kWarps][32], cand_s[kWarps][32];
     int *ci = cand_id[warp];
@@ -289,23 +328,23 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
         const float *row = a.logits + t * a.E;
         float v[kN];   // -inf: no expert, or one that cannot be chosen
         Norm n{0.f, 1.f};
-        const bool coarse = a.has_bias && !a.softmax && !a.grouped;
+        constexpr bool coarse = kMode == kCoarse;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int e = i * 32 + lane;
             v[i] = e < a.E ? row[e] : -INFINITY;
         }
-        if (a.softmax) {
+        if (softmax) {
             float m = v[0];
 #pragma unroll
             for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
             m = warp_fmax(m);
             n.m = m == -INFINITY ? 0.f : m;   // (no expert can be chosen: all scores are zero)
-            if (a.has_bias || a.grouped || !a.renorm) {
+            if (has_bias || grouped || !a.renorm) {
                 float z = 0.f;
 #pragma unroll
                 for (int i = 0; i < kN; ++i) z += exp_below_fast(v[i], n.m);
-                if (a.has_bias) {   // (v is the exponential from here on; -inf stays)
+                if (has_bias) {   // (v is the exponential from here on; -inf stays)
 #pragma unroll
                     for (int i = 0; i < kN; ++i) v[i] = v[i] == -INFINITY ? v[i] : exp_below_fast(v[i], n.m);
                 }
@@ -313,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
                 n.inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
             }
         }
-        if (a.has_bias) {
+        if (has_bias) {
             // (a loop for each form: a choice within one costs some 500 instructions a token)
             auto form = [&](auto score) {
 #pragma unroll
@@ -324,18 +363,18 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
                 }
             };
             if (coarse) form([](float l, float b) { return fmaf(tanh_approx(0.5f * l), 0.5f, b + 0.5f); });
-            else if (a.softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
+            else if (softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
             else form([](float l, float b) { return rcp(1.f + ex2(l * -1.4426950408889634f)) + b; });
         }
         // error of the difference of two c beside their own rounding: their scores are
         // off by less than 2^-21 of the largest one
-        const float terr = 9.5367432e-7f * (a.softmax ? n.inv : 1.f);
+        const float terr = 9.5367432e-7f * (softmax ? n.inv : 1.f);
         auto near = [&](float x, float y) {   // x >= y
             return y != -INFINITY && !(x - y > terr + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
         };
         int mine = 0, cnt = 0;
         bool whole = false;   // the groups are too close to call in FP32
-        if (a.grouped) {
+        if (grouped) {
             uint32_t *kb = (uint32_t *)buf;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
@@ -344,18 +383,19 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
             }
             __syncwarp();
             uint32_t in, out, kept;
-            if (a.has_bias || a.gsum == 1) {
+            if (has_bias || a.gsum == 1) {
                 const uint32_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) { return sum_of(a, x, y); });
                 kept = keep_groups(s, a.G, a.top, in, out);
-                if (a.has_bias) {
+                if (has_bias) {
                     const float x = of_key(in), y = of_key(out);
-                    whole = a.gsum == 1 ? near(x, y) : near(0.5f * x, 0.5f * y);
+                    if (a.gsum == 1 ? near(x, y) : near(0.5f * x, 0.5f * y))
+                        kept = keep_groups_exact(a, row, n, kb, near, whole);
                 }
             } else {   // sums of two scores, from the logits, in FP64 at once
                 const uint64_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) {
                     auto score = [&](uint32_t k) {
                         const double l = of_key(k);
-                        return k <= 1u || l == -INFINITY ? 0. : a.softmax ? exp(l - (double)n.m) : 1. / (1. + exp(-l));
+                        return k <= 1u || l == -INFINITY ? 0. : softmax ? exp(l - (double)n.m) : 1. / (1. + exp(-l));
                     };
                     if (x <= 1u || of_key(x) == -INFINITY) return key_of(-(double)INFINITY);
                     return key_of(score(x) + score(y));
@@ -368,7 +408,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
                 const uint32_t e = i * 32 + lane, g = a.gmagic ? __umulhi(e, a.gmagic) : e;
                 if (!(kept >> (g & 31u) & 1u)) v[i] = -INFINITY;
             }
-            if (!a.has_bias) {   // (for the search through keys, where it comes to that)
+            if (!has_bias) {   // (for the search through keys, where it comes to that)
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
                     const uint32_t e = i * 32 + lane, g = a.gmagic ? __umulhi(e, a.gmagic) : e;
@@ -398,7 +438,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
             const bool all = least == -INFINITY;
             // (twice the error of the values: 2^-12 by tanh.approx, and roundings)
             const float from = all          ? -3.402823466e38f
-                               : a.has_bias ? least - ((coarse ? 5.4e-4f : terr) + 4.8e-7f * fabsf(least))
+                               : has_bias ? least - ((coarse ? 5.4e-4f : terr) + 4.8e-7f * fabsf(least))
                                             : least;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
@@ -411,14 +451,14 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
                 }
             }
             __syncwarp();
-            if (cnt > 32 || cnt < a.k || (a.has_bias && cnt == a.k && !all)) {
+            if (cnt > 32 || cnt < a.k || (has_bias && cnt == a.k && !all)) {
                 whole = true;   // many equal ones, few that can be chosen, or k = 32
             } else {
                 const int e = lane < cnt ? ci[lane] : 0;
                 const float l = lane < cnt ? row[e] : -INFINITY;
                 float c = l;
-                if (a.has_bias) {
-                    s = a.softmax ? exp_below(l, n.m) * n.inv : sigmoid(l);
+                if (has_bias) {
+                    s = softmax ? exp_below(l, n.m) * n.inv : sigmoid(l);
                     if (lane < cnt) c = s + a.bias[e];
                 }
                 int rank = 0;
@@ -431,24 +471,24 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
                 __syncwarp();
                 mine = lane < cnt ? ci[lane] : 0;
                 c = lane < cnt ? cc[lane] : -INFINITY;
-                if (a.has_bias) {
+                if (has_bias) {
                     s = cs[lane];
                     const float nc = __shfl_down_sync(kAll, c, 1);
                     scored = !__any_sync(kAll, lane < a.k && lane + 1 < cnt && near(c, nc));
                     if (!scored) mine = order_exact(a, row, n, mine, cnt, ci);
                 } else {
-                    s = a.softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);
+                    s = softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);
                     scored = true;
                 }
             }
             __syncwarp();
         }
         if (whole) {
-            if (a.has_bias) {
+            if (has_bias) {
                 mine = choose_exact(a, row, n, buf);
             } else {
                 uint32_t *kb = (uint32_t *)buf;
-                if (!a.grouped) {
+                if (!grouped) {
 #pragma unroll
                     for (int i = 0; i < kN; ++i) {
                         const int e = i * 32 + lane;
@@ -468,7 +508,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 4 : 1) k_gate(const Ar
             w = a.renorm ? s / D : s;          // (1e-20 is below half a unit of D)
             scored = D > 0.25f;
         }
-        if (!scored) w = share(a.softmax, a.renorm, live ? row[mine] : 0.f, live, n);
+        if (!scored) w = share(softmax, a.renorm, live ? row[mine] : 0.f, live, n);
         if (live) {
             a.idx[t * a.k + lane] = mine;
             a.w[t * a.k + lane] = a.factor * w;
@@ -596,18 +636,24 @@ static bool by_size(int E, F f)
 }
 static unsigned ctas_of(int T, int warps)
 {
-    return (unsigned)std::min<int64_t>(cdiv(T, warps), (int64_t)gemm_num_sms() * 64);
+    return (unsigned)std::min<int64_t>(cdiv(T, warps), (int64_t)gemm_num_sms() * 128);
 }
 
 template <int kN>
 static bool launch_as(const Args &a, cudaStream_t st)
 {
-    constexpr int kWarps = kN > 32 ? 4 : 8;
+    constexpr int kWarps = 4;
     const size_t smem = (size_t)kWarps * (((a.E + a.E / 32 + 1) * (a.has_bias ? 8 : 4) + 7) & ~7);
-    if (smem > 40 * 1024 && !set_attribute<k_gate<kN, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize>(
-                                (int)(kWarps * (32 * kN + kN + 1) * 8)))
-        return false;
-    return launch_chained<k_gate<kN, kWarps>>(ctas_of(a.T, kWarps), 32 * kWarps, smem, 1, st, a);
+    auto launch = [&](auto mode) {
+        constexpr auto kern = k_gate<kN, kWarps, decltype(mode)::value>;
+        if (smem > 40 * 1024 &&
+            !set_attribute<kern, cudaFuncAttributeMaxDynamicSharedMemorySize>((int)(kWarps * (32 * kN + kN + 1) * 8)))
+            return false;
+        return launch_chained<kern>(ctas_of(a.T, kWarps), 32 * kWarps, smem, 1, st, a);
+    };
+    return a.grouped || (a.has_bias && a.softmax) ? launch(std::integral_constant<int, kAny>())
+           : a.has_bias                           ? launch(std::integral_constant<int, kCoarse>())
+                                                  : launch(std::integral_constant<int, kLogits>());
 }
 template <int kN, bool kSoftmax>
 static bool launch_backward(const BwdArgs &a, cudaStream_t st)
