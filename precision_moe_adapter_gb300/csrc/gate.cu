@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
 // and that of the logits
 //   sigmoid: dl_j = ds_j s_j (1 - s_j) of the chosen experts, else 0
 //   softmax: dl_e = s_e ([chosen] ds_e - sum_j ds_j s_j)
-// A warp a token; an expert that idx names twice takes both parts.
+// An expert that idx names twice takes both parts.
 struct BwdArgs {
     int T, E, k;
     int softmax, renorm, accumulate;
@@ -534,8 +534,90 @@ struct BwdArgs {
     float *dl;
 };
 
-template <int kN, bool kSoftmax, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) k_gate_backward(const BwdArgs a)
+// Sums over the kW lanes of a token
+template <int kW>
+__device__ __forceinline__ float token_sum(float v)
+{
+#pragma unroll
+    for (int o = kW / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+// The parts g of the same expert (e, and whose token: `same` has its lanes) summed in
+// order for the first lane that has it; false in the other lanes
+__device__ __forceinline__ bool first_of(uint32_t same, bool live, float &g)
+{
+    const int lane = threadIdx.x & 31;
+    const bool first = live && (same & ((1u << lane) - 1u)) == 0;
+    if (__any_sync(kAll, live && !first)) {
+        float sum = 0.f;
+        for (int j = 0; j < 32; ++j) {
+            const float o = __shfl_sync(kAll, g, j);
+            if (same >> j & 1u) sum += o;
+        }
+        g = sum;
+    }
+    return first;
+}
+
+// Sigmoid: kW lanes a token, as only the chosen logits are read.  (A warp a token, 8 of
+// its lanes at work, took 8.8 us for 8192 tokens of 384 experts.)
+template <int kW, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) k_gate_backward_sigmoid(const BwdArgs a)
+{
+    constexpr int kTok = 32 / kW;   // tokens of a warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % kW;
+    grid_wait();
+    grid_go();
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kWarps * kTok) {
+        const int64_t t = t0 + lane / kW;
+        int e = -1;
+        float dw = 0.f;
+        if (t < a.T && j < a.k) {
+            e = a.idx[t * a.k + j];
+            dw = a.dw[t * a.k + j];
+        }
+        const bool live = e >= 0 && e < a.E;
+        const float l = live ? a.logits[t * a.E + e] : -INFINITY;
+        if (!live) dw = 0.f;
+        if (!a.accumulate) {   // zeros around the chosen experts
+            float *out = a.dl + t0 * a.E;
+            const int n = (int)(a.T - t0 < kTok ? a.T - t0 : kTok) * a.E;
+            int i = 0;
+            if (((t0 * a.E) & 3) == 0) {
+                for (i = lane; i < n / 4; i += 32) ((float4 *)out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                i = n & ~3;
+            }
+            for (i += lane; i < n; i += 32) out[i] = 0.f;
+        }
+        float p = sigmoid(l);
+        if (a.renorm) {
+            const float D = token_sum<kW>(p);
+            p = p / (D + 1e-20f);
+            if (__any_sync(kAll, !(D > 0.25f))) {   // (small scores: relative to the largest one, as in share)
+                float base = l;
+#pragma unroll
+                for (int o = kW / 2; o; o >>= 1) base = fmaxf(base, __shfl_xor_sync(kAll, base, o));
+                const float r = base == -INFINITY ? 0.f : exp_below(l, base) * sigmoid(-l);
+                const float all = token_sum<kW>(r) + expf(kLnEps - base);
+                if (!(base > 0.f)) p = base == -INFINITY ? 0.f : r / all;
+            }
+        }
+        const float mean = a.renorm ? token_sum<kW>(dw * p) : 0.f;
+        // ds_j s_j = factor (dw_j - mean) p_j with p_j the weight before its factor;
+        // 1 - s as the score of the opposite logit: it keeps its accuracy near 0
+        float g = live ? a.factor * (dw - mean) * p * sigmoid(-l) : 0.f;
+        const bool first = first_of(__match_any_sync(kAll, live ? e << 5 | lane / kW : -1 - lane), live, g);
+        __syncwarp();   // (orders the zeros before what takes their place)
+        if (first) {
+            float *q = a.dl + t * a.E + e;
+            *q = a.accumulate ? *q + g : g;
+        }
+    }
+}
+
+// Softmax: a warp a token, experts 32 i + lane in a lane's registers
+template <int kN, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) k_gate_backward_softmax(const BwdArgs a)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_wait();
@@ -546,59 +628,32 @@ __global__ void __launch_bounds__(32 * kWarps) k_gate_backward(const BwdArgs a)
         const int e = lane < a.k ? a.idx[t * a.k + lane] : -1;
         const bool live = e >= 0 && e < a.E;
         const float dw = live ? a.dw[t * a.k + lane] : 0.f;
-        float v[kN], m = 0.f, inv = 1.f;
-        if constexpr (kSoftmax) {
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] = i * 32 + lane < a.E ? row[i * 32 + lane] : -INFINITY;
-            m = v[0];
-#pragma unroll
-            for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
-            m = warp_fmax(m);
-            if (m == -INFINITY) m = 0.f;
-        } else if (!a.accumulate) {   // zeros around the chosen experts
-            if (a.E % 4 == 0) {
-                for (int i = lane; i < a.E / 4; i += 32) ((float4 *)out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            } else {
-                for (int i = lane; i < a.E; i += 32) out[i] = 0.f;
-            }
-        }
         const float l = live ? row[e] : 0.f;
-        if constexpr (kSoftmax) {
-            float z = 0.f;
+        float v[kN];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) z += v[i] = exp_below_fast(v[i], m);
-            z = warp_sum(z);
-            inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
-        }
-        // ds_j s_j = factor (dw_j - mean) p_j with p_j the weight before its factor
-        const float p = share(kSoftmax, a.renorm, l, live, Norm{m, inv});
+        for (int i = 0; i < kN; ++i) v[i] = i * 32 + lane < a.E ? row[i * 32 + lane] : -INFINITY;
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < kN; ++i) m = fmaxf(m, v[i]);
+        m = warp_fmax(m);
+        if (m == -INFINITY) m = 0.f;
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) z += v[i] = exp_below_fast(v[i], m);
+        z = warp_sum(z);
+        const float inv = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;
+        const float p = share(true, a.renorm, l, live, Norm{m, inv});
         const float mean = a.renorm ? warp_sum(dw * p) : 0.f;
-        float g = a.factor * (dw - mean) * p;
-        // (1 - s as the score of the opposite logit: it keeps its accuracy near 0)
-        if constexpr (!kSoftmax) g *= sigmoid(-l);
-        if (!live) g = 0.f;
-        const float dot = kSoftmax ? warp_sum(g) : 0.f;
-        // the parts of the same expert, in order, by the first lane that has it
-        const uint32_t same = __match_any_sync(kAll, live ? e : -1 - lane);
-        const bool first = live && (same & ((1u << lane) - 1u)) == 0;
-        float sum = g;
-        if (__any_sync(kAll, live && !first)) {
-            sum = 0.f;
-            for (int j = 0; j < a.k; ++j) {
-                const float o = __shfl_sync(kAll, g, j);
-                if (same >> j & 1u) sum += o;
-            }
-        }
-        if constexpr (kSoftmax) {
-            const float c = -inv * dot;
+        float g = live ? a.factor * (dw - mean) * p : 0.f;
+        const float c = -inv * warp_sum(g);
+        const bool first = first_of(__match_any_sync(kAll, live ? e : -1 - lane), live, g);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const int j = i * 32 + lane;
-                if (j < a.E) out[j] = a.accumulate ? fmaf(v[i], c, out[j]) : v[i] * c;
-            }
+        for (int i = 0; i < kN; ++i) {
+            const int j = i * 32 + lane;
+            if (j < a.E) out[j] = a.accumulate ? fmaf(v[i], c, out[j]) : v[i] * c;
         }
         __syncwarp();   // (orders the row's stores before what is added to them)
-        if (first) out[e] = kSoftmax || a.accumulate ? out[e] + sum : sum;
+        if (first) out[e] += g;
         __syncwarp();
     }
 }
@@ -655,11 +710,21 @@ static bool launch_as(const Args &a, cudaStream_t st)
            : a.has_bias                           ? launch(std::integral_constant<int, kCoarse>())
                                                   : launch(std::integral_constant<int, kLogits>());
 }
-template <int kN, bool kSoftmax>
 static bool launch_backward(const BwdArgs &a, cudaStream_t st)
 {
-    constexpr int kWarps = kN > 32 ? 4 : 8;
-    return launch_chained<k_gate_backward<kN, kSoftmax, kWarps>>(ctas_of(a.T, kWarps), 32 * kWarps, 0, 1, st, a);
+    if (a.softmax)
+        return by_size(a.E, [&](auto n) {
+            constexpr int kN = decltype(n)::value, kWarps = kN > 32 ? 4 : 8;
+            return launch_chained<k_gate_backward_softmax<kN, kWarps>>(ctas_of(a.T, kWarps), 32 * kWarps, 0, 1, st, a);
+        });
+    auto launch = [&](auto w) {
+        constexpr int kW = decltype(w)::value;
+        return launch_chained<k_gate_backward_sigmoid<kW, 4>>(ctas_of(a.T, 4 * (32 / kW)), 128, 0, 1, st, a);
+    };
+    return a.k <= 4    ? launch(std::integral_constant<int, 4>())
+           : a.k <= 8  ? launch(std::integral_constant<int, 8>())
+           : a.k <= 16 ? launch(std::integral_constant<int, 16>())
+                       : launch(std::integral_constant<int, 32>());
 }
 
 }  // namespace gate
@@ -706,9 +771,7 @@ pmoe_status moe_gate_backward(pmoe_gate g, const float *logits, const int32_t *i
     if (g.T == 0) return PMOE_OK;
     gate::BwdArgs a{g.T, g.E, g.k, g.score == PMOE_SCORE_SOFTMAX, g.renorm != 0, accumulate != 0, g.factor,
                     logits, idx, d_topk_w, dlogits};
-    const bool done = a.softmax ? gate::by_size(g.E, [&](auto n) { return gate::launch_backward<decltype(n)::value, true>(a, stream); })
-                                : gate::launch_backward<1, false>(a, stream);
-    return done ? PMOE_OK : PMOE_ERR_CUDA;
+    return gate::launch_backward(a, stream) ? PMOE_OK : PMOE_ERR_CUDA;
 }
 
 }  // extern "C"
