@@ -653,8 +653,8 @@ pmoe_status dense_w8a8_backward(const void *qt, const float *st, int32_t N, int3
  *           entry's src or dst, nor its own src but in whole
  *   norm    f32 [1] (out)
  *   ws      >= grad_ws_bytes() bytes
- * max_norm > 0 and finite.  The squares are summed in FP64 (of at most 8 in FP32),
- * in a fixed order: results are run-to-run identical.  Where coef is 1, gradients
+ * max_norm > 0 and finite.  The squares are summed in FP64 (at most 64 of them in FP32
+ * before), in a fixed order: results are run-to-run identical.  Where coef is 1, gradients
  * in place are not written.
  */
 enum { PMOE_GRAD_F32 = 0, PMOE_GRAD_BF16 = 1 };

@@ -29,21 +29,13 @@ struct Entry {
 constexpr int kThreads = 256;
 constexpr int kVecs = 8;                                  // 16-byte loads a thread has in flight
 constexpr int64_t kChunkBytes = kThreads * kVecs * 16;    // 32 KB
-constexpr int kCtasPerSm = 8;
+constexpr int kCtasPerSm = 4;                             // (64 registers a thread)
 constexpr int kMaxParts = 4096;                           // partial sums in the workspace
 constexpr size_t kWsBytes = kHdrBytes + kMaxParts * sizeof(double);
 
 __host__ __device__ inline int64_t chunk_elems(int dtype) { return kChunkBytes / (dtype == PMOE_GRAD_F32 ? 4 : 2); }
 __host__ __device__ inline int64_t chunks_of(int64_t n, int dtype) { return cdiv(n, chunk_elems(dtype)); }
 
-// The chunks [c0, c1) of this CTA: equal runs of consecutive chunks
-struct Range {
-    int64_t c0, c1;
-};
-__device__ __forceinline__ Range my_range(int64_t chunks)
-{
-    return {chunks * blockIdx.x / gridDim.x, chunks * (blockIdx.x + 1) / gridDim.x};
-}
 // Entry that holds chunk c (entries without elements have no chunk)
 __device__ __forceinline__ int find(const Entry *e, int n, int64_t c)
 {
@@ -71,28 +63,27 @@ __device__ __forceinline__ void unpack(uint4 u, float *x)
     }
 }
 
-// Sum of a vector's squares.  In FP32 where that is safe: a sum that overflowed,
-// or that is so small that its terms may have lost bits below the normal
-// range, is formed again in FP64 (the products of FP32 numbers are exact there).
+// Whether a sum of squares formed in FP32 stands: it neither overflowed nor is it so
+// small that its terms may have lost bits below the normal range
+__device__ __forceinline__ bool stands(float s) { return s >= 8.0779357e-28f && s < __int_as_float(0x7f800000); }   // 2^-90
+// Sum of a vector's squares; where FP32 does not do, in FP64 (the products of FP32
+// numbers are exact there)
 template <int N>
-__device__ __forceinline__ double squares(const float *x)
+__device__ __forceinline__ float squares32(const float *x)
 {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fmaf(x[i], x[i], s);
-    if (s >= 8.0779357e-28f && s < __int_as_float(0x7f800000)) return (double)s;   // 2^-90
+    return s;
+}
+template <int N>
+__device__ __forceinline__ double squares(const float *x)
+{
+    const float s = squares32<N>(x);
+    if (stands(s)) return (double)s;
     double d = 0.;
-    uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) any |= __float_as_uint(x[i]);
-    if ((any & 0x7fffffffu) == 0) return 0.;
-#pragma unroll 1
-    for (int i = 0; i < N; ++i) {
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) v = i == j ? x[j] : v;
-        d = fma((double)v, (double)v, d);
-    }
+    for (int i = 0; i < N; ++i) d = fma((double)x[i], (double)x[i], d);
     return d;
 }
 
@@ -124,9 +115,26 @@ __device__ __forceinline__ double chunk_squares(const void *src, int64_t at, int
         uint4 u[kVecs];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) u[i] = p[i * kThreads + threadIdx.x];
+        // one FP64 addition for the thread's 8 vectors (one for each made the kernel
+        // FP64-bound: 906 MB took 180 us, the FP64 units having 2 lanes an SM)
+        float s[kVecs];
+        uint32_t any = 0;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             unpack<BF16>(u[i], x);
+            s[i] = squares32<kE>(x);
+            any |= u[i].x | u[i].y | u[i].z | u[i].w;
+        }
+#pragma unroll
+        for (int h = kVecs / 2; h; h /= 2) {
+#pragma unroll
+            for (int i = 0; i < h; ++i) s[i] += s[i + h];
+        }
+        if (stands(s[0])) return (double)s[0];
+        if ((any & (BF16 ? 0x7fff7fffu : 0x7fffffffu)) == 0) return 0.;
+#pragma unroll 1
+        for (int i = 0; i < kVecs; ++i) {   // (read again: rare, and it keeps the registers free)
+            unpack<BF16>(p[i * kThreads + threadIdx.x], x);
             d += squares<kE>(x);
         }
         return d;
@@ -144,25 +152,21 @@ __device__ __forceinline__ double chunk_squares(const void *src, int64_t at, int
     return d;
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_squares(const Entry *__restrict__ list, int n, int64_t chunks,
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_grad_squares(const Entry *__restrict__ list, int n, int64_t chunks,
                                                            double *__restrict__ parts)
 {
     grid_wait();
     grid_go();
-    const Range r = my_range(chunks);
     double d = 0.;
-    if (r.c0 < r.c1) {
-        int i = find(list, n, r.c0);
-        Entry e = list[i];
-        int64_t end = i + 1 < n ? list[i + 1].chunk0 : chunks;
-        for (int64_t c = r.c0; c < r.c1; ++c) {
-            while (c >= end) {
-                e = list[++i];
-                end = i + 1 < n ? list[i + 1].chunk0 : chunks;
-            }
-            const int64_t at = (c - e.chunk0) * chunk_elems(e.dtype);
-            d += e.dtype == PMOE_GRAD_F32 ? chunk_squares<false>(e.src, at, e.n) : chunk_squares<true>(e.src, at, e.n);
+    int64_t end = 0;
+    Entry e{};
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        if (c >= end) {
+            e = list[find(list, n, c)];
+            end = e.chunk0 + chunks_of(e.n, e.dtype);
         }
+        const int64_t at = (c - e.chunk0) * chunk_elems(e.dtype);
+        d += e.dtype == PMOE_GRAD_F32 ? chunk_squares<false>(e.src, at, e.n) : chunk_squares<true>(e.src, at, e.n);
     }
     d = block_sum(d);
     if (threadIdx.x == 0) parts[blockIdx.x] = d;
@@ -225,9 +229,8 @@ __device__ __forceinline__ void chunk_scale(const void *src, void *dst, int64_t 
     }
 }
 
-// Each CTA goes backwards through the run of chunks that it squared: the last
-// ones may still be in the L2.
-__global__ void __launch_bounds__(kThreads) k_grad_scale(const Entry *list, int n, int64_t chunks,
+// The chunks from the last one back: what k_grad_squares read last may still be in the L2
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_grad_scale(const Entry *list, int n, int64_t chunks,
                                                          const double *__restrict__ parts, int nparts, float max_norm,
                                                          float *__restrict__ norm)
 {
@@ -237,12 +240,13 @@ __global__ void __launch_bounds__(kThreads) k_grad_scale(const Entry *list, int 
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
     const double ratio = (double)max_norm / (v + 1e-6);
     const float coef = ratio >= 1. ? 1.f : (float)ratio;   // (a NaN stays one)
-    const Range r = my_range(chunks);
-    if (r.c0 >= r.c1) return;
-    int i = find(list, n, r.c1 - 1);
-    Entry e = list[i];
-    for (int64_t c = r.c1 - 1; c >= r.c0; --c) {
-        while (c < e.chunk0) e = list[--i];
+    int64_t first = chunks;
+    Entry e{};
+    for (int64_t c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+        if (c < first) {
+            e = list[find(list, n, c)];
+            first = e.chunk0;
+        }
         if (coef == 1.f && e.src == e.dst) continue;
         const int64_t at = (c - e.chunk0) * chunk_elems(e.dtype);
         if (e.dtype == PMOE_GRAD_F32) chunk_scale<false>(e.src, e.dst, at, e.n, coef);

@@ -1,8 +1,8 @@
 """The global gradient norm and clipping on the GPU against FP64.
 
-Tolerances.  Squares are summed in FP64, at most 8 of them in FP32 before (8
-roundings of 2^-24 of the sum): the norm is off by at most 4 of these, and by its
-own rounding: 2^-21.  coef takes the norm's error and one rounding, the product
+Tolerances.  Squares are summed in FP64, those of 8 vectors of a thread in FP32 before
+(at most 8 + 3 roundings of 2^-24 of the sum in a row): the norm is off by at most 5.5 of
+these, and by its own rounding: under 2^-21.  coef takes the norm's error and one rounding, the product
 one more: 2^-21 for f32, half a step of BF16 (2^-8) beside it for bf16.
 """
 import math
