@@ -36,14 +36,18 @@ constexpr size_t kWsBytes = kHdrBytes + kMaxParts * sizeof(double);
 __host__ __device__ inline int64_t chunk_elems(int dtype) { return kChunkBytes / (dtype == PMOE_GRAD_F32 ? 4 : 2); }
 __host__ __device__ inline int64_t chunks_of(int64_t n, int dtype) { return cdiv(n, chunk_elems(dtype)); }
 
-// Entry that holds chunk c (entries without elements have no chunk)
+// Entry that holds chunk c, the last one with chunk0 <= c (entries without elements have
+// no chunk): a whole warp looks at 32 entries at a time
 __device__ __forceinline__ int find(const Entry *e, int n, int64_t c)
 {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {   // the last entry with chunk0 <= c
-        const int mid = (lo + hi + 1) >> 1;
-        if (e[mid].chunk0 <= c) lo = mid;
-        else hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int step = (len + 31) / 32, at = lane * step;
+        const uint32_t b = __ballot_sync(0xffffffffu, at < len && e[lo + min(at, len - 1)].chunk0 <= c);
+        const int last = b ? 31 - __clz((int)b) : 0;   // (the first one always is)
+        len = min(step, len - last * step);
+        lo += last * step;
     }
     return lo;
 }
