@@ -218,7 +218,9 @@ def test_gemm_nan_stays_in_its_row_or_column():
 # ---------------------------------------------------------------- the layer
 
 @pytest.mark.parametrize("pow2", [False, True])
-@pytest.mark.parametrize("rows,N,K", [(1, 256, 384), (33, 1040, 2064), (333, 1104, 2064), (1500, 4096, 512)])
+@pytest.mark.parametrize("rows,N,K", [(1, 256, 384), (1, 16, 16), (2, 24576, 144), (3, 4096, 7168), (9, 1104, 2064),
+                                      (15, 25600, 640), (16, 7168, 4112), (17, 7168, 4112), (33, 1040, 2064),
+                                      (333, 1104, 2064), (1500, 4096, 512)])
 def test_layer(rows, N, K, pow2):
     X, dY = activations(rows, K, seed=1), activations(rows, N, seed=2)
     Wq, Ws = weight(N, K)
@@ -286,6 +288,30 @@ def test_gradient_is_that_of_the_layer_without_rounding():
     assert abs(num - want) <= slack           # (each BF16 rounding by half a step)
 
 
+@pytest.mark.parametrize("rows,N,K", [(1, 4096, 7168), (5, 24576, 272), (16, 1040, 2064), (700, 4096, 384)])
+def test_layer_is_its_two_calls(rows, N, K):
+    """The layer gives the same result bit for bit as fp8_quantize and fp8_gemm, NaN and
+    infinity among the rows too."""
+    X = activations(rows, K, seed=rows)
+    if rows > 1:
+        X[1, 5], X[rows - 1, K - 1] = math.nan, math.inf
+    Wq, Ws = weight(N, K)
+    KB = -(-K // 128)
+    q, s = torch.empty((rows, K), dtype=torch.uint8, device="cuda"), torch.empty((KB, rows), device="cuda")
+    ws = torch.zeros(pmoe.fp8_gemm_ws_bytes(rows, N, K), dtype=torch.uint8, device="cuda")
+    Y, Z = (torch.empty((rows, N), dtype=BF16, device="cuda") for _ in range(2))
+    lin = DeviceLinearW8A8(Wq, Ws, rows)
+    lin.forward(X, Y)
+    pmoe.fp8_quantize(rows, K, X, q, s)
+    pmoe.fp8_gemm(rows, N, K, q, s, Wq, Ws, Z, ws)
+    assert lin.status() == pmoe.PMOE_OK
+    assert torch.equal(Y.isnan(), Z.isnan()) and torch.equal(Y.nan_to_num(), Z.nan_to_num())
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    if rows > 1:
+        bad[1] = bad[rows - 1] = True
+    assert torch.equal(Y.isnan().all(1), bad) and torch.equal(Y.isnan().any(1), bad)
+
+
 def test_rows_do_not_depend_on_the_others():
     """Batches whose blocks are not shared out give the same rows bit for bit."""
     N, K = 4096, 1040
@@ -344,9 +370,9 @@ def test_streams_and_graphs():
     assert torch.equal(Y, ref[0] * 2) and torch.equal(dX, ref[1])
 
 
-@pytest.mark.parametrize("rows", [40, 5000])
+@pytest.mark.parametrize("rows", [9, 40, 5000])
 def test_a_wait_that_runs_out_is_reported(rows):
-    """Single CTAs and pairs: the first item's signal is withheld for 2 ms."""
+    """Few rows, single CTAs and pairs: the first item's signal is withheld for 2 ms."""
     N, K = 2048, 1024
     X = activations(rows, K)
     lin = DeviceLinearW8A8(*weight(N, K), rows)
