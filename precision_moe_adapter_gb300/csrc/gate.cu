@@ -329,11 +329,16 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
         float v[kN];   // -inf: no expert, or one that cannot be chosen
         Norm n{0.f, 1.f};
         constexpr bool coarse = kMode == kCoarse;
+        // (all loads on their way at once: the barrier keeps them from being put off to their uses)
+        constexpr bool kBiasFirst = kN <= 16;
+        float bias[kBiasFirst ? kN : 1];
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int e = i * 32 + lane;
             v[i] = e < a.E ? row[e] : -INFINITY;
+            if constexpr (kBiasFirst) bias[i] = has_bias && e < a.E ? a.bias[e] : 0.f;
         }
+        if constexpr (kBiasFirst) __syncwarp();
         if (softmax) {
             float m = v[0];
 #pragma unroll
@@ -357,8 +362,10 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             auto form = [&](auto score) {
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
-                    const int e = i * 32 + lane;
-                    const float c = score(v[i], e < a.E ? __ldg(a.bias + e) : 0.f);
+                    float b;
+                    if constexpr (kBiasFirst) b = bias[i];
+                    else b = i * 32 + lane < a.E ? __ldg(a.bias + i * 32 + lane) : 0.f;
+                    const float c = score(v[i], b);
                     v[i] = v[i] == -INFINITY ? -INFINITY : c;
                 }
             };
@@ -366,11 +373,14 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             else if (softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
             else form([](float l, float b) { return rcp(1.f + ex2(l * -1.4426950408889634f)) + b; });
         }
-        // error of the difference of two c beside their own rounding: their scores are
-        // off by less than 2^-21 of the largest one
-        const float terr = 9.5367432e-7f * (softmax ? n.inv : 1.f);
-        auto near = [&](float x, float y) {   // x >= y
-            return y != -INFINITY && !(x - y > terr + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
+        // Bounds of the error of the difference of two c beside their own rounding.  Sigmoid:
+        // a score by ex2 and rcp (v) is off by less than 2^-21 / 2, one by sigmoid() (the
+        // candidates') by less than 2^-22 (the exponential's 2 units times s (1 - s), a sum
+        // and a quotient).  Softmax: the row's sum adds a unit of 2^-24 a term.
+        const float terr = softmax ? n.inv * (float)(kN + 16) * 1.1920929e-7f : 9.5367432e-7f;
+        const float cerr = softmax ? terr : 4.7683716e-7f;
+        auto near = [&](float x, float y, float err) {   // x >= y
+            return y != -INFINITY && !(x - y > err + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
         };
         int mine = 0, cnt = 0;
         bool whole = false;   // the groups are too close to call in FP32
@@ -388,8 +398,9 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                 kept = keep_groups(s, a.G, a.top, in, out);
                 if (has_bias) {
                     const float x = of_key(in), y = of_key(out);
-                    if (a.gsum == 1 ? near(x, y) : near(0.5f * x, 0.5f * y))
-                        kept = keep_groups_exact(a, row, n, kb, near, whole);
+                    if (a.gsum == 1 ? near(x, y, terr) : near(0.5f * x, 0.5f * y, terr))
+                        kept = keep_groups_exact(
+                            a, row, n, kb, [&](float p, float q) { return near(p, q, terr); }, whole);
                 }
             } else {   // sums of two scores, from the logits, in FP64 at once
                 const uint64_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) {
@@ -462,6 +473,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                     if (lane < cnt) c = s + a.bias[e];
                 }
                 int rank = 0;
+#pragma unroll 4
                 for (int j = 0; j < cnt; ++j) {
                     const float o = __shfl_sync(kAll, c, j);
                     rank += o > c || (o == c && j < lane);
@@ -474,7 +486,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                 if (has_bias) {
                     s = cs[lane];
                     const float nc = __shfl_down_sync(kAll, c, 1);
-                    scored = !__any_sync(kAll, lane < a.k && lane + 1 < cnt && near(c, nc));
+                    scored = !__any_sync(kAll, lane < a.k && lane + 1 < cnt && near(c, nc, cerr));
                     if (!scored) mine = order_exact(a, row, n, mine, cnt, ci);
                 } else {
                     s = softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);
