@@ -175,20 +175,33 @@ static int active_clusters(int size)
 static Tiling tiling(int64_t M, int64_t N, int64_t ksteps)
 {
     Tiling t;
-    t.ctas = cdiv(M, 256) * cdiv(N, 256) >= kSms / 2 && M > 128 ? 2 : 1;
+    // Pairs on 256 x 256 read each operand half as often; a step of theirs takes 7/4 of one
+    // of a single CTA on 128 x 128, so it is the rounds of the GPU that decide.  us for
+    // quantisation and product, singles and pairs: 512 x 4096 (K 2048, one round each) 12.7
+    // and 13.8; 1024 x 4864 (two, one) 18.1 and 16.8; 2048 x 4864 (four, two) 28.2 and 26.7;
+    // 1024 x 4096 (K 7168; two, one) 41.1 and 36.3.
+    t.ctas = M > 128 && 7 * cdiv(cdiv(M, 256) * cdiv(N, 256), kSms / 2) <= 4 * cdiv(cdiv(M, 128) * cdiv(N, 128), kSms) ? 2 : 1;
     t.mt = (int)cdiv(M, 128 * t.ctas);
     t.nt = (int)cdiv(N, 128 * t.ctas);
-    // m tiles that run together: their rows of A stay in the L2 while the n tiles pass
+    // m tiles that run together: their rows of A stay in the L2 while the n tiles pass.
+    // 16384 rows, N = K = 7168: 727 us; with all of them together 800, in groups of 8 729 to 745.
     const int64_t stripe = 128ll * t.ctas * ksteps * kStep;
     const int64_t most = std::max<int64_t>(8, (48ll << 20) / std::max<int64_t>(stripe, 1));
     t.gm = (int)cdiv(t.mt, cdiv(t.mt, most));
-    // few tiles: the blocks of K are shared out, at least two a CTA, so that more SMs stream W
+    // Few tiles: the blocks of K are shared out among the CTAs of a cluster.  A step takes
+    // 0.24 us, the join 1 us and 0.3 a CTA, and 1.5 more where there are several tiles of rows.
+    // us, shared and not: 1 x 4096 x 7168 (rows x N x K; by 4) 9.1 and 17.5; 64 x 7168 x 7168
+    // (by 2) 15.9 and 21.3; 16 x 512 x 18432 (by 8) 10.1 and 37.6; 128 x 2048 x 2048 (by 4) 8.5,
+    // by 8 8.9, not 9.3; and 32 x 128 x 512 (by 2) 6.0 and 5.1; 333 x 1104 x 2064 (by 5) 11.7 and 10.3.
     t.splits = 1;
     t.kper = (int)ksteps;
     const int64_t tiles = (int64_t)t.mt * t.nt;
-    for (int s = kMaxSplits; s > 1 && t.ctas == 1 && t.splits == 1; --s) {
+    double least = 0.24 * ksteps;
+    for (int s = 2; s <= kMaxSplits && t.ctas == 1; ++s) {
         const int64_t per = cdiv(ksteps, s);
-        if (tiles * s > kSms || per < 2 || cdiv(ksteps, per) != s || tiles > active_clusters(s)) continue;
+        const double us = 0.24 * per + 1 + 0.3 * s + (t.mt > 1 ? 1.5 : 0);
+        if (us >= least || tiles * s > kSms || cdiv(ksteps, per) != s || tiles > active_clusters(s)) continue;
+        least = us;
         t.splits = s;
         t.kper = (int)per;
     }
