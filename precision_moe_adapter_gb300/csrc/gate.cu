@@ -74,12 +74,6 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float tanh_approx(float x)
-{
-    float y;
-    asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float warp_fmax(float v)
 {
 #pragma unroll
@@ -305,15 +299,14 @@ __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n,
 // largest values bounds the (k + 2)-th largest of all from below, and the experts from
 // there up (some 11 for k = 8, E = 384) are gathered, one a lane, and ranked.  (Taking the
 // largest k times over, each time looking through all of them again, took 1280 instructions
-// a token at k = 8, E = 384 and 23.7 us for 8192 tokens.)  With sigmoid scores, a bias and
-// no groups the values of that search are c by tanh.approx (2^-11); only the
-// candidates' scores are computed in full.
-enum Mode { kLogits = 0, kCoarse = 1, kAny = 2 };   // no bias or groups; sigmoid and bias, no groups; any
+// a token at k = 8, E = 384 and 23.7 us for 8192 tokens.)  The values
+// of that search are c by approximate exponentials; the candidates' scores are computed
+// in full.
+enum Mode { kLogits = 0, kAny = 1 };   // neither a bias nor groups; any
 template <int kN, int kWarps, int kMode>
 __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gate(const Args a)
 {
-    const bool has_bias = kMode == kAny ? a.has_bias : kMode == kCoarse, softmax = kMode == kCoarse ? false : a.softmax;
-    const bool grouped = kMode == kAny && a.grouped;
+    const bool has_bias = kMode == kAny && a.has_bias, grouped = kMode == kAny && a.grouped, softmax = a.softmax;
     extern __shared__ uint64_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // keys of a token: FP32 ones, of FP64 values for a close call
@@ -328,7 +321,6 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
         const float *row = a.logits + t * a.E;
         float v[kN];   // -inf: no expert, or one that cannot be chosen
         Norm n{0.f, 1.f};
-        constexpr bool coarse = kMode == kCoarse;
         // (all loads on their way at once: the barrier keeps them from being put off to their uses)
         constexpr bool kBiasFirst = kN <= 16;
         float bias[kBiasFirst ? kN : 1];
@@ -369,8 +361,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                     v[i] = v[i] == -INFINITY ? -INFINITY : c;
                 }
             };
-            if (coarse) form([](float l, float b) { return fmaf(tanh_approx(0.5f * l), 0.5f, b + 0.5f); });
-            else if (softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
+            if (softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
             else form([](float l, float b) { return rcp(1.f + ex2(l * -1.4426950408889634f)) + b; });
         }
         // Bounds of the error of the difference of two c beside their own rounding.  Sigmoid:
@@ -447,10 +438,10 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             // (-inf: fewer lanes have any that can be chosen, all are candidates)
             const float least = __shfl_sync(kAll, best, min(a.k + 2, 32) - 1);
             const bool all = least == -INFINITY;
-            // (twice the error of the values: 2^-12 by tanh.approx, and roundings)
-            const float from = all          ? -3.402823466e38f
-                               : has_bias ? least - ((coarse ? 5.4e-4f : terr) + 4.8e-7f * fabsf(least))
-                                            : least;
+            // (less by twice the error of the values)
+            const float from = all        ? -3.402823466e38f
+                               : has_bias ? least - (terr + 4.7683716e-7f * fabsf(least))
+                                          : least;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const bool in = v[i] >= from;
@@ -718,9 +709,8 @@ static bool launch_as(const Args &a, cudaStream_t st)
             return false;
         return launch_chained<kern>(ctas_of(a.T, kWarps), 32 * kWarps, smem, 1, st, a);
     };
-    return a.grouped || (a.has_bias && a.softmax) ? launch(std::integral_constant<int, kAny>())
-           : a.has_bias                           ? launch(std::integral_constant<int, kCoarse>())
-                                                  : launch(std::integral_constant<int, kLogits>());
+    // (the groups' and the bias's code costs the cases without them registers)
+    return a.grouped || a.has_bias ? launch(std::integral_constant<int, kAny>()) : launch(std::integral_constant<int, kLogits>());
 }
 static bool launch_backward(const BwdArgs &a, cudaStream_t st)
 {
