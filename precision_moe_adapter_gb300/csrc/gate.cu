@@ -26,6 +26,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 struct Args {
     int T, E, k, G, top, gsum, gsize;   // gsize: experts of a group
+    int sublog, per;                    // 2^sublog lanes look at a group, per experts each
     uint32_t gmagic;                    // e / gsize is the high half of e gmagic (0: e)
     int softmax, renorm, has_bias, grouped;
     float factor;
@@ -125,13 +126,18 @@ __device__ __forceinline__ float share(bool softmax, bool renorm, float l, bool 
     return s / (warp_sum(s) + eps);
 }
 
-// The two largest keys among `n` consecutive ones, joined over `sub` lanes
-template <class Key>
-__device__ __forceinline__ void top2(Key &a, Key &b, Key x)
+// The two largest values (keys, or FP32 numbers) seen so far
+__device__ __forceinline__ void top2(uint64_t &a, uint64_t &b, uint64_t x)
 {
-    const Key lo = x < a ? x : a;
+    const uint64_t lo = x < a ? x : a;
     a = x < a ? a : x;
     b = lo > b ? lo : b;
+}
+__device__ __forceinline__ void top2(float &a, float &b, float x)
+{
+    const float lo = fminf(x, a);
+    a = fmaxf(a, x);
+    b = fmaxf(b, lo);
 }
 
 // Keeps the best `top` of G groups: lane g < G gives its group's score; the kept
@@ -152,37 +158,26 @@ __device__ __forceinline__ uint32_t keep_groups(Key score, int G, int top, Key &
     return __ballot_sync(kAll, kept);
 }
 
-// Key of each group's score in lane g < G, from the keys of its experts in shared
-// memory (expert e at e + e / 32): `val` makes it of the two best ones' (0: none).
-template <class Key, class V>
-__device__ __forceinline__ auto group_score(const Key *buf, const Args &a, V val)
+// Each group's score in lane g < G, from the values of its experts in shared memory
+// (expert e at e + e / 32): `val` makes it of the two best ones (`none`: not there).
+template <class F, class V>
+__device__ __forceinline__ auto group_score(const F *buf, const Args &a, F none, V val)
 {
-    const int lane = threadIdx.x & 31;
-    int sub = 1;   // lanes of a group, a power of two
-    while (sub * 2 * a.G <= 32) sub *= 2;
-    const int g = lane / sub, j = lane - g * sub, per = (a.gsize + sub - 1) / sub;
-    Key x = 0, y = 0;
+    const int lane = threadIdx.x & 31, sub = 1 << a.sublog;   // lanes of a group
+    const int g = lane >> a.sublog, j = lane & (sub - 1);
+    F x = none, y = none;
     if (g < a.G) {
-        const int e1 = min((j + 1) * per, a.gsize);
-        for (int e = j * per; e < e1; ++e) {
-            const int at = g * a.gsize + e;
-            top2(x, y, buf[at + (at >> 5)]);
-        }
+        const int e0 = g * a.gsize;
+        const int e1 = e0 + min((j + 1) * a.per, a.gsize);
+#pragma unroll 4
+        for (int e = e0 + j * a.per; e < e1; ++e) top2(x, y, buf[e + (e >> 5)]);
     }
     for (int o = 1; o < sub; o *= 2) {
-        const Key x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
+        const F x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
         top2(x, y, x2);
         top2(x, y, y2);
     }
-    return __shfl_sync(kAll, val(x, y), min(lane * sub, 31));
-}
-// The key of a group's score from those of its two best c: experts that cannot
-// be chosen (-inf) add nothing
-template <class Key>
-__device__ __forceinline__ Key sum_of(const Args &a, Key x, Key y)
-{
-    if (a.gsum == 1 || y <= 1 || of_key(y) == -INFINITY) return x;
-    return key_of(of_key(x) + of_key(y));
+    return __shfl_sync(kAll, val(x, y), min(lane << a.sublog, 31));
 }
 
 __device__ __forceinline__ double exact_c(const Args &a, const float *row, int e, Norm n, double zinv)
@@ -199,40 +194,41 @@ __device__ __forceinline__ double exact_zinv(const Args &a, const float *row, No
     return 1. / warp_sum(z);
 }
 
-// The groups' choice from FP64 scores: of the experts that count in each group, by
-// their FP32 keys, FP64 values are formed.  `unsure` where those keys do not tell which ones count.
-template <class Near>
-__device__ __forceinline__ uint32_t keep_groups_exact(const Args &a, const float *row, Norm n, const uint32_t *buf, Near near,
-                                                      bool &unsure)
+// Whether FP32 cannot tell x >= y apart: values off by up to err / 2 and their rounding
+__device__ __forceinline__ bool near(float x, float y, float err)
 {
-    const int lane = threadIdx.x & 31;
-    int sub = 1;
-    while (sub * 2 * a.G <= 32) sub *= 2;
-    const int g = lane / sub, j = lane - g * sub, per = (a.gsize + sub - 1) / sub;
-    uint32_t x = 0, y = 0, z = 0;   // the three largest keys, and the experts of the first two
+    return y != -INFINITY && !(x - y > err + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
+}
+
+// The groups' choice from FP64 scores: FP64 values are formed of the experts that count
+// in each group by their FP32 ones; 0 where those (off by up to terr / 2) do not tell
+// which ones count.
+__device__ __noinline__ uint32_t keep_groups_exact(const Args &a, const float *row, Norm n, const float *buf, float terr)
+{
+    const int lane = threadIdx.x & 31, sub = 1 << a.sublog, g = lane >> a.sublog, j = lane & (sub - 1);
+    float x = -INFINITY, y = -INFINITY, z = -INFINITY;   // the three largest, and the experts of the first two
     int xi = 0, yi = 0;
-    auto put = [&](uint32_t k, int e) {
+    auto put = [&](float k, int e) {
         if (k > x) z = y, y = x, yi = xi, x = k, xi = e;
         else if (k > y) z = y, y = k, yi = e;
         else if (k > z) z = k;
     };
     if (g < a.G)
-        for (int e = g * a.gsize + j * per; e < g * a.gsize + min((j + 1) * per, a.gsize); ++e) put(buf[e + (e >> 5)], e);
+        for (int e = g * a.gsize + j * a.per; e < g * a.gsize + min((j + 1) * a.per, a.gsize); ++e) put(buf[e + (e >> 5)], e);
     for (int o = 1; o < sub; o *= 2) {
-        const uint32_t x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o), z2 = __shfl_xor_sync(kAll, z, o);
+        const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o), z2 = __shfl_xor_sync(kAll, z, o);
         const int xi2 = __shfl_xor_sync(kAll, xi, o), yi2 = __shfl_xor_sync(kAll, yi, o);
         put(x2, xi2);
         put(y2, yi2);
         put(z2, 0);   // (never among the first two of both)
     }
-    const uint32_t last = a.gsum == 2 ? y : x, next = a.gsum == 2 ? z : y;
-    unsure = __any_sync(kAll, g < a.G && next > 1u && near(of_key(last), of_key(next)));
-    if (unsure) return 0;
+    if (__any_sync(kAll, a.has_bias && g < a.G && near(a.gsum == 2 ? y : x, a.gsum == 2 ? z : y, terr))) return 0;
     const double zinv = exact_zinv(a, row, n);
     double s = exact_c(a, row, xi, n, zinv);
-    if (a.gsum == 2 && y > 1u && of_key(y) != -INFINITY) s += exact_c(a, row, yi, n, zinv);
+    if (a.gsum == 2 && y != -INFINITY) s += exact_c(a, row, yi, n, zinv);
+    if (x == -INFINITY) s = -INFINITY;
     uint64_t in, out;
-    return keep_groups(__shfl_sync(kAll, key_of(s), min(lane * sub, 31)), a.G, a.top, in, out);
+    return keep_groups(__shfl_sync(kAll, key_of(s), min(lane << a.sublog, 31)), a.G, a.top, in, out);
 }
 
 // The k largest keys in shared memory (expert e at e + e / 32), in order: lane j < k
@@ -266,7 +262,9 @@ __device__ __noinline__ int choose_exact(const Args &a, const float *row, Norm n
     __syncwarp();
     if (a.grouped) {
         uint64_t in, out;
-        const uint64_t s = group_score(buf, a, [&](uint64_t x, uint64_t y) { return sum_of(a, x, y); });
+        const uint64_t s = group_score(buf, a, (uint64_t)0, [&](uint64_t x, uint64_t y) {
+            return a.gsum == 1 || y <= 1 || of_key(y) == -INFINITY ? x : key_of(of_key(x) + of_key(y));
+        });
         const uint32_t kept = keep_groups(s, a.G, a.top, in, out);
         __syncwarp();
         for (int e = lane; e < a.E; e += 32)
@@ -302,11 +300,12 @@ __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n,
 // a token at k = 8, E = 384 and 23.7 us for 8192 tokens.)  The values
 // of that search are c by approximate exponentials; the candidates' scores are computed
 // in full.
-enum Mode { kLogits = 0, kAny = 1 };   // neither a bias nor groups; any
+enum Mode { kLogits = 0, kBias = 1, kGroups = 2 };   // neither a bias nor groups; a bias; groups
 template <int kN, int kWarps, int kMode>
 __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gate(const Args a)
 {
-    const bool has_bias = kMode == kAny && a.has_bias, grouped = kMode == kAny && a.grouped, softmax = a.softmax;
+    const bool has_bias = kMode == kGroups ? a.has_bias : kMode == kBias, softmax = a.softmax;
+    constexpr bool grouped = kMode == kGroups;
     extern __shared__ uint64_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // keys of a token: FP32 ones, of FP64 values for a close call
@@ -370,54 +369,38 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
         // and a quotient).  Softmax: the row's sum adds a unit of 2^-24 a term.
         const float terr = softmax ? n.inv * (float)(kN + 16) * 1.1920929e-7f : 9.5367432e-7f;
         const float cerr = softmax ? terr : 4.7683716e-7f;
-        auto near = [&](float x, float y, float err) {   // x >= y
-            return y != -INFINITY && !(x - y > err + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
-        };
         int mine = 0, cnt = 0;
         bool whole = false;   // the groups are too close to call in FP32
-        if (grouped) {
-            uint32_t *kb = (uint32_t *)buf;
+        uint32_t kept = kAll;
+        auto group_of = [&](uint32_t e) { return (a.gmagic ? __umulhi(e, a.gmagic) : e) & 31u; };
+        if constexpr (grouped) {
+            float *vb = (float *)buf;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int e = i * 32 + lane;
-                if (e < a.E) kb[e + (e >> 5)] = key_of(v[i]);
+                if (e < a.E) vb[e + (e >> 5)] = v[i];
             }
             __syncwarp();
-            uint32_t in, out, kept;
-            if (has_bias || a.gsum == 1) {
-                const uint32_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) { return sum_of(a, x, y); });
-                kept = keep_groups(s, a.G, a.top, in, out);
-                if (has_bias) {
-                    const float x = of_key(in), y = of_key(out);
-                    if (a.gsum == 1 ? near(x, y, terr) : near(0.5f * x, 0.5f * y, terr))
-                        kept = keep_groups_exact(
-                            a, row, n, kb, [&](float p, float q) { return near(p, q, terr); }, whole);
-                }
-            } else {   // sums of two scores, from the logits, in FP64 at once
-                const uint64_t s = group_score(kb, a, [&](uint32_t x, uint32_t y) {
-                    auto score = [&](uint32_t k) {
-                        const double l = of_key(k);
-                        return k <= 1u || l == -INFINITY ? 0. : softmax ? exp(l - (double)n.m) : 1. / (1. + exp(-l));
-                    };
-                    if (x <= 1u || of_key(x) == -INFINITY) return key_of(-(double)INFINITY);
-                    return key_of(score(x) + score(y));
-                });
-                uint64_t i64, o64;
-                kept = keep_groups(s, a.G, a.top, i64, o64);
+            // (without a bias v is the logit: sums of two are of the scores)
+            const float score = group_score(vb, a, -INFINITY, [&](float x, float y) {
+                if (a.gsum == 1 || x == -INFINITY) return x;
+                if (has_bias) return y == -INFINITY ? x : x + y;
+                if (softmax) return exp_below(x, n.m) + exp_below(y, n.m);
+                return sigmoid(x) + sigmoid(y);
+            });
+            uint32_t in, out;
+            kept = keep_groups(key_of(score), a.G, a.top, in, out);
+            const float x = of_key(in), y = of_key(out);   // the least score kept, the largest one not
+            bool close = false;
+            if (has_bias) close = a.gsum == 1 ? near(x, y, terr) : near(0.5f * x, 0.5f * y, terr);
+            else if (a.gsum == 2) close = y != -INFINITY && !(x - y > 1.9073486e-6f * x + 1e-36f);   // (each score to 2^-21)
+            if (close) {
+                kept = keep_groups_exact(a, row, n, vb, terr);
+                whole = kept == 0;
             }
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const uint32_t e = i * 32 + lane, g = a.gmagic ? __umulhi(e, a.gmagic) : e;
-                if (!(kept >> (g & 31u) & 1u)) v[i] = -INFINITY;
-            }
-            if (!has_bias) {   // (for the search through keys, where it comes to that)
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    const uint32_t e = i * 32 + lane, g = a.gmagic ? __umulhi(e, a.gmagic) : e;
-                    if (e < (uint32_t)a.E && !(kept >> (g & 31u) & 1u)) kb[e + (e >> 5)] = 0u;
-                }
-                __syncwarp();
-            }
+            for (int i = 0; i < kN; ++i) v[i] = kept >> group_of(i * 32 + lane) & 1u ? v[i] : -INFINITY;
+            __syncwarp();
         }
         float s = 0.f;
         bool scored = false;   // s is the lane's score
@@ -491,14 +474,12 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                 mine = choose_exact(a, row, n, buf);
             } else {
                 uint32_t *kb = (uint32_t *)buf;
-                if (!grouped) {
 #pragma unroll
-                    for (int i = 0; i < kN; ++i) {
-                        const int e = i * 32 + lane;
-                        if (e < a.E) kb[e + (e >> 5)] = key_of(v[i]);
-                    }
-                    __syncwarp();
+                for (int i = 0; i < kN; ++i) {   // (0: of a group that is out)
+                    const int e = i * 32 + lane;
+                    if (e < a.E) kb[e + (e >> 5)] = kept >> group_of(e) & 1u ? key_of(v[i]) : 0u;
                 }
+                __syncwarp();
                 mine = choose(a, kb);
             }
         }
@@ -710,7 +691,9 @@ static bool launch_as(const Args &a, cudaStream_t st)
         return launch_chained<kern>(ctas_of(a.T, kWarps), 32 * kWarps, smem, 1, st, a);
     };
     // (the groups' and the bias's code costs the cases without them registers)
-    return a.grouped || a.has_bias ? launch(std::integral_constant<int, kAny>()) : launch(std::integral_constant<int, kLogits>());
+    return a.grouped    ? launch(std::integral_constant<int, kGroups>())
+           : a.has_bias ? launch(std::integral_constant<int, kBias>())
+                        : launch(std::integral_constant<int, kLogits>());
 }
 static bool launch_backward(const BwdArgs &a, cudaStream_t st)
 {
@@ -750,6 +733,8 @@ pmoe_status moe_gate_forward(pmoe_gate g, const float *logits, const float *bias
     a.top = g.topk_groups;
     a.gsum = g.group_sum;
     a.gsize = g.E / g.groups;
+    while ((2 << a.sublog) * a.G <= 32) ++a.sublog;
+    a.per = (a.gsize + (1 << a.sublog) - 1) >> a.sublog;
     a.gmagic = a.gsize > 1 ? (uint32_t)(((1ull << 32) + a.gsize - 1) / a.gsize) : 0u;
     a.softmax = g.score == PMOE_SCORE_SOFTMAX;
     a.renorm = g.renorm != 0;
