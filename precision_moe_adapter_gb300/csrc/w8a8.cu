@@ -20,27 +20,26 @@ constexpr int kSms = 152;       // SMs of a GB300
 constexpr int kMaxSplits = 8;   // CTAs that share a tile: a portable cluster
 
 // ------------------------------------------------------------------ quantisation
-// Bound by HBM: 2 bytes read and 1 written per element.  A half-warp holds one
-// block of a row, 8 values a lane.
+// Bound by HBM: 2 bytes read and 1 written per element.  Eight lanes hold one block of a
+// row, 16 values each (with 16 lanes of 8 values the work per block, its maximum and scale,
+// made the kernel issue-bound: 15.3 instructions an element, 18.9 us for 4096 x 7168).
 //
 // q is the exact quotient 448 x / a rounded to E4M3.  x and a are BF16 numbers, so a
 // quotient that is not one of E4M3's rounding midpoints is at least 2^-13 of itself
 // away from all of them (their products with a are integers of at most 13 bits on one
-// scale): the FP32 product with an approximate 448 / a (2^-22) is rounded to 16 bits
-// first, which takes it back to a midpoint that it stands for, and across none.
+// scale).  The FP32 product with an approximate 448 / a (2^-21), 2^-16 above it, is cut
+// to 16 bits: that takes it back to a midpoint that it stands for, and across none.
 constexpr int kQThreads = 256;
-constexpr int kQBlocks = 4;   // blocks a half-warp has in flight
+constexpr int kQBlocks = 2;   // blocks that eight lanes have in flight
 
-__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t x)
+// max(|a|, |b|) of two BF16 pairs, signs left to chance; NaN if either is
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7FFF7FFFu));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float to_16_bits(float p)
-{
-    return __uint_as_float((__float_as_uint(p) + 0x80u) & 0xFFFFFF00u);
-}
+__device__ __forceinline__ float cut16(float p) { return __uint_as_float(__float_as_uint(p) & 0xFFFFFF00u); }
 __device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3)
 {
     uint16_t lo, hi;
@@ -48,7 +47,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
     return (uint32_t)lo | (uint32_t)hi << 16;
 }
-
+// Codes of four values, given as two BF16 pairs
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, float r)
+{
+    return e4m3x4(cut16(__uint_as_float(a << 16) * r), cut16(__uint_as_float(a & 0xFFFF0000u) * r),
+                  cut16(__uint_as_float(b << 16) * r), cut16(__uint_as_float(b & 0xFFFF0000u) * r));
+}
 // a / 448, correctly rounded: the remainder of a first quotient is exact, as a has 8
 // bits (checked for every BF16 number)
 __device__ __forceinline__ float over_448(float a)
@@ -58,39 +62,41 @@ __device__ __forceinline__ float over_448(float a)
     return fmaf(fmaf(-q, 448.f, a), r, q);
 }
 
-// A half-warp takes kQBlocks consecutive blocks (of the row-major order of blocks)
 template <bool POW2>
 __global__ void __launch_bounds__(kQThreads) k_fp8_quantize(int rows, int K, int KB, const uint16_t *__restrict__ X,
                                                             uint8_t *__restrict__ q, float *__restrict__ s)
 {
     grid_wait();
     grid_go();
-    const int lane = threadIdx.x & 15;
+    const uint32_t l = threadIdx.x & 7;
     const uint32_t nblk = (uint32_t)rows * KB;   // (< 2^30)
-    const uint32_t per = gridDim.x * (kQThreads / 16) * kQBlocks;
-    // (both halves of a warp make the same turns)
-    for (uint32_t w0 = (blockIdx.x * (kQThreads / 16) + threadIdx.x / 32 * 2) * kQBlocks; w0 < nblk; w0 += per) {
-        const uint32_t b0 = w0 + (threadIdx.x / 16 & 1) * kQBlocks;
+    const uint32_t per = gridDim.x * (kQThreads / 8) * kQBlocks;
+    // (all of a warp make the same turns)
+    for (uint32_t w0 = (blockIdx.x * (kQThreads / 8) + threadIdx.x / 32 * 4) * kQBlocks; w0 < nblk; w0 += per) {
+        const uint32_t b0 = w0 + (threadIdx.x / 8 & 3) * kQBlocks;
         const uint32_t row0 = b0 / (uint32_t)KB, kb0 = b0 % (uint32_t)KB;
-        uint4 u[kQBlocks];
+        uint4 u[kQBlocks], v[kQBlocks];   // columns 8 l .. and 64 + 8 l .. of the block
         uint32_t row = row0, kb = kb0;
 #pragma unroll
         for (int i = 0; i < kQBlocks; ++i) {
-            const uint32_t c = kb * 128 + lane * 8;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (b0 + i < nblk && c < (uint32_t)K) u[i] = __ldcs((const uint4 *)(X + (int64_t)row * K + c));
+            const uint32_t c = kb * 128 + l * 8;
+            const uint16_t *p = X + (int64_t)row * K + c;
+            u[i] = v[i] = make_uint4(0, 0, 0, 0);
+            if (b0 + i < nblk && c < (uint32_t)K) u[i] = __ldcs((const uint4 *)p);
+            if (b0 + i < nblk && c + 64 < (uint32_t)K) v[i] = __ldcs((const uint4 *)(p + 64));
             if (++kb == (uint32_t)KB) kb = 0, ++row;
         }
         row = row0, kb = kb0;
 #pragma unroll
         for (int i = 0; i < kQBlocks; ++i) {
-            uint32_t m = absmax2(absmax2(u[i].x & 0x7FFF7FFFu, u[i].y), absmax2(u[i].z & 0x7FFF7FFFu, u[i].w));
+            uint32_t m = absmax2(absmax2(absmax2(u[i].x, u[i].y), absmax2(u[i].z, u[i].w)),
+                                 absmax2(absmax2(v[i].x, v[i].y), absmax2(v[i].z, v[i].w)));
 #pragma unroll
-            for (int o = 8; o; o >>= 1) m = absmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
-            m = absmax2(m, m >> 16 | m << 16);
-            float a = __uint_as_float(m << 16);
+            for (int o = 4; o; o >>= 1) m = absmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = absmax2(m, m >> 16) & 0x7FFFu;
+            float a = __uint_as_float(m << 16), r;
             a = a < 7.8886091e-31f ? 7.8886091e-31f : a;   // 2^-100; a NaN stays
-            float sc = over_448(a), r;
+            float sc = over_448(a);
             if constexpr (POW2) {
                 // (a / 448 in FP32 is a power of two only where the quotient is: 448 = 7 * 2^6)
                 sc = __uint_as_float((__float_as_uint(sc) + 0x7FFFFFu) & 0x7F800000u);
@@ -98,19 +104,14 @@ __global__ void __launch_bounds__(kQThreads) k_fp8_quantize(int rows, int K, int
             } else {
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc));   // (sc and 1 / sc are normal numbers)
             }
+            r *= 1.0000152587890625f;                               // 1 + 2^-16
             if (!(a <= 3.4e38f)) sc = __int_as_float(0x7fffffff);   // an infinity makes its block NaN too
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = to_16_bits(__uint_as_float(w[j] << 16) * r);
-                v[2 * j + 1] = to_16_bits(__uint_as_float(w[j] & 0xFFFF0000u) * r);
-            }
-            const uint32_t c = kb * 128 + lane * 8;
-            if (b0 + i < nblk && c < (uint32_t)K) {
-                *(uint2 *)(q + (int64_t)row * K + c) =
-                    make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
-                if (lane == 0) s[(int64_t)kb * rows + row] = sc;
+            const uint32_t c = kb * 128 + l * 8;
+            uint8_t *p = q + (int64_t)row * K + c;
+            if (b0 + i < nblk) {
+                if (c < (uint32_t)K) *(uint2 *)p = make_uint2(codes4(u[i].x, u[i].y, r), codes4(u[i].z, u[i].w, r));
+                if (c + 64 < (uint32_t)K) *(uint2 *)(p + 64) = make_uint2(codes4(v[i].x, v[i].y, r), codes4(v[i].z, v[i].w, r));
+                if (l == 0) s[(int64_t)kb * rows + row] = sc;
             }
             if (++kb == (uint32_t)KB) kb = 0, ++row;
         }
@@ -261,7 +262,7 @@ static bool product(int rows, int N, int K, const void *A, const float *As, cons
 static bool quantize(int rows, int K, const void *X, bool pow2, void *q, float *s, cudaStream_t st)
 {
     const int KB = (int)cdiv(K, 128);
-    const int64_t ctas = cdiv((int64_t)rows * KB, kQThreads / 16 * (int64_t)kQBlocks);
+    const int64_t ctas = cdiv((int64_t)rows * KB, kQThreads / 8 * (int64_t)kQBlocks);
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)gemm_num_sms() * 32));
     return pow2 ? launch_chained<k_fp8_quantize<true>>(grid, kQThreads, 0, 1, st, rows, K, KB, (const uint16_t *)X,
                                                        (uint8_t *)q, s)
