@@ -297,9 +297,13 @@ __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n,
 // largest values bounds the (k + 2)-th largest of all from below, and the experts from
 // there up (some 11 for k = 8, E = 384) are gathered, one a lane, and ranked.  (Taking the
 // largest k times over, each time looking through all of them again, took 1280 instructions
-// a token at k = 8, E = 384 and 23.7 us for 8192 tokens.)  The values
-// of that search are c by approximate exponentials; the candidates' scores are computed
-// in full.
+// a token at k = 8, E = 384, against 840, and 18.6 us for 8192 tokens against 11.)  The values
+// of that search are c by approximate exponentials (by tanh.approx it was no faster); the
+// candidates' scores are computed in full.
+//
+// Bound by the issue of instructions, 60 to 70% of the slots at 32 warps an SM: 840 a token for
+// E = 384 without groups, 1190 for E = 256 with 8 (20 us for 16384 tokens; their logits are 2.5
+// us of HBM).  Fewer registers (12 CTAs of 4 warps an SM) or more (6) take the same or 10% longer.
 enum Mode { kLogits = 0, kBias = 1, kGroups = 2 };   // neither a bias nor groups; a bias; groups
 template <int kN, int kWarps, int kMode>
 __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gate(const Args a)
@@ -543,8 +547,8 @@ __device__ __forceinline__ bool first_of(uint32_t same, bool live, float &g)
     return first;
 }
 
-// Sigmoid: kW lanes a token, as only the chosen logits are read.  (A warp a token, 8 of
-// its lanes at work, took 8.8 us for 8192 tokens of 384 experts.)
+// Sigmoid: kW lanes a token, the least power of two that holds k, as only the chosen logits
+// are read.  (8192 tokens of 384 experts, k = 8: 7.1 us alone with 8 lanes, 10 with a warp a token.)
 template <int kW, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) k_gate_backward_sigmoid(const BwdArgs a)
 {

@@ -5,7 +5,10 @@
 //
 // Bound by HBM: the norm reads every gradient once, the clip reads it again
 // and writes it.  (The coefficient needs the last gradient's square before the
-// first one can be scaled, so two reads it is, but for what the L2 still holds.)
+// first one can be scaled, so two reads it is, but for what the L2 still holds.)  906 MB
+// of f32 in two tensors take 421 us, 6.5 TB/s of these 2.7 GB (0.95 of a copy's rate); 691 MB
+// in 60 tensors, half of them BF16, 261 us.  Chunks go round the CTAs in turn, as BF16 ones
+// take longer: with a run of chunks for each CTA the latter took 300 us.
 #include <algorithm>
 #include <cmath>
 #include <vector>
