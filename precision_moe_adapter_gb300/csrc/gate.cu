@@ -231,14 +231,15 @@ __device__ __noinline__ uint32_t keep_groups_exact(const Args &a, const float *r
     return keep_groups(__shfl_sync(kAll, key_of(s), min(lane << a.sublog, 31)), a.G, a.top, in, out);
 }
 
-// The k largest keys in shared memory (expert e at e + e / 32), in order: lane j < k
-// returns the j-th expert
+// The largest keys in shared memory (expert e at e + e / 32), in order: lane j < rounds
+// returns the j-th expert (and leaves the keys in `keys`)
 template <class Key>
-__device__ __forceinline__ int choose(const Args &a, Key *buf)
+__device__ __noinline__ int choose(const Args &a, Key *buf, int rounds, Key *keys)
 {
     const int lane = threadIdx.x & 31;
     int mine = 0;
-    for (int j = 0; j < a.k; ++j) {
+    Key key = 0;
+    for (int j = 0; j < rounds; ++j) {
         Key best = 0;
         int id = 0x7fffffff;
         for (int e = lane; e < a.E; e += 32) {
@@ -249,8 +250,10 @@ __device__ __forceinline__ int choose(const Args &a, Key *buf)
         const int e = (int)__reduce_min_sync(kAll, best == m ? (uint32_t)id : 0x7fffffffu);
         if (e < a.E && e % 32 == lane) buf[e + (e >> 5)] = 0;
         __syncwarp();
-        if (lane == j && e < a.E) mine = e;
+        if (lane == j && e < a.E) mine = e, key = m;
     }
+    if (keys) keys[lane] = key;
+    __syncwarp();
     return mine;
 }
 // The whole choice in FP64
@@ -271,7 +274,7 @@ __device__ __noinline__ int choose_exact(const Args &a, const float *row, Norm n
             if (!(kept >> (e / a.gsize) & 1u)) buf[e + (e >> 5)] = 0;
         __syncwarp();
     }
-    return choose(a, buf);
+    return choose(a, buf, a.k, (uint64_t *)nullptr);
 }
 // The FP64 order of a few candidates (lane < cnt has one): lane j < k returns the j-th
 __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n, int e, int cnt, int *slot)
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
         const float terr = softmax ? n.inv * (float)(kN + 16) * 1.1920929e-7f : 9.5367432e-7f;
         const float cerr = softmax ? terr : 4.7683716e-7f;
         int mine = 0, cnt = 0;
-        bool whole = false;   // the groups are too close to call in FP32
+        bool whole = false;   // too close to call in FP32, for the groups or among many
         uint32_t kept = kAll;
         auto group_of = [&](uint32_t e) { return (a.gmagic ? __umulhi(e, a.gmagic) : e) & 31u; };
         if constexpr (grouped) {
@@ -441,7 +444,22 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             }
             __syncwarp();
             if (cnt > 32 || cnt < a.k || (has_bias && cnt == a.k && !all)) {
-                whole = true;   // many equal ones, few that can be chosen, or k = 32
+                // many candidates (k near the number of lanes, many equal ones) or few that can be chosen
+                whole = has_bias && a.k == 32;
+                if (!whole) {   // by FP32 keys, the largest one at a time
+                    uint32_t *kb = (uint32_t *)buf;
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) {   // (0: of a group that is out)
+                        const int e = i * 32 + lane;
+                        if (e < a.E) kb[e + (e >> 5)] = kept >> group_of(e) & 1u ? key_of(v[i]) : 0u;
+                    }
+                    __syncwarp();
+                    mine = choose(a, kb, has_bias ? a.k + 1 : a.k, (uint32_t *)cc);
+                    if (has_bias) {
+                        const uint32_t mk = ((uint32_t *)cc)[lane], nk = __shfl_down_sync(kAll, mk, 1);
+                        whole = __any_sync(kAll, lane < a.k && mk > 1u && nk > 1u && near(of_key(mk), of_key(nk), terr));
+                    }
+                }
             } else {
                 const int e = lane < cnt ? ci[lane] : 0;
                 const float l = lane < cnt ? row[e] : -INFINITY;
@@ -473,20 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             }
             __syncwarp();
         }
-        if (whole) {
-            if (has_bias) {
-                mine = choose_exact(a, row, n, buf);
-            } else {
-                uint32_t *kb = (uint32_t *)buf;
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {   // (0: of a group that is out)
-                    const int e = i * 32 + lane;
-                    if (e < a.E) kb[e + (e >> 5)] = kept >> group_of(e) & 1u ? key_of(v[i]) : 0u;
-                }
-                __syncwarp();
-                mine = choose(a, kb);
-            }
-        }
+        if (whole) mine = choose_exact(a, row, n, buf);
         // the weights: the scores without the bias
         const bool live = lane < a.k;
         float w = 0.f;

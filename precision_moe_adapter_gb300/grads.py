@@ -11,7 +11,7 @@ from __future__ import annotations
 import torch
 
 from . import pmoe
-from .layer import check_current, check_tensor
+from .layer import check_cuda, check_current, check_tensor
 
 _DTYPES = {torch.float32: pmoe.GRAD_F32, torch.bfloat16: pmoe.GRAD_BF16}
 
@@ -46,6 +46,7 @@ class GradList:
     def _norm_ok(self, norm):
         check_current(self.device)
         check_tensor("norm", norm, (torch.float32,), (1,), self.device)
+        check_cuda(self.device)
 
     def norm(self, norm):
         """norm (f32 [1]): the root of the sum of all squares."""

@@ -47,6 +47,12 @@ def check_current(device):
                            f"on {device}: call under torch.cuda.device({index})")
 
 
+def check_cuda(device):
+    """Raises unless the device is a GPU, whose memory the kernels are given."""
+    if device.type != "cuda":
+        raise RuntimeError(f"the tensors are on {device}, the kernels run on a GPU")
+
+
 def _dev(a, device) -> torch.Tensor:
     if isinstance(a, torch.Tensor):   # already a tensor (e.g. drawn on the device)
         return a.to(device)
@@ -162,6 +168,7 @@ class DeviceLayer:
         if (g.T, g.E, g.k) != (cfg.T, cfg.E, cfg.k):
             raise ValueError(f"gate of T={g.T}, E={g.E}, k={g.k} on a layer of T={cfg.T}, E={cfg.E}, k={cfg.k}")
         check_tensor("logits", logits, (torch.float32,), (cfg.T, cfg.E), self.device)
+        check_cuda(self.device)
 
     def gate(self, g: pmoe.Gate, logits, rt: Routing, bias=None):
         """The choice and the weights of ``rt`` by scores (``pmoe.gate``) of

@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import pmoe
-from .layer import check_current, check_tensor
+from .layer import check_cuda, check_current, check_tensor
 
 _BF16 = (torch.bfloat16, torch.int16)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
@@ -71,6 +71,7 @@ class DeviceLinearW8A8:
         """Y (BF16 [rows, N]) of X (BF16 [rows, K])."""
         n = self._rows("X", X, self.K)
         check_tensor("Y", Y, _BF16, (n, self.N), self.device)
+        check_cuda(self.device)
         pmoe.dense_w8a8_forward(self.q, self.s, self.N, self.K, self.block, self.R, n, X, Y, self._ws,
                                 self.pow2)
 
@@ -88,6 +89,7 @@ class DeviceLinearW8A8:
             check_tensor("dR", dR, (torch.float32,), tuple(self.R.shape), self.device)
         elif dR is not None:
             raise ValueError("dR: the layer has no adapter")
+        check_cuda(self.device)
         pmoe.dense_w8a8_backward(self.qt, self.st, self.N, self.K, self.block, self.R, n, X, dY, dX, dR,
                                  self._ws, self.pow2)
 

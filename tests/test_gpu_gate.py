@@ -125,7 +125,7 @@ def compare(l, b, k, seed=0, **kw):
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 2, 1), (5, 2, 2), (64, 8, 2), (33, 31, 7), (9, 32, 32), (130, 33, 8),
                                    (200, 60, 6), (77, 127, 9), (500, 128, 8), (65, 255, 4), (1000, 256, 8),
-                                   (300, 384, 8), (100, 511, 16), (50, 1000, 8), (20, 1024, 32), (10, 1025, 8),
+                                   (300, 384, 8), (400, 256, 24), (300, 384, 31), (100, 511, 16), (50, 1000, 8), (20, 1024, 32), (10, 1025, 8),
                                    (7, 4096, 32), (3, 4095, 5)])
 def test_sizes(T, E, k, bias, kind):
     l, b, _ = inputs(T, E, seed=T + E, bias=bias)
@@ -157,7 +157,7 @@ def test_many_tokens_and_equal_logits(kind, groups):
     assert torch.equal(idx, torch.arange(6, dtype=torch.int32, device="cuda").expand_as(idx))
 
 
-@pytest.mark.parametrize("k", [1, 8, 31, 32])
+@pytest.mark.parametrize("k", [1, 8, 20, 31, 32])
 def test_close_calls_between_experts(k):
     """Pairs of experts whose score + bias is the same to a few units of FP32 or
     less, at every place of the order."""

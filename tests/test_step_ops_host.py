@@ -140,6 +140,11 @@ def test_linear_checks_its_tensors(monkeypatch):
         m.forward(X[:, :64], Y)
     with pytest.raises(RuntimeError):
         m.backward(X, Y, X)                              # made without
+    with pytest.raises(RuntimeError, match="GPU"):       # host memory
+        m.forward(X, Y)
+    m.qt = m.q
+    with pytest.raises(RuntimeError, match="GPU"):
+        m.backward(X, Y, X)
 
 
 # ---------------------------------------------------------------- gradient list
@@ -210,6 +215,10 @@ def test_grad_list_checks_its_tensors():
         g.norm(torch.zeros(1, dtype=torch.float64))
     with pytest.raises(ValueError):
         g.clip(1.0, torch.zeros(2))
+    with pytest.raises(RuntimeError, match="GPU"):                            # host memory
+        g.clip(1.0, torch.zeros(1))
+    with pytest.raises(RuntimeError, match="GPU"):
+        g.norm(torch.zeros(1))
 
 
 def test_calls_on_another_device_are_refused(monkeypatch):
