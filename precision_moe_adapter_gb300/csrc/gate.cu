@@ -454,10 +454,18 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                         if (e < a.E) kb[e + (e >> 5)] = kept >> group_of(e) & 1u ? key_of(v[i]) : 0u;
                     }
                     __syncwarp();
-                    mine = choose(a, kb, has_bias ? a.k + 1 : a.k, (uint32_t *)cc);
+                    mine = choose(a, kb, has_bias ? min(a.k + 2, 32) : a.k, (uint32_t *)cc);
                     if (has_bias) {
+                        // close ones among the best k + 1 are put in order by their FP64 values, unless the
+                        // one behind is close too
                         const uint32_t mk = ((uint32_t *)cc)[lane], nk = __shfl_down_sync(kAll, mk, 1);
-                        whole = __any_sync(kAll, lane < a.k && mk > 1u && nk > 1u && near(of_key(mk), of_key(nk), terr));
+                        const uint32_t b =
+                            __ballot_sync(kAll, lane < 31 && mk > 1u && nk > 1u && near(of_key(mk), of_key(nk), terr));
+                        const uint32_t there = __ballot_sync(kAll, mk != 0u);
+                        if (b & ((1u << a.k) - 1u)) {
+                            whole = a.k == 31 || (b >> a.k & 1u);
+                            if (!whole) mine = order_exact(a, row, n, mine, min(a.k + 1, __popc(there)), ci);
+                        }
                     }
                 }
             } else {
