@@ -398,10 +398,10 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             uint32_t in, out;
             kept = keep_groups(key_of(score), a.G, a.top, in, out);
             const float x = of_key(in), y = of_key(out);   // the least score kept, the largest one not
-            bool close = false;
-            if (has_bias) close = a.gsum == 1 ? near(x, y, terr) : near(0.5f * x, 0.5f * y, terr);
-            else if (a.gsum == 2) close = y != -INFINITY && !(x - y > 1.9073486e-6f * x + 1e-36f);   // (each score to 2^-21)
-            if (close) {
+            bool tie = false;
+            if (has_bias) tie = a.gsum == 1 ? near(x, y, terr) : near(0.5f * x, 0.5f * y, terr);
+            else if (a.gsum == 2) tie = y != -INFINITY && !(x - y > 1.9073486e-6f * x + 1e-36f);   // (each score to 2^-21)
+            if (tie) {
                 kept = keep_groups_exact(a, row, n, vb, terr);
                 whole = kept == 0;
             }
@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
         }
         float s = 0.f;
         bool scored = false;   // s is the lane's score
+        int close = 0;         // the first so many lanes' experts are to be put in order by FP64 values
         if (!whole) {
             float best = v[0];
 #pragma unroll
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                         const uint32_t there = __ballot_sync(kAll, mk != 0u);
                         if (b & ((1u << a.k) - 1u)) {
                             whole = a.k == 31 || (b >> a.k & 1u);
-                            if (!whole) mine = order_exact(a, row, n, mine, min(a.k + 1, __popc(there)), ci);
+                            close = min(a.k + 1, __popc(there));
                         }
                     }
                 }
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                     s = cs[lane];
                     const float nc = __shfl_down_sync(kAll, c, 1);
                     scored = !__any_sync(kAll, lane < a.k && lane + 1 < cnt && near(c, nc, cerr));
-                    if (!scored) mine = order_exact(a, row, n, mine, cnt, ci);
+                    if (!scored) close = cnt;
                 } else {
                     s = softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);
                     scored = true;
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
             __syncwarp();
         }
         if (whole) mine = choose_exact(a, row, n, buf);
+        else if (close) mine = order_exact(a, row, n, mine, close, ci);
         // the weights: the scores without the bias
         const bool live = lane < a.k;
         float w = 0.f;

@@ -149,3 +149,50 @@ def test_steps_repeat_and_replay(block):
             t.zero_()
         g.replay()
         assert all(torch.equal(a, b) for a, b in zip(ref, block.outputs()))
+
+
+def test_two_blocks_at_once():
+    """Two blocks with workspaces of their own, on two streams at the same time."""
+    blocks = [Block(seed=s) for s in (1, 2)]
+    refs = []
+    for b in blocks:
+        b.step()
+        torch.cuda.synchronize()
+        refs.append(b.outputs())
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for _ in range(5):
+        for b, st in zip(blocks, streams):
+            with torch.cuda.stream(st):
+                b.step()
+    torch.cuda.synchronize()
+    for b, ref in zip(blocks, refs):
+        assert all(torch.equal(x, y) for x, y in zip(ref, b.outputs()))
+        assert b.layer.status() == pmoe.PMOE_OK and b.lin.status() == pmoe.PMOE_OK
+
+
+@pytest.mark.parametrize("rows", [[1, 700], [64, 64], [3000, 17]])
+def test_two_projections_at_once(rows):
+    """Shared tiles in clusters beside pairs and single CTAs, on two streams."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    lins, Xs, Ys = [], [], []
+    for n in rows:
+        q = torch.randn((4096, 2048), generator=g, device="cuda").to(torch.float8_e4m3fn)
+        lins.append(DeviceLinearW8A8(q, torch.full((32, 16), 0.01, device="cuda"), n))
+        Xs.append(torch.randn((n, 2048), generator=g, device="cuda").to(BF16))
+        Ys.append(torch.empty((n, 4096), dtype=BF16, device="cuda"))
+    refs = []
+    for lin, X, Y in zip(lins, Xs, Ys):
+        lin.forward(X, Y)
+        torch.cuda.synchronize()
+        refs.append(Y.clone())
+        Y.zero_()
+    streams = [torch.cuda.Stream() for _ in rows]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for lin, X, Y, st in zip(lins, Xs, Ys, streams):
+            with torch.cuda.stream(st):
+                lin.forward(X, Y)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, r) for y, r in zip(Ys, refs))
+    assert all(lin.status() == pmoe.PMOE_OK for lin in lins)
