@@ -200,29 +200,38 @@ __device__ __forceinline__ bool near(float x, float y, float err)
     return y != -INFINITY && !(x - y > err + 2.3841858e-7f * (fabsf(x) + fabsf(y)));
 }
 
+// Whether two experts have the same logit and bias, and so the same c to the last bit: a
+// tie, which goes to the lower id without a closer look
+__device__ __forceinline__ bool same(const Args &a, const float *row, int e, int f)
+{
+    return row[e] == row[f] && (!a.has_bias || a.bias[e] == a.bias[f]);
+}
+
 // The groups' choice from FP64 scores: FP64 values are formed of the experts that count
 // in each group by their FP32 ones; 0 where those (off by up to terr / 2) do not tell
 // which ones count.
 __device__ __noinline__ uint32_t keep_groups_exact(const Args &a, const float *row, Norm n, const float *buf, float terr)
 {
     const int lane = threadIdx.x & 31, sub = 1 << a.sublog, g = lane >> a.sublog, j = lane & (sub - 1);
-    float x = -INFINITY, y = -INFINITY, z = -INFINITY;   // the three largest, and the experts of the first two
-    int xi = 0, yi = 0;
+    float x = -INFINITY, y = -INFINITY, z = -INFINITY;   // the three largest, and their experts
+    int xi = 0, yi = 0, zi = 0;
     auto put = [&](float k, int e) {
-        if (k > x) z = y, y = x, yi = xi, x = k, xi = e;
-        else if (k > y) z = y, y = k, yi = e;
-        else if (k > z) z = k;
+        if (k > x) z = y, zi = yi, y = x, yi = xi, x = k, xi = e;
+        else if (k > y) z = y, zi = yi, y = k, yi = e;
+        else if (k > z) z = k, zi = e;
     };
     if (g < a.G)
         for (int e = g * a.gsize + j * a.per; e < g * a.gsize + min((j + 1) * a.per, a.gsize); ++e) put(buf[e + (e >> 5)], e);
     for (int o = 1; o < sub; o *= 2) {
         const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o), z2 = __shfl_xor_sync(kAll, z, o);
-        const int xi2 = __shfl_xor_sync(kAll, xi, o), yi2 = __shfl_xor_sync(kAll, yi, o);
+        const int xi2 = __shfl_xor_sync(kAll, xi, o), yi2 = __shfl_xor_sync(kAll, yi, o), zi2 = __shfl_xor_sync(kAll, zi, o);
         put(x2, xi2);
         put(y2, yi2);
-        put(z2, 0);   // (never among the first two of both)
+        put(z2, zi2);
     }
-    if (__any_sync(kAll, a.has_bias && g < a.G && near(a.gsum == 2 ? y : x, a.gsum == 2 ? z : y, terr))) return 0;
+    const float last = a.gsum == 2 ? y : x, next = a.gsum == 2 ? z : y;   // the last one that counts, the next one
+    const int li = a.gsum == 2 ? yi : xi, ni = a.gsum == 2 ? zi : yi;
+    if (__any_sync(kAll, a.has_bias && g < a.G && near(last, next, terr) && !same(a, row, li, ni))) return 0;
     const double zinv = exact_zinv(a, row, n);
     double s = exact_c(a, row, xi, n, zinv);
     if (a.gsum == 2 && y != -INFINITY) s += exact_c(a, row, yi, n, zinv);
@@ -358,13 +367,23 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
         if (has_bias) {
             // (a loop for each form: a choice within one costs some 500 instructions a token)
             auto form = [&](auto score) {
+                constexpr int kB = kN < 8 ? kN : 8;   // biases loaded at once where not all were
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    float b;
-                    if constexpr (kBiasFirst) b = bias[i];
-                    else b = i * 32 + lane < a.E ? __ldg(a.bias + i * 32 + lane) : 0.f;
-                    const float c = score(v[i], b);
-                    v[i] = v[i] == -INFINITY ? -INFINITY : c;
+                for (int i0 = 0; i0 < kN; i0 += kB) {
+                    float late[kB];
+                    if constexpr (!kBiasFirst) {
+#pragma unroll
+                        for (int i = 0; i < kB; ++i) {
+                            const int e = (i0 + i) * 32 + lane;
+                            late[i] = e < a.E ? a.bias[e] : 0.f;
+                        }
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int i = i0; i < i0 + kB && i < kN; ++i) {
+                        const float c = score(v[i], kBiasFirst ? bias[kBiasFirst ? i : 0] : late[i - i0]);
+                        v[i] = v[i] == -INFINITY ? -INFINITY : c;
+                    }
                 }
             };
             if (softmax) form([&](float x, float b) { return fmaf(x, n.inv, b); });
@@ -460,8 +479,10 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                         // close ones among the best k + 1 are put in order by their FP64 values, unless the
                         // one behind is close too
                         const uint32_t mk = ((uint32_t *)cc)[lane], nk = __shfl_down_sync(kAll, mk, 1);
-                        const uint32_t b =
-                            __ballot_sync(kAll, lane < 31 && mk > 1u && nk > 1u && near(of_key(mk), of_key(nk), terr));
+                        const int nid = __shfl_down_sync(kAll, mine, 1);
+                        const uint32_t b = __ballot_sync(kAll, lane < 31 && mk > 1u && nk > 1u &&
+                                                                   near(of_key(mk), of_key(nk), terr) &&
+                                                                   !same(a, row, mine, nid));
                         const uint32_t there = __ballot_sync(kAll, mk != 0u);
                         if (b & ((1u << a.k) - 1u)) {
                             whole = a.k == 31 || (b >> a.k & 1u);
@@ -491,7 +512,12 @@ __global__ void __launch_bounds__(32 * kWarps, kN <= 12 ? 32 / kWarps : 1) k_gat
                 if (has_bias) {
                     s = cs[lane];
                     const float nc = __shfl_down_sync(kAll, c, 1);
-                    scored = !__any_sync(kAll, lane < a.k && lane + 1 < cnt && near(c, nc, cerr));
+                    bool tie = lane < a.k && lane + 1 < cnt && near(c, nc, cerr);
+                    if (__any_sync(kAll, tie)) {
+                        const int nid = __shfl_down_sync(kAll, mine, 1);
+                        tie = tie && !same(a, row, mine, nid);
+                    }
+                    scored = !__any_sync(kAll, tie);
                     if (!scored) close = cnt;
                 } else {
                     s = softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);
