@@ -35,10 +35,11 @@ struct Args {
     float *w;
 };
 
-// Keys in the order of the values; 0 is an expert that is taken or out
+// Keys in the order of the values, -0 as +0 (the sum with +0 is +0); 0 is an expert that
+// is taken or out
 __device__ __forceinline__ uint32_t key_of(float v)
 {
-    const uint32_t u = __float_as_uint(v);
+    const uint32_t u = __float_as_uint(v + 0.f);
     return max(u ^ ((uint32_t)((int)u >> 31) | 0x80000000u), 1u);
 }
 __device__ __forceinline__ float of_key(uint32_t k)
@@ -47,7 +48,7 @@ __device__ __forceinline__ float of_key(uint32_t k)
 }
 __device__ __forceinline__ uint64_t key_of(double v)
 {
-    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.);
     const uint64_t k = (u >> 63) ? ~u : u | 0x8000000000000000ull;
     return k ? k : 1ull;
 }
