@@ -5,8 +5,10 @@
 // The choice is the one of the exact scores.  Without a bias the order of the
 // experts is that of their logits, and keys of the logits decide.  With one, c =
 // score + bias is formed in FP32 first; where two experts that the choice has to
-// tell apart (neighbours among the best k + 1) lie within the error of their c,
-// the candidates' c are formed again in FP64, one candidate a lane.  The same
+// tell apart lie within the error of their c, the candidates' c are formed again in
+// FP64, one candidate a lane.  They are neighbours down to the k-th place and on through
+// those that are close to it, each to the next: among equal ones, whose order needs no
+// closer look, the last may have a neighbour that stands before all of them.  The same
 // holds for the last group in and the first one out, with the c of the experts that
 // count for their groups.  Where that does not settle it, all of the token's c are
 // formed in FP64.
@@ -214,25 +216,32 @@ __device__ __forceinline__ bool same(const Args &a, const float *row, int e, int
 __device__ __noinline__ uint32_t keep_groups_exact(const Args &a, const float *row, Norm n, const float *buf, float terr)
 {
     const int lane = threadIdx.x & 31, sub = 1 << a.sublog, g = lane >> a.sublog, j = lane & (sub - 1);
-    float x = -INFINITY, y = -INFINITY, z = -INFINITY;   // the three largest, and their experts
-    int xi = 0, yi = 0, zi = 0;
+    const int e0 = g * a.gsize + j * a.per, e1 = g < a.G ? g * a.gsize + min((j + 1) * a.per, a.gsize) : 0;
+    float x = -INFINITY, y = -INFINITY;   // the two largest, and their experts
+    int xi = 0, yi = 0;
     auto put = [&](float k, int e) {
-        if (k > x) z = y, zi = yi, y = x, yi = xi, x = k, xi = e;
-        else if (k > y) z = y, zi = yi, y = k, yi = e;
-        else if (k > z) z = k, zi = e;
+        if (k > x) y = x, yi = xi, x = k, xi = e;
+        else if (k > y) y = k, yi = e;
     };
-    if (g < a.G)
-        for (int e = g * a.gsize + j * a.per; e < g * a.gsize + min((j + 1) * a.per, a.gsize); ++e) put(buf[e + (e >> 5)], e);
+    for (int e = e0; e < e1; ++e) put(buf[e + (e >> 5)], e);
     for (int o = 1; o < sub; o *= 2) {
-        const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o), z2 = __shfl_xor_sync(kAll, z, o);
-        const int xi2 = __shfl_xor_sync(kAll, xi, o), yi2 = __shfl_xor_sync(kAll, yi, o), zi2 = __shfl_xor_sync(kAll, zi, o);
+        const float x2 = __shfl_xor_sync(kAll, x, o), y2 = __shfl_xor_sync(kAll, y, o);
+        const int xi2 = __shfl_xor_sync(kAll, xi, o), yi2 = __shfl_xor_sync(kAll, yi, o);
         put(x2, xi2);
         put(y2, yi2);
-        put(z2, zi2);
     }
-    const float last = a.gsum == 2 ? y : x, next = a.gsum == 2 ? z : y;   // the last one that counts, the next one
-    const int li = a.gsum == 2 ? yi : xi, ni = a.gsum == 2 ? zi : yi;
-    if (__any_sync(kAll, a.has_bias && g < a.G && near(last, next, terr) && !same(a, row, li, ni))) return 0;
+    xi = __shfl_sync(kAll, xi, lane - j);   // (of equal ones each lane may have found others)
+    yi = __shfl_sync(kAll, yi, lane - j);
+    if (a.has_bias) {   // one that does not count and is close to the last that does, unless all of them are the same
+        const float last = a.gsum == 2 ? y : x;
+        const int li = a.gsum == 2 ? yi : xi;
+        const bool other = a.gsum == 2 && near(x, y, terr) && !same(a, row, xi, yi);
+        bool close = false;
+        for (int e = e0; e < e1; ++e)
+            if (e != xi && (a.gsum == 1 || e != yi) && near(last, buf[e + (e >> 5)], terr))
+                close = close || other || !same(a, row, e, li);
+        if (__any_sync(kAll, close)) return 0;
+    }
     const double zinv = exact_zinv(a, row, n);
     double s = exact_c(a, row, xi, n, zinv);
     if (a.gsum == 2 && y != -INFINITY) s += exact_c(a, row, yi, n, zinv);
@@ -266,6 +275,23 @@ __device__ __noinline__ int choose(const Args &a, Key *buf, int rounds, Key *key
     __syncwarp();
     return mine;
 }
+// Whether an expert that `choose` has left is close to the one at place `at` (off by up to
+// err / 2, lane j has the key and the expert of place j), the same ones only if `alike`
+__device__ __noinline__ bool close_left(const Args &a, const float *row, const uint32_t *buf, uint32_t key, int id, int at,
+                                        bool alike, float err)
+{
+    const float x = of_key(__shfl_sync(kAll, key, at));
+    const int f = __shfl_sync(kAll, id, at);
+    bool close = false;
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+        const uint32_t k = buf[e + (e >> 5)];
+        if (k && near(x, of_key(k), err)) close = close || alike || !same(a, row, e, f);
+    }
+    return __any_sync(kAll, close);
+}
+// The first place from the k-th on that the next one is not close to (bit j: places j and
+// j + 1 are close; bit 31 is clear)
+__device__ __forceinline__ int run_end(uint32_t close, int k) { return k - 1 + __ffs((int)~(close >> (k - 1))) - 1; }
 // The whole choice in FP64
 __device__ __noinline__ int choose_exact(const Args &a, const float *row, Norm n, uint64_t *buf)
 {
@@ -486,17 +512,15 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_an_sm(kN)) k_gate(const Args
                     __syncwarp();
                     mine = choose(a, kb, has_bias ? min(a.k + 2, 32) : a.k, (uint32_t *)cc);
                     if (has_bias) {
-                        // close ones among the best k + 1 are put in order by their FP64 values, unless the
-                        // one behind is close too
+                        // close ones are put in order by their FP64 values, unless they go on behind the
+                        // places that were found.  (Where all are the same, the same ones behind them may.)
                         const uint32_t mk = ((uint32_t *)cc)[lane], nk = __shfl_down_sync(kAll, mk, 1);
-                        const int nid = __shfl_down_sync(kAll, mine, 1);
-                        const uint32_t b = __ballot_sync(kAll, lane < 31 && mk > 1u && nk > 1u &&
-                                                                   near(of_key(mk), of_key(nk), terr) &&
-                                                                   !same(a, row, mine, nid));
-                        const uint32_t there = __ballot_sync(kAll, mk != 0u);
-                        if (b & ((1u << a.k) - 1u)) {
-                            whole = a.k == 31 || (b >> a.k & 1u);
-                            close = min(a.k + 1, __popc(there));
+                        const uint32_t nb = __ballot_sync(kAll, lane < 31 && mk && nk && near(of_key(mk), of_key(nk), terr));
+                        if (nb << (32 - a.k)) {
+                            const int nid = __shfl_down_sync(kAll, mine, 1), end = run_end(nb, a.k);
+                            const uint32_t b = __ballot_sync(kAll, (nb >> lane & 1u) && !same(a, row, mine, nid));
+                            if (b & ((1u << end) - 1u)) close = end + 1;
+                            whole = end + 1 == min(a.k + 2, 32) && close_left(a, row, kb, mk, mine, end, close != 0, terr);
                         }
                     }
                 }
@@ -522,12 +546,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_an_sm(kN)) k_gate(const Args
                 if (has_bias) {
                     s = cs[lane];
                     const float nc = __shfl_down_sync(kAll, c, 1);
-                    bool tie = lane < a.k && lane + 1 < cnt && near(c, nc, cerr);
-                    if (__any_sync(kAll, tie)) {
+                    const uint32_t nb = __ballot_sync(kAll, lane + 1 < cnt && near(c, nc, cerr));
+                    scored = true;
+                    if (nb << (32 - a.k)) {
                         const int nid = __shfl_down_sync(kAll, mine, 1);
-                        tie = tie && !same(a, row, mine, nid);
+                        const uint32_t b = __ballot_sync(kAll, (nb >> lane & 1u) && !same(a, row, mine, nid));
+                        scored = !(b & ((1u << run_end(nb, a.k)) - 1u));
                     }
-                    scored = !__any_sync(kAll, tie);
                     if (!scored) close = cnt;
                 } else {
                     s = softmax ? exp_below(c, n.m) * n.inv : sigmoid(c);

@@ -71,3 +71,71 @@ def test_zeros_of_both_signs_in_groups(E, groups, top, k, gsum, bias, kind):
     if E == 2:
         l = torch.tensor([[-0.0, 0.0], [0.0, -0.0]], device="cuda")
         assert call(l, b, 1, kind=kind, groups=2, top=1, gsum=gsum)[0].tolist() == [[0], [0]]
+
+
+# ---------------------------------------------------------------- equal experts beside close ones
+
+def shuffled(l, seed):
+    """Each row in an order of its own."""
+    o = torch.rand(l.shape, generator=gen(seed), device="cuda").argsort(1)
+    return l.gather(1, o)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("alike", [2, 3, 7, 40, 200])
+@pytest.mark.parametrize("k", [1, 2, 8, 30, 31, 32])
+def test_a_close_expert_behind_equal_ones(k, alike, kind):
+    """The k-th place is taken among experts that are exactly alike and one whose score is
+    1e-8 of itself above theirs: the same FP32 number, and behind them where its id is."""
+    T, E = 300, 384
+    row = torch.full((E,), -9.0)
+    row[:k - 1] = torch.linspace(4.0, 1.0, k - 1)
+    row[k - 1:k - 1 + alike] = 0.0
+    row[k - 1 + alike] = 1e-8
+    row = row.cuda()
+    z = torch.zeros(E, device="cuda")
+    check(shuffled(row.expand(T, E), k + alike), z, k, kind)
+    row[k + alike] = -1e-8                     # and one below them
+    check(shuffled(row.expand(T, E), k + alike + 1), z, k, kind)
+    l = torch.full((1, E), -9.0, device="cuda")          # the least case, with its ids
+    l[0, :alike] = 0.0
+    l[0, E - 1] = 1e-8
+    assert call(l, z, 1, kind=kind)[0].item() == E - 1
+
+
+def nearly_alike(T, E, seed, share):
+    """Logits that are 0 but for a share of values beside it (sums of two of them differ)."""
+    g = gen(seed)
+    near = torch.tensor([1e-8, -1.1e-8, 0.3e-8, 2.7e-8], device="cuda")
+    l = near[torch.randint(0, 4, (T, E), generator=g, device="cuda")]
+    return torch.where(torch.rand((T, E), generator=g, device="cuda") < share, l, 0.0)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E", [24, 128, 384, 1030])
+@pytest.mark.parametrize("k", [1, 4, 8, 20, 24])
+def test_experts_that_are_nearly_alike(k, E, kind):
+    g = gen(E + k)
+    steps = torch.randint(0, 3, (E,), generator=g, device="cuda") / 8.0
+    for share in (0.005, 0.05, 0.5):
+        l = nearly_alike(300, E, E + k, share)
+        for b in (torch.zeros(E, device="cuda"), steps):
+            check(l, b, k, kind)
+        # few of them, the others far below
+        check(torch.where(torch.rand(l.shape, generator=g, device="cuda") < 20 / E, l, -9.0), steps, k, kind)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("gsum", [1, 2])
+@pytest.mark.parametrize("E,groups", [(64, 8), (64, 2), (384, 4), (96, 32)])
+def test_groups_whose_experts_are_nearly_alike(E, groups, gsum, kind):
+    """A group's best experts are alike to FP32, equal ones before one that is above them."""
+    z = torch.zeros(E, device="cuda")
+    for share in (0.02, 0.1, 0.5):
+        for top in sorted({1, groups // 2}):
+            check(nearly_alike(400, E, E + groups, share), z, 2, kind, groups, top, gsum)
+    n = E // groups
+    if n >= 8 and gsum == 1:                   # the least case: the best one behind two equal ones
+        l = torch.full((1, E), -9.0, device="cuda")
+        l[0, 0:2], l[0, 2], l[0, n] = 0.0, 1e-8, 0.5e-8
+        assert call(l, z, 1, kind=kind, groups=groups, top=1, gsum=1)[0].item() == 2
