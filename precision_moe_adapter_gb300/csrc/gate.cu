@@ -444,9 +444,14 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_an_sm(kN)) k_gate(const Args
             }
             __syncwarp();
             // (without a bias v is the logit: sums of two are of the scores)
+            float size = 0.f;   // of what the lane's group is the sum of
             const float score = group_score(vb, a, -INFINITY, [&](float x, float y) {
                 if (a.gsum == 1 || x == -INFINITY) return x;
-                if (has_bias) return y == -INFINITY ? x : x + y;
+                if (has_bias) {
+                    if (y == -INFINITY) return x;
+                    size = fabsf(x) + fabsf(y);
+                    return x + y;
+                }
                 if (softmax) return exp_below(x, n.m) + exp_below(y, n.m);
                 return sigmoid(x) + sigmoid(y);
             });
@@ -454,7 +459,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_an_sm(kN)) k_gate(const Args
             kept = keep_groups(key_of(score), a.G, a.top, in, out);
             const float x = of_key(in), y = of_key(out);   // the least score kept, the largest one not
             bool tie = false;
-            if (has_bias) tie = a.gsum == 1 ? near(x, y, terr) : near(0.5f * x, 0.5f * y, terr);
+            if (has_bias && a.gsum == 1) tie = near(x, y, terr);
+            else if (has_bias) {
+                // (terms of opposite sign leave of their sum less than they are rounded by: the largest of
+                // all groups bounds that)
+                const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
+                tie = near(0.5f * x, 0.5f * y, terr + 1.1920929e-7f * most) || most > 3.4e38f;
+            }
             else if (a.gsum == 2) tie = y != -INFINITY && !(x - y > 1.9073486e-6f * x + 1e-36f);   // (each score to 2^-21)
             if (tie) {
                 kept = keep_groups_exact(a, row, n, vb, terr);

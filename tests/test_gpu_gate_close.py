@@ -139,3 +139,40 @@ def test_groups_whose_experts_are_nearly_alike(E, groups, gsum, kind):
         l = torch.full((1, E), -9.0, device="cuda")
         l[0, 0:2], l[0, 2], l[0, n] = 0.0, 1e-8, 0.5e-8
         assert call(l, z, 1, kind=kind, groups=groups, top=1, gsum=1)[0].item() == 2
+
+
+# ---------------------------------------------------------------- groups of large biases
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("spread", [0.0, 0.1])
+@pytest.mark.parametrize("B", [4.0, 16.0, 1e3, 1e4])
+def test_groups_of_biases_that_cancel(B, spread, kind):
+    """Groups of two experts with biases of opposite sign: their sums are small beside what
+    FP32 rounds away of each.  The first group out is moved beside the last one in."""
+    T, G, top = 4000, 8, 4
+    g = gen(int(B))
+    l = torch.randn((T, 2 * G), generator=g, device="cuda")
+    b = torch.tensor([B, -B], device="cuda").repeat(G) + spread * torch.randn(2 * G, generator=g, device="cuda")
+
+    def sums(l):
+        s = torch.sigmoid(l.to(D)) if kind == "sigmoid" else torch.softmax(l.to(D), 1)
+        return (s + b.to(D)).view(T, G, 2).sum(2)
+
+    gs = sums(l)
+    order = torch.argsort(gs, dim=1, descending=True)
+    a, o = order[:, top - 1:top], order[:, top:top + 1]
+    delta = (2 * torch.rand((T, 1), generator=g, device="cuda", dtype=D) - 1) * B * 2.0 ** -23
+    if kind == "sigmoid":
+        want = gs.gather(1, a) + delta - (torch.sigmoid(l.to(D)) + b.to(D)).gather(1, 2 * o + 1) - b.to(D)[2 * o]
+        l.scatter_(1, 2 * o, torch.log(want.clamp(0.001, 0.999) / (1 - want.clamp(0.001, 0.999))).float())
+    else:                                      # (equal logits, but for a few units)
+        l.scatter_(1, 2 * o, (l.gather(1, 2 * a) + delta).float())
+        l.scatter_(1, 2 * o + 1, l.gather(1, 2 * a + 1))
+    s = torch.sort(sums(l), dim=1, descending=True).values
+    gap = (s[:, :-1] - s[:, 1:]).amin(1)
+    # (a sum in FP64 is off by 2^-52 of B; tokens whose sums are within 100 times that are left out)
+    clear = gap > 100 * 2.0 ** -52 * B
+    assert clear.float().mean() > 0.9
+    if kind == "sigmoid" and spread == 0:
+        assert ((s[:, top - 1] - s[:, top]) < B * 2.0 ** -22).float().mean() > 0.3
+    check(l, b, 4, kind, G, top, 2, rows=clear)
