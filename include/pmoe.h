@@ -600,6 +600,8 @@ pmoe_status moe_router_logits(pmoe_dims dims, const void *X, const float *Wr, fl
  *   For few rows the blocks are shared among several CTAs, whose FP32 sums are
  *   added in order: a row's result may differ in its last bit with the number of
  *   rows in the call, not between runs.
+ * fp8_gemm_one_order: the same without the sharing.  A row's result is that of the
+ *   blocks added in their order, bit for bit, whatever the number of rows.
  *   ws >= fp8_gemm_ws_bytes(rows, N, K) (the error word)
  * rows, N, K <= 2^20 (rows 2^24).  q, qt, A and W are E4M3 codes.
  */
@@ -611,6 +613,9 @@ size_t fp8_gemm_ws_bytes(int32_t rows, int32_t N, int32_t K);
 pmoe_status fp8_gemm(int32_t rows, int32_t N, int32_t K, const void *A, const float *As,
                      const void *W, const float *Ws, void *Y, void *ws, size_t ws_bytes,
                      cudaStream_t stream);
+pmoe_status fp8_gemm_one_order(int32_t rows, int32_t N, int32_t K, const void *A, const float *As,
+                               const void *W, const float *Ws, void *Y, void *ws, size_t ws_bytes,
+                               cudaStream_t stream);
 
 /*
  * dense_w8a8_forward / dense_w8a8_backward -- dense_linear_* with the activations
@@ -627,6 +632,10 @@ pmoe_status fp8_gemm(int32_t rows, int32_t N, int32_t K, const void *A, const fl
  *   Y, dY   bf16 [rows, N]    dX bf16 [rows, K]    dR f32 shaped like R (iff R)
  *   ws      >= dense_w8a8_ws_bytes(rows, N, K, adapter), which does not fall as
  *           rows grow: one of the largest batch serves smaller ones
+ * dense_w8a8_forward_one_order / dense_w8a8_backward_one_order: the same by
+ *   fp8_gemm_one_order.  A row's Y and dX do not depend on the number of rows in the
+ *   call, as with dense_linear_*: a token has the same numbers in a rollout's batch
+ *   and in a training batch.
  */
 size_t dense_w8a8_ws_bytes(int32_t rows, int32_t N, int32_t K, int adapter);
 pmoe_status dense_w8a8_forward(const void *q, const float *s, int32_t N, int32_t K, int32_t block,
@@ -636,6 +645,14 @@ pmoe_status dense_w8a8_backward(const void *qt, const float *st, int32_t N, int3
                                 int32_t block, const void *R, int32_t rows, const void *X,
                                 const void *dY, int pow2, void *dX, float *dR, void *ws,
                                 size_t ws_bytes, cudaStream_t stream);
+pmoe_status dense_w8a8_forward_one_order(const void *q, const float *s, int32_t N, int32_t K,
+                                         int32_t block, const void *R, int32_t rows, const void *X,
+                                         int pow2, void *Y, void *ws, size_t ws_bytes,
+                                         cudaStream_t stream);
+pmoe_status dense_w8a8_backward_one_order(const void *qt, const float *st, int32_t N, int32_t K,
+                                          int32_t block, const void *R, int32_t rows, const void *X,
+                                          const void *dY, int pow2, void *dX, float *dR, void *ws,
+                                          size_t ws_bytes, cudaStream_t stream);
 
 /*
  * grad_norm / grad_clip -- the global norm of a list of gradients (the adapter's dS

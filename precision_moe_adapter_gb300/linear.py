@@ -28,12 +28,14 @@ class DeviceLinearW8A8:
 
     ``R`` (BF16 [K/b, b, b]) is the adapter, or None; ``pow2`` makes the
     activations' scales powers of two; ``backward=False`` leaves out the transposed
-    weight.  Calls on one layer share its workspace and must be ordered (one
+    weight.  A row's results may differ in their last bit with the number of rows in
+    the call; ``one_order=True`` makes them the same in any call, which takes longer
+    for few rows.  Calls on one layer share its workspace and must be ordered (one
     stream, or events); they are made on torch's current device, which must be
     the weight's."""
 
     def __init__(self, q: torch.Tensor, s: torch.Tensor, rows: int, R: torch.Tensor | None = None,
-                 pow2: bool = False, backward: bool = True):
+                 pow2: bool = False, backward: bool = True, one_order: bool = False):
         if q.dim() != 2:
             raise ValueError(f"q: shape {tuple(q.shape)}, expected [N, K]")
         N, K = q.shape
@@ -49,6 +51,7 @@ class DeviceLinearW8A8:
         check_current(q.device)
         self.q, self.s, self.R, self.N, self.K = q, s, R, N, K
         self.rows, self.pow2, self.device = int(rows), bool(pow2), q.device
+        self.one_order = bool(one_order)
         n = pmoe.dense_w8a8_ws_bytes(self.rows, N, K, R is not None)
         if n == 0:
             raise ValueError(f"unsupported layer: rows={rows}, N={N}, K={K}")
@@ -73,7 +76,7 @@ class DeviceLinearW8A8:
         check_tensor("Y", Y, _BF16, (n, self.N), self.device)
         check_cuda(self.device)
         pmoe.dense_w8a8_forward(self.q, self.s, self.N, self.K, self.block, self.R, n, X, Y, self._ws,
-                                self.pow2)
+                                self.pow2, one_order=self.one_order)
 
     def backward(self, X, dY, dX, dR=None):
         """dX (BF16 [rows, K]) and, with an adapter, dR (f32, shaped like R, over-
@@ -91,7 +94,7 @@ class DeviceLinearW8A8:
             raise ValueError("dR: the layer has no adapter")
         check_cuda(self.device)
         pmoe.dense_w8a8_backward(self.qt, self.st, self.N, self.K, self.block, self.R, n, X, dY, dX, dR,
-                                 self._ws, self.pow2)
+                                 self._ws, self.pow2, one_order=self.one_order)
 
     def status(self) -> int:
         """First device error recorded by the calls so far (synchronizes)."""

@@ -38,7 +38,8 @@ EXPORTS = ("moe_route", "moe_permute", "moe_chunked_forward", "moe_backward_data
            "moe_balance_ws_bytes", "moe_balance_forward", "moe_route_backward",
            "moe_router_logits", "moe_gate_forward", "moe_gate_backward",
            "fp8_quantize", "fp8_transpose", "fp8_gemm_ws_bytes", "fp8_gemm",
-           "dense_w8a8_ws_bytes", "dense_w8a8_forward", "dense_w8a8_backward",
+           "fp8_gemm_one_order", "dense_w8a8_ws_bytes", "dense_w8a8_forward", "dense_w8a8_backward",
+           "dense_w8a8_forward_one_order", "dense_w8a8_backward_one_order",
            "grad_list_bytes", "grad_list_fill", "grad_ws_bytes", "grad_norm", "grad_clip")
 PERMUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 KT_GEMM_GATE_UP, KT_GEMM_DOWN, KT_GEMM_BWD_G, KT_GEMM_BWD_DX, KT_ROUTER = 0, 1, 2, 3, 4
@@ -158,6 +159,8 @@ def _declare(L):
         "moe_clear_status": [p, p],
         "moe_query_status": [p, p],
     }
+    for name in ("fp8_gemm", "dense_w8a8_forward", "dense_w8a8_backward"):
+        sig[name + "_one_order"] = sig[name]
     for name, args in sig.items():
         f = getattr(L, name)
         f.argtypes = args
@@ -461,25 +464,27 @@ def fp8_gemm_ws_bytes(rows, N, K) -> int:
     return int(lib().fp8_gemm_ws_bytes(rows, N, K))
 
 
-def fp8_gemm(rows, N, K, A, As, W, Ws, Y, ws, stream=None):
-    _check(lib().fp8_gemm(rows, N, K, _ptr(A), _ptr(As), _ptr(W), _ptr(Ws), _ptr(Y), _ptr(ws),
-                          _nbytes(ws), _stream(stream)), "fp8_gemm")
+def fp8_gemm(rows, N, K, A, As, W, Ws, Y, ws, stream=None, one_order=False):
+    f = lib().fp8_gemm_one_order if one_order else lib().fp8_gemm
+    _check(f(rows, N, K, _ptr(A), _ptr(As), _ptr(W), _ptr(Ws), _ptr(Y), _ptr(ws), _nbytes(ws),
+             _stream(stream)), "fp8_gemm")
 
 
 def dense_w8a8_ws_bytes(rows, N, K, adapter=False) -> int:
     return int(lib().dense_w8a8_ws_bytes(rows, N, K, int(adapter)))
 
 
-def dense_w8a8_forward(q, s, N, K, block, R, rows, X, Y, ws, pow2=False, stream=None):
-    _check(lib().dense_w8a8_forward(_ptr(q), _ptr(s), N, K, block, _ptr(R), rows, _ptr(X), int(pow2),
-                                    _ptr(Y), _ptr(ws), _nbytes(ws), _stream(stream)),
-           "dense_w8a8_forward")
+def dense_w8a8_forward(q, s, N, K, block, R, rows, X, Y, ws, pow2=False, stream=None, one_order=False):
+    f = lib().dense_w8a8_forward_one_order if one_order else lib().dense_w8a8_forward
+    _check(f(_ptr(q), _ptr(s), N, K, block, _ptr(R), rows, _ptr(X), int(pow2), _ptr(Y), _ptr(ws),
+             _nbytes(ws), _stream(stream)), "dense_w8a8_forward")
 
 
-def dense_w8a8_backward(qt, st, N, K, block, R, rows, X, dY, dX, dR, ws, pow2=False, stream=None):
-    _check(lib().dense_w8a8_backward(_ptr(qt), _ptr(st), N, K, block, _ptr(R), rows, _ptr(X), _ptr(dY),
-                                     int(pow2), _ptr(dX), _ptr(dR), _ptr(ws), _nbytes(ws),
-                                     _stream(stream)), "dense_w8a8_backward")
+def dense_w8a8_backward(qt, st, N, K, block, R, rows, X, dY, dX, dR, ws, pow2=False, stream=None,
+                        one_order=False):
+    f = lib().dense_w8a8_backward_one_order if one_order else lib().dense_w8a8_backward
+    _check(f(_ptr(qt), _ptr(st), N, K, block, _ptr(R), rows, _ptr(X), _ptr(dY), int(pow2), _ptr(dX),
+             _ptr(dR), _ptr(ws), _nbytes(ws), _stream(stream)), "dense_w8a8_backward")
 
 
 def grad_ws_bytes() -> int:
