@@ -534,9 +534,10 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
  *   its group_sum (1 or 2) largest c, the best topk_groups groups stay
  *   idx = the k experts of these groups with the largest c, in descending order
  *   w_j = factor s_j / (sum_i s_i + 1e-20)          (renorm; else factor s_j)
- * Ties go to the lower group or expert.  The choice is that of the exact c: where
- * FP32 cannot tell two of them apart they are formed in FP64 (of equal c in FP64
- * the lower id is taken).  Without a bias the order is that of the logits.
+ * Ties go to the lower group or expert (-0 and +0 are equal).  The choice is that of
+ * the exact c: where FP32 cannot tell two of them apart they are formed in FP64 (of
+ * equal c in FP64 the lower id is taken).  Without a bias the order is that of the
+ * logits.
  * A logit of -inf is an expert that is chosen only where fewer than k others are
  * left (with the weight 0), and adds nothing to its group; other logits and the
  * bias are finite.
@@ -553,7 +554,9 @@ pmoe_status moe_route_backward(pmoe_dims dims, const float *logits, const int32_
  *          part of moe_route_backward), else written
  * Requires 1 <= E <= 4096, 1 <= k <= 32, groups <= 32, E % groups == 0,
  * k <= topk_groups E / groups, factor finite.  No workspace; a token's results do
- * not depend on the other tokens.
+ * not depend on the other tokens.  Made for k up to about 16 and E up to 1024; beyond
+ * that slower searches serve (8192 tokens of 384 experts with a bias: 13 us at k = 8,
+ * 42 at k = 24, 182 at k = 32; of 4096 experts 200 at k = 8).
  */
 enum { PMOE_SCORE_SIGMOID = 0, PMOE_SCORE_SOFTMAX = 1 };
 typedef struct {
@@ -603,7 +606,9 @@ pmoe_status moe_router_logits(pmoe_dims dims, const void *X, const float *Wr, fl
  * fp8_gemm_one_order: the same without the sharing.  A row's result is that of the
  *   blocks added in their order, bit for bit, whatever the number of rows.
  *   ws >= fp8_gemm_ws_bytes(rows, N, K) (the error word)
- * rows, N, K <= 2^20 (rows 2^24).  q, qt, A and W are E4M3 codes.
+ * N, K <= 2^20, rows <= 2^24 and rows ceil(max(N, K) / 128) < 2^30 (fp8_quantize: of K
+ * alone); beyond that the calls are refused and the size functions return 0.  q, qt, A
+ * and W are E4M3 codes.
  */
 pmoe_status fp8_quantize(int32_t rows, int32_t K, const void *X, int pow2, void *q, float *s,
                          cudaStream_t stream);

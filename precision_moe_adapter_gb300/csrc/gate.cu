@@ -336,12 +336,12 @@ __device__ __noinline__ int order_exact(const Args &a, const float *row, Norm n,
 // largest values bounds the (k + 2)-th largest of all from below, and the experts from
 // there up (some 11 for k = 8, E = 384) are gathered, one a lane, and ranked.  (Taking the
 // largest k times over, each time looking through all of them again, took 1280 instructions
-// a token at k = 8, E = 384, against 840, and 18.6 us for 8192 tokens against 11.)  The values
+// a token at k = 8, E = 384, against 870, and 18.6 us for 8192 tokens against 12.)  The values
 // of that search are c by approximate exponentials (by tanh.approx it was no faster); the
 // candidates' scores are computed in full.
 //
-// Bound by the issue of instructions, 60 to 70% of the slots at 32 warps an SM: 840 a token for
-// E = 384 without groups, 1190 for E = 256 with 8 (20 us for 16384 tokens; their logits are 2.5
+// Bound by the issue of instructions, 60 to 70% of the slots at 32 warps an SM: 870 a token for
+// E = 384 without groups, 1180 for E = 256 with 8 (23 us for 16384 tokens; their logits are 2.5
 // us of HBM).  Fewer registers (12 CTAs of 4 warps an SM) or more (6) take the same or 10% longer.
 // CTAs of 4 warps an SM: 8 (64 registers) up to 512 experts, 5 up to 1024.  With the registers
 // that the compiler takes by itself 8192 tokens of 512 experts, biased, take 16.7 us instead of

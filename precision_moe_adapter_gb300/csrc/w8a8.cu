@@ -190,8 +190,8 @@ static Tiling tiling(int64_t M, int64_t N, int64_t ksteps, bool one_order)
     const int64_t most = std::max<int64_t>(8, (48ll << 20) / std::max<int64_t>(stripe, 1));
     t.gm = (int)cdiv(t.mt, cdiv(t.mt, most));
     // Few tiles: the blocks of K are shared out among the CTAs of a cluster.  A step takes
-    // 0.24 us, the join 1 us and 0.3 a CTA, and 1.5 more where there are several tiles of rows.
-    // us, shared and not: 1 x 4096 x 7168 (rows x N x K; by 4) 9.1 and 17.5; 64 x 7168 x 7168
+    // 0.24 us (one row, while HBM keeps up), the join 1 us and 0.3 a CTA, and 1.5 more where there are several tiles of rows.
+    // us (W in the L2 in part), shared and not: 1 x 4096 x 7168 (rows x N x K; by 4) 9.1 and 17.5; 64 x 7168 x 7168
     // (by 2) 15.9 and 21.3; 16 x 512 x 18432 (by 8) 10.1 and 37.6; 128 x 2048 x 2048 (by 4) 8.5,
     // by 8 8.9, not 9.3; and 32 x 128 x 512 (by 2) 6.0 and 5.1; 333 x 1104 x 2064 (by 5) 11.7 and 10.3.
     t.splits = 1;
@@ -329,8 +329,8 @@ static pmoe_status check_dense(const void *q, const float *s, int N, int K, int 
 
 // The entry points; one_order: no sharing of a tile's blocks of K, so that they are added
 // in the same order whatever the rows of the call.  The layer's forward in a graph, each weight
-// read from HBM, shared and in one order: 1 x 4096 x 7168 11.2 and 18.1 us, 64 x 7168 x 7168
-// 16.3 and 21.4, 128 x 4096 x 4096 11.1 and 14.0; the same where nothing is shared.
+// read from HBM, shared and in one order: 1 x 4096 x 7168 11.1 and 17.9 us, 64 x 7168 x 7168
+// 16.1 and 21.3, 128 x 4096 x 4096 11.1 and 13.9; the same where nothing is shared.
 static pmoe_status gemm(int32_t rows, int32_t N, int32_t K, const void *A, const float *As, const void *W, const float *Ws,
                         void *Y, void *ws, size_t ws_bytes, bool one_order, cudaStream_t stream)
 {

@@ -13,13 +13,17 @@
 // through distributed shared memory and are added in order, each CTA a share of the
 // rows, so that neither a second kernel nor FP32 sums in memory are needed.
 //
-// What bounds it.  Many rows: the card's power.  16384 rows, N = K = 7168 take 670 us (2.5
-// PFLOP/s, 1.46 times the BF16 rate that the card sustains), as much as without the drain of
-// the TMEM buffers.  Shorter products: 4096 x 4096 x 7168 takes 115 us (2.1 PFLOP/s, 3.4 rounds
+// What bounds it.  Many rows: 16384 rows, N = K = 7168 take 670 us (2.5 PFLOP/s, 1.46 times the
+// BF16 rate that the card sustains), as much as without the drain of the TMEM buffers; for seconds
+// on end 689 us at the card's power limit, which takes 6% off the SM clock (1366 W, 1942 MHz of
+// 2070).  Shorter products: 4096 x 4096 x 7168 takes 115 us (2.1 PFLOP/s, 3.4 rounds
 // of tiles taking 4, the tensor pipe 54% active); without the drain (8 loads of 16 columns
-// and 128 multiply-adds a thread and step) forward and dX are 22% faster.  Few rows: the read of W, 16 KB a CTA
-// and 0.27 us; and, beside it, some 5 us of launches, of the wait for the codes of A and of the join
-// (64 rows, N = K = 7168: 15.6 us, of which W at the rate of a copy is 7.6).
+// and 128 multiply-adds a thread and step) forward and dX are 22% faster.  Few rows: a step of a CTA,
+// 16 KB of W, takes 0.24 us at one row and 0.27 at 64 while up to 56 CTAs run, a rate of the CTA
+// and not of the memory; with 112 CTAs 0.27 at one row, 6.8 TB/s, and 0.35 at 64, 5.3 TB/s.
+// Beside the steps stand some 5 us of launches, of the wait for the codes of A and of the join
+// (64 rows, N = K = 7168, the layer in a graph: 16.1 us where W comes from HBM, of which at a
+// copy's rate it is 7.6; 15.3 with two weights, which the L2 holds in part).
 // Kept from what was tried: the buffer is released before the last columns are added; eight
 // epilogue warps; W's first stages on their way before the kernel before is done (0.2 to 0.4
 // us).  Not kept: pairs of sums in one instruction (fma.rn.f32x2: 1943 us against 1438 for
